@@ -431,6 +431,120 @@ MOE_API moe_status_t moe_permute_static_scratch(moe_handle_t h, const moe_config
                                                 int32_t* flat_to_perm, void* x_perm,
                                                 uint8_t* x_perm_scale, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around the layer, and its gradient. Python: add_rmsnorm, combine_backward
+ * and so on; MoEBlock runs them together.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of a residual stream. */
+typedef enum { MOE_RES_BF16 = 0, MOE_RES_F32 = 1 } moe_residual_t;
+
+/* Residual add + RMS norm in front of the layer:
+ *   s = x + residual;  h_out = s in the residual's type
+ *   rstd = 1 / sqrt(mean_c(s^2) + eps);  n = s * rstd * weight
+ *   out = bf16(n);  (q, q_scale) = n as MXFP8, by the rule of
+ *   moe_quantize_mxfp8 applied to the fp32 n (rounded once); a block that
+ *   holds a NaN keeps it (scale code 247, element code 0x7F).
+ * s, rstd and n are fp32. out is the router's and the bf16 layer's input; q
+ * and q_scale are the MX layers' x and x_scale_or_null (moe_layer_forward).
+ * x (device): [rows, H] bf16. residual (device, nullable: s = x): [rows, H] of
+ * res_type. weight (device): [H] bf16. Outputs (device), each nullable, at
+ * least one of out and q given: h_out [rows, H] of res_type, out [rows, H]
+ * bf16, q [rows, H] with q_scale [rows, H/32] uint8 (both or neither, H % 32
+ * == 0), rstd [rows] fp32 (for moe_add_rmsnorm_backward). h_out may be the
+ * residual itself (or x, in bf16) and out may be x; no other overlap.
+ * Limits: 1 <= H <= 16384, rows < 2^31, eps finite and >= 0. A row whose
+ * H * 2 bytes are not a multiple of 16 (H % 8 != 0) is read element by
+ * element. */
+MOE_API moe_status_t moe_add_rmsnorm(moe_handle_t h, int64_t rows, int H, moe_residual_t res_type, const void* x,
+                                     const void* residual, const void* weight, float eps, void* h_out, void* out,
+                                     uint8_t* q, uint8_t* q_scale, float* rstd, moe_stream_t stream);
+
+/* Scratch bytes moe_add_rmsnorm_backward needs (host-only). */
+MOE_API moe_status_t moe_add_rmsnorm_backward_workspace_size(int64_t rows, int H, size_t* bytes);
+
+/* Gradient of moe_add_rmsnorm at the stored h (= h_out) and rstd:
+ *   xhat = h * rstd;  g = dout * weight
+ *   dh = rstd * (g - xhat * mean_c(g * xhat)) + dh_in
+ *   dweight = sum over the rows of dout * xhat
+ * dh is the gradient of both x and residual. The rounding to MXFP8 counts as
+ * the identity: dout is the gradient of n.
+ * dout (device): [rows, H] bf16. dh_in (device, nullable): [rows, H] of
+ * res_type, the gradient that reaches h_out on its own path. h: [rows, H] of
+ * res_type. Outputs: dh [rows, H] of res_type; dx (nullable) [rows, H], the
+ * same rounded to bf16 (for an fp32 stream's x); dweight (nullable) [H] fp32,
+ * summed in a fixed order. dh may be dh_in or h, and dx may be dout; no other
+ * overlap. ws: moe_add_rmsnorm_backward_workspace_size bytes (may be NULL
+ * without dweight). Limits as moe_add_rmsnorm. */
+MOE_API moe_status_t moe_add_rmsnorm_backward(moe_handle_t h, int64_t rows, int H, moe_residual_t res_type,
+                                              const void* dout, const void* dh_in, const void* h_res,
+                                              const void* weight, const float* rstd, void* dh, void* dx,
+                                              float* dweight, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of moe_combine, and (with logits) of moe_route. p is
+ * flat_to_perm[t*K + k]:
+ *   dy_perm[p] = bf16(topk_w[t,k] * dout[t]);  dtopk_w[t,k] = <dout[t], y_perm[p]>
+ *   dlogits as moe_route_backward.
+ * The gradient of shared_out is dout itself. dout (device): [T, H] bf16;
+ * y_perm [T*K, H] fp32, topk_w, flat_to_perm as moe_combine took them. Outputs
+ * (device): dy_perm [T*K, H] bf16 (a row that no pair maps to is not written),
+ * dtopk_w [T, K] fp32 (0 for a dropped pair, -1 in flat_to_perm). topk_idx
+ * [T, K], logits [T, E] and dlogits [T, E] fp32 out: all three or none. Other
+ * entries out of range are treated and reported as in moe_combine and
+ * moe_route_backward. cfg->dtype and I are not looked at beyond their checks. */
+MOE_API moe_status_t moe_combine_backward(moe_handle_t h, const moe_config_t* cfg, const void* dout,
+                                          const float* y_perm, const float* topk_w, const int32_t* flat_to_perm,
+                                          const int32_t* topk_idx, const float* logits, void* dy_perm,
+                                          float* dtopk_w, float* dlogits, moe_stream_t stream);
+
+/* Gradient of moe_route at the chosen experts: with s_k = sigma(logits[t,
+ * topk_idx[t,k]]) and S = sum_j s_j,
+ *   dlogits[t, topk_idx[t,k]] = scaling s_k (1 - s_k) sum_j s_j (dw_k - dw_j) / S^2  (route_norm)
+ *                             = scaling s_k (1 - s_k) dw_k                           (else)
+ * and 0 for every other expert (the choice itself has no gradient). logits
+ * [T, E], dtopk_w [T, K], dlogits [T, E] fp32 (device), distinct. An id outside
+ * [0, E) counts as s_k = 0 and records MOE_DEV_BAD_EXPERT_ID. */
+MOE_API moe_status_t moe_route_backward(moe_handle_t h, const moe_config_t* cfg, const float* logits,
+                                        const int32_t* topk_idx, const float* dtopk_w, float* dlogits,
+                                        moe_stream_t stream);
+
+/* Gradient of moe_permute's row gather:
+ *   dx[t] = bf16( sum_{k=0..K-1} dx_perm[flat_to_perm[t*K+k]] + dx_add[t] )
+ * summed in fp32 in that order. dx_perm (device): [T*K, H] bf16; dx_add
+ * (device, nullable): [T, H] bf16, for example the shared expert's gradient;
+ * dx (device): [T, H] bf16 out, may be dx_add. Entries of flat_to_perm out of
+ * range as in moe_combine. */
+MOE_API moe_status_t moe_permute_backward(moe_handle_t h, const moe_config_t* cfg, const void* dx_perm,
+                                          const int32_t* flat_to_perm, const void* dx_add, void* dx,
+                                          moe_stream_t stream);
+
+/* Scratch bytes moe_grouped_swiglu_backward needs: 10 bytes per row and
+ * intermediate feature. */
+MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_groups, int H, int I,
+                                                                moe_dtype_t dtype, size_t* bytes);
+
+/* Gradient of moe_grouped_swiglu_gemm (bf16): with the same a, offsets and
+ * weights, and dy the gradient of y,
+ *   gate = a W_gate^T, up = a W_up^T (computed again), q = dy W_down
+ *   h = silu(gate) up;  dup = q silu(gate);
+ *   dgate = q up sigma(gate) (1 + gate (1 - sigma(gate)))
+ *   da = dgate W_gate + dup W_up
+ *   dw_down = dy^T h;  dw_gate = dgate^T a;  dw_up = dup^T a   per group
+ * fp32 accumulation; h, dgate and dup are rounded to bf16 once (as the tensor
+ * cores take them), and so is each output.
+ * a, dy (device): [rows, H] bf16. Outputs (device): da [rows, H] bf16
+ * (nullable; rows outside every group are not written); dw_gate, dw_up
+ * [num_groups, I, H] and dw_down [num_groups, H, I] bf16 (all three or none;
+ * overwritten; a group without rows gets zeros). At least one of da and the
+ * dw's. No output overlaps an input. dtype: MOE_BF16 (else
+ * MOE_ERR_UNSUPPORTED). offsets, limits: as moe_grouped_swiglu_gemm, and H,
+ * I <= 65536. */
+MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups, int rows, int H, int I,
+                                                 moe_dtype_t dtype, const void* a, const void* dy,
+                                                 const int32_t* offsets, const void* w_gate, const void* w_up,
+                                                 const void* w_down, void* da, void* dw_gate, void* dw_up,
+                                                 void* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Launch one block whose thread waits on an mbarrier that nothing ever
  * arrives on, with the handle's wait limit; the wait gives up, records
  * MOE_DEV_TIMEOUT_SELFTEST in the status word and the kernel returns. Used to

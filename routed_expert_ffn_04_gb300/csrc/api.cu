@@ -238,6 +238,10 @@ cudaError_t gate_route(moe_handle_t h, const moe_config_t* c, const void* x, con
 namespace moe {
 int handle_device(moe_handle_t h) { return h->device; }
 int* handle_status_word(moe_handle_t h) { return h->status; }
+int handle_num_sms(moe_handle_t h) { return h->num_sms; }
+uint64_t handle_wait_limit_ns(moe_handle_t h) { return h->wait_limit_ns; }
+moe_status_t check_config(const moe_config_t* cfg) { return check_cfg(cfg); }
+moe_status_t bind_handle(moe_handle_t h) { return check_handle(h); }
 }  // namespace moe
 
 extern "C" {
@@ -269,7 +273,7 @@ MOE_API moe_status_t moe_create(int device, moe_handle_t* out) {
   h->device = device;
   h->num_sms = sms;
   if (gemm_prepare_device() != cudaSuccess || gemm_mx_prepare_device() != cudaSuccess ||
-      permute_prepare_device() != cudaSuccess ||
+      permute_prepare_device() != cudaSuccess || gemm_grad_prepare_device() != cudaSuccess ||
       gate_small_prepare_device() != cudaSuccess ||
       cudaMalloc(&h->status, 64) != cudaSuccess ||
       cudaMemset(h->status, 0, 64) != cudaSuccess ||

@@ -1,0 +1,268 @@
+// Gradient of the token dispatch: of the weighted combine (step 4), of the
+// routing weights (step 1) and of the permutation (step 2). p(t,k) is
+// flat_to_perm[t*K + k], sigma_k the sigmoid of the k-th chosen expert's logit.
+//
+//   combine: out[t] = sum_k w[t,k] y[p(t,k)] + shared[t]
+//     dy[p(t,k)] = w[t,k] * dout[t];  dw[t,k] = <dout[t], y[p(t,k)]>;  dshared = dout
+//   routing: w_k = scaling * sigma_k / S, S = sum_j sigma_j (route_norm), or scaling * sigma_k
+//     dl_k = scaling * sigma_k (1 - sigma_k) * sum_j sigma_j (dw_k - dw_j) / S^2   (route_norm)
+//     dl_k = scaling * sigma_k (1 - sigma_k) * dw_k                                (else)
+//     and 0 for the experts that were not chosen. The differences dw_k - dw_j
+//     are taken before the sum, which keeps the digits that dw_k S - sum_j
+//     sigma_j dw_j would cancel.
+//   permutation: x_perm[p(t,k)] = x[t]
+//     dx[t] = sum_k dx_perm[p(t,k)] + dx_add[t]
+//
+// Bound: HBM. The combine's gradient reads the K fp32 rows of y once and
+// writes the K bf16 rows of dy; dout[t] is read once per token. Sums are fp32
+// in a fixed order (no atomics); dy and dx are rounded once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxK = 32;
+constexpr int kBatch = 8;  // slots whose rows one pass over the columns holds in flight
+
+__device__ __forceinline__ void unpack8(const uint4& a, float (&f)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(w[j] << 16);
+    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// dlogits[0..E-1] of one token, by one warp; lane k holds slot k's dw. The
+// row has been zeroed before (and that is visible to this warp).
+__device__ __forceinline__ void route_grad_warp(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                                                float dw, int E, int K, float scaling, int route_norm, float* dlogits,
+                                                int* status) {
+  const int lane = threadIdx.x & 31;
+  int e = -1;
+  float sg = 0.0f, om = 0.0f;  // sigma and 1 - sigma
+  if (lane < K) {
+    e = idx[lane];
+    if ((unsigned)e < (unsigned)E) {
+      const float l = logits[e];
+      sg = 1.0f / (1.0f + expf(-l));
+      om = 1.0f / (1.0f + expf(l));
+    } else {
+      atomicCAS(status, 0, MOE_DEV_BAD_EXPERT_ID);
+      e = -1;
+    }
+  }
+  float d = dw;
+  if (route_norm) {
+    float S = 0.0f, a = 0.0f;
+    for (int j = 0; j < K; ++j) {
+      const float sj = __shfl_sync(0xFFFFFFFFu, sg, j), dj = __shfl_sync(0xFFFFFFFFu, dw, j);
+      S += sj;
+      a = fmaf(sj, dw - dj, a);
+    }
+    d = a / S / S;
+  }
+  if (e >= 0) dlogits[e] = scaling * sg * om * d;
+}
+
+// One block per token: every thread takes 8 columns at a time of dout and of
+// up to kBatch of the token's y rows (two 16-byte loads each, all in flight
+// together), writes the dy rows and keeps the slots' partial dot products.
+__global__ void __launch_bounds__(512) combine_bwd_kernel(const __nv_bfloat16* __restrict__ dout,
+                                                          const float* __restrict__ y, const float* __restrict__ topk_w,
+                                                          const int32_t* __restrict__ f2p, int T, int K, int H, int E,
+                                                          float scaling, int route_norm,
+                                                          const int32_t* __restrict__ topk_idx,
+                                                          const float* __restrict__ logits,
+                                                          __nv_bfloat16* __restrict__ dy, float* __restrict__ dtopk_w,
+                                                          float* __restrict__ dlogits, int* status) {
+  __shared__ float sw[kMaxK];
+  __shared__ int32_t sp[kMaxK];
+  __shared__ float part[16][kBatch];
+  __shared__ float sdw[kMaxK];
+  const int t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (threadIdx.x < K) {
+    const size_t f = (size_t)t * K + threadIdx.x;
+    int32_t p = f2p[f];
+    if ((unsigned)p >= (unsigned)(T * K)) {
+      // -1: a pair that the permutation dropped and has reported already.
+      if (p != -1) atomicCAS(status, 0, MOE_DEV_BAD_PERM_INDEX);
+      p = -1;
+    }
+    sp[threadIdx.x] = p;
+    sw[threadIdx.x] = topk_w[f];
+  }
+  if (dlogits)
+    for (int e = threadIdx.x; e < E; e += blockDim.x) dlogits[(size_t)t * E + e] = 0.0f;
+  __syncthreads();
+  const int H8 = H >> 3;
+  const uint4* drow = reinterpret_cast<const uint4*>(dout + (size_t)t * H);
+  for (int k0 = 0; k0 < K; k0 += kBatch) {
+    float acc[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) acc[j] = 0.0f;
+    for (int c = threadIdx.x; c < H8; c += blockDim.x) {
+      float d[8];
+      unpack8(__ldg(drow + c), d);
+      float4 v[kBatch][2];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int p = k0 + j < K ? sp[k0 + j] : -1;
+        if (p >= 0) {
+          const float4* yr = reinterpret_cast<const float4*>(y + (size_t)p * H) + 2 * c;
+          v[j][0] = __ldg(yr);
+          v[j][1] = __ldg(yr + 1);
+        } else {
+          v[j][0] = v[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int p = k0 + j < K ? sp[k0 + j] : -1;
+        if (p < 0) continue;
+        acc[j] = fmaf(d[0], v[j][0].x, acc[j]);
+        acc[j] = fmaf(d[1], v[j][0].y, acc[j]);
+        acc[j] = fmaf(d[2], v[j][0].z, acc[j]);
+        acc[j] = fmaf(d[3], v[j][0].w, acc[j]);
+        acc[j] = fmaf(d[4], v[j][1].x, acc[j]);
+        acc[j] = fmaf(d[5], v[j][1].y, acc[j]);
+        acc[j] = fmaf(d[6], v[j][1].z, acc[j]);
+        acc[j] = fmaf(d[7], v[j][1].w, acc[j]);
+        const float w = sw[k0 + j];
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = w * d[i];
+        reinterpret_cast<uint4*>(dy + (size_t)p * H)[c] = pack8(o);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], off);
+      if (lane == 0) part[warp][j] = acc[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < kBatch && k0 + threadIdx.x < K) {
+      float s = 0.0f;
+      for (int i = 0; i < nw; ++i) s += part[i][threadIdx.x];
+      sdw[k0 + threadIdx.x] = s;
+      dtopk_w[(size_t)t * K + k0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+  if (dlogits && warp == 0)
+    route_grad_warp(logits + (size_t)t * E, topk_idx + (size_t)t * K, lane < K ? sdw[lane] : 0.0f, E, K, scaling,
+                    route_norm, dlogits + (size_t)t * E, status);
+}
+
+// The routing's gradient alone: one warp per token.
+__global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict__ logits,
+                                                        const int32_t* __restrict__ topk_idx,
+                                                        const float* __restrict__ dtopk_w, int T, int E, int K,
+                                                        float scaling, int route_norm, float* __restrict__ dlogits,
+                                                        int* status) {
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= T) return;
+  float* dl = dlogits + (size_t)t * E;
+  for (int e = lane; e < E; e += 32) dl[e] = 0.0f;
+  __syncwarp();
+  route_grad_warp(logits + (size_t)t * E, topk_idx + (size_t)t * K, lane < K ? dtopk_w[(size_t)t * K + lane] : 0.0f, E,
+                  K, scaling, route_norm, dl, status);
+}
+
+// dx: a work unit is one token's chunk of 8 * blockDim columns; a thread adds
+// its 8 columns of the K rows (batches of 8 loads in flight), k ascending.
+__global__ void __launch_bounds__(256) permute_bwd_kernel(const __nv_bfloat16* __restrict__ dxp,
+                                                          const int32_t* __restrict__ f2p, int T, int K, int H,
+                                                          int chunks, const __nv_bfloat16* add, __nv_bfloat16* dx,
+                                                          int* status) {
+  __shared__ int32_t sp[kMaxK];
+  const long long u = blockIdx.x;
+  const int t = (int)(u / chunks);
+  const int c = (int)(u - (long long)t * chunks) * blockDim.x + threadIdx.x;
+  if (threadIdx.x < K) {
+    int32_t p = f2p[(size_t)t * K + threadIdx.x];
+    if ((unsigned)p >= (unsigned)(T * K)) {
+      if (p != -1) atomicCAS(status, 0, MOE_DEV_BAD_PERM_INDEX);
+      p = -1;
+    }
+    sp[threadIdx.x] = p;
+  }
+  __syncthreads();
+  if (c >= (H >> 3)) return;
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+  uint4 a = make_uint4(0u, 0u, 0u, 0u);
+  if (add) a = reinterpret_cast<const uint4*>(add + (size_t)t * H)[c];
+  for (int k0 = 0; k0 < K; k0 += kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int p = k0 + j < K ? sp[k0 + j] : -1;
+      v[j] = p >= 0 ? __ldg(reinterpret_cast<const uint4*>(dxp + (size_t)p * H) + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      float f[8];
+      unpack8(v[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += f[i];
+    }
+  }
+  float f[8];
+  unpack8(a, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] += f[i];
+  reinterpret_cast<uint4*>(dx + (size_t)t * H)[c] = pack8(s);
+}
+
+}  // namespace
+
+cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  int threads = (a.H / 8 + 31) / 32 * 32;
+  threads = threads > 512 ? 512 : (threads < 32 ? 32 : threads);
+  combine_bwd_kernel<<<a.T, threads, 0, s>>>(static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w,
+                                             a.flat_to_perm, a.T, a.K, a.H, a.E, a.scaling, a.route_norm, a.topk_idx,
+                                             a.logits, static_cast<__nv_bfloat16*>(a.dy_perm), a.dtopk_w, a.dlogits,
+                                             a.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_route_backward(const float* logits, const int32_t* topk_idx, const float* dtopk_w, int T, int E,
+                                  int K, float scaling, int route_norm, float* dlogits, int* status, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  route_bwd_kernel<<<(T + 7) / 8, 256, 0, s>>>(logits, topk_idx, dtopk_w, T, E, K, scaling, route_norm, dlogits, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_permute_backward(const void* dx_perm, const int32_t* flat_to_perm, int T, int K, int H,
+                                    const void* dx_add, void* dx, int* status, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  int threads = (H / 8 + 31) / 32 * 32;
+  threads = threads > 256 ? 256 : threads;
+  const int chunks = (H / 8 + threads - 1) / threads;
+  const long long grid = (long long)T * chunks;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  permute_bwd_kernel<<<(unsigned)grid, threads, 0, s>>>(static_cast<const __nv_bfloat16*>(dx_perm), flat_to_perm, T, K,
+                                                        H, chunks, static_cast<const __nv_bfloat16*>(dx_add),
+                                                        static_cast<__nv_bfloat16*>(dx), status);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,668 @@
+// Gradient of the grouped SwiGLU expert products (step 3), bf16 operands, fp32
+// accumulation on the 5th-generation tensor cores. For the rows r of group g,
+// with a the rows' inputs and dy the gradient of their outputs:
+//
+//   gate = a Wg^T, up = a Wu^T, h = silu(gate) * up, y = h Wd^T   (the forward)
+//   Q  (DOWN):   q = dy Wd                                        [rows, I] fp32
+//   GU (SWIGLU): gate and up once more, then
+//                h = silu(gate) up;  du = q silu(gate);
+//                dg = q up sigma(gate) (1 + gate (1 - sigma(gate)))  [rows, I] bf16
+//   DX (INPUT):  da = dg Wg + du Wu                               [rows, H] bf16
+//   DW (WEIGHT): dWd = dy^T h;  dWg = dg^T a;  dWu = du^T a       per group, bf16
+//
+// 16 rows H I FLOP in all: 12 for the gradient and 4 to recompute gate and up,
+// which the forward does not keep. q stays fp32 between the launches; h, dg
+// and du are rounded to bf16 once, as the tensor cores read them.
+//
+// One kernel, four modes. Persistent, one CTA per SM, tiles of 128 x 256 fp32
+// accumulators double-buffered in TMEM (512 columns), K in steps of 64 through
+// a ring of 48 KB stages written by TMA:
+//   warp 0      TMA producer (one thread); modes with more than three boxes per
+//               stage split them with warp 6;
+//   warp 1      TMEM allocation and tcgen05.mma (M = 128, N = 256, K = 16);
+//   warps 2..5  epilogue, 32 accumulator rows each.
+//
+// Operands. The forward's weights are K-major for the forward products; three
+// of the four products here reduce over another axis, so their operands are
+// read MN-major from the same row-major tensors, with no transposed copy: a
+// box of 64 columns x 64 rows lands as 64 rows (the reduction axis) of 128
+// swizzled bytes, the tensor cores' MN-major operand layout, and the
+// instruction descriptor's transpose bit is set.
+//   mode  A (128 rows of M)              B (256 rows of N)           reduction
+//   Q     dy rows, K-major               Wd columns, MN-major        H
+//   GU    a rows, K-major                Wg | Wu rows, K-major       H
+//   DX    dg rows, then du rows, K-major Wg, then Wu columns, MN     I, twice
+//   DW    dy / dg / du columns, MN       h / a columns, MN           the group's rows
+//
+// In DW the reduction runs over a group's rows, which end anywhere: the last
+// stage's box also holds rows of the next group. The MMA runs in steps of 16
+// rows, and the rows between the group's end and the step's end are zeroed in
+// shared memory in both operands first (a zero times another group's infinity
+// would not be zero). A group without rows gives zero gradients.
+//
+// Every wait is bounded; on expiry the CTA records an error code in the status
+// word, drains its in-flight copies and MMAs, frees TMEM and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+#include "gemm_sched.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+enum GradMode { kQ = 0, kGU = 1, kDX = 2, kDW = 3 };
+
+constexpr int kBK = 64;           // reduction elements per stage
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxSmem = 232448;  // 227 KB dynamic shared memory per CTA
+constexpr int kChunk = 64 * 128;  // an MN-major box: 64 rows of 128 bytes
+
+template <int MODE>
+struct GradGeo {
+  static constexpr bool A_MN = MODE == kDW, B_MN = MODE != kGU;
+  static constexpr int A_BYTES = 128 * 128;  // 16 KB: 128 rows of K, or two chunks of 64 columns
+  static constexpr int B_BYTES = 256 * 128;  // 32 KB
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr bool TWO_PRODUCERS = MODE != kGU;
+  static constexpr int THREADS = TWO_PRODUCERS ? 224 : 192;
+  static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 8) * 4;  // tile starts, row starts
+  static constexpr int BAR_BYTES = 512;
+  static constexpr int EPI_WARP = 4096;  // one warp's staging block: 32 rows of 128 bytes
+  static constexpr int EPI_BYTES = 4 * EPI_WARP;
+  static constexpr int EXTRA = 1024 + TABLE_BYTES + BAR_BYTES + EPI_BYTES;
+  static constexpr int S = (kMaxSmem - EXTRA) / STAGE_BYTES;
+  static constexpr int RING_BYTES = S * STAGE_BYTES;
+  static constexpr int SMEM = EXTRA + RING_BYTES;
+  static constexpr int NBARS = 2 * S + 5;
+  static constexpr int TILE_N = MODE == kGU ? 128 : 256;  // output columns per tile
+  static_assert(S >= 4, "ring too shallow");
+  static_assert(RING_BYTES % 1024 == 0 && EPI_WARP % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+  static_assert(NBARS * 8 + 8 <= BAR_BYTES, "barrier area");
+  static_assert(SMEM <= kMaxSmem, "shared memory budget");
+};
+
+struct GradParams {
+  KParams k;              // offsets, G, rows, status, limit_ns; N = output columns
+  int H, I;
+  int num_kb;             // stages per tile (Q, GU: H / 64; DX: 2 I / 64; DW: by group)
+  float* q;               // [rows, I]
+  __nv_bfloat16 *h, *dg, *du;  // [rows, I]
+  __nv_bfloat16* da;      // [rows, H]
+};
+
+// Shared-memory descriptor of an MN-major operand: chunks of 64 columns (128
+// swizzled bytes) by 64 rows of the reduction axis, `kChunk` bytes apart;
+// groups of 8 rows 1024 bytes apart. A step of 16 rows is 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);  // [0,14)  start address >> 4
+  d |= (uint64_t)(kChunk >> 4) << 16;            // [16,30) leading byte offset: next 64 columns
+  d |= (uint64_t)(1024 >> 4) << 32;              // [32,46) stride byte offset: next 8 rows
+  d |= (uint64_t)1 << 46;                        // [46,48) descriptor version (tcgen05)
+  d |= (uint64_t)2 << 61;                        // [61,64) layout: 128-byte swizzle
+  return d;
+}
+
+// One tile of DW: its group, which of the three products, and its corner.
+struct DwTile {
+  int g, which, m0, n0;  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
+};
+__device__ __forceinline__ DwTile dw_tile(const GradParams& p, int tile) {
+  const int nd = ((p.H + 127) / 128) * ((p.I + 255) / 256), ng = ((p.I + 127) / 128) * ((p.H + 255) / 256);
+  DwTile t;
+  t.g = tile / (nd + 2 * ng);
+  int l = tile - t.g * (nd + 2 * ng);
+  t.which = l < nd ? 0 : (l < nd + ng ? 1 : 2);
+  l -= t.which == 0 ? 0 : (t.which == 1 ? nd : nd + ng);
+  const int ncols = t.which == 0 ? (p.I + 255) / 256 : (p.H + 255) / 256;
+  t.m0 = (l / ncols) * 128;
+  t.n0 = (l - (l / ncols) * ncols) * 256;
+  return t;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A warp's block of 32 rows x 64 bf16 columns (lane = row, TMEM columns taddr
+// .. taddr + 63) into its staging buffer, 128-byte rows, 16-byte chunk j of row
+// r at chunk j ^ (r % 8).
+__device__ __forceinline__ void stage_bf16_block(uint32_t taddr, uint8_t* stg, int lane) {
+  uint32_t v[32], u[32];
+  tmem_ld_32x32b_x32(taddr, v);
+  tmem_ld_32x32b_x32(taddr + 32, u);
+  tmem_ld_wait();
+  if (lane == 0) bulk_wait_group_read0();  // the last store has read the buffer
+  __syncwarp();
+  uint8_t* row = stg + lane * 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t w[4], x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
+      x[i] = pack_bf16(__uint_as_float(u[8 * j + 2 * i]), __uint_as_float(u[8 * j + 2 * i + 1]));
+    }
+    *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(row + (((j + 4) ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// The staged block's first `nr` rows to rows row0.. of a row-major bf16 or
+// fp32 matrix whose rows are `pitch` bytes long, at byte `col` (a block that
+// ends inside it: a TMA box would also write the next group's rows).
+__device__ __forceinline__ void copy_staged_rows(const uint8_t* stg, int lane, int nr, uint8_t* base, size_t row0,
+                                                 size_t pitch, size_t col) {
+  __syncwarp();
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int r = it * 4 + (lane >> 3), j = lane & 7;
+    if (r < nr)
+      *reinterpret_cast<uint4*>(base + (row0 + r) * pitch + col + j * 16) =
+          *reinterpret_cast<const uint4*>(stg + r * 128 + ((j ^ (r & 7)) << 4));
+  }
+  __syncwarp();
+}
+
+// Epilogue of one 128 x TILE_N tile by one warp (32 accumulator rows).
+template <int MODE>
+__device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInfo& ti, uint32_t tb, int q, int lane,
+                                              uint8_t* stg, const CUtensorMap* map_out) {
+  const int r0 = ti.tt * 128 + q * 32;  // the warp's first row in the group
+  const int nr = ti.nrows - r0;         // rows of the group from there on
+  if (nr <= 0) return;
+  if (MODE == kGU) {
+    const bool rv = lane < nr;
+    const size_t row = (size_t)ti.row0 + r0 + (rv ? lane : 0);
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      const int col = ti.wt * 128 + c;
+      if (col >= p.I) break;  // I % 64 == 0: a block of 32 columns is whole or absent
+      uint32_t g[32], u[32];
+      tmem_ld_32x32b_x32(tb + c, g);
+      tmem_ld_32x32b_x32(tb + 128 + c, u);
+      tmem_ld_wait();
+      const size_t at = row * p.I + col;
+      uint32_t ph[16], pg[16], pu[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 qv = rv ? reinterpret_cast<const float4*>(p.q + at)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float qq[4] = {qv.x, qv.y, qv.z, qv.w};
+        float hv[4], gv[4], uv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float gt = __uint_as_float(g[4 * j + i]), up = __uint_as_float(u[4 * j + i]);
+          const float sg = 1.0f / (1.0f + __expf(-gt));
+          const float act = gt * sg;
+          hv[i] = act * up;
+          uv[i] = qq[i] * act;
+          gv[i] = qq[i] * up * sg * fmaf(gt, 1.0f - sg, 1.0f);
+        }
+        ph[2 * j] = pack_bf16(hv[0], hv[1]);
+        ph[2 * j + 1] = pack_bf16(hv[2], hv[3]);
+        pg[2 * j] = pack_bf16(gv[0], gv[1]);
+        pg[2 * j + 1] = pack_bf16(gv[2], gv[3]);
+        pu[2 * j] = pack_bf16(uv[0], uv[1]);
+        pu[2 * j + 1] = pack_bf16(uv[2], uv[3]);
+      }
+      if (rv) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          reinterpret_cast<uint4*>(p.h + at)[j] = make_uint4(ph[4 * j], ph[4 * j + 1], ph[4 * j + 2], ph[4 * j + 3]);
+          reinterpret_cast<uint4*>(p.dg + at)[j] = make_uint4(pg[4 * j], pg[4 * j + 1], pg[4 * j + 2], pg[4 * j + 3]);
+          reinterpret_cast<uint4*>(p.du + at)[j] = make_uint4(pu[4 * j], pu[4 * j + 1], pu[4 * j + 2], pu[4 * j + 3]);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (MODE == kQ) {
+    const size_t row = (size_t)ti.row0 + r0;
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 32) {
+      const int col = ti.wt * 256 + c;
+      if (col >= p.I) break;
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tb + c, v);
+      tmem_ld_wait();
+      if (lane == 0) bulk_wait_group_read0();
+      __syncwarp();
+      uint8_t* srow = stg + lane * 128;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(srow + ((j ^ (lane & 7)) << 4)) =
+            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      if (nr >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(map_out, smem_u32(stg), col, (int)row);
+          bulk_commit_group();
+        }
+      } else {
+        copy_staged_rows(stg, lane, nr, reinterpret_cast<uint8_t*>(p.q), row, (size_t)p.I * 4, (size_t)col * 4);
+      }
+    }
+  } else {  // DX
+    const size_t row = (size_t)ti.row0 + r0;
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 64) {
+      const int col = ti.wt * 256 + c;
+      if (col >= p.H) break;
+      stage_bf16_block(tb + c, stg, lane);
+      if (nr >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(map_out, smem_u32(stg), col, (int)row);
+          bulk_commit_group();
+        }
+      } else {
+        copy_staged_rows(stg, lane, nr, reinterpret_cast<uint8_t*>(p.da), row, (size_t)p.H * 2, (size_t)col * 2);
+      }
+    }
+  }
+}
+
+// Operand and output maps. Q: a = dy, b0 = Wd, out = q. GU: a = a, b0 / b1 =
+// Wg / Wu. DX: a = dg, a2 = du, b0 / b1 = Wg / Wu, out = da. DW: by product:
+// A = dy, dg, du (a, a2, a3), B = h (b0) or a (b1); out, out2, out3.
+struct GradMaps {
+  CUtensorMap a, a2, a3, b0, b1, out, out2, out3;
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
+    grouped_grad_kernel(const __grid_constant__ GradMaps m, const GradParams p) {
+  using Gm = GradGeo<MODE>;
+  constexpr int NS = Gm::S;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
+  uint8_t* base = smem_raw + pad;
+  const uint32_t base_u32 = raw_addr + pad;
+  // Shared memory: ring | epilogue staging | tile table | barriers.
+  uint8_t* epi_stage = base + Gm::RING_BYTES;
+  int32_t* tile_start = reinterpret_cast<int32_t*>(epi_stage + Gm::EPI_BYTES);
+  int32_t* row_start = tile_start + kMaxGroups + 8;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + Gm::EPI_BYTES + Gm::TABLE_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Gm::NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (NS + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * NS + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * NS + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.k.G;
+
+  // ---- row starts; tile_start[g] = tiles of groups before g (not DW, where
+  // every group has the same number of tiles).
+  fill_row_start(p.k, row_start, threadIdx.x, Gm::THREADS);
+  if (MODE != kDW) {
+    const int n_wt = (p.k.N + Gm::TILE_N - 1) / Gm::TILE_N;
+    for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
+      int r0, nr;
+      group_rows(p.k, g, r0, nr);
+      tile_start[g] = n_wt * ((nr + 127) / 128);
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&m.a);
+    prefetch_tensormap(&m.b0);
+    if (MODE != kQ) prefetch_tensormap(&m.b1);
+  }
+  __syncthreads();
+  if (MODE != kDW && warp == 0) {  // exclusive scan of the per-group tile counts
+    const int per = (G + 31) / 32;
+    const int b = lane * per < G ? lane * per : G;
+    const int e = (b + per < G) ? b + per : G;
+    int local = 0;
+    for (int g = b; g < e; ++g) local += tile_start[g];
+    int incl = local;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    int run = incl - local;
+    for (int g = b; g < e; ++g) {
+      const int c = tile_start[g];
+      tile_start[g] = run;
+      run += c;
+    }
+    if (lane == 31) tile_start[G] = incl;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int dw_per_group = ((p.H + 127) / 128) * ((p.I + 255) / 256) + 2 * ((p.I + 127) / 128) * ((p.H + 255) / 256);
+  const int total = MODE == kDW ? G * dw_per_group : tile_start[G];
+  auto rows_of = [&](int g) {
+    const int n = row_start[g + 1] - row_start[g];
+    return n > 0 ? n : 0;
+  };
+
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------ producers
+    // Boxes of a stage: A, then B's in order. Warp 0 arms the stage's barrier
+    // with all its bytes; warp 6 (modes with more than three boxes) issues the
+    // last ones (a transaction may land before it is expected).
+    if (lane == 0) {
+      const bool first = warp == 0;
+      Ring rg;
+      Armed armed;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        TileInfo ti = {};
+        DwTile dt = {};
+        int nkb = p.num_kb;
+        if (MODE == kDW) {
+          dt = dw_tile(p, tile);
+          nkb = (rows_of(dt.g) + kBK - 1) / kBK;
+        } else {
+          ti = decode_tile_s<128>(G, tile_start, row_start, tile);
+        }
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status, MOE_DEV_TIMEOUT_PRODUCER,
+                                 p.k.limit_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = full_bar(rg.s);
+          const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
+          if (first) mbar_arrive_expect_tx(fb, Gm::STAGE_BYTES);
+          if (MODE == kGU) {
+            tma_load_2d(sa, &m.a, fb, kb * kBK, ti.row0 + ti.tt * 128);
+            tma_load_2d(sb, &m.b0, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
+            tma_load_2d(sb + Gm::A_BYTES, &m.b1, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
+          } else if (MODE == kQ || MODE == kDX) {
+            // DX: the first half of the stages is dg Wg, the second du Wu.
+            const int half = p.num_kb >> 1;
+            const bool second = MODE == kDX && kb >= half;
+            const int kx = (second ? kb - half : kb) * kBK;
+            const CUtensorMap* mb = second ? &m.b1 : &m.b0;
+            const int krow = ti.g * (MODE == kQ ? p.H : p.I) + kx;
+            if (first) {
+              tma_load_2d(sa, second ? &m.a2 : &m.a, fb, kx, ti.row0 + ti.tt * 128);
+              tma_load_2d(sb, mb, fb, ti.wt * 256, krow);
+            } else {
+#pragma unroll
+              for (int j = 1; j < 4; ++j) tma_load_2d(sb + j * kChunk, mb, fb, ti.wt * 256 + j * 64, krow);
+            }
+          } else {
+            const int krow = row_start[dt.g] + kb * kBK;
+            const CUtensorMap* mb = dt.which == 0 ? &m.b0 : &m.b1;
+            if (first) {
+              const CUtensorMap* ma = dt.which == 0 ? &m.a : (dt.which == 1 ? &m.a2 : &m.a3);
+              tma_load_2d(sa, ma, fb, dt.m0, krow);
+              tma_load_2d(sa + kChunk, ma, fb, dt.m0 + 64, krow);
+              tma_load_2d(sb, mb, fb, dt.n0, krow);
+            } else {
+#pragma unroll
+              for (int j = 1; j < 4; ++j) tma_load_2d(sb + j * kChunk, mb, fb, dt.n0 + j * 64, krow);
+            }
+          }
+          armed.mark(rg);
+          rg.next(NS);
+        }
+      }
+      if (!ok) {  // let copies already issued land before the CTA exits
+        for (int s = 0; s < NS; ++s)
+          if (armed.mask & (1u << s)) drain_wait(full_bar(s), (armed.phase >> s) & 1u, 100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the loop (DW's last stage is cleared by all lanes);
+    // lane 0 waits and issues.
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, 256) | (Gm::A_MN ? 1u << 15 : 0u) | (Gm::B_MN ? 1u << 16 : 0u);
+    constexpr uint32_t kStepA = Gm::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = Gm::B_MN ? 2048 >> 4 : 32 >> 4;
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      int v = 0;
+      if (lane == 0)
+        v = mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA, p.k.limit_ns) ? 1 : 0;
+      return __shfl_sync(0xFFFFFFFFu, v, 0) != 0;
+    };
+    Ring rg;
+    bool ok = true, issued = false;
+    int local = 0;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++local) {
+      const int acc = local & 1;
+      const uint32_t ap = (uint32_t)(local >> 1) & 1u;
+      if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+      int nkb = p.num_kb, nrows = 0;
+      if (MODE == kDW) {
+        nrows = rows_of(dw_tile(p, tile).g);
+        nkb = (nrows + kBK - 1) / kBK;
+      }
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!wait_all(full_bar(rg.s), rg.ph)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
+        int steps = kBK / 16;
+        if (MODE == kDW) {
+          const int left = nrows - kb * kBK;
+          if (left < kBK) {
+            steps = (left + 15) >> 4;
+            // Rows left .. 16 * steps - 1 of all six chunks: eight lanes clear
+            // one 128-byte row. (A row's swizzle stays inside the row.)
+            const int tail = steps * 16 - left;
+            __syncwarp();
+            uint8_t* st = base + rg.s * Gm::STAGE_BYTES;
+            for (int i = lane >> 3; i < tail * 6; i += 4) {
+              const int chunk = i / tail, r = left + (i - chunk * tail);
+              *reinterpret_cast<uint4*>(st + chunk * kChunk + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t da = Gm::A_MN ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
+          const uint64_t db = Gm::B_MN ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
+          for (int k = 0; k < steps; ++k)
+            umma_bf16(d, da + (uint64_t)k * kStepA, db + (uint64_t)k * kStepB, kIdesc, (kb | k) ? 1u : 0u);
+          umma_commit(empty_bar(rg.s));
+        }
+        __syncwarp();
+        issued = true;
+        rg.next(NS);
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(tfull_bar(acc));
+      __syncwarp();
+    }
+    if (!ok && issued && lane == 0) {  // wait for every issued MMA before TMEM is freed
+      umma_commit(drain_bar);
+      drain_wait(drain_bar, 0, 100000000ull);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
+    uint8_t* stg = epi_stage + q * Gm::EPI_WARP;
+    int local = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++local) {
+      const int acc = local & 1;
+      const uint32_t ap = (uint32_t)(local >> 1) & 1u;
+      int ok = 1;
+      if (lane == 0)
+        ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+      if (MODE == kDW) {
+        // 32 x 64 blocks by TMA; H and I are multiples of 64, so a block's rows
+        // all belong to the group's matrix or none does.
+        const DwTile dt = dw_tile(p, tile);
+        const int M = dt.which == 0 ? p.H : p.I, N = dt.which == 0 ? p.I : p.H;
+        const int m0 = dt.m0 + q * 32;
+        const bool empty = rows_of(dt.g) == 0;
+        const CUtensorMap* mo = dt.which == 0 ? &m.out : (dt.which == 1 ? &m.out2 : &m.out3);
+        if (m0 < M) {
+#pragma unroll 1
+          for (int c = 0; c < 256 && dt.n0 + c < N; c += 64) {
+            if (empty) {
+              if (lane == 0) bulk_wait_group_read0();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+            } else {
+              stage_bf16_block(tb + c, stg, lane);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(mo, smem_u32(stg), dt.n0 + c, dt.g * M + m0);
+              bulk_commit_group();
+            }
+          }
+        }
+      } else {
+        const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
+        grad_epilogue<MODE>(p, ti, tb, q, lane, stg, &m.out);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(acc));
+    }
+    if (lane == 0) bulk_wait_group0();  // this warp's bulk stores are complete
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int MODE>
+cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long max_tiles, int num_sms, cudaStream_t s) {
+  if (max_tiles <= 0) return cudaSuccess;
+  const int grid = (int)(max_tiles < num_sms ? max_tiles : num_sms);
+  grouped_grad_kernel<MODE><<<grid, GradGeo<MODE>::THREADS, GradGeo<MODE>::SMEM, s>>>(m, p);
+  return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(grouped_grad_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              GradGeo<MODE>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t gemm_grad_prepare_device() {
+  const cudaError_t errs[] = {set_smem<kQ>(), set_smem<kGU>(), set_smem<kDX>(), set_smem<kDW>()};
+  for (cudaError_t e : errs)
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
+cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_t s) {
+  const int G = a.offsets ? a.G : 1, H = a.H, I = a.I;
+  const bool want_dw = a.dw_gate != nullptr;
+  if (a.rows == 0) {  // no operand to map: every weight gradient is zero
+    cudaError_t e = cudaSuccess;
+    const size_t bytes = (size_t)G * H * I * 2;
+    for (void* d : {a.dw_gate, a.dw_up, a.dw_down})
+      if (d && e == cudaSuccess) e = cudaMemsetAsync(d, 0, bytes, s);
+    return e;
+  }
+  GradParams p = {};
+  p.k.offsets = a.offsets;
+  p.k.G = G;
+  p.k.rows = a.rows;
+  p.k.status = a.status;
+  p.k.limit_ns = a.wait_limit_ns;
+  p.k.fold_group = -1;
+  p.H = H;
+  p.I = I;
+  p.q = a.q;
+  p.h = static_cast<__nv_bfloat16*>(a.h);
+  p.dg = static_cast<__nv_bfloat16*>(a.dg);
+  p.du = static_cast<__nv_bfloat16*>(a.du);
+  p.da = static_cast<__nv_bfloat16*>(a.da);
+  const uint64_t R = a.rows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
+  const long long row_tiles = (a.rows + 127) / 128 + (long long)G;  // at most: one ragged tile per group
+  auto ceil_div = [](long long v, long long d) { return (v + d - 1) / d; };
+  cudaError_t e = cudaSuccess;
+  bool maps = true;
+  {
+    GradMaps m = {};
+    maps = make_tmap_bf16(&m.a, a.dy, H, R, 128) && make_tmap_bf16(&m.b0, a.w_down, I, GH, 64) &&
+           make_tmap_f32_store(&m.out, a.q, I, R);
+    if (!maps) return cudaErrorInvalidValue;
+    p.k.N = I;
+    p.num_kb = H / kBK;
+    e = run_mode<kQ>(m, p, row_tiles * ceil_div(I, 256), a.num_sms, s);
+  }
+  if (e == cudaSuccess) {
+    GradMaps m = {};
+    maps = make_tmap_bf16(&m.a, a.a, H, R, 128) && make_tmap_bf16(&m.b0, a.w_gate, H, GI, 128) &&
+           make_tmap_bf16(&m.b1, a.w_up, H, GI, 128);
+    if (!maps) return cudaErrorInvalidValue;
+    p.k.N = I;
+    p.num_kb = H / kBK;
+    e = run_mode<kGU>(m, p, row_tiles * ceil_div(I, 128), a.num_sms, s);
+  }
+  if (e == cudaSuccess && a.da) {
+    GradMaps m = {};
+    maps = make_tmap_bf16(&m.a, a.dg, I, R, 128) && make_tmap_bf16(&m.a2, a.du, I, R, 128) &&
+           make_tmap_bf16(&m.b0, a.w_gate, H, GI, 64) && make_tmap_bf16(&m.b1, a.w_up, H, GI, 64) &&
+           make_tmap_bf16(&m.out, a.da, H, R, 32);
+    if (!maps) return cudaErrorInvalidValue;
+    p.k.N = H;
+    p.num_kb = 2 * (I / kBK);
+    e = run_mode<kDX>(m, p, row_tiles * ceil_div(H, 256), a.num_sms, s);
+  }
+  if (e == cudaSuccess && want_dw) {
+    GradMaps m = {};
+    maps = make_tmap_bf16(&m.a, a.dy, H, R, 64) && make_tmap_bf16(&m.a2, a.dg, I, R, 64) &&
+           make_tmap_bf16(&m.a3, a.du, I, R, 64) && make_tmap_bf16(&m.b0, a.h, I, R, 64) &&
+           make_tmap_bf16(&m.b1, a.a, H, R, 64) && make_tmap_bf16(&m.out, a.dw_down, I, GH, 32) &&
+           make_tmap_bf16(&m.out2, a.dw_gate, H, GI, 32) && make_tmap_bf16(&m.out3, a.dw_up, H, GI, 32);
+    if (!maps) return cudaErrorInvalidValue;
+    const long long tiles =
+        G * (ceil_div(H, 128) * ceil_div(I, 256) + 2 * ceil_div(I, 128) * ceil_div(H, 256));
+    e = run_mode<kDW>(m, p, tiles, a.num_sms, s);
+  }
+  return e;
+}
+
+}  // namespace moe

@@ -14,6 +14,13 @@ namespace moe {
 // Handle accessors for translation units other than api.cu.
 int handle_device(moe_handle_t h);
 int* handle_status_word(moe_handle_t h);
+int handle_num_sms(moe_handle_t h);
+uint64_t handle_wait_limit_ns(moe_handle_t h);
+// The checks every entry point makes: the layer config, and the handle (made
+// current: its device becomes the calling thread's device).
+moe_status_t check_config(const moe_config_t* cfg);
+moe_status_t bind_handle(moe_handle_t h);
+inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
 
@@ -165,6 +172,87 @@ cudaError_t launch_gate_route(const GroupedGemmArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const float* y_perm, const float* topk_w, const int32_t* flat_to_perm,
                            const float* shared_out, int T, int K, int H, void* out, int* status,
                            cudaStream_t s);
+
+// ---- residual add + RMS norm and its gradient (norm.cu)
+struct NormArgs {
+  long long rows;
+  int H;
+  const void* x;         // [rows, H] bf16
+  const void* residual;  // [rows, H] bf16 or fp32, or nullptr
+  const void* weight;    // [H] bf16
+  float eps;
+  void* h_out;           // [rows, H], the residual's type, or nullptr
+  void* out;             // [rows, H] bf16, or nullptr
+  uint8_t* q;            // [rows, H] E4M3 codes, or nullptr
+  uint8_t* q_scale;      // [rows, H/32]
+  float* rstd;           // [rows], or nullptr
+  bool res_f32;          // the residual stream (residual, h_out) is fp32
+};
+struct NormGradArgs {
+  long long rows;
+  int H;
+  const void* dout;    // [rows, H] bf16
+  const void* dh_in;   // [rows, H], the residual's type, or nullptr
+  const void* h;       // [rows, H], the residual's type
+  const void* weight;  // [H] bf16
+  const float* rstd;   // [rows]
+  void* dh;            // [rows, H], the residual's type
+  void* dx;            // [rows, H] bf16, or nullptr
+  float* dweight;      // [H], or nullptr
+  float* partials;     // [norm_grad_blocks(rows, H), H]
+  bool res_f32;
+};
+int norm_grad_blocks(long long rows, int H);
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_add_rmsnorm_backward(const NormGradArgs& a, cudaStream_t s);
+
+// ---- gradient of the token dispatch (dispatch_grad.cu)
+struct CombineGradArgs {
+  int T, K, H, E;
+  float scaling;
+  int route_norm;
+  const void* dout;             // [T, H] bf16
+  const float* y_perm;          // [T*K, H]
+  const float* topk_w;          // [T, K]
+  const int32_t* flat_to_perm;  // [T*K]
+  const int32_t* topk_idx;      // [T, K]; with logits and dlogits, or nullptr
+  const float* logits;          // [T, E]
+  void* dy_perm;                // [T*K, H] bf16
+  float* dtopk_w;               // [T, K]
+  float* dlogits;               // [T, E], or nullptr
+  int* status;
+};
+cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(const float* logits, const int32_t* topk_idx, const float* dtopk_w, int T, int E,
+                                  int K, float scaling, int route_norm, float* dlogits, int* status, cudaStream_t s);
+// dx_perm [T*K, H] bf16, dx_add [T, H] bf16 or nullptr, dx [T, H] bf16.
+cudaError_t launch_permute_backward(const void* dx_perm, const int32_t* flat_to_perm, int T, int K, int H,
+                                    const void* dx_add, void* dx, int* status, cudaStream_t s);
+
+// ---- gradient of the grouped SwiGLU GEMM (gemm_grad.cu)
+struct GroupedGradArgs {
+  int G;                   // number of groups
+  const int32_t* offsets;  // [G+1] device, or nullptr: one group of `rows`
+  int rows, H, I;
+  const void* a;           // [rows, H] bf16
+  const void* dy;          // [rows, H] bf16
+  const void* w_gate;      // [G, I, H] bf16
+  const void* w_up;        // [G, I, H] bf16
+  const void* w_down;      // [G, H, I] bf16
+  float* q;                // [rows, I] scratch
+  void* h;                 // [rows, I] bf16 scratch
+  void* dg;                // [rows, I] bf16 scratch
+  void* du;                // [rows, I] bf16 scratch
+  void* da;                // [rows, H] bf16, or nullptr
+  void* dw_gate;           // [G, I, H] bf16, or nullptr (all three)
+  void* dw_up;             // [G, I, H] bf16
+  void* dw_down;           // [G, H, I] bf16
+  int num_sms;
+  int* status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t gemm_grad_prepare_device();
+cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_t s);
 
 // ---- MX quantiser (mxquant.cu)
 // q / scale / atoms may each be null. scale: row-major [rows, cols/32];
