@@ -68,11 +68,14 @@ struct GradGeo {
   static constexpr int B_BYTES = 256 * 128;  // 32 KB
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr bool TWO_PRODUCERS = MODE != kGU;
-  static constexpr int THREADS = TWO_PRODUCERS ? 224 : 192;
+  // DW stores a tile every few stages: eight epilogue warps (2-5 and 7-10),
+  // each half of the columns; elsewhere four.
+  static constexpr int EPI_WARPS = MODE == kDW ? 8 : 4;
+  static constexpr int THREADS = MODE == kDW ? 352 : (TWO_PRODUCERS ? 224 : 192);
   static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 8) * 4;  // tile starts, row starts
   static constexpr int BAR_BYTES = 512;
-  static constexpr int EPI_WARP = 4096;  // one warp's staging block: 32 rows of 128 bytes
-  static constexpr int EPI_BYTES = 4 * EPI_WARP;
+  static constexpr int EPI_WARP = MODE == kDW ? 2048 : 4096;  // one warp's staging block: 32 rows of 64 or 128 bytes
+  static constexpr int EPI_BYTES = EPI_WARPS * EPI_WARP;
   static constexpr int EXTRA = 1024 + TABLE_BYTES + BAR_BYTES + EPI_BYTES;
   static constexpr int S = (kMaxSmem - EXTRA) / STAGE_BYTES;
   static constexpr int RING_BYTES = S * STAGE_BYTES;
@@ -92,6 +95,7 @@ struct GradParams {
   float* q;               // [rows, I]
   __nv_bfloat16 *h, *dg, *du;  // [rows, I]
   __nv_bfloat16* da;      // [rows, H]
+  __nv_bfloat16 *dw_down, *dw_gate, *dw_up;  // [G, H, I], [G, I, H], [G, I, H]
 };
 
 // Shared-memory descriptor of an MN-major operand: chunks of 64 columns (128
@@ -107,15 +111,28 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
   return d;
 }
 
-// One tile of DW: its group, which of the three products, and its corner.
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
+// One tile of DW: its group, which of the three products, and its corner. The
+// groups come in `order`: longest first.
 struct DwTile {
   int g, which, m0, n0;  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
 };
-__device__ __forceinline__ DwTile dw_tile(const GradParams& p, int tile) {
+__device__ __forceinline__ DwTile dw_tile(const GradParams& p, const int32_t* order, int tile) {
   const int nd = ((p.H + 127) / 128) * ((p.I + 255) / 256), ng = ((p.I + 127) / 128) * ((p.H + 255) / 256);
   DwTile t;
-  t.g = tile / (nd + 2 * ng);
-  int l = tile - t.g * (nd + 2 * ng);
+  const int slot = tile / (nd + 2 * ng);
+  t.g = order[slot];
+  int l = tile - slot * (nd + 2 * ng);
   t.which = l < nd ? 0 : (l < nd + ng ? 1 : 2);
   l -= t.which == 0 ? 0 : (t.which == 1 ? nd : nd + ng);
   const int ncols = t.which == 0 ? (p.I + 255) / 256 : (p.H + 255) / 256;
@@ -153,6 +170,27 @@ __device__ __forceinline__ void stage_bf16_block(uint32_t taddr, uint8_t* stg, i
   }
 }
 
+// A warp's block of 32 rows x 32 bf16 columns (lane = row, its 32 values packed
+// in w) to global memory, the first `nr` rows: staged as 64-byte rows (16-byte
+// chunk j of row r at chunk j ^ (r / 2 % 4)), then eight rows per store
+// instruction, four lanes to a row.
+__device__ __forceinline__ void store_block32(const uint32_t (&w)[16], uint8_t* stg, int lane, int nr,
+                                              __nv_bfloat16* dst, size_t pitch) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 8 + (lane >> 2), j = lane & 3;
+    if (r < nr)
+      *reinterpret_cast<uint4*>(dst + r * pitch + j * 8) =
+          *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+  }
+}
+
 // The staged block's first `nr` rows to rows row0.. of a row-major bf16 or
 // fp32 matrix whose rows are `pitch` bytes long, at byte `col` (a block that
 // ends inside it: a TMA box would also write the next group's rows).
@@ -177,48 +215,66 @@ __device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInf
   const int nr = ti.nrows - r0;         // rows of the group from there on
   if (nr <= 0) return;
   if (MODE == kGU) {
-    const bool rv = lane < nr;
-    const size_t row = (size_t)ti.row0 + r0 + (rv ? lane : 0);
+    // q comes in coalesced (four rows of 128 bytes per load instruction), one
+    // block of 32 columns ahead, and goes through the staging buffer to the
+    // lane that holds the row's accumulators.
+    const size_t row = (size_t)ti.row0 + r0;
+    const int c0 = ti.wt * 128;
+    const int ncol = p.I - c0 < 128 ? p.I - c0 : 128;  // a multiple of 64
+    float4 nq[8];
+    auto load_q = [&](int c) {
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int r = it * 4 + (lane >> 3);
+        nq[it] = r < nr ? *reinterpret_cast<const float4*>(p.q + (row + r) * p.I + c0 + c + (lane & 7) * 4)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    load_q(0);
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      const int col = ti.wt * 128 + c;
-      if (col >= p.I) break;  // I % 64 == 0: a block of 32 columns is whole or absent
+    for (int c = 0; c < ncol; c += 32) {
+      __syncwarp();
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int r = it * 4 + (lane >> 3);
+        *reinterpret_cast<float4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = nq[it];
+      }
+      __syncwarp();
+      float qv[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 t = *reinterpret_cast<const float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4));
+        qv[4 * j] = t.x;
+        qv[4 * j + 1] = t.y;
+        qv[4 * j + 2] = t.z;
+        qv[4 * j + 3] = t.w;
+      }
+      if (c + 32 < ncol) load_q(c + 32);
       uint32_t g[32], u[32];
       tmem_ld_32x32b_x32(tb + c, g);
       tmem_ld_32x32b_x32(tb + 128 + c, u);
       tmem_ld_wait();
-      const size_t at = row * p.I + col;
       uint32_t ph[16], pg[16], pu[16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 qv = rv ? reinterpret_cast<const float4*>(p.q + at)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float qq[4] = {qv.x, qv.y, qv.z, qv.w};
-        float hv[4], gv[4], uv[4];
+      for (int j = 0; j < 16; ++j) {
+        float hv[2], gv[2], uv[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float gt = __uint_as_float(g[4 * j + i]), up = __uint_as_float(u[4 * j + i]);
-          const float sg = 1.0f / (1.0f + __expf(-gt));
+        for (int i = 0; i < 2; ++i) {
+          const float gt = __uint_as_float(g[2 * j + i]), up = __uint_as_float(u[2 * j + i]), qq = qv[2 * j + i];
+          const float sg = __fdividef(1.0f, 1.0f + __expf(-gt));
           const float act = gt * sg;
           hv[i] = act * up;
-          uv[i] = qq[i] * act;
-          gv[i] = qq[i] * up * sg * fmaf(gt, 1.0f - sg, 1.0f);
+          uv[i] = qq * act;
+          gv[i] = qq * up * sg * fmaf(gt, 1.0f - sg, 1.0f);
         }
-        ph[2 * j] = pack_bf16(hv[0], hv[1]);
-        ph[2 * j + 1] = pack_bf16(hv[2], hv[3]);
-        pg[2 * j] = pack_bf16(gv[0], gv[1]);
-        pg[2 * j + 1] = pack_bf16(gv[2], gv[3]);
-        pu[2 * j] = pack_bf16(uv[0], uv[1]);
-        pu[2 * j + 1] = pack_bf16(uv[2], uv[3]);
+        ph[j] = pack_bf16(hv[0], hv[1]);
+        pg[j] = pack_bf16(gv[0], gv[1]);
+        pu[j] = pack_bf16(uv[0], uv[1]);
       }
-      if (rv) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          reinterpret_cast<uint4*>(p.h + at)[j] = make_uint4(ph[4 * j], ph[4 * j + 1], ph[4 * j + 2], ph[4 * j + 3]);
-          reinterpret_cast<uint4*>(p.dg + at)[j] = make_uint4(pg[4 * j], pg[4 * j + 1], pg[4 * j + 2], pg[4 * j + 3]);
-          reinterpret_cast<uint4*>(p.du + at)[j] = make_uint4(pu[4 * j], pu[4 * j + 1], pu[4 * j + 2], pu[4 * j + 3]);
-        }
-      }
-      __syncwarp();
+      const size_t at = row * p.I + c0 + c;
+      store_block32(ph, stg, lane, nr, p.h + at, p.I);
+      store_block32(pg, stg + 2048, lane, nr, p.dg + at, p.I);
+      store_block32(pu, stg, lane, nr, p.du + at, p.I);
     }
   } else if (MODE == kQ) {
     const size_t row = (size_t)ti.row0 + r0;
@@ -269,15 +325,27 @@ __device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInf
 }
 
 // Operand and output maps. Q: a = dy, b0 = Wd, out = q. GU: a = a, b0 / b1 =
-// Wg / Wu. DX: a = dg, a2 = du, b0 / b1 = Wg / Wu, out = da. DW: by product:
-// A = dy, dg, du (a, a2, a3), B = h (b0) or a (b1); out, out2, out3.
+// Wg / Wu. DX: a = dg, a2 = du, b0 / b1 = Wg / Wu, out = da.
 struct GradMaps {
-  CUtensorMap a, a2, a3, b0, b1, out, out2, out3;
+  CUtensorMap a, a2, b0, b1, out;
+};
+// DW: A = dy, dg, du; B = h, then a twice. Three box heights each (64, 32 and
+// 16 rows): a group's last stage takes the lowest that covers its rows.
+struct GradMapsDw {
+  CUtensorMap dy[3], dg[3], du[3], h[3], a[3];
+};
+template <int MODE>
+struct MapsOf {
+  using T = GradMaps;
+};
+template <>
+struct MapsOf<kDW> {
+  using T = GradMapsDw;
 };
 
 template <int MODE>
 __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
-    grouped_grad_kernel(const __grid_constant__ GradMaps m, const GradParams p) {
+    grouped_grad_kernel(const __grid_constant__ typename MapsOf<MODE>::T m, const GradParams p) {
   using Gm = GradGeo<MODE>;
   constexpr int NS = Gm::S;
   extern __shared__ uint8_t smem_raw[];
@@ -305,7 +373,22 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   // ---- row starts; tile_start[g] = tiles of groups before g (not DW, where
   // every group has the same number of tiles).
   fill_row_start(p.k, row_start, threadIdx.x, Gm::THREADS);
-  if (MODE != kDW) {
+  int32_t* order = tile_start;  // DW
+  if (MODE == kDW) {
+    // order[rank] = group, by length, longest first (equal lengths by number).
+    // Tiles are dealt in that order, forwards and backwards in turn, which
+    // keeps the CTAs' shares of unequal groups within a fraction of a tile.
+    __syncthreads();
+    for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
+      const int n = row_start[g + 1] - row_start[g];
+      int rank = 0;
+      for (int j = 0; j < G; ++j) {
+        const int o = row_start[j + 1] - row_start[j];
+        rank += (o > n || (o == n && j < g)) ? 1 : 0;
+      }
+      order[rank] = g;
+    }
+  } else {
     const int n_wt = (p.k.N + Gm::TILE_N - 1) / Gm::TILE_N;
     for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
       int r0, nr;
@@ -320,7 +403,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 4);
+      mbar_init(tempty_bar(a), Gm::EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -329,11 +412,6 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
-  }
-  if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&m.a);
-    prefetch_tensormap(&m.b0);
-    if (MODE != kQ) prefetch_tensormap(&m.b1);
   }
   __syncthreads();
   if (MODE != kDW && warp == 0) {  // exclusive scan of the per-group tile counts
@@ -362,6 +440,12 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int dw_per_group = ((p.H + 127) / 128) * ((p.I + 255) / 256) + 2 * ((p.I + 127) / 128) * ((p.H + 255) / 256);
   const int total = MODE == kDW ? G * dw_per_group : tile_start[G];
+  // Tile of this CTA's round r (dealt back and forth in DW).
+  auto tile_of = [&](int r) {
+    const int b = MODE == kDW && (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+    return r * (int)gridDim.x + b;
+  };
+  const int rounds = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   auto rows_of = [&](int g) {
     const int n = row_start[g + 1] - row_start[g];
     return n > 0 ? n : 0;
@@ -377,13 +461,16 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
       Ring rg;
       Armed armed;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int r = 0; ok && r < rounds; ++r) {
+        const int tile = tile_of(r);
+        if (tile >= total) break;  // the last round
         TileInfo ti = {};
         DwTile dt = {};
-        int nkb = p.num_kb;
-        if (MODE == kDW) {
-          dt = dw_tile(p, tile);
-          nkb = (rows_of(dt.g) + kBK - 1) / kBK;
+        int nkb = p.num_kb, dw_rows = 0;
+        if constexpr (MODE == kDW) {
+          dt = dw_tile(p, order, tile);
+          dw_rows = rows_of(dt.g);
+          nkb = (dw_rows + kBK - 1) / kBK;
         } else {
           ti = decode_tile_s<128>(G, tile_start, row_start, tile);
         }
@@ -395,12 +482,15 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
           }
           const uint32_t fb = full_bar(rg.s);
           const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
-          if (first) mbar_arrive_expect_tx(fb, Gm::STAGE_BYTES);
-          if (MODE == kGU) {
+          // DW: the box height of this stage (0: 64 rows, 1: 32, 2: 16).
+          const int left = dw_rows - kb * kBK;
+          const int low = MODE == kDW ? (left <= 16 ? 2 : (left <= 32 ? 1 : 0)) : 0;
+          if (first) mbar_arrive_expect_tx(fb, (uint32_t)Gm::STAGE_BYTES >> low);
+          if constexpr (MODE == kGU) {
             tma_load_2d(sa, &m.a, fb, kb * kBK, ti.row0 + ti.tt * 128);
             tma_load_2d(sb, &m.b0, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
             tma_load_2d(sb + Gm::A_BYTES, &m.b1, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
-          } else if (MODE == kQ || MODE == kDX) {
+          } else if constexpr (MODE == kQ || MODE == kDX) {
             // DX: the first half of the stages is dg Wg, the second du Wu.
             const int half = p.num_kb >> 1;
             const bool second = MODE == kDX && kb >= half;
@@ -416,9 +506,9 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
             }
           } else {
             const int krow = row_start[dt.g] + kb * kBK;
-            const CUtensorMap* mb = dt.which == 0 ? &m.b0 : &m.b1;
+            const CUtensorMap* mb = dt.which == 0 ? &m.h[low] : &m.a[low];
             if (first) {
-              const CUtensorMap* ma = dt.which == 0 ? &m.a : (dt.which == 1 ? &m.a2 : &m.a3);
+              const CUtensorMap* ma = dt.which == 0 ? &m.dy[low] : (dt.which == 1 ? &m.dg[low] : &m.du[low]);
               tma_load_2d(sa, ma, fb, dt.m0, krow);
               tma_load_2d(sa + kChunk, ma, fb, dt.m0 + 64, krow);
               tma_load_2d(sb, mb, fb, dt.n0, krow);
@@ -438,71 +528,79 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the loop (DW's last stage is cleared by all lanes);
-    // lane 0 waits and issues.
+    // The whole warp walks the loop in step, polls included, so that tile, stage
+    // and descriptor values are warp-uniform (the tensor core instructions take
+    // uniform registers); one elected lane issues. DW's last stage is cleared
+    // by all lanes.
     constexpr uint32_t kIdesc = idesc_bf16_f32(128, 256) | (Gm::A_MN ? 1u << 15 : 0u) | (Gm::B_MN ? 1u << 16 : 0u);
     constexpr uint32_t kStepA = Gm::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = Gm::B_MN ? 2048 >> 4 : 32 >> 4;
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
-      int v = 0;
-      if (lane == 0)
-        v = mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA, p.k.limit_ns) ? 1 : 0;
-      return __shfl_sync(0xFFFFFFFFu, v, 0) != 0;
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+      return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA,
+                                                       p.k.limit_ns)) != 0;
     };
     Ring rg;
     bool ok = true, issued = false;
     int local = 0;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++local) {
+    for (int r = 0; ok && r < rounds; ++r, ++local) {
+      const int tile = tile_of(r);
+      if (tile >= total) break;
       const int acc = local & 1;
       const uint32_t ap = (uint32_t)(local >> 1) & 1u;
+      int nkb = p.num_kb, nrows = 0;
+      if (MODE == kDW) {
+        nrows = rows_of(order[tile / dw_per_group]);
+        nkb = (nrows + kBK - 1) / kBK;
+      }
       if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
         ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-      int nkb = p.num_kb, nrows = 0;
-      if (MODE == kDW) {
-        nrows = rows_of(dw_tile(p, tile).g);
-        nkb = (nrows + kBK - 1) / kBK;
-      }
       for (int kb = 0; kb < nkb; ++kb) {
+        const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
+        const uint64_t da = Gm::A_MN ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
+        const uint64_t db = Gm::B_MN ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
         if (!wait_all(full_bar(rg.s), rg.ph)) {
           ok = false;
           break;
         }
-        const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
-        int steps = kBK / 16;
-        if (MODE == kDW) {
-          const int left = nrows - kb * kBK;
-          if (left < kBK) {
-            steps = (left + 15) >> 4;
+        const int left = nrows - kb * kBK;
+        if (MODE == kDW && left < kBK) {
+          const int steps = (left + 15) >> 4;
+          if (left & 15) {
             // Rows left .. 16 * steps - 1 of all six chunks: eight lanes clear
             // one 128-byte row. (A row's swizzle stays inside the row.)
-            const int tail = steps * 16 - left;
-            __syncwarp();
-            uint8_t* st = base + rg.s * Gm::STAGE_BYTES;
-            for (int i = lane >> 3; i < tail * 6; i += 4) {
-              const int chunk = i / tail, r = left + (i - chunk * tail);
-              *reinterpret_cast<uint4*>(st + chunk * kChunk + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            uint8_t* st = base + rg.s * Gm::STAGE_BYTES + (lane & 7) * 16;
+            for (int i = left + (lane >> 3); i < steps * 16; i += 4) {
+#pragma unroll
+              for (int c = 0; c < 6; ++c) *reinterpret_cast<uint4*>(st + c * kChunk + i * 128) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
           }
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t da = Gm::A_MN ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
-          const uint64_t db = Gm::B_MN ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
-          for (int k = 0; k < steps; ++k)
-            umma_bf16(d, da + (uint64_t)k * kStepA, db + (uint64_t)k * kStepB, kIdesc, (kb | k) ? 1u : 0u);
-          umma_commit(empty_bar(rg.s));
+          tc_fence_after();
+          if (elect_one()) {
+            for (int k = 0; k < steps; ++k)
+              umma_bf16(d, da + (uint64_t)k * kStepA, db + (uint64_t)k * kStepB, kIdesc, (kb | k) ? 1u : 0u);
+            umma_commit(empty_bar(rg.s));
+          }
+        } else {
+          tc_fence_after();
+          if (elect_one()) {
+            umma_bf16(d, da, db, kIdesc, kb ? 1u : 0u);
+#pragma unroll
+            for (int k = 1; k < kBK / 16; ++k) umma_bf16(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
+            umma_commit(empty_bar(rg.s));
+          }
         }
         __syncwarp();
         issued = true;
         rg.next(NS);
       }
       if (!ok) break;
-      if (lane == 0) umma_commit(tfull_bar(acc));
+      if (elect_one()) umma_commit(tfull_bar(acc));
       __syncwarp();
     }
     if (!ok && issued && lane == 0) {  // wait for every issued MMA before TMEM is freed
@@ -512,9 +610,12 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
-    uint8_t* stg = epi_stage + q * Gm::EPI_WARP;
+    const int half = warp > 6 ? 1 : 0;  // DW: its 128 columns
+    uint8_t* stg = epi_stage + (half * 4 + q) * Gm::EPI_WARP;
     int local = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++local) {
+    for (int r = 0; r < rounds; ++r, ++local) {
+      const int tile = tile_of(r);
+      if (tile >= total) break;
       const int acc = local & 1;
       const uint32_t ap = (uint32_t)(local >> 1) & 1u;
       int ok = 1;
@@ -524,31 +625,30 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      if (MODE == kDW) {
-        // 32 x 64 blocks by TMA; H and I are multiples of 64, so a block's rows
-        // all belong to the group's matrix or none does.
-        const DwTile dt = dw_tile(p, tile);
+      if constexpr (MODE == kDW) {
+        // H and I are multiples of 64, so a block of 32 rows or columns is all
+        // inside the group's matrix or all outside.
+        const DwTile dt = dw_tile(p, order, tile);
         const int M = dt.which == 0 ? p.H : p.I, N = dt.which == 0 ? p.I : p.H;
-        const int m0 = dt.m0 + q * 32;
+        const int m0 = dt.m0 + q * 32, n0 = dt.n0 + half * 128;
         const bool empty = rows_of(dt.g) == 0;
-        const CUtensorMap* mo = dt.which == 0 ? &m.out : (dt.which == 1 ? &m.out2 : &m.out3);
+        __nv_bfloat16* out = (dt.which == 0 ? p.dw_down : (dt.which == 1 ? p.dw_gate : p.dw_up)) +
+                             ((size_t)dt.g * M + m0) * N + n0;
         if (m0 < M) {
 #pragma unroll 1
-          for (int c = 0; c < 256 && dt.n0 + c < N; c += 64) {
+          for (int c = 0; c < 128 && n0 + c < N; c += 32) {
+            uint32_t w[16];
             if (empty) {
-              if (lane == 0) bulk_wait_group_read0();
-              __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < 16; ++j) w[j] = 0u;
             } else {
-              stage_bf16_block(tb + c, stg, lane);
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(tb + half * 128 + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(mo, smem_u32(stg), dt.n0 + c, dt.g * M + m0);
-              bulk_commit_group();
-            }
+            store_block32(w, stg, lane, 32, out + c, N);
           }
         }
       } else {
@@ -572,7 +672,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
 }
 
 template <int MODE>
-cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long max_tiles, int num_sms, cudaStream_t s) {
+cudaError_t run_mode(const typename MapsOf<MODE>::T& m, const GradParams& p, long long max_tiles, int num_sms, cudaStream_t s) {
   if (max_tiles <= 0) return cudaSuccess;
   const int grid = (int)(max_tiles < num_sms ? max_tiles : num_sms);
   grouped_grad_kernel<MODE><<<grid, GradGeo<MODE>::THREADS, GradGeo<MODE>::SMEM, s>>>(m, p);
@@ -652,12 +752,17 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
     e = run_mode<kDX>(m, p, row_tiles * ceil_div(H, 256), a.num_sms, s);
   }
   if (e == cudaSuccess && want_dw) {
-    GradMaps m = {};
-    maps = make_tmap_bf16(&m.a, a.dy, H, R, 64) && make_tmap_bf16(&m.a2, a.dg, I, R, 64) &&
-           make_tmap_bf16(&m.a3, a.du, I, R, 64) && make_tmap_bf16(&m.b0, a.h, I, R, 64) &&
-           make_tmap_bf16(&m.b1, a.a, H, R, 64) && make_tmap_bf16(&m.out, a.dw_down, I, GH, 32) &&
-           make_tmap_bf16(&m.out2, a.dw_gate, H, GI, 32) && make_tmap_bf16(&m.out3, a.dw_up, H, GI, 32);
-    if (!maps) return cudaErrorInvalidValue;
+    GradMapsDw m = {};
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t box = 64u >> i;
+      if (!make_tmap_bf16(&m.dy[i], a.dy, H, R, box) || !make_tmap_bf16(&m.dg[i], a.dg, I, R, box) ||
+          !make_tmap_bf16(&m.du[i], a.du, I, R, box) || !make_tmap_bf16(&m.h[i], a.h, I, R, box) ||
+          !make_tmap_bf16(&m.a[i], a.a, H, R, box))
+        return cudaErrorInvalidValue;
+    }
+    p.dw_down = static_cast<__nv_bfloat16*>(a.dw_down);
+    p.dw_gate = static_cast<__nv_bfloat16*>(a.dw_gate);
+    p.dw_up = static_cast<__nv_bfloat16*>(a.dw_up);
     const long long tiles =
         G * (ceil_div(H, 128) * ceil_div(I, 256) + 2 * ceil_div(I, 128) * ceil_div(H, 256));
     e = run_mode<kDW>(m, p, tiles, a.num_sms, s);
