@@ -347,10 +347,23 @@ def _arg(h: Handle, what: str, name: str, t, dtype, numel: int, optional: bool =
         if optional:
             return None
         raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: {name} is missing")
-    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != h.device:
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != h.device or not t.is_contiguous():
         raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: {name} must be a dense {dtype} tensor of {numel} elements on "
                        f"cuda:{h.device}, got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device}")
     return t.data_ptr()
+
+
+# The current stream's address without building a Stream object (3 us of a small call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(h: Handle, s) -> int:
+    """cudaStream_t of s, or of the current stream of the handle's device."""
+    if s is not None:
+        return s.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(h.device)
+    return torch.cuda.current_stream(h.device).cuda_stream
 
 
 def _res_type(what: str, dtype) -> int:
@@ -384,7 +397,7 @@ def add_rmsnorm(h: Handle, x, weight, eps: float, residual=None, h_out=None, out
         _arg(h, what, "residual", residual, rt, n, True), _arg(h, what, "weight", weight, _BF16, H), float(eps),
         _arg(h, what, "h_out", h_out, rt, n, True), _arg(h, what, "out", out, _BF16, n, True),
         _arg(h, what, "q", q, _U8, n, True), _arg(h, what, "q_scale", q_scale, _U8, n // 32, True),
-        _arg(h, what, "rstd", rstd, _F32, rows, True), _stream(stream)), what)
+        _arg(h, what, "rstd", rstd, _F32, rows, True), _stream_of(h, stream)), what)
 
 
 def add_rmsnorm_backward_workspace_size(rows: int, H: int) -> int:
@@ -407,7 +420,7 @@ def add_rmsnorm_backward(h: Handle, dout, h_res, weight, rstd, dh, ws=None, dh_i
         _arg(h, what, "weight", weight, _BF16, H), _arg(h, what, "rstd", rstd, _F32, rows),
         _arg(h, what, "dh", dh, rt, n), _arg(h, what, "dx", dx, _BF16, n, True),
         _arg(h, what, "dweight", dweight, _F32, H, True), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-        _stream(stream)), what)
+        _stream_of(h, stream)), what)
 
 
 def combine_backward(h: Handle, cfg: Config, dout, y_perm, topk_w, flat_to_perm, dy_perm, dtopk_w, topk_idx=None,
@@ -422,7 +435,7 @@ def combine_backward(h: Handle, cfg: Config, dout, y_perm, topk_w, flat_to_perm,
         _arg(h, what, "flat_to_perm", flat_to_perm, _I32, T * K),
         _arg(h, what, "topk_idx", topk_idx, _I32, T * K, True), _arg(h, what, "logits", logits, _F32, T * E, True),
         _arg(h, what, "dy_perm", dy_perm, _BF16, T * K * H), _arg(h, what, "dtopk_w", dtopk_w, _F32, T * K),
-        _arg(h, what, "dlogits", dlogits, _F32, T * E, True), _stream(stream)), what)
+        _arg(h, what, "dlogits", dlogits, _F32, T * E, True), _stream_of(h, stream)), what)
 
 
 def route_backward(h: Handle, cfg: Config, logits, topk_idx, dtopk_w, dlogits, stream=None):
@@ -432,7 +445,7 @@ def route_backward(h: Handle, cfg: Config, logits, topk_idx, dtopk_w, dlogits, s
     _check(load().moe_route_backward(
         h.ptr, ctypes.byref(cfg), _arg(h, what, "logits", logits, _F32, T * E),
         _arg(h, what, "topk_idx", topk_idx, _I32, T * K), _arg(h, what, "dtopk_w", dtopk_w, _F32, T * K),
-        _arg(h, what, "dlogits", dlogits, _F32, T * E), _stream(stream)), what)
+        _arg(h, what, "dlogits", dlogits, _F32, T * E), _stream_of(h, stream)), what)
 
 
 def permute_backward(h: Handle, cfg: Config, dx_perm, flat_to_perm, dx, dx_add=None, stream=None):
@@ -442,7 +455,7 @@ def permute_backward(h: Handle, cfg: Config, dx_perm, flat_to_perm, dx, dx_add=N
     _check(load().moe_permute_backward(
         h.ptr, ctypes.byref(cfg), _arg(h, what, "dx_perm", dx_perm, _BF16, T * K * H),
         _arg(h, what, "flat_to_perm", flat_to_perm, _I32, T * K), _arg(h, what, "dx_add", dx_add, _BF16, T * H, True),
-        _arg(h, what, "dx", dx, _BF16, T * H), _stream(stream)), what)
+        _arg(h, what, "dx", dx, _BF16, T * H), _stream_of(h, stream)), what)
 
 
 def grouped_gemm_backward_workspace_size(rows: int, H: int, I: int, dtype: int = MOE_BF16, num_groups: int = 1) -> int:
@@ -467,7 +480,7 @@ def grouped_swiglu_backward(h: Handle, a, dy, offsets, w_gate, w_up, w_down, da,
         _arg(h, what, "w_gate", w_gate, _BF16, m), _arg(h, what, "w_up", w_up, _BF16, m),
         _arg(h, what, "w_down", w_down, _BF16, m), _arg(h, what, "da", da, _BF16, n, True),
         _arg(h, what, "dw_gate", dw_gate, _BF16, m, True), _arg(h, what, "dw_up", dw_up, _BF16, m, True),
-        _arg(h, what, "dw_down", dw_down, _BF16, m, True), _p(ws), ws.numel() * ws.element_size(), _stream(stream)),
+        _arg(h, what, "dw_down", dw_down, _BF16, m, True), _p(ws), ws.numel() * ws.element_size(), _stream_of(h, stream)),
         what)
 
 

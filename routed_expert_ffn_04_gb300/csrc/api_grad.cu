@@ -26,7 +26,11 @@ bool norm_shape_ok(int64_t rows, int H, int res_type) {
          (res_type == MOE_RES_BF16 || res_type == MOE_RES_F32);
 }
 
-size_t norm_grad_ws(int64_t rows, int H) { return align_up((size_t)norm_grad_blocks(rows, H) * H * 4 + 1, 256); }
+// Enough for either residual type.
+size_t norm_grad_ws(int64_t rows, int H) {
+  const int a = norm_grad_blocks(rows, H, false), b = norm_grad_blocks(rows, H, true);
+  return align_up((size_t)(a > b ? a : b) * H * 4 + 1, 256);
+}
 
 // moe_grouped_swiglu_backward workspace: q fp32, then h, dgate and dup bf16.
 struct GradWs {

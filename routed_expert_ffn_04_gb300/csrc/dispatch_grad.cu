@@ -78,95 +78,92 @@ __device__ __forceinline__ void route_grad_warp(const float* __restrict__ logits
   if (e >= 0) dlogits[e] = scaling * sg * om * d;
 }
 
-// One block per token: every thread takes 8 columns at a time of dout and of
-// up to kBatch of the token's y rows (two 16-byte loads each, all in flight
-// together), writes the dy rows and keeps the slots' partial dot products.
-__global__ void __launch_bounds__(512) combine_bwd_kernel(const __nv_bfloat16* __restrict__ dout,
-                                                          const float* __restrict__ y, const float* __restrict__ topk_w,
-                                                          const int32_t* __restrict__ f2p, int T, int K, int H, int E,
-                                                          float scaling, int route_norm,
-                                                          const int32_t* __restrict__ topk_idx,
-                                                          const float* __restrict__ logits,
-                                                          __nv_bfloat16* __restrict__ dy, float* __restrict__ dtopk_w,
-                                                          float* __restrict__ dlogits, int* status) {
-  __shared__ float sw[kMaxK];
-  __shared__ int32_t sp[kMaxK];
-  __shared__ float part[16][kBatch];
-  __shared__ float sdw[kMaxK];
-  const int t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (threadIdx.x < K) {
-    const size_t f = (size_t)t * K + threadIdx.x;
-    int32_t p = f2p[f];
-    if ((unsigned)p >= (unsigned)(T * K)) {
-      // -1: a pair that the permutation dropped and has reported already.
-      if (p != -1) atomicCAS(status, 0, MOE_DEV_BAD_PERM_INDEX);
-      p = -1;
-    }
-    sp[threadIdx.x] = p;
-    sw[threadIdx.x] = topk_w[f];
-  }
-  if (dlogits)
-    for (int e = threadIdx.x; e < E; e += blockDim.x) dlogits[(size_t)t * E + e] = 0.0f;
-  __syncthreads();
+// One warp per (token, slot, part): it reads its share of the token's dout and
+// of one y row, writes the same share of the dy row and keeps the dot product;
+// nothing is exchanged until the end, so every warp's loads stay in flight.
+// dout[t] comes from L1 for the token's other warps.
+//   parts    1, or 4 when the tokens are too few to fill the SMs: part q takes
+//            every fourth run of 256 columns
+//   tokens   per block so that it has at least 8 warps (few slots per token)
+constexpr int kUnroll = 4;      // 256-column runs a warp has in flight
+constexpr int kMaxWarps = 16;   // per block
+
+__global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
+    const __nv_bfloat16* __restrict__ dout, const float* __restrict__ y, const float* __restrict__ topk_w,
+    const int32_t* __restrict__ f2p, int T, int K, int H, int E, int parts, int slot_warps, int tokens, float scaling,
+    int route_norm, const int32_t* __restrict__ topk_idx, const float* __restrict__ logits,
+    __nv_bfloat16* __restrict__ dy, float* __restrict__ dtopk_w, float* __restrict__ dlogits, int* status) {
+  __shared__ float dots[4 * kMaxK];  // [token][slot][part]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp % parts, sw = (warp / parts) % slot_warps, tok = warp / (parts * slot_warps);
+  const int t = blockIdx.x * tokens + tok;
   const int H8 = H >> 3;
-  const uint4* drow = reinterpret_cast<const uint4*>(dout + (size_t)t * H);
-  for (int k0 = 0; k0 < K; k0 += kBatch) {
-    float acc[kBatch];
+  if (t < T) {
+    if (dlogits)
+      for (int e = (sw * parts + part) * 32 + lane; e < E; e += 32 * parts * slot_warps) dlogits[(size_t)t * E + e] = 0.0f;
+    const uint4* drow = reinterpret_cast<const uint4*>(dout + (size_t)t * H);
+    for (int k = sw; k < K; k += slot_warps) {
+      const size_t f = (size_t)t * K + k;
+      int32_t p = f2p[f];
+      const float w = topk_w[f];
+      if ((unsigned)p >= (unsigned)(T * K)) {
+        // -1: a pair that the permutation dropped and has reported already.
+        if (p != -1 && lane == 0) atomicCAS(status, 0, MOE_DEV_BAD_PERM_INDEX);
+        p = -1;
+      }
+      float acc = 0.0f;
+      if (p >= 0) {
+        const float4* yr = reinterpret_cast<const float4*>(y + (size_t)p * H);
+        uint4* dyr = reinterpret_cast<uint4*>(dy + (size_t)p * H);
+        const int step = 32 * parts;
+        for (int c = part * 32 + lane; c < H8; c += step * kUnroll) {
+          uint4 d[kUnroll];
+          float4 v[kUnroll][2];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) acc[j] = 0.0f;
-    for (int c = threadIdx.x; c < H8; c += blockDim.x) {
-      float d[8];
-      unpack8(__ldg(drow + c), d);
-      float4 v[kBatch][2];
+          for (int u = 0; u < kUnroll; ++u) {
+            const int cc = c + u * step;
+            if (cc < H8) {
+              d[u] = __ldg(drow + cc);
+              v[u][0] = __ldcs(yr + 2 * cc);
+              v[u][1] = __ldcs(yr + 2 * cc + 1);
+            }
+          }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int p = k0 + j < K ? sp[k0 + j] : -1;
-        if (p >= 0) {
-          const float4* yr = reinterpret_cast<const float4*>(y + (size_t)p * H) + 2 * c;
-          v[j][0] = __ldg(yr);
-          v[j][1] = __ldg(yr + 1);
-        } else {
-          v[j][0] = v[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int u = 0; u < kUnroll; ++u) {
+            const int cc = c + u * step;
+            if (cc >= H8) break;
+            float g[8], o[8];
+            unpack8(d[u], g);
+            acc = fmaf(g[0], v[u][0].x, acc);
+            acc = fmaf(g[1], v[u][0].y, acc);
+            acc = fmaf(g[2], v[u][0].z, acc);
+            acc = fmaf(g[3], v[u][0].w, acc);
+            acc = fmaf(g[4], v[u][1].x, acc);
+            acc = fmaf(g[5], v[u][1].y, acc);
+            acc = fmaf(g[6], v[u][1].z, acc);
+            acc = fmaf(g[7], v[u][1].w, acc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = w * g[i];
+            dyr[cc] = pack8(o);
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int p = k0 + j < K ? sp[k0 + j] : -1;
-        if (p < 0) continue;
-        acc[j] = fmaf(d[0], v[j][0].x, acc[j]);
-        acc[j] = fmaf(d[1], v[j][0].y, acc[j]);
-        acc[j] = fmaf(d[2], v[j][0].z, acc[j]);
-        acc[j] = fmaf(d[3], v[j][0].w, acc[j]);
-        acc[j] = fmaf(d[4], v[j][1].x, acc[j]);
-        acc[j] = fmaf(d[5], v[j][1].y, acc[j]);
-        acc[j] = fmaf(d[6], v[j][1].z, acc[j]);
-        acc[j] = fmaf(d[7], v[j][1].w, acc[j]);
-        const float w = sw[k0 + j];
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = w * d[i];
-        reinterpret_cast<uint4*>(dy + (size_t)p * H)[c] = pack8(o);
-      }
+      for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, off);
+      if (lane == 0) dots[(tok * K + k) * parts + part] = acc;
     }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], off);
-      if (lane == 0) part[warp][j] = acc[j];
-    }
-    __syncthreads();
-    if (threadIdx.x < kBatch && k0 + threadIdx.x < K) {
-      float s = 0.0f;
-      for (int i = 0; i < nw; ++i) s += part[i][threadIdx.x];
-      sdw[k0 + threadIdx.x] = s;
-      dtopk_w[(size_t)t * K + k0 + threadIdx.x] = s;
-    }
-    __syncthreads();
   }
-  if (dlogits && warp == 0)
-    route_grad_warp(logits + (size_t)t * E, topk_idx + (size_t)t * K, lane < K ? sdw[lane] : 0.0f, E, K, scaling,
-                    route_norm, dlogits + (size_t)t * E, status);
+  __syncthreads();
+  // One warp per token: lane k adds slot k's parts in order.
+  if (part != 0 || sw != 0 || t >= T) return;
+  float dw = 0.0f;
+  if (lane < K) {
+    for (int q = 0; q < parts; ++q) dw += dots[(tok * K + lane) * parts + q];
+    dtopk_w[(size_t)t * K + lane] = dw;
+  }
+  if (dlogits)
+    route_grad_warp(logits + (size_t)t * E, topk_idx + (size_t)t * K, dw, E, K, scaling, route_norm,
+                    dlogits + (size_t)t * E, status);
 }
 
 // The routing's gradient alone: one warp per token.
@@ -235,12 +232,17 @@ __global__ void __launch_bounds__(256) permute_bwd_kernel(const __nv_bfloat16* _
 
 cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  int threads = (a.H / 8 + 31) / 32 * 32;
-  threads = threads > 512 ? 512 : (threads < 32 ? 32 : threads);
-  combine_bwd_kernel<<<a.T, threads, 0, s>>>(static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w,
-                                             a.flat_to_perm, a.T, a.K, a.H, a.E, a.scaling, a.route_norm, a.topk_idx,
-                                             a.logits, static_cast<__nv_bfloat16*>(a.dy_perm), a.dtopk_w, a.dlogits,
-                                             a.status);
+  // Four parts while the (token, slot) rows alone are fewer than 16 warps for
+  // each of 152 SMs (61 tokens x 8 slots: 3.9 us with four, 5.6 with one).
+  const int parts = (long long)a.T * a.K < 152 * 16 && a.H >= 1024 ? 4 : 1;
+  const int most = kMaxWarps / parts;
+  const int slot_warps = a.K < most ? a.K : most;
+  const int tokens = parts == 1 && slot_warps <= 4 ? 8 / slot_warps : 1;
+  const int threads = 32 * parts * slot_warps * tokens;
+  combine_bwd_kernel<<<(a.T + tokens - 1) / tokens, threads, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w, a.flat_to_perm, a.T, a.K, a.H, a.E, parts,
+      slot_warps, tokens, a.scaling, a.route_norm, a.topk_idx, a.logits, static_cast<__nv_bfloat16*>(a.dy_perm),
+      a.dtopk_w, a.dlogits, a.status);
   return cudaGetLastError();
 }
 

@@ -49,6 +49,7 @@
 #include "../../include/moe.h"
 #include "gemm_sched.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -369,6 +370,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.k.G;
+  allow_next_launch();
 
   // ---- row starts; tile_start[g] = tiles of groups before g (not DW, where
   // every group has the same number of tiles).
@@ -437,6 +439,9 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Up to here nothing was read that the launch before this one writes (its
+  // blocks may still be running: programmatic dependent launch).
+  wait_for_previous_launch();
   const uint32_t tmem_base = *tmem_slot;
   const int dw_per_group = ((p.H + 127) / 128) * ((p.I + 255) / 256) + 2 * ((p.I + 127) / 128) * ((p.H + 255) / 256);
   const int total = MODE == kDW ? G * dw_per_group : tile_start[G];
@@ -675,8 +680,9 @@ template <int MODE>
 cudaError_t run_mode(const typename MapsOf<MODE>::T& m, const GradParams& p, long long max_tiles, int num_sms, cudaStream_t s) {
   if (max_tiles <= 0) return cudaSuccess;
   const int grid = (int)(max_tiles < num_sms ? max_tiles : num_sms);
-  grouped_grad_kernel<MODE><<<grid, GradGeo<MODE>::THREADS, GradGeo<MODE>::SMEM, s>>>(m, p);
-  return cudaGetLastError();
+  // Q starts after everything before it; the others' prologues may overlap the
+  // end of the launch before them (its offsets were there before Q).
+  return launch_dependent(grouped_grad_kernel<MODE>, grid, GradGeo<MODE>::THREADS, GradGeo<MODE>::SMEM, s, MODE != kQ, m, p);
 }
 
 template <int MODE>

@@ -199,10 +199,12 @@ struct NormGradArgs {
   void* dh;            // [rows, H], the residual's type
   void* dx;            // [rows, H] bf16, or nullptr
   float* dweight;      // [H], or nullptr
-  float* partials;     // [norm_grad_blocks(rows, H), H]
+  float* partials;     // [norm_grad_blocks(rows, H, res_f32), H]
   bool res_f32;
 };
-int norm_grad_blocks(long long rows, int H);
+// Opt the backward kernels into their dynamic shared memory (once per device).
+cudaError_t norm_prepare_device();
+int norm_grad_blocks(long long rows, int H, bool f32);
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_add_rmsnorm_backward(const NormGradArgs& a, cudaStream_t s);
 

@@ -13,7 +13,8 @@
 //
 // Bound: HBM. One pass: a row's elements stay in the registers of the threads
 // that loaded them (8 consecutive columns per vector), so each input is read
-// once. Rows of at most 1024 columns take one warp each, longer rows (up to
+// once (8192 x 4096 with MXFP8 output: 45 us, 6.7 TB/s, the copy rate). Rows of
+// at most 1024 columns take one warp each, longer rows (up to
 // 16384) one block each. Every thread reads its elements of a row before it
 // writes them, so the outputs may overwrite the inputs of their own type.
 #include <cuda_bf16.h>
@@ -21,6 +22,7 @@
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx.cuh"
 
 namespace moe {
@@ -214,17 +216,75 @@ __global__ void add_rmsnorm_any_kernel(int H, const __nv_bfloat16* x, const RT* 
 // dw in registers; the blocks' partial sums go to `part_dw` [gridDim, H] and
 // a second kernel adds them in block order (no atomics: the result does not
 // change from run to run).
-template <typename RT, int NV, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 512) add_rmsnorm_bwd_kernel(long long rows, int H, const __nv_bfloat16* dout,
-                                       const RT* dh_in, const RT* h, const __nv_bfloat16* __restrict__ w,
-                                       const float* __restrict__ rstd, RT* dh, __nv_bfloat16* dx,
-                                       float* __restrict__ part_dw) {
-  __shared__ float part[2][32];
-  extern __shared__ float warp_dw[];  // WARP_ROW: [kWarpRows][H]
-  const int tid = WARP_ROW ? (threadIdx.x & 31) : threadIdx.x;
-  const int nt = WARP_ROW ? 32 : blockDim.x;
-  const long long first = WARP_ROW ? (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : (long long)blockIdx.x;
-  const long long step = WARP_ROW ? (long long)gridDim.x * kWarpRows : (long long)gridDim.x;
+//
+// A row's sum needs the whole row before its first output, so loads that wait
+// for the previous row would leave the memory idle in between. Each thread
+// therefore copies its own columns of the next rows into shared memory
+// (cp.async) and reads back only what it copied, twice: for the sum and for
+// the outputs. A block is several groups of threads, each with a row of its
+// own and a barrier of its own (a group of 32 needs none); 32 columns per
+// thread keep the groups small and the sum's exchange cheap.
+template <typename RT, int NV>
+struct BwdShape {
+  // 16-byte pieces of one vector of 8 columns: dout, h, and a bf16 dh_in. (An
+  // fp32 dh_in would take the room of a row more in flight: it is prefetched
+  // into L2 when the row's copies start and loaded while the row is summed.)
+  static constexpr int RP = sizeof(RT) / 2;
+  static constexpr bool RING_IN = RP == 1;
+  static constexpr int PIECES = 3;
+  static constexpr int kBytes = NV * PIECES * 16;  // per thread and row
+};
+constexpr int kBwdThreads = 256;  // per block, or one group's if that is more
+// Rows a group holds: four or three where that leaves room for two blocks per
+// SM, else two (at most 192 KB: 512 threads of 4 vectors).
+int bwd_stages(int bytes_per_thread, int threads) {
+  const int row = bytes_per_thread * threads;
+  return 4 * row <= 112 * 1024 ? 4 : (3 * row <= 112 * 1024 ? 3 : 2);
+}
+
+__device__ __forceinline__ void copy16(void* smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
+               "l"(g)
+               : "memory");
+}
+
+template <typename RT, int NV, int STAGES>
+__global__ void __launch_bounds__(512)
+    add_rmsnorm_bwd_kernel(long long rows, int H, int nt, const __nv_bfloat16* dout, const RT* dh_in, const RT* h,
+                           const __nv_bfloat16* __restrict__ w, const float* __restrict__ rstd, RT* dh,
+                           __nv_bfloat16* dx, float* __restrict__ part_dw) {
+  using Sh = BwdShape<RT, NV>;
+  __shared__ float part[2][16];  // [buffer][warp of the block]
+  extern __shared__ uint4 ring[];  // [stage][vector][piece][thread]; at the end the groups' dw
+  const int group = threadIdx.x / nt, groups = blockDim.x / nt, tid = threadIdx.x - group * nt;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group_warps = nt >> 5;
+  const long long first = (long long)blockIdx.x * groups + group, step = (long long)gridDim.x * groups;
+  auto slot = [&](int st, int v, int piece) {
+    return ring + ((st * NV + v) * Sh::PIECES + piece) * blockDim.x + threadIdx.x;
+  };
+  auto fetch = [&](int st, long long row) {
+    if (row < rows) {
+      const size_t at = (size_t)row * H;
+      const __nv_bfloat16* pd = dout + at;
+      const RT *ph = h + at, *pi = dh_in + at;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * nt + tid) * 8;
+        if (c >= H) continue;
+        copy16(slot(st, v, 0), pd + c);
+#pragma unroll
+        for (int i = 0; i < Sh::RP; ++i) {
+          copy16(slot(st, v, 1 + i), reinterpret_cast<const uint4*>(ph + c) + i);
+          if (Sh::RING_IN && dh_in) copy16(slot(st, v, 1 + Sh::RP + i), reinterpret_cast<const uint4*>(pi + c) + i);
+        }
+        if (!Sh::RING_IN && dh_in && (lane & 3) == 0)  // four lanes' columns are one 128-byte line
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(pi + c));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i, first + i * step);
   float dw[NV][8];
   Vec8<__nv_bfloat16> vw[NV];
 #pragma unroll
@@ -236,77 +296,93 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 512) add_rmsnorm_b
     for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
   }
   const float inv_h = 1.0f / (float)H;
-  int buf = 0;
+  int buf = 0, st = 0;
+  float rs = first < rows ? rstd[first] : 0.0f;
   for (long long row = first; row < rows; row += step, buf ^= 1) {
+    const float rs_next = row + step < rows ? rstd[row + step] : 0.0f;  // a row ahead, like the copies
+    fetch(st == 0 ? STAGES - 1 : st - 1, row + (STAGES - 1) * step);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
     const size_t at = (size_t)row * H;
-    Vec8<__nv_bfloat16> vd[NV];
-    Vec8<RT> vh[NV], vi[NV];
-    const float rs = rstd[row];
+    Vec8<RT> vi[Sh::RING_IN ? 1 : NV];
+    if (!Sh::RING_IN) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * nt + tid) * 8;
-      vd[v].zero();
-      vh[v].zero();
-      vi[v].zero();
-      if (c < H) {
-        vd[v].load(dout + at + c);
-        vh[v].load(h + at + c);
-        if (dh_in) vi[v].load(dh_in + at + c);
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * nt + tid) * 8;
+        vi[v].zero();
+        if (dh_in && c < H) vi[v].load(dh_in + at + c);
       }
     }
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      if ((v * nt + tid) * 8 >= H) continue;
+      Vec8<__nv_bfloat16> vd;
+      Vec8<RT> vh;
+      vd.a = *slot(st, v, 0);
+#pragma unroll
+      for (int i = 0; i < Sh::RP; ++i) reinterpret_cast<uint4*>(&vh)[i] = *slot(st, v, 1 + i);
       float d[8], xh[8], g[8];
-      vd[v].unpack(d);
-      vh[v].unpack(xh);
+      vd.unpack(d);
+      vh.unpack(xh);
       vw[v].unpack(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[j] *= rs;
-        dw[v][j] = fmaf(d[j], xh[j], dw[v][j]);
-        dot = fmaf(d[j] * g[j], xh[j], dot);
+        const float t = d[j] * (xh[j] * rs);
+        dw[v][j] += t;
+        dot = fmaf(t, g[j], dot);
       }
     }
-    dot = WARP_ROW ? warp_sum(dot) : block_sum(dot, part[buf]);
-    const float m = dot * inv_h;
+    dot = warp_sum(dot);
+    if (group_warps > 1) {
+      if (lane == 0) part[buf][warp] = dot;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(nt) : "memory");
+      dot = warp_sum(lane < group_warps ? part[buf][group * group_warps + lane] : 0.0f);
+    }
+    const float m = dot * inv_h * rs * rs;  // dh = rs g - h rs^2 mean(g xhat) + dh_in
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * nt + tid) * 8;
       if (c >= H) continue;
-      float d[8], xh[8], g[8], r[8];
-      vd[v].unpack(d);
-      vh[v].unpack(xh);
-      vw[v].unpack(g);
-      vi[v].unpack(r);
+      Vec8<__nv_bfloat16> vd;
+      Vec8<RT> vh;
+      vd.a = *slot(st, v, 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = fmaf(rs, d[j] * g[j] - xh[j] * rs * m, r[j]);
+      for (int i = 0; i < Sh::RP; ++i) reinterpret_cast<uint4*>(&vh)[i] = *slot(st, v, 1 + i);
+      Vec8<RT>& in = vi[Sh::RING_IN ? 0 : v];
+      if (Sh::RING_IN) {
+        in.zero();
+        if (dh_in) *reinterpret_cast<uint4*>(&in) = *slot(st, v, 2);
+      }
+      float d[8], hh[8], g[8], r[8];
+      vd.unpack(d);
+      vh.unpack(hh);
+      vw[v].unpack(g);
+      in.unpack(r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = fmaf(rs, d[j] * g[j], r[j] - hh[j] * m);
       Vec8<RT>::store(dh + at + c, r);
       if (dx) Vec8<__nv_bfloat16>::store(dx + at + c, r);
     }
+    st = st + 1 == STAGES ? 0 : st + 1;
+    rs = rs_next;
   }
   if (!part_dw) return;
+  allow_next_launch();
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();  // every group is done with the ring
   float* mine = part_dw + (size_t)blockIdx.x * H;
-  if (WARP_ROW) {
-    float* sw = warp_dw + (threadIdx.x >> 5) * H;
+  float* all = reinterpret_cast<float*>(ring);  // [groups][H]
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * nt + tid) * 8;
-      if (c < H) Vec8<float>::store(sw + c, dw[v]);
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < H; c += blockDim.x) {
-      float t = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kWarpRows; ++k) t += warp_dw[k * H + c];
-      mine[c] = t;
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * nt + tid) * 8;
-      if (c < H) Vec8<float>::store(mine + c, dw[v]);
-    }
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * nt + tid) * 8;
+    if (c < H) Vec8<float>::store(groups > 1 ? all + group * H + c : mine + c, dw[v]);
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
+    float t = all[c];
+    for (int k = 1; k < groups; ++k) t += all[k * H + c];
+    mine[c] = t;
   }
 }
 
@@ -346,27 +422,37 @@ __global__ void add_rmsnorm_dw_any_kernel(long long rows, int H, const __nv_bflo
   }
 }
 
-// dw[c] = sum of part[0 .. n-1][c] in a fixed order: 32 columns per block, 8
-// threads per column over every eighth partial, then those 8 in order.
-__global__ void __launch_bounds__(256) sum_partials_kernel(const float* __restrict__ part, int n, int H,
-                                                           float* __restrict__ dw) {
-  __shared__ float s[8][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+// dw[c] = sum of part[0 .. n-1][c] in a fixed order: 32 columns per block, 32
+// threads per column over every 32nd partial, then those 32 in order.
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restrict__ part, int n, int H,
+                                                            float* __restrict__ dw) {
+  __shared__ float s[32][33];
+  const int x = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+  wait_for_previous_launch();
   float t = 0.0f;
-  if (c < H)
-    for (int i = k; i < n; i += 8) t += part[(size_t)i * H + c];
-  s[k][threadIdx.x & 31] = t;
-  __syncthreads();
-  if (k == 0 && c < H) {
-    t = s[0][threadIdx.x];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) t += s[j][threadIdx.x];
-    dw[c] = t;
+  if (c < H) {
+#pragma unroll 4
+    for (int i = k; i < n; i += 32) t += part[(size_t)i * H + c];
   }
+  s[k][x] = t;
+  __syncthreads();
+  t = warp_sum(s[x][k]);  // the column of this warp: blockIdx.x * 32 + k
+  if (x == 0 && blockIdx.x * 32 + k < H) dw[blockIdx.x * 32 + k] = t;
 }
 
 // Threads of a block that holds one row in NV vectors of 8 per thread.
 int row_threads(int H, int nv) { return ((H + 8 * nv - 1) / (8 * nv) + 31) / 32 * 32; }
+
+// Backward: vectors of 8 columns per thread (an fp32 row of up to 4096 columns
+// takes two, for its wider loads), and row groups per block: one while every
+// row can have a block of its own.
+constexpr int kBwdBlocks = 304;  // two per SM of a GB300 (152)
+int norm_grad_vectors(int H, bool f32) { return H <= 256 ? 1 : (H <= 512 || (f32 && H <= 4096) ? 2 : 4); }
+int norm_grad_groups(long long rows, int H, bool f32) {
+  if (H % 8 || rows <= kBwdBlocks) return 1;
+  const int g = kBwdThreads / row_threads(H, norm_grad_vectors(H, f32));
+  return g < 1 ? 1 : g;
+}
 
 template <typename RT, bool MX>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t s) {
@@ -405,40 +491,58 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
   auto* dh = static_cast<RT*>(a.dh);
   auto* dx = static_cast<__nv_bfloat16*>(a.dx);
   float* part = a.dweight ? a.partials : nullptr;
-  const int n = norm_grad_blocks(a.rows, a.H);
+  const int n = norm_grad_blocks(a.rows, a.H, a.res_f32);
   if (a.H % 8) {
     if (part) add_rmsnorm_dw_any_kernel<RT><<<n, 256, 0, s>>>(a.rows, a.H, dout, h, a.rstd, part);
     add_rmsnorm_bwd_any_kernel<RT><<<n, 256, 0, s>>>(a.rows, a.H, dout, di, h, w, a.rstd, dh, dx);
   } else {
-#define MOE_NORM(NV, WR, THREADS, SMEM)                                                                           \
-  add_rmsnorm_bwd_kernel<RT, NV, WR><<<n, (THREADS), (SMEM), s>>>(a.rows, a.H, dout, di, h, w, a.rstd, dh, dx, part)
-    if (a.H <= kWarpRowCols) {
-      const int smem = part ? kWarpRows * a.H * 4 : 0;
-      if (a.H <= 256) MOE_NORM(1, true, 32 * kWarpRows, smem);
-      else if (a.H <= 512) MOE_NORM(2, true, 32 * kWarpRows, smem);
-      else MOE_NORM(4, true, 32 * kWarpRows, smem);
-    } else if (a.H <= 8192) {
-      MOE_NORM(2, false, row_threads(a.H, 2), 0);
-    } else {
-      MOE_NORM(4, false, row_threads(a.H, 4), 0);
-    }
+    const int nv = norm_grad_vectors(a.H, a.res_f32), nt = row_threads(a.H, nv);
+    const int threads = norm_grad_groups(a.rows, a.H, a.res_f32) * nt;
+    const int bytes = nv * 3 * 16, stages = bwd_stages(bytes, threads);
+#define MOE_NORM(NV, ST)                                                                                      \
+  if (nv == NV && stages == ST)                                                                               \
+  add_rmsnorm_bwd_kernel<RT, NV, ST>                                                                          \
+      <<<n, threads, (size_t)ST * bytes * threads, s>>>(a.rows, a.H, nt, dout, di, h, w, a.rstd, dh, dx, part)
+    MOE_NORM(1, 4);
+    MOE_NORM(2, 4);
+    MOE_NORM(4, 4);
+    MOE_NORM(4, 3);
+    MOE_NORM(4, 2);
 #undef MOE_NORM
   }
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.dweight) {
-    sum_partials_kernel<<<(a.H + 31) / 32, 256, 0, s>>>(part, n, a.H, a.dweight);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && a.dweight)
+    e = launch_dependent(sum_partials_kernel, (a.H + 31) / 32, 1024, 0, s, true, part, n, a.H, a.dweight);
   return e;
+}
+
+template <typename RT>
+cudaError_t set_all_bwd_smem() {
+  const void* kernels[] = {reinterpret_cast<const void*>(add_rmsnorm_bwd_kernel<RT, 1, 4>),
+                           reinterpret_cast<const void*>(add_rmsnorm_bwd_kernel<RT, 2, 4>),
+                           reinterpret_cast<const void*>(add_rmsnorm_bwd_kernel<RT, 4, 4>),
+                           reinterpret_cast<const void*>(add_rmsnorm_bwd_kernel<RT, 4, 3>),
+                           reinterpret_cast<const void*>(add_rmsnorm_bwd_kernel<RT, 4, 2>)};
+  for (const void* k : kernels) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 192 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-// Blocks of the backward pass: two per SM of a GB300 (152), fewer when the
-// rows are fewer. A constant, so dw's summation order is the same everywhere.
-int norm_grad_blocks(long long rows, int H) {
-  const long long units = (H % 8 == 0 && H <= kWarpRowCols) ? (rows + kWarpRows - 1) / kWarpRows : rows;
-  return (int)(units < 304 ? units : 304);
+cudaError_t norm_prepare_device() {
+  const cudaError_t e = set_all_bwd_smem<float>();
+  return e != cudaSuccess ? e : set_all_bwd_smem<__nv_bfloat16>();
+}
+
+// Blocks of the backward pass, fewer when the rows are fewer; a function of the
+// shape alone, so dw's summation order is the same everywhere.
+int norm_grad_blocks(long long rows, int H, bool f32) {
+  const int groups = norm_grad_groups(rows, H, f32);
+  const long long units = (rows + groups - 1) / groups;
+  return (int)(units < kBwdBlocks ? units : kBwdBlocks);
 }
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
