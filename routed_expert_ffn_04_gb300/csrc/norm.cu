@@ -224,6 +224,7 @@ __global__ void add_rmsnorm_any_kernel(int H, const __nv_bfloat16* x, const RT* 
 // the outputs. A block is several groups of threads, each with a row of its
 // own and a barrier of its own (a group of 32 needs none); 32 columns per
 // thread keep the groups small and the sum's exchange cheap.
+constexpr int kPieces = 3;
 template <typename RT, int NV>
 struct BwdShape {
   // 16-byte pieces of one vector of 8 columns: dout, h, and a bf16 dh_in. (An
@@ -231,8 +232,7 @@ struct BwdShape {
   // into L2 when the row's copies start and loaded while the row is summed.)
   static constexpr int RP = sizeof(RT) / 2;
   static constexpr bool RING_IN = RP == 1;
-  static constexpr int PIECES = 3;
-  static constexpr int kBytes = NV * PIECES * 16;  // per thread and row
+  static constexpr int PIECES = kPieces;
 };
 constexpr int kBwdThreads = 256;  // per block, or one group's if that is more
 // Rows a group holds: four or three where that leaves room for two blocks per
@@ -498,7 +498,7 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
   } else {
     const int nv = norm_grad_vectors(a.H, a.res_f32), nt = row_threads(a.H, nv);
     const int threads = norm_grad_groups(a.rows, a.H, a.res_f32) * nt;
-    const int bytes = nv * 3 * 16, stages = bwd_stages(bytes, threads);
+    const int bytes = nv * kPieces * 16, stages = bwd_stages(bytes, threads);
 #define MOE_NORM(NV, ST)                                                                                      \
   if (nv == NV && stages == ST)                                                                               \
   add_rmsnorm_bwd_kernel<RT, NV, ST>                                                                          \
