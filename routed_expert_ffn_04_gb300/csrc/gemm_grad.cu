@@ -47,6 +47,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
+#include "gemm_grad.cuh"
 #include "gemm_sched.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -55,131 +56,43 @@
 namespace moe {
 namespace {
 
-enum GradMode { kQ = 0, kGU = 1, kDX = 2, kDW = 3 };
+enum GradMode { kQ = 0, kGU = 1, kDX = 2 };
 
 constexpr int kBK = 64;           // reduction elements per stage
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSmem = 232448;  // 227 KB dynamic shared memory per CTA
-constexpr int kChunk = 64 * 128;  // an MN-major box: 64 rows of 128 bytes
 
 template <int MODE>
 struct GradGeo {
-  static constexpr bool A_MN = MODE == kDW, B_MN = MODE != kGU;
-  static constexpr int A_BYTES = 128 * 128;  // 16 KB: 128 rows of K, or two chunks of 64 columns
+  static constexpr bool B_MN = MODE != kGU;
+  static constexpr int A_BYTES = 128 * 128;  // 16 KB
   static constexpr int B_BYTES = 256 * 128;  // 32 KB
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // Warps beyond the producer (0), the MMA issuer (1) and four epilogue warps
-  // (2-5): a second producer (6) where a stage has more than three boxes; in DW
-  // a third one (11), a warp that clears the rows past a group's end (12), and
-  // four more epilogue warps (7-10), as a tile lasts a few stages only there.
-  static constexpr int EPI_WARPS = MODE == kDW ? 8 : 4;
-  static constexpr int THREADS = MODE == kDW ? 416 : (MODE == kGU ? 192 : 224);
+  // Warp 6 is a second producer where a stage has more than three boxes.
+  static constexpr int THREADS = MODE == kGU ? 192 : 224;
+  static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 8) * 4;  // row starts, tile starts
+  static constexpr int BAR_BYTES = 512;
   static constexpr int EPI_WARP = 4096;  // one warp's staging block: 32 rows of 128 bytes
-  static constexpr int EPI_BYTES = EPI_WARPS * EPI_WARP;
-  // Stages of the ring: four, and in DW three when the groups are so many that
-  // four do not leave room for the tables (more than 314).
-  static constexpr int MAX_S = 4;
-  static constexpr int BAR_BYTES = 8 * (3 * MAX_S + 5) + 24;
-  // Tables: row starts, and the tile starts (int32) or DW's order (int16).
-  static constexpr int table_bytes(int G) { return ((G + 1) * 4 + (MODE == kDW ? 2 * G : 4 * (G + 1)) + 15) / 16 * 16; }
-  static constexpr int smem(int G, int stages) {
-    return 1024 + stages * STAGE_BYTES + EPI_BYTES + BAR_BYTES + table_bytes(G);
-  }
-  static constexpr int stages(int G) { return smem(G, 4) <= kMaxSmem ? 4 : 3; }
+  static constexpr int EPI_BYTES = 4 * EPI_WARP;
+  static constexpr int EXTRA = 1024 + TABLE_BYTES + BAR_BYTES + EPI_BYTES;
+  static constexpr int S = (kMaxSmem - EXTRA) / STAGE_BYTES;
+  static constexpr int RING_BYTES = S * STAGE_BYTES;
+  static constexpr int SMEM = EXTRA + RING_BYTES;
+  static constexpr int NBARS = 2 * S + 5;
   static constexpr int TILE_N = MODE == kGU ? 128 : 256;  // output columns per tile
-  static_assert(BAR_BYTES % 16 == 0, "the tables follow the barriers");
-  static_assert(smem(kMaxGroups, 3) <= kMaxSmem && (MODE == kDW || smem(kMaxGroups, 4) <= kMaxSmem), "shared memory");
+  static_assert(S >= 4, "ring too shallow");
+  static_assert(NBARS * 8 + 8 <= BAR_BYTES, "barrier area");
+  static_assert(SMEM <= kMaxSmem, "shared memory budget");
 };
 
 struct GradParams {
   KParams k;              // offsets, G, rows, status, limit_ns; N = output columns
   int H, I;
-  int nd, ng, nc_d, nc_g; // DW: tiles of dWd and of dWg (= of dWu) per group; their tiles per row of tiles
-  uint32_t r_group, r_d, r_g;  // floor(2^32 / d) of nd + 2 ng, nc_d, nc_g (div_by)
-  int stages;             // of the ring
-  int num_kb;             // stages per tile (Q, GU: H / 64; DX: 2 I / 64; DW: by group)
+  int num_kb;             // stages per tile (Q, GU: H / 64; DX: 2 I / 64)
   float* q;               // [rows, I]
   __nv_bfloat16 *h, *dg, *du;  // [rows, I]
   __nv_bfloat16* da;      // [rows, H]
 };
-
-// Shared-memory descriptor of an MN-major operand: chunks of 64 columns (128
-// swizzled bytes) by 64 rows of the reduction axis, `kChunk` bytes apart;
-// groups of 8 rows 1024 bytes apart. A step of 16 rows is 2048 bytes.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);  // [0,14)  start address >> 4
-  d |= (uint64_t)(kChunk >> 4) << 16;            // [16,30) leading byte offset: next 64 columns
-  d |= (uint64_t)(1024 >> 4) << 32;              // [32,46) stride byte offset: next 8 rows
-  d |= (uint64_t)1 << 46;                        // [46,48) descriptor version (tcgen05)
-  d |= (uint64_t)2 << 61;                        // [61,64) layout: 128-byte swizzle
-  return d;
-}
-
-// One lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is = 0;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(is));
-  return is != 0;
-}
-
-// n / d for n, d < 2^31 with r = floor(2^32 / d): the estimate is at most one low.
-__device__ __forceinline__ int div_by(int n, int d, uint32_t r) {
-  int q = (int)__umulhi((uint32_t)n, r);
-  if (n - q * d >= d) ++q;
-  return q;
-}
-
-// One tile of DW: its group, which of the three products, and its corner. The
-// groups come in `order`: longest first.
-struct DwTile {
-  int g, which, m0, n0;  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
-};
-__device__ __forceinline__ DwTile dw_tile(const GradParams& p, const uint16_t* order, int tile) {
-  DwTile t;
-  const int per = p.nd + 2 * p.ng, slot = div_by(tile, per, p.r_group);
-  t.g = order[slot];
-  int l = tile - slot * per;
-  t.which = l < p.nd ? 0 : (l < p.nd + p.ng ? 1 : 2);
-  l -= t.which == 0 ? 0 : (t.which == 1 ? p.nd : p.nd + p.ng);
-  const int nc = t.which == 0 ? p.nc_d : p.nc_g, row = div_by(l, nc, t.which == 0 ? p.r_d : p.r_g);
-  t.m0 = row * 128;
-  t.n0 = (l - row * nc) * 256;
-  return t;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// A warp's block of 32 rows x 64 bf16 columns (lane = row, TMEM columns taddr
-// .. taddr + 63) into its staging buffer, 128-byte rows, 16-byte chunk j of row
-// r at chunk j ^ (r % 8).
-__device__ __forceinline__ void stage_bf16_block(uint32_t taddr, uint8_t* stg, int lane) {
-  uint32_t v[32], u[32];
-  tmem_ld_32x32b_x32(taddr, v);
-  tmem_ld_32x32b_x32(taddr + 32, u);
-  tmem_ld_wait();
-  if (lane == 0) bulk_wait_group_read0();  // the last store has read the buffer
-  __syncwarp();
-  uint8_t* row = stg + lane * 128;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t w[4], x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
-      x[i] = pack_bf16(__uint_as_float(u[8 * j + 2 * i]), __uint_as_float(u[8 * j + 2 * i + 1]));
-    }
-    *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(row + (((j + 4) ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-  }
-}
 
 // A warp's block of 32 rows x 32 bf16 columns (lane = row, its 32 values packed
 // in w) to global memory, the first `nr` rows: staged as 64-byte rows (16-byte
@@ -340,38 +253,22 @@ __device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInf
 struct GradMaps {
   CUtensorMap a, a2, b0, b1, out;
 };
-// DW: A = dy, dg, du; B = h, then a twice. Three box heights each (64, 32 and
-// 16 rows): a group's last stage takes the lowest that covers its rows.
-struct GradMapsDw {
-  CUtensorMap dy[3], dg[3], du[3], h[3], a[3];
-  CUtensorMap dw[3];  // dWd, dWg, dWu
-};
-template <int MODE>
-struct MapsOf {
-  using T = GradMaps;
-};
-template <>
-struct MapsOf<kDW> {
-  using T = GradMapsDw;
-};
-
 template <int MODE>
 __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
-    grouped_grad_kernel(const __grid_constant__ typename MapsOf<MODE>::T m, const GradParams p) {
+    grouped_grad_kernel(const __grid_constant__ GradMaps m, const GradParams p) {
   using Gm = GradGeo<MODE>;
-  const int NS = MODE == kDW ? p.stages : Gm::MAX_S;
+  constexpr int NS = Gm::S;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
   uint8_t* base = smem_raw + pad;
   const uint32_t base_u32 = raw_addr + pad;
-  // Shared memory: ring | epilogue staging | barriers | tables.
-  uint8_t* epi_stage = base + NS * Gm::STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + Gm::EPI_BYTES);
-  int32_t* row_start = reinterpret_cast<int32_t*>(epi_stage + Gm::EPI_BYTES + Gm::BAR_BYTES);
-  int32_t* tile_start = row_start + p.k.G + 1;                     // not DW
-  uint16_t* order = reinterpret_cast<uint16_t*>(tile_start);  // DW
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * Gm::MAX_S + 5);
+  // Shared memory: ring | epilogue staging | tables | barriers.
+  uint8_t* epi_stage = base + Gm::RING_BYTES;
+  int32_t* tile_start = reinterpret_cast<int32_t*>(epi_stage + Gm::EPI_BYTES);
+  int32_t* row_start = tile_start + kMaxGroups + 8;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + Gm::EPI_BYTES + Gm::TABLE_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Gm::NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -379,47 +276,27 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * NS + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * NS + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
-  // DW: stage s holds a group's last rows and those past its end are cleared.
-  auto clear_bar = [&](int s) { return bar0 + 8u * (2 * NS + 5 + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.k.G;
   allow_next_launch();
 
-  // ---- row starts; tile_start[g] = tiles of groups before g (not DW, where
-  // every group has the same number of tiles).
+  // ---- row starts; tile_start[g] = tiles of groups before g.
   fill_row_start(p.k, row_start, threadIdx.x, Gm::THREADS);
-  if (MODE == kDW) {
-    // order[rank] = group, by length, longest first (equal lengths by number).
-    // Tiles are dealt in that order, forwards and backwards in turn, which
-    // keeps the CTAs' shares of unequal groups within a fraction of a tile.
-    __syncthreads();
-    for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
-      const int n = row_start[g + 1] - row_start[g];
-      int rank = 0;
-      for (int j = 0; j < G; ++j) {
-        const int o = row_start[j + 1] - row_start[j];
-        rank += (o > n || (o == n && j < g)) ? 1 : 0;
-      }
-      order[rank] = (uint16_t)g;
-    }
-  } else {
-    const int n_wt = (p.k.N + Gm::TILE_N - 1) / Gm::TILE_N;
-    for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
-      int r0, nr;
-      group_rows(p.k, g, r0, nr);
-      tile_start[g] = n_wt * ((nr + 127) / 128);
-    }
+  const int n_wt = (p.k.N + Gm::TILE_N - 1) / Gm::TILE_N;
+  for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
+    int r0, nr;
+    group_rows(p.k, g, r0, nr);
+    tile_start[g] = n_wt * ((nr + 127) / 128);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), MODE == kDW ? 2 : 1);  // the MMAs' commit; DW: the clearing warp too
-      mbar_init(clear_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), Gm::EPI_WARPS);
+      mbar_init(tempty_bar(a), 4);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -430,7 +307,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     tmem_relinquish();
   }
   __syncthreads();
-  if (MODE != kDW && warp == 0) {  // exclusive scan of the per-group tile counts
+  if (warp == 0) {  // exclusive scan of the per-group tile counts
     const int per = (G + 31) / 32;
     const int b = lane * per < G ? lane * per : G;
     const int e = (b + per < G) ? b + per : G;
@@ -457,19 +334,9 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   // blocks may still be running: programmatic dependent launch).
   wait_for_previous_launch();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = MODE == kDW ? G * (p.nd + 2 * p.ng) : tile_start[G];
-  // Tile of this CTA's round r (dealt back and forth in DW).
-  auto tile_of = [&](int r) {
-    const int b = MODE == kDW && (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-    return r * (int)gridDim.x + b;
-  };
-  const int rounds = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  auto rows_of = [&](int g) {
-    const int n = row_start[g + 1] - row_start[g];
-    return n > 0 ? n : 0;
-  };
+  const int total = tile_start[G];
 
-  if (warp == 0 || warp == 6 || (MODE == kDW && warp == 11)) {
+  if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers
     // Boxes of a stage: A, then B's in order. Warp 0 arms the stage's barrier
     // with all its bytes and issues the first; the others issue the rest (a
@@ -480,20 +347,9 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
       Ring rg;
       Armed armed;
       bool ok = true;
-      for (int r = 0; ok && r < rounds; ++r) {
-        const int tile = tile_of(r);
-        if (tile >= total) break;  // the last round
-        TileInfo ti = {};
-        DwTile dt = {};
-        int nkb = p.num_kb, dw_rows = 0;
-        if constexpr (MODE == kDW) {
-          dt = dw_tile(p, order, tile);
-          dw_rows = rows_of(dt.g);
-          nkb = (dw_rows + kBK - 1) / kBK;
-        } else {
-          ti = decode_tile_s<128>(G, tile_start, row_start, tile);
-        }
-        for (int kb = 0; kb < nkb; ++kb) {
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status, MOE_DEV_TIMEOUT_PRODUCER,
                                  p.k.limit_ns)) {
             ok = false;
@@ -501,15 +357,12 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
           }
           const uint32_t fb = full_bar(rg.s);
           const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
-          // DW: the box height of this stage (0: 64 rows, 1: 32, 2: 16).
-          const int left = dw_rows - kb * kBK;
-          const int low = MODE == kDW ? (left <= 16 ? 2 : (left <= 32 ? 1 : 0)) : 0;
-          if (first) mbar_arrive_expect_tx(fb, (uint32_t)Gm::STAGE_BYTES >> low);
+          if (first) mbar_arrive_expect_tx(fb, Gm::STAGE_BYTES);
           if constexpr (MODE == kGU) {
             tma_load_2d(sa, &m.a, fb, kb * kBK, ti.row0 + ti.tt * 128);
             tma_load_2d(sb, &m.b0, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
             tma_load_2d(sb + Gm::A_BYTES, &m.b1, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
-          } else if constexpr (MODE == kQ || MODE == kDX) {
+          } else {
             // DX: the first half of the stages is dg Wg, the second du Wu.
             const int half = p.num_kb >> 1;
             const bool second = MODE == kDX && kb >= half;
@@ -522,18 +375,6 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
             } else {
 #pragma unroll
               for (int j = 1; j < 4; ++j) tma_load_2d(sb + j * kChunk, mb, fb, ti.wt * 256 + j * 64, krow);
-            }
-          } else {
-            const int krow = row_start[dt.g] + kb * kBK;
-            const CUtensorMap* mb = dt.which == 0 ? &m.h[low] : &m.a[low];
-            if (first) {
-              const CUtensorMap* ma = dt.which == 0 ? &m.dy[low] : (dt.which == 1 ? &m.dg[low] : &m.du[low]);
-              tma_load_2d(sa, ma, fb, dt.m0, krow);
-              tma_load_2d(sa + kChunk, ma, fb, dt.m0 + 64, krow);
-            } else {
-              const int j = warp == 6 ? 0 : 2;
-              tma_load_2d(sb + j * kChunk, mb, fb, dt.n0 + j * 64, krow);
-              tma_load_2d(sb + (j + 1) * kChunk, mb, fb, dt.n0 + (j + 1) * 64, krow);
             }
           }
           armed.mark(rg);
@@ -551,8 +392,8 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     // and descriptor values are warp-uniform (the tensor core instructions take
     // uniform registers: 290 cycles to issue a stage, against 360 from one
     // diverged lane); one elected lane issues.
-    constexpr uint32_t kIdesc = idesc_bf16_f32(128, 256) | (Gm::A_MN ? 1u << 15 : 0u) | (Gm::B_MN ? 1u << 16 : 0u);
-    constexpr uint32_t kStepA = Gm::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = Gm::B_MN ? 2048 >> 4 : 32 >> 4;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, 256) | (Gm::B_MN ? 1u << 16 : 0u);
+    constexpr uint32_t kStepA = 32 >> 4, kStepB = Gm::B_MN ? 2048 >> 4 : 32 >> 4;
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
       if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
       return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA,
@@ -561,50 +402,29 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     Ring rg;
     bool ok = true, issued = false;
     int local = 0;
-    uint32_t clear_ph = 0;
-    for (int r = 0; ok && r < rounds; ++r, ++local) {
-      const int tile = tile_of(r);
-      if (tile >= total) break;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++local) {
       const int acc = local & 1;
       const uint32_t ap = (uint32_t)(local >> 1) & 1u;
-      int nkb = p.num_kb, nrows = 0;
-      if (MODE == kDW) {
-        nrows = rows_of(order[div_by(tile, p.nd + 2 * p.ng, p.r_group)]);
-        nkb = (nrows + kBK - 1) / kBK;
-      }
       if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
         ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = 0; kb < p.num_kb; ++kb) {
         const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
-        const uint64_t da = Gm::A_MN ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
+        const uint64_t da = sw128_kmajor_desc(sa);
         const uint64_t db = Gm::B_MN ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
-        const int left = nrows - kb * kBK;
-        const bool cleared = MODE == kDW && left < kBK && (left & 15);
-        if (!wait_all(cleared ? clear_bar(rg.s) : full_bar(rg.s), cleared ? (clear_ph >> rg.s) & 1u : rg.ph)) {
+        if (!wait_all(full_bar(rg.s), rg.ph)) {
           ok = false;
           break;
         }
-        if (cleared) clear_ph ^= 1u << rg.s;
-        if (MODE == kDW && left < kBK) {
-          const int steps = (left + 15) >> 4;
-          tc_fence_after();
-          if (elect_one()) {
-            for (int k = 0; k < steps; ++k)
-              umma_bf16(d, da + (uint64_t)k * kStepA, db + (uint64_t)k * kStepB, kIdesc, (kb | k) ? 1u : 0u);
-            umma_commit(empty_bar(rg.s));
-          }
-        } else {
-          tc_fence_after();
-          if (elect_one()) {
-            umma_bf16(d, da, db, kIdesc, kb ? 1u : 0u);
+        tc_fence_after();
+        if (elect_one()) {
+          umma_bf16(d, da, db, kIdesc, kb ? 1u : 0u);
 #pragma unroll
-            for (int k = 1; k < kBK / 16; ++k) umma_bf16(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
-            umma_commit(empty_bar(rg.s));
-          }
+          for (int k = 1; k < kBK / 16; ++k) umma_bf16(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
+          umma_commit(empty_bar(rg.s));
         }
         __syncwarp();
         issued = true;
@@ -618,49 +438,12 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
       umma_commit(drain_bar);
       drain_wait(drain_bar, 0, 100000000ull);
     }
-  } else if (MODE == kDW && warp == 12) {
-    // ------------------------------------------------------------ clearing
-    // Where a group's last stage ends inside a step of 16 rows: once it has
-    // landed, clear the rest of the step in both operands and hand it on. The
-    // warp looks at every stage and arrives on its empty barrier beside the
-    // MMAs' commit, so it can neither fall behind the ring nor run ahead of it
-    // (a phase's parity tells it from the next one only).
-    Ring rg;
-    bool ok = true;
-    for (int r = 0; ok && r < rounds; ++r) {
-      const int tile = tile_of(r);
-      if (tile >= total) break;
-      const int nrows = rows_of(order[div_by(tile, p.nd + 2 * p.ng, p.r_group)]);
-      for (int left = nrows; left > 0; left -= kBK) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full_bar(rg.s), rg.ph, abort_flag, p.k.status,
-                                                       MOE_DEV_TIMEOUT_MMA, p.k.limit_ns))) {
-          ok = false;
-          break;
-        }
-        if (left < kBK && (left & 15)) {
-          // Eight lanes clear one 128-byte row (a row's swizzle stays inside it).
-          uint8_t* st = base + rg.s * Gm::STAGE_BYTES + (lane & 7) * 16;
-          for (int i = left + (lane >> 3); i < ((left + 15) & ~15); i += 4) {
-#pragma unroll
-            for (int c = 0; c < 6; ++c) *reinterpret_cast<uint4*>(st + c * kChunk + i * 128) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(clear_bar(rg.s));
-        }
-        if (lane == 0) mbar_arrive(empty_bar(rg.s));
-        rg.next(NS);
-      }
-    }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
-    const int half = warp > 6 ? 1 : 0;  // DW: its 128 columns
-    uint8_t* stg = epi_stage + (half * 4 + q) * Gm::EPI_WARP;
+    uint8_t* stg = epi_stage + q * Gm::EPI_WARP;
     int local = 0;
-    for (int r = 0; r < rounds; ++r, ++local) {
-      const int tile = tile_of(r);
-      if (tile >= total) break;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++local) {
       const int acc = local & 1;
       const uint32_t ap = (uint32_t)(local >> 1) & 1u;
       int ok = 1;
@@ -670,39 +453,8 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      if constexpr (MODE == kDW) {
-        // 32 x 64 blocks by TMA (no global stores from registers: 32 rows of a
-        // warp are 32 lines per instruction, and the queue they form delays the
-        // producers and the clearing warp as well: 2.70 ms against 2.45 ms at
-        // 192 experts and 8192 tokens). H and I are multiples of 64, so a
-        // block is all inside the group's matrix or all outside.
-        const DwTile dt = dw_tile(p, order, tile);
-        const int M = dt.which == 0 ? p.H : p.I, N = dt.which == 0 ? p.I : p.H;
-        const int m0 = dt.m0 + q * 32, n0 = dt.n0 + half * 128;
-        const bool empty = rows_of(dt.g) == 0;
-        if (m0 < M) {
-#pragma unroll 1
-          for (int c = 0; c < 128 && n0 + c < N; c += 64) {
-            if (empty) {
-              if (lane == 0) bulk_wait_group_read0();
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-            } else {
-              stage_bf16_block(tb + half * 128 + c, stg, lane);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&m.dw[dt.which], smem_u32(stg), n0 + c, dt.g * M + m0);
-              bulk_commit_group();
-            }
-          }
-        }
-      } else {
-        const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
-        grad_epilogue<MODE>(p, ti, tb, q, lane, stg, &m.out);
-      }
+      const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
+      grad_epilogue<MODE>(p, ti, tb, q, lane, stg, &m.out);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty_bar(acc));
@@ -720,26 +472,25 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
 }
 
 template <int MODE>
-cudaError_t run_mode(const typename MapsOf<MODE>::T& m, GradParams p, long long max_tiles, int num_sms, cudaStream_t s) {
+cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long max_tiles, int num_sms, cudaStream_t s) {
   using Gm = GradGeo<MODE>;
   if (max_tiles <= 0) return cudaSuccess;
   const int grid = (int)(max_tiles < num_sms ? max_tiles : num_sms);
-  p.stages = Gm::stages(p.k.G);
   // Q starts after everything before it; the others' prologues may overlap the
   // end of the launch before them (its offsets were there before Q).
-  return launch_dependent(grouped_grad_kernel<MODE>, grid, Gm::THREADS, Gm::smem(p.k.G, p.stages), s, MODE != kQ, m, p);
+  return launch_dependent(grouped_grad_kernel<MODE>, grid, Gm::THREADS, Gm::SMEM, s, MODE != kQ, /*cluster=*/1, m, p);
 }
 
 template <int MODE>
 cudaError_t set_smem() {
   return cudaFuncSetAttribute(grouped_grad_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kMaxSmem);
+                              GradGeo<MODE>::SMEM);
 }
 
 }  // namespace
 
 cudaError_t gemm_grad_prepare_device() {
-  const cudaError_t errs[] = {set_smem<kQ>(), set_smem<kGU>(), set_smem<kDX>(), set_smem<kDW>()};
+  const cudaError_t errs[] = {set_smem<kQ>(), set_smem<kGU>(), set_smem<kDX>(), gemm_grad_dw_prepare_device()};
   for (cudaError_t e : errs)
     if (e != cudaSuccess) return e;
   return cudaSuccess;
@@ -769,13 +520,6 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
   p.dg = static_cast<__nv_bfloat16*>(a.dg);
   p.du = static_cast<__nv_bfloat16*>(a.du);
   p.da = static_cast<__nv_bfloat16*>(a.da);
-  p.nc_d = (I + 255) / 256;
-  p.nc_g = (H + 255) / 256;
-  p.nd = ((H + 127) / 128) * p.nc_d;
-  p.ng = ((I + 127) / 128) * p.nc_g;
-  p.r_group = (uint32_t)((1ull << 32) / (uint32_t)(p.nd + 2 * p.ng));
-  p.r_d = p.nc_d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)p.nc_d) : 0xFFFFFFFFu;
-  p.r_g = p.nc_g > 1 ? (uint32_t)((1ull << 32) / (uint32_t)p.nc_g) : 0xFFFFFFFFu;
   const uint64_t R = a.rows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
   const long long row_tiles = (a.rows + 127) / 128 + (long long)G;  // at most: one ragged tile per group
   auto ceil_div = [](long long v, long long d) { return (v + d - 1) / d; };
@@ -809,20 +553,7 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
     p.num_kb = 2 * (I / kBK);
     e = run_mode<kDX>(m, p, row_tiles * ceil_div(H, 256), a.num_sms, s);
   }
-  if (e == cudaSuccess && want_dw) {
-    GradMapsDw m = {};
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t box = 64u >> i;
-      if (!make_tmap_bf16(&m.dy[i], a.dy, H, R, box) || !make_tmap_bf16(&m.dg[i], a.dg, I, R, box) ||
-          !make_tmap_bf16(&m.du[i], a.du, I, R, box) || !make_tmap_bf16(&m.h[i], a.h, I, R, box) ||
-          !make_tmap_bf16(&m.a[i], a.a, H, R, box))
-        return cudaErrorInvalidValue;
-    }
-    if (!make_tmap_bf16(&m.dw[0], a.dw_down, I, GH, 32) || !make_tmap_bf16(&m.dw[1], a.dw_gate, H, GI, 32) ||
-        !make_tmap_bf16(&m.dw[2], a.dw_up, H, GI, 32))
-      return cudaErrorInvalidValue;
-    e = run_mode<kDW>(m, p, (long long)G * (p.nd + 2 * p.ng), a.num_sms, s);
-  }
+  if (e == cudaSuccess && want_dw) e = launch_grouped_weight_grad(a, s);
   return e;
 }
 

@@ -1,0 +1,458 @@
+// Weight gradients of the grouped SwiGLU expert products, per group g:
+//   dWd[g] = dy^T h   [H, I]      dWg[g] = dg^T a,  dWu[g] = du^T a   [I, H]
+// The reduction runs over the group's rows (rows offsets[g] .. offsets[g+1]-1),
+// bf16 operands, fp32 accumulation, bf16 results.
+//
+// Both operands are read MN-major from row-major tensors (boxes of 64 columns
+// by 64 rows, see gemm_grad.cu). Tiles of 256 x 256 results are computed by a
+// pair of CTAs on the two SMs of a TPC (tcgen05 .cta_group::2): each holds 128
+// of the M columns and half of the N columns, 32 KB per 64 rows, and in its
+// TMEM its 128 rows of the result, double-buffered.
+//
+// Why pairs: an SM takes in about 64 bytes a cycle for loads and 32 for stores,
+// and a result tile is short here (rows per expert / 16 MMAs). A 128 x 256 tile
+// on one SM costs 48 KB of loads per 64 rows, which with the result's 64 KB
+// outlasts its MMAs; the pair's tile costs each SM 32 KB for the same MMAs.
+// 192 experts x 341 rows, H = 4096, I = 1536: one SM per tile 2.45 ms.
+//
+// The reduction's last stage also holds rows of the next group (or past the
+// last one). The MMA runs in steps of 16 rows; the rows between the group's
+// end and the step's end are cleared in shared memory in both operands first
+// (a zero times another group's infinity would not be zero). A group without
+// rows gives zero gradients.
+//
+// Roles per CTA (12 warps): 0 loads A's boxes and arms the stage; 6 loads B's;
+// 1 (of the even CTA, the leader) issues the pair's MMAs; 11 clears ragged
+// stages; 2-5 and 7-10 store the result, 32 rows by 64 columns at a time. A
+// stage's copies in both CTAs complete on the leader's full barrier; a ragged
+// stage's on each CTA's own tail barrier, whose clearing warp then arrives on
+// the leader's full barrier. Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+#include "gemm_grad.cuh"
+#include "gemm_sched.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 64;  // rows per stage
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxSmem = 232448;       // 227 KB dynamic shared memory per CTA
+constexpr int kStageBytes = 4 * kChunk;  // A: two chunks of 64 columns; B: two
+constexpr int kMaxStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 384;
+constexpr int kEpiBytes = kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
+constexpr int kBarBytes = 8 * (3 * kMaxStages + 5) + 8;
+constexpr uint16_t kPairMask = 0x3;
+
+constexpr int table_bytes(int G) { return ((G + 1) * 4 + 2 * G + 15) / 16 * 16; }
+constexpr int smem_bytes(int G, int stages) {
+  return 1024 + stages * kStageBytes + kEpiBytes + kBarBytes + table_bytes(G);
+}
+// Six stages, or five when the tables of many groups (more than 289) need the room.
+constexpr int ring_stages(int G) { return smem_bytes(G, kMaxStages) <= kMaxSmem ? kMaxStages : kMaxStages - 1; }
+static_assert(kBarBytes % 16 == 0, "the tables follow the barriers");
+static_assert(smem_bytes(kMaxGroups, kMaxStages - 1) <= kMaxSmem, "shared memory");
+
+struct DwParams {
+  KParams k;  // offsets, G, rows, status, limit_ns
+  int H, I;
+  int stages;
+  int nd, ng, nc_d, nc_g;      // tiles of dWd and of dWg (= of dWu) per group; per row of tiles
+  uint32_t r_group, r_d, r_g;  // floor(2^32 / d) of nd + 2 ng, nc_d, nc_g (div_by)
+};
+
+// A = dy, dg, du; B = h, then a twice. Three box heights each (64, 32 and 16
+// rows): a group's last stage takes the lowest that covers its rows.
+struct DwMaps {
+  CUtensorMap dy[3], dg[3], du[3], h[3], a[3];
+  CUtensorMap dw[3];  // dWd, dWg, dWu
+};
+
+// One tile: its group, which of the three products, and its corner. The groups
+// come in `order`: longest first.
+struct DwTile {
+  int g, which, m0, n0;  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
+};
+__device__ __forceinline__ DwTile dw_tile(const DwParams& p, const uint16_t* order, int tile) {
+  DwTile t;
+  const int per = p.nd + 2 * p.ng, slot = div_by(tile, per, p.r_group);
+  t.g = order[slot];
+  int l = tile - slot * per;
+  t.which = l < p.nd ? 0 : (l < p.nd + p.ng ? 1 : 2);
+  l -= t.which == 0 ? 0 : (t.which == 1 ? p.nd : p.nd + p.ng);
+  const int nc = t.which == 0 ? p.nc_d : p.nc_g, row = div_by(l, nc, t.which == 0 ? p.r_d : p.r_g);
+  t.m0 = row * 256;
+  t.n0 = (l - row * nc) * 256;
+  return t;
+}
+
+// A copy into this CTA that completes on a barrier of either CTA of the pair
+// (`bar` from mapa_shared, or this CTA's own).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Arrive on a barrier of another CTA of the cluster, releasing this CTA's
+// writes, and the wait's other half (the phase has been seen complete).
+__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_weight_grad_kernel(const __grid_constant__ DwMaps m, const DwParams p) {
+  const int NS = p.stages, G = p.k.G;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
+  uint8_t* base = smem_raw + pad;
+  const uint32_t base_u32 = raw_addr + pad;
+  // Shared memory (the same in both CTAs): ring | epilogue staging | barriers | tables.
+  uint8_t* epi_stage = base + NS * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + kEpiBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* row_start = reinterpret_cast<int32_t*>(epi_stage + kEpiBytes + kBarBytes);
+  uint16_t* order = reinterpret_cast<uint16_t*>(row_start + G + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };                         // leader: both CTAs' stage s
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };         // each CTA
+  auto tail_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };      // each CTA: a ragged stage
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * kMaxStages + a); };     // each CTA
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * kMaxStages + 2 + a); };  // leader
+  const uint32_t drain_bar = bar0 + 8u * (3 * kMaxStages + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: leader
+  const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
+  allow_next_launch();
+
+  fill_row_start(p.k, row_start, threadIdx.x, kThreads);
+  __syncthreads();
+  // order[rank] = group, by length, longest first (equal lengths by number).
+  // Tiles are dealt to the pairs in that order, forwards and backwards in turn,
+  // which keeps their shares of unequal groups within a fraction of a tile.
+  for (int g = threadIdx.x; g < G; g += kThreads) {
+    const int n = row_start[g + 1] - row_start[g];
+    int at = 0;
+    for (int j = 0; j < G; ++j) {
+      const int o = row_start[j + 1] - row_start[j];
+      at += (o > n || (o == n && j < g)) ? 1 : 0;
+    }
+    order[at] = (uint16_t)g;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full_bar(s), 2);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(tail_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {  // one warp of each CTA of the pair, together
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers and TMEM are there
+  tc_fence_after();
+  // Up to here nothing was read that the launch before this one writes.
+  wait_for_previous_launch();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = G * (p.nd + 2 * p.ng);
+  const int rounds = (total + npairs - 1) / npairs;
+  auto tile_of = [&](int r) { return r * npairs + ((r & 1) ? npairs - 1 - pair : pair); };
+  auto rows_of = [&](int g) {
+    const int n = row_start[g + 1] - row_start[g];
+    return n > 0 ? n : 0;
+  };
+  auto rows_of_tile = [&](int tile) { return rows_of(order[div_by(tile, p.nd + 2 * p.ng, p.r_group)]); };
+  // A stage with `left` rows of the group from its first row on is ragged when
+  // the group ends inside one of its steps.
+  auto ragged = [](int left) { return left < kBK && (left & 15) != 0; };
+
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------ producers
+    if (lane == 0) {
+      const bool is_a = warp == 0;
+      Ring rg;
+      bool ok = true;
+      for (int r = 0; ok && r < rounds; ++r) {
+        const int tile = tile_of(r);
+        if (tile >= total) break;
+        const DwTile dt = dw_tile(p, order, tile);
+        int krow = row_start[dt.g];
+        const int x = is_a ? dt.m0 + (int)rank * 128 : dt.n0 + (int)rank * 128;
+        for (int left = rows_of(dt.g); left > 0; left -= kBK, krow += kBK) {
+          if (!mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status, MOE_DEV_TIMEOUT_PRODUCER,
+                                 p.k.limit_ns)) {
+            ok = false;
+            break;
+          }
+          const int low = left <= 16 ? 2 : (left <= 32 ? 1 : 0);  // box height 64 >> low
+          const CUtensorMap* map;
+          if (is_a) map = dt.which == 0 ? &m.dy[low] : (dt.which == 1 ? &m.dg[low] : &m.du[low]);
+          else map = dt.which == 0 ? &m.h[low] : &m.a[low];
+          uint32_t bar;
+          if (ragged(left)) {
+            bar = tail_bar(rg.s);
+            if (is_a) mbar_arrive_expect_tx(bar, (uint32_t)kStageBytes >> low);
+          } else {
+            bar = rank == 0 ? full_bar(rg.s) : mapa_shared(full_bar(rg.s), 0);
+            if (is_a && rank == 0) {  // both CTAs' bytes (the other's may land first)
+              mbar_arrive_expect_tx(bar, 2u * ((uint32_t)kStageBytes >> low));
+              mbar_arrive(bar);
+            }
+          }
+          const uint32_t dst = base_u32 + rg.s * kStageBytes + (is_a ? 0 : 2 * kChunk);
+          tma_load_2d_pair(dst, map, bar, x, krow);
+          tma_load_2d_pair(dst + kChunk, map, bar, x + 64, krow);
+          rg.next(NS);
+        }
+      }
+      if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 5000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the loop in step (warp-uniform descriptors); one
+    // elected lane issues.
+    if (rank == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256) | 1u << 15 | 1u << 16;
+      constexpr uint32_t kStep = 2048 >> 4;  // 16 rows
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA,
+                                                         p.k.limit_ns)) != 0;
+      };
+      Ring rg;
+      bool ok = true, issued = false;
+      int local = 0;
+      for (int r = 0; ok && r < rounds; ++r, ++local) {
+        const int tile = tile_of(r);
+        if (tile >= total) break;
+        const int acc = local & 1;
+        const uint32_t ap = (uint32_t)(local >> 1) & 1u;
+        const int nrows = rows_of_tile(tile);
+        if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        uint32_t accumulate = 0;
+        for (int left = nrows; left > 0; left -= kBK) {
+          const uint32_t sa = base_u32 + rg.s * kStageBytes;
+          const uint64_t da = sw128_mnmajor_desc(sa), db = sw128_mnmajor_desc(sa + 2 * kChunk);
+          if (!wait_all(full_bar(rg.s), rg.ph)) {
+            ok = false;
+            break;
+          }
+          if (ragged(left)) mbar_acquire_cluster(full_bar(rg.s), rg.ph);  // the other CTA's cleared rows
+          tc_fence_after();
+          if (left >= kBK) {
+            if (elect_one()) {
+              umma_bf16_pair(d, da, db, kIdesc, accumulate);
+#pragma unroll
+              for (int k = 1; k < kBK / 16; ++k) umma_bf16_pair(d, da + k * kStep, db + k * kStep, kIdesc, 1u);
+              umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
+            }
+          } else {
+            const int steps = (left + 15) >> 4;
+            if (elect_one()) {
+              for (int k = 0; k < steps; ++k)
+                umma_bf16_pair(d, da + (uint64_t)k * kStep, db + (uint64_t)k * kStep, kIdesc, accumulate | (k ? 1u : 0u));
+              umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
+            }
+          }
+          __syncwarp();
+          accumulate = 1u;
+          issued = true;
+          rg.next(NS);
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), kPairMask);
+        __syncwarp();
+      }
+      if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
+        umma_commit_pair(drain_bar);
+        drain_wait(drain_bar, 0, 200000000ull);
+      }
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ clearing
+    // A ragged stage, once this CTA's copies of it have landed: clear the rows
+    // from the group's end to the step's end in both operands, and hand the
+    // stage to the leader. A stage's tail barrier has one phase per ragged use.
+    Ring rg;
+    uint32_t phase = 0;
+    for (int r = 0; r < rounds; ++r) {
+      const int tile = tile_of(r);
+      if (tile >= total) break;
+      bool ok = true;
+      for (int left = rows_of_tile(tile); left > 0; left -= kBK) {
+        if (ragged(left)) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail_bar(rg.s), (phase >> rg.s) & 1u, abort_flag, p.k.status,
+                                                         MOE_DEV_TIMEOUT_MMA, p.k.limit_ns));
+          if (!ok) break;
+          phase ^= 1u << rg.s;
+          // Eight lanes clear one 128-byte row (a row's swizzle stays inside it).
+          uint8_t* st = base + rg.s * kStageBytes + (lane & 7) * 16;
+          for (int i = left + (lane >> 3); i < ((left + 15) & ~15); i += 4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(st + c * kChunk + i * 128) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive(full_bar(rg.s));
+            else mbar_arrive_remote_release(mapa_shared(full_bar(rg.s), 0));
+          }
+        }
+        rg.next(NS);
+      }
+      if (!ok) break;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;             // this warp may access TMEM lanes 32q .. 32q+31
+    const int half = warp > 6 ? 1 : 0;  // its 128 columns
+    uint8_t* stg = epi_stage + (half * 4 + q) * 4096;
+    int local = 0;
+    for (int r = 0; r < rounds; ++r, ++local) {
+      const int tile = tile_of(r);
+      if (tile >= total) break;
+      const int acc = local & 1;
+      const uint32_t ap = (uint32_t)(local >> 1) & 1u;
+      const DwTile dt = dw_tile(p, order, tile);
+      int ok = 1;
+      if (lane == 0)
+        ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256 + half * 128);
+      // 32 x 64 blocks by TMA. (Stores from registers are 32 lines per warp
+      // instruction, and the queue they form delays the loads: one SM per tile
+      // 2.70 ms against 2.45.) H and I are multiples of 64, so a block is all
+      // inside the group's matrix or all outside.
+      const int M = dt.which == 0 ? p.H : p.I, N = dt.which == 0 ? p.I : p.H;
+      const int m0 = dt.m0 + (int)rank * 128 + q * 32, n0 = dt.n0 + half * 128;
+      const bool empty = rows_of(dt.g) == 0;
+      if (m0 < M) {
+#pragma unroll 1
+        for (int c = 0; c < 128 && n0 + c < N; c += 64) {
+          if (empty) {
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+          } else {
+            stage_bf16_block(tb + c, stg, lane);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&m.dw[dt.which], smem_u32(stg), n0 + c, dt.g * M + m0);
+            bulk_commit_group();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(tempty_bar(acc));
+        else mbar_arrive_remote(mapa_shared(tempty_bar(acc), 0));
+      }
+    }
+    if (lane == 0) bulk_wait_group0();  // this warp's bulk stores are complete
+  }
+
+  // Both CTAs arrive here only when their roles are done (every wait is
+  // bounded), so neither frees TMEM or leaves while the other may still touch
+  // its shared memory or barriers.
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t gemm_grad_dw_prepare_device() {
+  return cudaFuncSetAttribute(grouped_weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+}
+
+cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s) {
+  const int G = a.offsets ? a.G : 1, H = a.H, I = a.I;
+  const uint64_t R = a.rows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
+  DwMaps m = {};
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t box = 64u >> i;
+    if (!make_tmap_bf16(&m.dy[i], a.dy, H, R, box) || !make_tmap_bf16(&m.dg[i], a.dg, I, R, box) ||
+        !make_tmap_bf16(&m.du[i], a.du, I, R, box) || !make_tmap_bf16(&m.h[i], a.h, I, R, box) ||
+        !make_tmap_bf16(&m.a[i], a.a, H, R, box))
+      return cudaErrorInvalidValue;
+  }
+  if (!make_tmap_bf16(&m.dw[0], a.dw_down, I, GH, 32) || !make_tmap_bf16(&m.dw[1], a.dw_gate, H, GI, 32) ||
+      !make_tmap_bf16(&m.dw[2], a.dw_up, H, GI, 32))
+    return cudaErrorInvalidValue;
+  DwParams p = {};
+  p.k.offsets = a.offsets;
+  p.k.G = G;
+  p.k.rows = a.rows;
+  p.k.status = a.status;
+  p.k.limit_ns = a.wait_limit_ns;
+  p.H = H;
+  p.I = I;
+  p.stages = ring_stages(G);
+  p.nc_d = (I + 255) / 256;
+  p.nc_g = (H + 255) / 256;
+  p.nd = ((H + 255) / 256) * p.nc_d;
+  p.ng = ((I + 255) / 256) * p.nc_g;
+  auto recip = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d) : 0xFFFFFFFFu; };
+  p.r_group = recip(p.nd + 2 * p.ng);
+  p.r_d = recip(p.nc_d);
+  p.r_g = recip(p.nc_g);
+  const long long tiles = (long long)G * (p.nd + 2 * p.ng);
+  const int pairs = (int)(tiles < a.num_sms / 2 ? tiles : a.num_sms / 2);
+  if (pairs < 1) return cudaErrorInvalidValue;
+  return launch_dependent(grouped_weight_grad_kernel, 2 * pairs, kThreads, smem_bytes(G, p.stages), s, true, /*cluster=*/2, m,
+                          p);
+}
+
+}  // namespace moe

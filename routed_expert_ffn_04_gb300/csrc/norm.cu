@@ -512,7 +512,8 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
   }
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.dweight)
-    e = launch_dependent(sum_partials_kernel, (a.H + 31) / 32, 1024, 0, s, true, part, n, a.H, a.dweight);
+    e = launch_dependent(sum_partials_kernel, (a.H + 31) / 32, 1024, 0, s, true, /*cluster=*/1, part, n, a.H,
+                         a.dweight);
   return e;
 }
 
