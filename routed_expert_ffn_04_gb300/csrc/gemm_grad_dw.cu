@@ -194,54 +194,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = row_start[g + 1] - row_start[g];
     return n > 0 ? n : 0;
   };
-  auto rows_of_tile = [&](int tile) { return rows_of(order[div_by(tile, p.nd + 2 * p.ng, p.r_group)]); };
+  // Tiles are decoded 32 rounds at a time, one by each lane of a role's warp,
+  // and read back by shuffles: decoding a tile alone cost a role's thread 1000
+  // to 1500 cycles, as long as half the tile's MMAs.
+  struct Tile {
+    int rows, row0, m0, n0, g_which;  // g * 4 + which
+  };
+  auto decode = [&](int r) {
+    Tile t = {0, 0, 0, 0, 0};
+    const int tile = tile_of(r);
+    if (r < rounds && tile < total) {
+      const DwTile d = dw_tile(p, order, tile);
+      t = {rows_of(d.g), row_start[d.g], d.m0, d.n0, d.g * 4 + d.which};
+    }
+    return t;
+  };
+  auto at_round = [&](int v, int r) { return __shfl_sync(0xFFFFFFFFu, v, r & 31); };
+  const int my_rounds = total > tile_of(rounds - 1) ? rounds : rounds - 1;  // the last round may be short
   // A stage with `left` rows of the group from its first row on is ragged when
   // the group ends inside one of its steps.
   auto ragged = [](int left) { return left < kBK && (left & 15) != 0; };
 
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers
-    if (lane == 0) {
-      const bool is_a = warp == 0;
-      Ring rg;
-      bool ok = true;
-      for (int r = 0; ok && r < rounds; ++r) {
-        const int tile = tile_of(r);
-        if (tile >= total) break;
-        const DwTile dt = dw_tile(p, order, tile);
-        int krow = row_start[dt.g];
-        const int x = is_a ? dt.m0 + (int)rank * 128 : dt.n0 + (int)rank * 128;
-        for (int left = rows_of(dt.g); left > 0; left -= kBK, krow += kBK) {
-          if (!mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status, MOE_DEV_TIMEOUT_PRODUCER,
-                                 p.k.limit_ns)) {
-            ok = false;
-            break;
+    // The whole warp walks the loop in step; one elected lane issues.
+    const bool is_a = warp == 0;
+    Ring rg;
+    bool ok = true;
+    Tile mine = {};
+    for (int r = 0; ok && r < my_rounds; ++r) {
+      if ((r & 31) == 0) mine = decode(r + lane);
+      int krow = at_round(mine.row0, r);
+      const int nrows = at_round(mine.rows, r), which = at_round(mine.g_which, r) & 3;
+      const int x = at_round(is_a ? mine.m0 : mine.n0, r) + (int)rank * 128;
+      const CUtensorMap* maps = is_a ? (which == 0 ? m.dy : (which == 1 ? m.dg : m.du)) : (which == 0 ? m.h : m.a);
+      for (int left = nrows; left > 0; left -= kBK, krow += kBK) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
+                                                       MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
+          ok = false;
+          break;
+        }
+        const int low = left <= 16 ? 2 : (left <= 32 ? 1 : 0);  // box height 64 >> low
+        const CUtensorMap* map = maps + low;
+        const uint32_t dst = base_u32 + rg.s * kStageBytes + (is_a ? 0 : 2 * kChunk);
+        const bool own = ragged(left);  // completes on this CTA's tail barrier
+        const uint32_t bar = own ? tail_bar(rg.s) : (rank == 0 ? full_bar(rg.s) : mapa_shared(full_bar(rg.s), 0));
+        if (elect_one()) {
+          if (is_a && own) {
+            mbar_arrive_expect_tx(bar, (uint32_t)kStageBytes >> low);
+          } else if (is_a && rank == 0) {  // both CTAs' bytes (the other's may land first)
+            mbar_arrive_expect_tx(bar, 2u * ((uint32_t)kStageBytes >> low));
+            mbar_arrive(bar);
           }
-          const int low = left <= 16 ? 2 : (left <= 32 ? 1 : 0);  // box height 64 >> low
-          const CUtensorMap* map;
-          if (is_a) map = dt.which == 0 ? &m.dy[low] : (dt.which == 1 ? &m.dg[low] : &m.du[low]);
-          else map = dt.which == 0 ? &m.h[low] : &m.a[low];
-          uint32_t bar;
-          if (ragged(left)) {
-            bar = tail_bar(rg.s);
-            if (is_a) mbar_arrive_expect_tx(bar, (uint32_t)kStageBytes >> low);
-          } else {
-            bar = rank == 0 ? full_bar(rg.s) : mapa_shared(full_bar(rg.s), 0);
-            if (is_a && rank == 0) {  // both CTAs' bytes (the other's may land first)
-              mbar_arrive_expect_tx(bar, 2u * ((uint32_t)kStageBytes >> low));
-              mbar_arrive(bar);
-            }
-          }
-          const uint32_t dst = base_u32 + rg.s * kStageBytes + (is_a ? 0 : 2 * kChunk);
           tma_load_2d_pair(dst, map, bar, x, krow);
           tma_load_2d_pair(dst + kChunk, map, bar, x + 64, krow);
-          rg.next(NS);
         }
+        __syncwarp();
+        rg.next(NS);
       }
-      if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 5000000ull) {
-        }
+    }
+    if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 5000000ull) {
       }
     }
   } else if (warp == 1) {
@@ -258,13 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Ring rg;
       bool ok = true, issued = false;
-      int local = 0;
-      for (int r = 0; ok && r < rounds; ++r, ++local) {
-        const int tile = tile_of(r);
-        if (tile >= total) break;
-        const int acc = local & 1;
-        const uint32_t ap = (uint32_t)(local >> 1) & 1u;
-        const int nrows = rows_of_tile(tile);
+      int rows32 = 0;
+      for (int r = 0; ok && r < my_rounds; ++r) {
+        if ((r & 31) == 0) rows32 = decode(r + lane).rows;
+        const int acc = r & 1;
+        const uint32_t ap = (uint32_t)(r >> 1) & 1u;
+        const int nrows = at_round(rows32, r);
         if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
           ok = false;
           break;
@@ -317,11 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stage to the leader. A stage's tail barrier has one phase per ragged use.
     Ring rg;
     uint32_t phase = 0;
-    for (int r = 0; r < rounds; ++r) {
-      const int tile = tile_of(r);
-      if (tile >= total) break;
+    int rows32 = 0;
+    for (int r = 0; r < my_rounds; ++r) {
+      if ((r & 31) == 0) rows32 = decode(r + lane).rows;
       bool ok = true;
-      for (int left = rows_of_tile(tile); left > 0; left -= kBK) {
+      for (int left = at_round(rows32, r); left > 0; left -= kBK) {
         if (ragged(left)) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail_bar(rg.s), (phase >> rg.s) & 1u, abort_flag, p.k.status,
                                                          MOE_DEV_TIMEOUT_MMA, p.k.limit_ns));
@@ -349,13 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;             // this warp may access TMEM lanes 32q .. 32q+31
     const int half = warp > 6 ? 1 : 0;  // its 128 columns
     uint8_t* stg = epi_stage + (half * 4 + q) * 4096;
-    int local = 0;
-    for (int r = 0; r < rounds; ++r, ++local) {
-      const int tile = tile_of(r);
-      if (tile >= total) break;
-      const int acc = local & 1;
-      const uint32_t ap = (uint32_t)(local >> 1) & 1u;
-      const DwTile dt = dw_tile(p, order, tile);
+    Tile mine = {};
+    for (int r = 0; r < my_rounds; ++r) {
+      if ((r & 31) == 0) mine = decode(r + lane);
+      const int acc = r & 1;
+      const uint32_t ap = (uint32_t)(r >> 1) & 1u;
+      const int which = at_round(mine.g_which, r) & 3, g = at_round(mine.g_which, r) >> 2;
+      const int m0 = at_round(mine.m0, r) + (int)rank * 128 + q * 32, n0 = at_round(mine.n0, r) + half * 128;
+      const bool empty = at_round(mine.rows, r) == 0;
       int ok = 1;
       if (lane == 0)
         ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
@@ -367,9 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // instruction, and the queue they form delays the loads: one SM per tile
       // 2.70 ms against 2.45.) H and I are multiples of 64, so a block is all
       // inside the group's matrix or all outside.
-      const int M = dt.which == 0 ? p.H : p.I, N = dt.which == 0 ? p.I : p.H;
-      const int m0 = dt.m0 + (int)rank * 128 + q * 32, n0 = dt.n0 + half * 128;
-      const bool empty = rows_of(dt.g) == 0;
+      const int M = which == 0 ? p.H : p.I, N = which == 0 ? p.I : p.H;
       if (m0 < M) {
 #pragma unroll 1
         for (int c = 0; c < 128 && n0 + c < N; c += 64) {
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&m.dw[dt.which], smem_u32(stg), n0 + c, dt.g * M + m0);
+            tma_store_2d(&m.dw[which], smem_u32(stg), n0 + c, g * M + m0);
             bulk_commit_group();
           }
         }
