@@ -518,8 +518,8 @@ MOE_API moe_status_t moe_permute_backward(moe_handle_t h, const moe_config_t* cf
                                           const int32_t* flat_to_perm, const void* dx_add, void* dx,
                                           moe_stream_t stream);
 
-/* Scratch bytes moe_grouped_swiglu_backward needs: 10 bytes per row and
- * intermediate feature. */
+/* Scratch bytes moe_grouped_swiglu_backward needs: about 10 bytes per row and
+ * 90 per group, for each intermediate feature. */
 MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_groups, int H, int I,
                                                                 moe_dtype_t dtype, size_t* bytes);
 

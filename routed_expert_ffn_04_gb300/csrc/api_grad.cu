@@ -32,17 +32,19 @@ size_t norm_grad_ws(int64_t rows, int H) {
   return align_up((size_t)(a > b ? a : b) * H * 4 + 1, 256);
 }
 
-// moe_grouped_swiglu_backward workspace: q fp32, then h, dgate and dup bf16.
+// moe_grouped_swiglu_backward workspace: a flag, q fp32, then h, dgate and dup
+// bf16 with each group's rows padded to a multiple of 16.
 struct GradWs {
-  size_t h, dg, du, total;
+  size_t q, h, dg, du, total;
 };
-GradWs grad_ws(int rows, int I) {
-  const size_t n = (size_t)rows * I;
+GradWs grad_ws(int rows, int G, int I) {
+  const size_t n = (size_t)rows * I, np = ((size_t)rows + 15 * (size_t)G) * I;
   GradWs L;
-  L.h = align_up(n * 4 + 1, 256);
-  L.dg = L.h + align_up(n * 2 + 1, 256);
-  L.du = L.dg + align_up(n * 2 + 1, 256);
-  L.total = L.du + align_up(n * 2 + 1, 256);
+  L.q = 256;
+  L.h = L.q + align_up(n * 4 + 1, 256);
+  L.dg = L.h + align_up(np * 2 + 1, 256);
+  L.du = L.dg + align_up(np * 2 + 1, 256);
+  L.total = L.du + align_up(np * 2 + 1, 256);
   return L;
 }
 
@@ -154,7 +156,7 @@ MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_
                                                                 moe_dtype_t dtype, size_t* bytes) {
   if (!bytes || !grad_shape_ok(num_groups, rows, H, I)) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16) return is_mx_dtype(dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
-  *bytes = grad_ws(rows, I).total;
+  *bytes = grad_ws(rows, num_groups, I).total;
   return MOE_OK;
 }
 
@@ -170,7 +172,7 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
   if ((dws != 0 && dws != 3) || (dws == 0 && !da)) return MOE_ERR_INVALID_ARG;
   if (!w_gate || !w_up || !w_down || !ws || (rows > 0 && (!a || !dy))) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(a, dy, offsets, w_gate, w_up, w_down, da, dw_gate, dw_up, dw_down, ws)) return MOE_ERR_INVALID_ARG;
-  const GradWs L = grad_ws(rows, I);
+  const GradWs L = grad_ws(rows, num_groups, I);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   const moe_status_t st = bind_handle(h);
   if (st != MOE_OK) return st;
@@ -186,7 +188,8 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
   g.w_gate = w_gate;
   g.w_up = w_up;
   g.w_down = w_down;
-  g.q = reinterpret_cast<float*>(w);
+  g.odd = reinterpret_cast<int*>(w);
+  g.q = reinterpret_cast<float*>(w + L.q);
   g.h = w + L.h;
   g.dg = w + L.dg;
   g.du = w + L.du;

@@ -8,13 +8,13 @@
 //                h = silu(gate) up;  du = q silu(gate);
 //                dg = q up sigma(gate) (1 + gate (1 - sigma(gate)))  [rows, I] bf16
 //   DX (INPUT):  da = dg Wg + du Wu                               [rows, H] bf16
-//   DW (WEIGHT): dWd = dy^T h;  dWg = dg^T a;  dWu = du^T a       per group, bf16
+//   and, in gemm_grad_dw.cu, dWd = dy^T h;  dWg = dg^T a;  dWu = du^T a   per group
 //
 // 16 rows H I FLOP in all: 12 for the gradient and 4 to recompute gate and up,
 // which the forward does not keep. q stays fp32 between the launches; h, dg
 // and du are rounded to bf16 once, as the tensor cores read them.
 //
-// One kernel, four modes. Persistent, one CTA per SM, tiles of 128 x 256 fp32
+// One kernel, three modes. Persistent, one CTA per SM, tiles of 128 x 256 fp32
 // accumulators double-buffered in TMEM (512 columns), K in steps of 64 through
 // a ring of 48 KB stages written by TMA:
 //   warp 0      TMA producer (one thread); modes with more than three boxes per
@@ -32,13 +32,7 @@
 //   Q     dy rows, K-major               Wd columns, MN-major        H
 //   GU    a rows, K-major                Wg | Wu rows, K-major       H
 //   DX    dg rows, then du rows, K-major Wg, then Wu columns, MN     I, twice
-//   DW    dy / dg / du columns, MN       h / a columns, MN           the group's rows
-//
-// In DW the reduction runs over a group's rows, which end anywhere: the last
-// stage's box also holds rows of the next group. The MMA runs in steps of 16
-// rows, and the rows between the group's end and the step's end are zeroed in
-// shared memory in both operands first (a zero times another group's infinity
-// would not be zero). A group without rows gives zero gradients.
+// The weight gradients (gemm_grad_dw.cu) reduce over the rows.
 //
 // Every wait is bounded; on expiry the CTA records an error code in the status
 // word, drains its in-flight copies and MMAs, frees TMEM and exits.
@@ -70,7 +64,7 @@ struct GradGeo {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   // Warp 6 is a second producer where a stage has more than three boxes.
   static constexpr int THREADS = MODE == kGU ? 192 : 224;
-  static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 8) * 4;  // row starts, tile starts
+  static constexpr int TABLE_BYTES = 3 * (kMaxGroups + 8) * 4;  // tile, row and padded row starts
   static constexpr int BAR_BYTES = 512;
   static constexpr int EPI_WARP = 4096;  // one warp's staging block: 32 rows of 128 bytes
   static constexpr int EPI_BYTES = 4 * EPI_WARP;
@@ -90,7 +84,9 @@ struct GradParams {
   int H, I;
   int num_kb;             // stages per tile (Q, GU: H / 64; DX: 2 I / 64)
   float* q;               // [rows, I]
-  __nv_bfloat16 *h, *dg, *du;  // [rows, I]
+  __nv_bfloat16 *h, *dg, *du;  // [prows, I], padded (padded_rows)
+  int prows;
+  int* odd;               // set where gate or q is not finite
   __nv_bfloat16* da;      // [rows, H]
 };
 
@@ -133,16 +129,22 @@ __device__ __forceinline__ void copy_staged_rows(const uint8_t* stg, int lane, i
 
 // Epilogue of one 128 x TILE_N tile by one warp (32 accumulator rows).
 template <int MODE>
-__device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInfo& ti, uint32_t tb, int q, int lane,
-                                              uint8_t* stg, const CUtensorMap* map_out) {
+__device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInfo& ti, int pad0, uint32_t tb, int q,
+                                              int lane, uint8_t* stg, const CUtensorMap* map_out) {
   const int r0 = ti.tt * 128 + q * 32;  // the warp's first row in the group
   const int nr = ti.nrows - r0;         // rows of the group from there on
-  if (nr <= 0) return;
+  if (nr <= 0) return;                  // (r0 % 16 == 0: no padding here either)
   if (MODE == kGU) {
     // q comes in coalesced (four rows of 128 bytes per load instruction), one
     // block of 32 columns ahead, and goes through the staging buffer to the
     // lane that holds the row's accumulators.
     const size_t row = (size_t)ti.row0 + r0;
+    // h, dg, du: the group's rows and the zero rows that fill its last step.
+    const size_t prow = (size_t)pad0 + r0;
+    const bool live = lane < nr;
+    int np = pad16(ti.nrows) - r0;
+    if ((long long)prow + np > p.prows) np = (int)(p.prows - (long long)prow);  // decreasing offsets
+    bool odd = false;
     const int c0 = ti.wt * 128;
     const int ncol = p.I - c0 < 128 ? p.I - c0 : 128;  // a multiple of 64
     float4 nq[8];
@@ -178,6 +180,9 @@ __device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInf
       tmem_ld_32x32b_x32(tb + c, g);
       tmem_ld_32x32b_x32(tb + 128 + c, u);
       tmem_ld_wait();
+      // An infinity or NaN in the row of a or of dy leaves none of its gate
+      // values, or of its q values, finite.
+      odd = odd || !(fabsf(__uint_as_float(g[0])) <= 3.402823466e38f) || !(fabsf(qv[0]) <= 3.402823466e38f);
       uint32_t ph[16], pg[16], pu[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -191,15 +196,16 @@ __device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInf
           uv[i] = qq * act;
           gv[i] = qq * up * sg * fmaf(gt, 1.0f - sg, 1.0f);
         }
-        ph[j] = pack_bf16(hv[0], hv[1]);
-        pg[j] = pack_bf16(gv[0], gv[1]);
-        pu[j] = pack_bf16(uv[0], uv[1]);
+        ph[j] = live ? pack_bf16(hv[0], hv[1]) : 0u;
+        pg[j] = live ? pack_bf16(gv[0], gv[1]) : 0u;
+        pu[j] = live ? pack_bf16(uv[0], uv[1]) : 0u;
       }
-      const size_t at = row * p.I + c0 + c;
-      store_block32(ph, stg, lane, nr, p.h + at, p.I);
-      store_block32(pg, stg + 2048, lane, nr, p.dg + at, p.I);
-      store_block32(pu, stg, lane, nr, p.du + at, p.I);
+      const size_t at = prow * p.I + c0 + c;
+      store_block32(ph, stg, lane, np, p.h + at, p.I);
+      store_block32(pg, stg + 2048, lane, np, p.dg + at, p.I);
+      store_block32(pu, stg, lane, np, p.du + at, p.I);
     }
+    if (odd && live) *p.odd = 1;
   } else if (MODE == kQ) {
     const size_t row = (size_t)ti.row0 + r0;
 #pragma unroll 1
@@ -267,6 +273,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   uint8_t* epi_stage = base + Gm::RING_BYTES;
   int32_t* tile_start = reinterpret_cast<int32_t*>(epi_stage + Gm::EPI_BYTES);
   int32_t* row_start = tile_start + kMaxGroups + 8;
+  int32_t* pad_start = row_start + kMaxGroups + 8;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + Gm::EPI_BYTES + Gm::TABLE_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Gm::NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -288,6 +295,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     int r0, nr;
     group_rows(p.k, g, r0, nr);
     tile_start[g] = n_wt * ((nr + 127) / 128);
+    pad_start[g] = pad16(nr);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -307,32 +315,15 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
     tmem_relinquish();
   }
   __syncthreads();
-  if (warp == 0) {  // exclusive scan of the per-group tile counts
-    const int per = (G + 31) / 32;
-    const int b = lane * per < G ? lane * per : G;
-    const int e = (b + per < G) ? b + per : G;
-    int local = 0;
-    for (int g = b; g < e; ++g) local += tile_start[g];
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    int run = incl - local;
-    for (int g = b; g < e; ++g) {
-      const int c = tile_start[g];
-      tile_start[g] = run;
-      run += c;
-    }
-    if (lane == 31) tile_start[G] = incl;
-  }
+  if (warp == 0) scan_warp(tile_start, G, lane);
+  if (MODE != kQ && warp == 2) scan_warp(pad_start, G, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   // Up to here nothing was read that the launch before this one writes (its
   // blocks may still be running: programmatic dependent launch).
   wait_for_previous_launch();
+  if (MODE == kQ && blockIdx.x == 0 && threadIdx.x == 0) *p.odd = 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[G];
 
@@ -370,7 +361,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
             const CUtensorMap* mb = second ? &m.b1 : &m.b0;
             const int krow = ti.g * (MODE == kQ ? p.H : p.I) + kx;
             if (first) {
-              tma_load_2d(sa, second ? &m.a2 : &m.a, fb, kx, ti.row0 + ti.tt * 128);
+              tma_load_2d(sa, second ? &m.a2 : &m.a, fb, kx, (MODE == kDX ? pad_start[ti.g] : ti.row0) + ti.tt * 128);
               tma_load_2d(sb, mb, fb, ti.wt * 256, krow);
             } else {
 #pragma unroll
@@ -454,7 +445,7 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
       const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
-      grad_epilogue<MODE>(p, ti, tb, q, lane, stg, &m.out);
+      grad_epilogue<MODE>(p, ti, pad_start[ti.g], tb, q, lane, stg, &m.out);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty_bar(acc));
@@ -519,6 +510,8 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
   p.h = static_cast<__nv_bfloat16*>(a.h);
   p.dg = static_cast<__nv_bfloat16*>(a.dg);
   p.du = static_cast<__nv_bfloat16*>(a.du);
+  p.prows = (int)padded_rows(a.rows, G);
+  p.odd = a.odd;
   p.da = static_cast<__nv_bfloat16*>(a.da);
   const uint64_t R = a.rows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
   const long long row_tiles = (a.rows + 127) / 128 + (long long)G;  // at most: one ragged tile per group
@@ -545,7 +538,8 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
   }
   if (e == cudaSuccess && a.da) {
     GradMaps m = {};
-    maps = make_tmap_bf16(&m.a, a.dg, I, R, 128) && make_tmap_bf16(&m.a2, a.du, I, R, 128) &&
+    const uint64_t P = p.prows;
+    maps = make_tmap_bf16(&m.a, a.dg, I, P, 128) && make_tmap_bf16(&m.a2, a.du, I, P, 128) &&
            make_tmap_bf16(&m.b0, a.w_gate, H, GI, 64) && make_tmap_bf16(&m.b1, a.w_up, H, GI, 64) &&
            make_tmap_bf16(&m.out, a.da, H, R, 32);
     if (!maps) return cudaErrorInvalidValue;

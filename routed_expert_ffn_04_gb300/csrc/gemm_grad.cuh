@@ -48,6 +48,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// h, dg and du keep a group's rows together with zero rows up to the next
+// multiple of 16, the tensor cores' step along the rows: row r of group g is
+// row pad_start[g] + r of them. The rows they need for at most `rows` rows in G
+// groups:
+__host__ __device__ inline long long padded_rows(int rows, int G) { return (long long)rows + 15ll * G; }
+__device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
+
+// v[0..G-1] to their exclusive sums, v[G] the total, by one warp.
+__device__ __forceinline__ void scan_warp(int32_t* v, int G, int lane) {
+  const int per = (G + 31) / 32;
+  const int b = lane * per < G ? lane * per : G;
+  const int e = (b + per < G) ? b + per : G;
+  int local = 0;
+  for (int g = b; g < e; ++g) local += v[g];
+  int incl = local;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += u;
+  }
+  int run = incl - local;
+  for (int g = b; g < e; ++g) {
+    const int c = v[g];
+    v[g] = run;
+    run += c;
+  }
+  if (lane == 31) v[G] = incl;
+}
+
 // A warp's block of 32 rows x 64 bf16 columns (lane = row, TMEM columns taddr
 // .. taddr + 63) into its staging buffer, 128-byte rows, 16-byte chunk j of row
 // r at chunk j ^ (r % 8).

@@ -15,15 +15,18 @@
 // outlasts its MMAs; the pair's tile costs each SM 32 KB for the same MMAs.
 // 192 experts x 341 rows, H = 4096, I = 1536: one SM per tile 2.45 ms.
 //
-// The reduction's last stage also holds rows of the next group (or past the
-// last one). The MMA runs in steps of 16 rows; the rows between the group's
-// end and the step's end are cleared in shared memory in both operands first
-// (a zero times another group's infinity would not be zero). A group without
-// rows gives zero gradients.
+// A group's rows end anywhere; the MMA runs in steps of 16 rows. One operand of
+// each product is h, dg or du, whose groups are followed by zero rows up to a
+// multiple of 16, so whatever finite rows of the next group the other operand
+// holds there adds nothing. A zero times an infinity or NaN would: when the
+// launch before has met one (p.odd), the rows past the group's end are
+// cleared in shared memory first (the careful way: 0.3 to 0.5 ms more at the
+// size below, as every tile's last stage waits for it). A group without rows
+// gives zero gradients.
 //
 // Roles per CTA (12 warps): 0 loads A's boxes and arms the stage; 6 loads B's;
 // 1 (of the even CTA, the leader) issues the pair's MMAs; 11 clears ragged
-// stages; 2-5 and 7-10 store the result, 32 rows by 64 columns at a time. A
+// stages (the careful way); 2-5 and 7-10 store the result, 32 rows by 64 columns at a time. A
 // stage's copies in both CTAs complete on the leader's full barrier; a ragged
 // stage's on each CTA's own tail barrier, whose clearing warp then arrives on
 // the leader's full barrier. Every wait is bounded.
@@ -52,11 +55,11 @@ constexpr int kEpiBytes = kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
 constexpr int kBarBytes = 8 * (3 * kMaxStages + 5) + 8;
 constexpr uint16_t kPairMask = 0x3;
 
-constexpr int table_bytes(int G) { return ((G + 1) * 4 + 2 * G + 15) / 16 * 16; }
+constexpr int table_bytes(int G) { return ((G + 1) * 4 + 2 * G + 2 * G + 15) / 16 * 16; }
 constexpr int smem_bytes(int G, int stages) {
   return 1024 + stages * kStageBytes + kEpiBytes + kBarBytes + table_bytes(G);
 }
-// Six stages, or five when the tables of many groups (more than 289) need the room.
+// Six stages, or five when the tables of many groups (more than 229) need the room.
 constexpr int ring_stages(int G) { return smem_bytes(G, kMaxStages) <= kMaxSmem ? kMaxStages : kMaxStages - 1; }
 static_assert(kBarBytes % 16 == 0, "the tables follow the barriers");
 static_assert(smem_bytes(kMaxGroups, kMaxStages - 1) <= kMaxSmem, "shared memory");
@@ -65,6 +68,7 @@ struct DwParams {
   KParams k;  // offsets, G, rows, status, limit_ns
   int H, I;
   int stages;
+  const int* odd;              // not 0: a row of a or dy may hold an infinity or NaN
   int nd, ng, nc_d, nc_g;      // tiles of dWd and of dWg (= of dWu) per group; per row of tiles
   uint32_t r_group, r_d, r_g;  // floor(2^32 / d) of nd + 2 ng, nc_d, nc_g (div_by)
 };
@@ -134,7 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* row_start = reinterpret_cast<int32_t*>(epi_stage + kEpiBytes + kBarBytes);
-  uint16_t* order = reinterpret_cast<uint16_t*>(row_start + G + 1);
+  // Group g's first row in h, dg and du (gemm_grad.cuh) is row_start[g] -
+  // row_start[0] + pad_extra[g].
+  uint16_t* pad_extra = reinterpret_cast<uint16_t*>(row_start + G + 1);
+  uint16_t* order = pad_extra + G;
+  int32_t* pads = reinterpret_cast<int32_t*>(epi_stage);  // until the loop starts
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };                         // leader: both CTAs' stage s
   auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };         // each CTA
@@ -161,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += (o > n || (o == n && j < g)) ? 1 : 0;
     }
     order[at] = (uint16_t)g;
+    pads[g] = n > 0 ? pad16(n) - n : 0;
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -182,10 +191,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 2) {
+    scan_warp(pads, G, lane);
+    __syncwarp();
+    for (int g = lane; g < G; g += 32) pad_extra[g] = (uint16_t)pads[g];
+  }
+  __syncthreads();
   cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
   // Up to here nothing was read that the launch before this one writes.
   wait_for_previous_launch();
+  const bool careful = *static_cast<const volatile int*>(p.odd) != 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = G * (p.nd + 2 * p.ng);
   const int rounds = (total + npairs - 1) / npairs;
@@ -198,22 +214,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // and read back by shuffles: decoding a tile alone cost a role's thread 1000
   // to 1500 cycles, as long as half the tile's MMAs.
   struct Tile {
-    int rows, row0, m0, n0, g_which;  // g * 4 + which
+    int rows, row0, prow0, m0, n0, g_which;  // prow0: in h, dg, du; g * 4 + which
   };
   auto decode = [&](int r) {
-    Tile t = {0, 0, 0, 0, 0};
+    Tile t = {};
     const int tile = tile_of(r);
     if (r < rounds && tile < total) {
       const DwTile d = dw_tile(p, order, tile);
-      t = {rows_of(d.g), row_start[d.g], d.m0, d.n0, d.g * 4 + d.which};
+      t = {rows_of(d.g), row_start[d.g], row_start[d.g] - row_start[0] + pad_extra[d.g], d.m0, d.n0, d.g * 4 + d.which};
     }
     return t;
   };
   auto at_round = [&](int v, int r) { return __shfl_sync(0xFFFFFFFFu, v, r & 31); };
   const int my_rounds = total > tile_of(rounds - 1) ? rounds : rounds - 1;  // the last round may be short
-  // A stage with `left` rows of the group from its first row on is ragged when
-  // the group ends inside one of its steps.
-  auto ragged = [](int left) { return left < kBK && (left & 15) != 0; };
+  // A stage with `left` rows of the group from its first row on needs clearing
+  // when the group ends inside one of its steps.
+  auto ragged = [&](int left) { return careful && left < kBK && (left & 15) != 0; };
 
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers
@@ -224,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tile mine = {};
     for (int r = 0; ok && r < my_rounds; ++r) {
       if ((r & 31) == 0) mine = decode(r + lane);
-      int krow = at_round(mine.row0, r);
       const int nrows = at_round(mine.rows, r), which = at_round(mine.g_which, r) & 3;
+      // A: dy (rows as given), dg, du; B: h, then a (rows as given).
+      int krow = at_round(is_a == (which == 0) ? mine.row0 : mine.prow0, r);
       const int x = at_round(is_a ? mine.m0 : mine.n0, r) + (int)rank * 128;
       const CUtensorMap* maps = is_a ? (which == 0 ? m.dy : (which == 1 ? m.dg : m.du)) : (which == 0 ? m.h : m.a);
       for (int left = nrows; left > 0; left -= kBK, krow += kBK) {
@@ -431,12 +448,12 @@ cudaError_t gemm_grad_dw_prepare_device() {
 
 cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s) {
   const int G = a.offsets ? a.G : 1, H = a.H, I = a.I;
-  const uint64_t R = a.rows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
+  const uint64_t R = a.rows, P = padded_rows(a.rows, G), GI = (uint64_t)G * I, GH = (uint64_t)G * H;
   DwMaps m = {};
   for (int i = 0; i < 3; ++i) {
     const uint32_t box = 64u >> i;
-    if (!make_tmap_bf16(&m.dy[i], a.dy, H, R, box) || !make_tmap_bf16(&m.dg[i], a.dg, I, R, box) ||
-        !make_tmap_bf16(&m.du[i], a.du, I, R, box) || !make_tmap_bf16(&m.h[i], a.h, I, R, box) ||
+    if (!make_tmap_bf16(&m.dy[i], a.dy, H, R, box) || !make_tmap_bf16(&m.dg[i], a.dg, I, P, box) ||
+        !make_tmap_bf16(&m.du[i], a.du, I, P, box) || !make_tmap_bf16(&m.h[i], a.h, I, P, box) ||
         !make_tmap_bf16(&m.a[i], a.a, H, R, box))
       return cudaErrorInvalidValue;
   }
@@ -452,6 +469,7 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s)
   p.H = H;
   p.I = I;
   p.stages = ring_stages(G);
+  p.odd = a.odd;
   p.nc_d = (I + 255) / 256;
   p.nc_g = (H + 255) / 256;
   p.nd = ((H + 255) / 256) * p.nc_d;

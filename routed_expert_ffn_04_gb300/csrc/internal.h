@@ -242,9 +242,10 @@ struct GroupedGradArgs {
   const void* w_up;        // [G, I, H] bf16
   const void* w_down;      // [G, H, I] bf16
   float* q;                // [rows, I] scratch
-  void* h;                 // [rows, I] bf16 scratch
-  void* dg;                // [rows, I] bf16 scratch
-  void* du;                // [rows, I] bf16 scratch
+  void* h;                 // [rows + 15 G, I] bf16 scratch (padded_rows in gemm_grad.cuh)
+  void* dg;                // the same
+  void* du;                // the same
+  int* odd;                // one word of scratch
   void* da;                // [rows, H] bf16, or nullptr
   void* dw_gate;           // [G, I, H] bf16, or nullptr (all three)
   void* dw_up;             // [G, I, H] bf16
