@@ -14,28 +14,39 @@
 // which the forward does not keep. q stays fp32 between the launches; h, dg
 // and du are rounded to bf16 once, as the tensor cores read them.
 //
-// One kernel, three modes. Persistent, one CTA per SM, tiles of 128 x 256 fp32
-// accumulators double-buffered in TMEM (512 columns), K in steps of 64 through
-// a ring of 48 KB stages written by TMA:
-//   warp 0      TMA producer (one thread); modes with more than three boxes per
-//               stage split them with warp 6;
-//   warp 1      TMEM allocation and tcgen05.mma (M = 128, N = 256, K = 16);
-//   warps 2..5  epilogue, 32 accumulator rows each.
+// One kernel, three modes. Persistent, a pair of CTAs on the two SMs of a TPC
+// per tile (tcgen05 .cta_group::2): the weights are the M = 256 rows of the MMA,
+// 128 in each SM, and a chunk of up to 256 of the group's rows (tokens) is N,
+// half loaded by each SM. A group of n rows is cut into ceil(n / 256) chunks of
+// about one size, each rounded up to 32: 341 rows take 192 + 160. With the
+// tokens as M instead, a tile of 128 rows on one SM, 341 rows take 384, and an
+// SM takes in 48 KB per 64 elements of the reduction for 512 cycles of MMAs
+// (it can take in about 64 bytes a cycle); the pair's tile costs it at most
+// 32 KB. In TMEM an accumulator's lane is a weight row (an output feature), its
+// column a token; two accumulators of 256 columns.
 //
-// Operands. The forward's weights are K-major for the forward products; three
-// of the four products here reduce over another axis, so their operands are
-// read MN-major from the same row-major tensors, with no transposed copy: a
-// box of 64 columns x 64 rows lands as 64 rows (the reduction axis) of 128
-// swizzled bytes, the tensor cores' MN-major operand layout, and the
-// instruction descriptor's transpose bit is set.
-//   mode  A (128 rows of M)              B (256 rows of N)           reduction
-//   Q     dy rows, K-major               Wd columns, MN-major        H
-//   GU    a rows, K-major                Wg | Wu rows, K-major       H
-//   DX    dg rows, then du rows, K-major Wg, then Wu columns, MN     I, twice
-// The weight gradients (gemm_grad_dw.cu) reduce over the rows.
+// Operands. The forward's weights are K-major for the forward products; Q and
+// DX reduce over their other axis, so they are read MN-major from the same
+// row-major tensors, with no transposed copy: a box of 64 columns x 64 rows
+// lands as 64 rows (the reduction axis) of 128 swizzled bytes, the tensor
+// cores' MN-major operand layout, and the instruction descriptor's transpose
+// bit is set.
+//   mode  A (M: weights)                   B (N: tokens)              reduction
+//   Q     Wd columns, MN-major             dy rows, K-major           H
+//   GU    64 Wg rows, 64 Wu rows, K-major  a rows, K-major            H
+//   DX    Wg, then Wu columns, MN-major    dg rows, then du rows      I, twice
+//
+// Roles per CTA (7 warps, each walking its tiles in step with warp-uniform
+// values and one elected lane issuing): 0 loads A's boxes and arms the stage,
+// 6 loads B's, 1 (of the even CTA, the leader) issues the pair's MMAs, 2-5 are
+// the epilogue, 32 accumulator lanes each. Both CTAs' copies of a stage complete
+// on the leader's full barrier. In GU lanes 0-63 hold the gates and 64-127 the
+// ups of the same 64 features: warps q and q + 2 exchange half of each block
+// of 32 tokens through shared memory and finish 16 tokens each. A warp's store
+// of one token is 32 neighbouring features.
 //
 // Every wait is bounded; on expiry the CTA records an error code in the status
-// word, drains its in-flight copies and MMAs, frees TMEM and exits.
+// word, lets its in-flight copies and MMAs end, frees TMEM and exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -52,35 +63,24 @@ namespace {
 
 enum GradMode { kQ = 0, kGU = 1, kDX = 2 };
 
-constexpr int kBK = 64;           // reduction elements per stage
+constexpr int kBK = 64;  // reduction elements per stage
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSmem = 232448;  // 227 KB dynamic shared memory per CTA
-
-template <int MODE>
-struct GradGeo {
-  static constexpr bool B_MN = MODE != kGU;
-  static constexpr int A_BYTES = 128 * 128;  // 16 KB
-  static constexpr int B_BYTES = 256 * 128;  // 32 KB
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // Warp 6 is a second producer where a stage has more than three boxes.
-  static constexpr int THREADS = MODE == kGU ? 192 : 224;
-  static constexpr int TABLE_BYTES = 3 * (kMaxGroups + 8) * 4;  // tile, row and padded row starts
-  static constexpr int BAR_BYTES = 512;
-  static constexpr int EPI_WARP = 4096;  // one warp's staging block: 32 rows of 128 bytes
-  static constexpr int EPI_BYTES = 4 * EPI_WARP;
-  static constexpr int EXTRA = 1024 + TABLE_BYTES + BAR_BYTES + EPI_BYTES;
-  static constexpr int S = (kMaxSmem - EXTRA) / STAGE_BYTES;
-  static constexpr int RING_BYTES = S * STAGE_BYTES;
-  static constexpr int SMEM = EXTRA + RING_BYTES;
-  static constexpr int NBARS = 2 * S + 5;
-  static constexpr int TILE_N = MODE == kGU ? 128 : 256;  // output columns per tile
-  static_assert(S >= 4, "ring too shallow");
-  static_assert(NBARS * 8 + 8 <= BAR_BYTES, "barrier area");
-  static_assert(SMEM <= kMaxSmem, "shared memory budget");
-};
+constexpr int kMaxN = 256;        // tokens per tile
+constexpr int kABytes = 128 * 128;         // 128 weight rows (or columns) x 64
+constexpr int kBBytes = kMaxN / 2 * 128;   // half of the tokens x 64
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 6;
+constexpr int kThreads = 224;
+constexpr int kExchange = 4 * 2 * 2048;  // GU: per epilogue warp two buffers of 16 tokens x 32 features
+constexpr int kBarBytes = 8 * (2 * kStages + 5) + 24;
+constexpr int kTableBytes = (kMaxGroups + 8) * (4 + 4 + 2);  // tile starts, row starts, padding before a group
+constexpr int kSmem = 1024 + kStages * kStageBytes + kExchange + kBarBytes + kTableBytes;
+constexpr uint16_t kPairMask = 0x3;
+static_assert(kBarBytes % 16 == 0 && kSmem <= kMaxSmem, "shared memory");
 
 struct GradParams {
-  KParams k;              // offsets, G, rows, status, limit_ns; N = output columns
+  KParams k;              // offsets, G, rows, status, limit_ns; N = weight rows or columns (output features)
   int H, I;
   int num_kb;             // stages per tile (Q, GU: H / 64; DX: 2 I / 64)
   float* q;               // [rows, I]
@@ -90,235 +90,116 @@ struct GradParams {
   __nv_bfloat16* da;      // [rows, H]
 };
 
-// A warp's block of 32 rows x 32 bf16 columns (lane = row, its 32 values packed
-// in w) to global memory, the first `nr` rows: staged as 64-byte rows (16-byte
-// chunk j of row r at chunk j ^ (r / 2 % 4)), then eight rows per store
-// instruction, four lanes to a row.
-__device__ __forceinline__ void store_block32(const uint32_t (&w)[16], uint8_t* stg, int lane, int nr,
-                                              __nv_bfloat16* dst, size_t pitch) {
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  __syncwarp();
-#pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int r = it * 8 + (lane >> 2), j = lane & 3;
-    if (r < nr)
-      *reinterpret_cast<uint4*>(dst + r * pitch + j * 8) =
-          *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
-  }
-}
-
-// The staged block's first `nr` rows to rows row0.. of a row-major bf16 or
-// fp32 matrix whose rows are `pitch` bytes long, at byte `col` (a block that
-// ends inside it: a TMA box would also write the next group's rows).
-__device__ __forceinline__ void copy_staged_rows(const uint8_t* stg, int lane, int nr, uint8_t* base, size_t row0,
-                                                 size_t pitch, size_t col) {
-  __syncwarp();
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int r = it * 4 + (lane >> 3), j = lane & 7;
-    if (r < nr)
-      *reinterpret_cast<uint4*>(base + (row0 + r) * pitch + col + j * 16) =
-          *reinterpret_cast<const uint4*>(stg + r * 128 + ((j ^ (r & 7)) << 4));
-  }
-  __syncwarp();
-}
-
-// Epilogue of one 128 x TILE_N tile by one warp (32 accumulator rows).
-template <int MODE>
-__device__ __forceinline__ void grad_epilogue(const GradParams& p, const TileInfo& ti, int pad0, uint32_t tb, int q,
-                                              int lane, uint8_t* stg, const CUtensorMap* map_out) {
-  const int r0 = ti.tt * 128 + q * 32;  // the warp's first row in the group
-  const int nr = ti.nrows - r0;         // rows of the group from there on
-  if (nr <= 0) return;                  // (r0 % 16 == 0: no padding here either)
-  if (MODE == kGU) {
-    // q comes in coalesced (four rows of 128 bytes per load instruction), one
-    // block of 32 columns ahead, and goes through the staging buffer to the
-    // lane that holds the row's accumulators.
-    const size_t row = (size_t)ti.row0 + r0;
-    // h, dg, du: the group's rows and the zero rows that fill its last step.
-    const size_t prow = (size_t)pad0 + r0;
-    const bool live = lane < nr;
-    int np = pad16(ti.nrows) - r0;
-    if ((long long)prow + np > p.prows) np = (int)(p.prows - (long long)prow);  // decreasing offsets
-    bool odd = false;
-    const int c0 = ti.wt * 128;
-    const int ncol = p.I - c0 < 128 ? p.I - c0 : 128;  // a multiple of 64
-    float4 nq[8];
-    auto load_q = [&](int c) {
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int r = it * 4 + (lane >> 3);
-        nq[it] = r < nr ? *reinterpret_cast<const float4*>(p.q + (row + r) * p.I + c0 + c + (lane & 7) * 4)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    };
-    load_q(0);
-#pragma unroll 1
-    for (int c = 0; c < ncol; c += 32) {
-      __syncwarp();
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int r = it * 4 + (lane >> 3);
-        *reinterpret_cast<float4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = nq[it];
-      }
-      __syncwarp();
-      float qv[32];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 t = *reinterpret_cast<const float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4));
-        qv[4 * j] = t.x;
-        qv[4 * j + 1] = t.y;
-        qv[4 * j + 2] = t.z;
-        qv[4 * j + 3] = t.w;
-      }
-      if (c + 32 < ncol) load_q(c + 32);
-      uint32_t g[32], u[32];
-      tmem_ld_32x32b_x32(tb + c, g);
-      tmem_ld_32x32b_x32(tb + 128 + c, u);
-      tmem_ld_wait();
-      // An infinity or NaN in the row of a or of dy leaves none of its gate
-      // values, or of its q values, finite.
-      odd = odd || !(fabsf(__uint_as_float(g[0])) <= 3.402823466e38f) || !(fabsf(qv[0]) <= 3.402823466e38f);
-      uint32_t ph[16], pg[16], pu[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float hv[2], gv[2], uv[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float gt = __uint_as_float(g[2 * j + i]), up = __uint_as_float(u[2 * j + i]), qq = qv[2 * j + i];
-          const float sg = __fdividef(1.0f, 1.0f + __expf(-gt));
-          const float act = gt * sg;
-          hv[i] = act * up;
-          uv[i] = qq * act;
-          gv[i] = qq * up * sg * fmaf(gt, 1.0f - sg, 1.0f);
-        }
-        ph[j] = live ? pack_bf16(hv[0], hv[1]) : 0u;
-        pg[j] = live ? pack_bf16(gv[0], gv[1]) : 0u;
-        pu[j] = live ? pack_bf16(uv[0], uv[1]) : 0u;
-      }
-      const size_t at = prow * p.I + c0 + c;
-      store_block32(ph, stg, lane, np, p.h + at, p.I);
-      store_block32(pg, stg + 2048, lane, np, p.dg + at, p.I);
-      store_block32(pu, stg, lane, np, p.du + at, p.I);
-    }
-    if (odd && live) *p.odd = 1;
-  } else if (MODE == kQ) {
-    const size_t row = (size_t)ti.row0 + r0;
-#pragma unroll 1
-    for (int c = 0; c < 256; c += 32) {
-      const int col = ti.wt * 256 + c;
-      if (col >= p.I) break;
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(tb + c, v);
-      tmem_ld_wait();
-      if (lane == 0) bulk_wait_group_read0();
-      __syncwarp();
-      uint8_t* srow = stg + lane * 128;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(srow + ((j ^ (lane & 7)) << 4)) =
-            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      if (nr >= 32) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(map_out, smem_u32(stg), col, (int)row);
-          bulk_commit_group();
-        }
-      } else {
-        copy_staged_rows(stg, lane, nr, reinterpret_cast<uint8_t*>(p.q), row, (size_t)p.I * 4, (size_t)col * 4);
-      }
-    }
-  } else {  // DX
-    const size_t row = (size_t)ti.row0 + r0;
-#pragma unroll 1
-    for (int c = 0; c < 256; c += 64) {
-      const int col = ti.wt * 256 + c;
-      if (col >= p.H) break;
-      stage_bf16_block(tb + c, stg, lane);
-      if (nr >= 32) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(map_out, smem_u32(stg), col, (int)row);
-          bulk_commit_group();
-        }
-      } else {
-        copy_staged_rows(stg, lane, nr, reinterpret_cast<uint8_t*>(p.da), row, (size_t)p.H * 2, (size_t)col * 2);
-      }
-    }
-  }
-}
-
-// Operand and output maps. Q: a = dy, b0 = Wd, out = q. GU: a = a, b0 / b1 =
-// Wg / Wu. DX: a = dg, a2 = du, b0 / b1 = Wg / Wu, out = da.
+// a0 / a1: the weights; b0 / b1: the rows, in boxes of 64, 32 and 16 rows.
+// Q: Wd; dy. GU: Wg, Wu; a. DX: Wg, Wu; dg, du.
 struct GradMaps {
-  CUtensorMap a, a2, b0, b1, out;
+  CUtensorMap a0, a1, b0[3], b1[3];
 };
+
+// Tokens of chunk c of a group of n rows: [first, first + count), and the MMA's
+// N. (A chunk is at most 256, so the last one is never empty.)
+struct Chunk {
+  int first, count, N;
+};
+__device__ __forceinline__ Chunk chunk_of(int n, int c) {
+  const int chunks = (n + kMaxN - 1) / kMaxN;
+  const int size = ((n + chunks - 1) / chunks + 31) & ~31;
+  Chunk k;
+  k.first = c * size;
+  k.count = n - k.first < size ? n - k.first : size;
+  k.N = (k.count + 31) & ~31;
+  return k;
+}
+
+// All threads of `threads` (a multiple of 32) agree: true if every one says so.
+__device__ __forceinline__ bool agree(int id, int threads, bool mine) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 q, %3, 0;\n\t"
+      "bar.red.and.pred p, %1, %2, q;\n\t"
+      "selp.s32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"((int)mine)
+      : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+
 template <int MODE>
-__global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     grouped_grad_kernel(const __grid_constant__ GradMaps m, const GradParams p) {
-  using Gm = GradGeo<MODE>;
-  constexpr int NS = Gm::S;
+  constexpr int kTileM = MODE == kGU ? 128 : 256;  // output features per pair tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
   uint8_t* base = smem_raw + pad;
   const uint32_t base_u32 = raw_addr + pad;
-  // Shared memory: ring | epilogue staging | tables | barriers.
-  uint8_t* epi_stage = base + Gm::RING_BYTES;
-  int32_t* tile_start = reinterpret_cast<int32_t*>(epi_stage + Gm::EPI_BYTES);
-  int32_t* row_start = tile_start + kMaxGroups + 8;
-  int32_t* pad_start = row_start + kMaxGroups + 8;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + Gm::EPI_BYTES + Gm::TABLE_BYTES);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Gm::NBARS);
+  // Shared memory (the same in both CTAs): ring | exchange | barriers | tables.
+  float* exchange = reinterpret_cast<float*>(base + kStages * kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kStages * kStageBytes + kExchange);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* tile_start = reinterpret_cast<int32_t*>(base + kStages * kStageBytes + kExchange + kBarBytes);
+  int32_t* row_start = tile_start + kMaxGroups + 8;
+  // Group g's first row in h, dg and du (gemm_grad.cuh) is row_start[g] -
+  // row_start[0] + pad_extra[g].
+  uint16_t* pad_extra = reinterpret_cast<uint16_t*>(row_start + kMaxGroups + 8);
+  int32_t* pads = reinterpret_cast<int32_t*>(base);  // until the loop starts
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (NS + s); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * NS + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * NS + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };                       // leader: both CTAs' stage s
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };          // each CTA
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kStages + a); };      // each CTA
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kStages + 2 + a); };  // leader
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: leader
+  const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
   const int G = p.k.G;
   allow_next_launch();
 
-  // ---- row starts; tile_start[g] = tiles of groups before g.
-  fill_row_start(p.k, row_start, threadIdx.x, Gm::THREADS);
-  const int n_wt = (p.k.N + Gm::TILE_N - 1) / Gm::TILE_N;
-  for (int g = threadIdx.x; g < G; g += Gm::THREADS) {
+  // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
+  fill_row_start(p.k, row_start, threadIdx.x, kThreads);
+  const int n_wt = (p.k.N + kTileM - 1) / kTileM;
+  for (int g = threadIdx.x; g < G; g += kThreads) {
     int r0, nr;
     group_rows(p.k, g, r0, nr);
-    tile_start[g] = n_wt * ((nr + 127) / 128);
-    pad_start[g] = pad16(nr);
+    tile_start[g] = n_wt * ((nr + kMaxN - 1) / kMaxN);
+    pads[g] = pad16(nr) - nr;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 4);
+      mbar_init(tempty_bar(a), 8);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+  if (warp == 1) {  // one warp of each CTA of the pair, together
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
   }
   __syncthreads();
   if (warp == 0) scan_warp(tile_start, G, lane);
-  if (MODE != kQ && warp == 2) scan_warp(pad_start, G, lane);
+  if (warp == 2) {
+    scan_warp(pads, G, lane);
+    __syncwarp();
+    for (int g = lane; g < G; g += 32) pad_extra[g] = (uint16_t)pads[g];
+  }
+  // pads' bytes become a stage: written by the async proxy from here on.
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
   // Up to here nothing was read that the launch before this one writes (its
   // blocks may still be running: programmatic dependent launch).
@@ -326,156 +207,280 @@ __global__ void __launch_bounds__(GradGeo<MODE>::THREADS, 1)
   if (MODE == kQ && blockIdx.x == 0 && threadIdx.x == 0) *p.odd = 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[G];
+  const int my_tiles = total > pair ? (total - pair + npairs - 1) / npairs : 0;
+
+  // This pair's tiles, decoded 32 at a time, one by each lane of a role's warp,
+  // and read back by shuffles.
+  struct Tile {
+    int g, wt, row, prow, count, N, npad;  // npad: count and the zero rows after a group's last token
+  };
+  auto decode = [&](int i) {
+    Tile t = {};
+    if (i >= my_tiles) return t;
+    const int tile = pair + i * npairs;
+    int lo = 0, hi = G;  // tile_start[lo] <= tile < tile_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile_start[mid] <= tile) lo = mid; else hi = mid;
+    }
+    const int n = row_start[lo + 1] - row_start[lo], chunks = (n + kMaxN - 1) / kMaxN;
+    const int local = tile - tile_start[lo];
+    t.g = lo;
+    t.wt = local / chunks;
+    const Chunk c = chunk_of(n, local - t.wt * chunks);
+    t.row = row_start[lo] + c.first;
+    t.prow = row_start[lo] - row_start[0] + pad_extra[lo] + c.first;
+    t.count = c.count;
+    t.N = c.N;
+    t.npad = c.first + c.count == n ? pad16(n) - c.first : c.count;
+    return t;
+  };
+  auto at_tile = [&](int v, int i) { return __shfl_sync(0xFFFFFFFFu, v, i & 31); };
 
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers
-    // Boxes of a stage: A, then B's in order. Warp 0 arms the stage's barrier
-    // with all its bytes and issues the first; the others issue the rest (a
-    // transaction may land before it is expected). A box costs its thread about
-    // 100 to 150 cycles, a stage's MMAs take 512.
-    if (lane == 0) {
-      const bool first = warp == 0;
-      Ring rg;
-      Armed armed;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status, MOE_DEV_TIMEOUT_PRODUCER,
-                                 p.k.limit_ns)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = full_bar(rg.s);
-          const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
-          if (first) mbar_arrive_expect_tx(fb, Gm::STAGE_BYTES);
-          if constexpr (MODE == kGU) {
-            tma_load_2d(sa, &m.a, fb, kb * kBK, ti.row0 + ti.tt * 128);
-            tma_load_2d(sb, &m.b0, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
-            tma_load_2d(sb + Gm::A_BYTES, &m.b1, fb, kb * kBK, ti.g * p.I + ti.wt * 128);
-          } else {
-            // DX: the first half of the stages is dg Wg, the second du Wu.
-            const int half = p.num_kb >> 1;
-            const bool second = MODE == kDX && kb >= half;
-            const int kx = (second ? kb - half : kb) * kBK;
-            const CUtensorMap* mb = second ? &m.b1 : &m.b0;
-            const int krow = ti.g * (MODE == kQ ? p.H : p.I) + kx;
-            if (first) {
-              tma_load_2d(sa, second ? &m.a2 : &m.a, fb, kx, (MODE == kDX ? pad_start[ti.g] : ti.row0) + ti.tt * 128);
-              tma_load_2d(sb, mb, fb, ti.wt * 256, krow);
-            } else {
-#pragma unroll
-              for (int j = 1; j < 4; ++j) tma_load_2d(sb + j * kChunk, mb, fb, ti.wt * 256 + j * 64, krow);
-            }
-          }
-          armed.mark(rg);
-          rg.next(NS);
+    const bool is_a = warp == 0;
+    const uint32_t bar_base = rank == 0 ? bar0 : mapa_shared(bar0, 0);  // the leader's full barriers
+    Ring rg;
+    bool ok = true;
+    Tile mine = {};
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      if ((i & 31) == 0) mine = decode(i + lane);
+      const int g = at_tile(mine.g, i), wt = at_tile(mine.wt, i), half = at_tile(mine.N, i) >> 1;
+      const int row = at_tile(MODE == kDX ? mine.prow : mine.row, i) + (int)rank * half;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
+                                                       MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
+          ok = false;
+          break;
         }
+        // DX: the first half of the stages is dg Wg, the second du Wu.
+        const bool second = MODE == kDX && kb >= (p.num_kb >> 1);
+        const int kx = (second ? kb - (p.num_kb >> 1) : kb) * kBK;
+        const uint32_t bar = bar_base + 8u * rg.s;
+        const uint32_t sa = base_u32 + rg.s * kStageBytes, sb = sa + kABytes;
+        if (elect_one()) {
+          if (is_a) {
+            // Both CTAs' bytes (the other's may land first).
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(rg.s), 2u * (kABytes + (uint32_t)half * 128u));
+            if (MODE == kGU) {
+              const int f = g * p.I + wt * kTileM + (int)rank * 64;
+              tma_load_2d_pair(sa, &m.a0, bar, kx, f);
+              tma_load_2d_pair(sa + kChunk, &m.a1, bar, kx, f);
+            } else {
+              const CUtensorMap* map = second ? &m.a1 : &m.a0;
+              const int f = wt * kTileM + (int)rank * 128, krow = g * (MODE == kQ ? p.H : p.I) + kx;
+              tma_load_2d_pair(sa, map, bar, f, krow);
+              tma_load_2d_pair(sa + kChunk, map, bar, f + 64, krow);
+            }
+          } else {
+            // `half` rows (a multiple of 16) in boxes of 64, 32 and 16.
+            const CUtensorMap* map = second ? m.b1 : m.b0;
+            int at = 0;
+            for (; half - at >= 64; at += 64) tma_load_2d_pair(sb + at * 128, map, bar, kx, row + at);
+            if (half - at >= 32) {
+              tma_load_2d_pair(sb + at * 128, map + 1, bar, kx, row + at);
+              at += 32;
+            }
+            if (half - at >= 16) tma_load_2d_pair(sb + at * 128, map + 2, bar, kx, row + at);
+          }
+        }
+        __syncwarp();
+        rg.next(kStages);
       }
-      if (!ok) {  // let copies already issued land before the CTA exits
-        for (int s = 0; s < NS; ++s)
-          if (armed.mask & (1u << s)) drain_wait(full_bar(s), (armed.phase >> s) & 1u, 100000000ull);
+    }
+    if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 5000000ull) {
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the loop in step, polls included, so that tile, stage
-    // and descriptor values are warp-uniform (the tensor core instructions take
-    // uniform registers: 290 cycles to issue a stage, against 360 from one
-    // diverged lane); one elected lane issues.
-    constexpr uint32_t kIdesc = idesc_bf16_f32(128, 256) | (Gm::B_MN ? 1u << 16 : 0u);
-    constexpr uint32_t kStepA = 32 >> 4, kStepB = Gm::B_MN ? 2048 >> 4 : 32 >> 4;
-    auto wait_all = [&](uint32_t bar, uint32_t parity) {
-      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-      return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA,
-                                                       p.k.limit_ns)) != 0;
-    };
-    Ring rg;
-    bool ok = true, issued = false;
-    int local = 0;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++local) {
-      const int acc = local & 1;
-      const uint32_t ap = (uint32_t)(local >> 1) & 1u;
-      if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        const uint32_t sa = base_u32 + rg.s * Gm::STAGE_BYTES, sb = sa + Gm::A_BYTES;
-        const uint64_t da = sw128_kmajor_desc(sa);
-        const uint64_t db = Gm::B_MN ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
-        if (!wait_all(full_bar(rg.s), rg.ph)) {
+    if (rank == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16_f32(256, 0) | (MODE == kGU ? 0u : 1u << 15);
+      constexpr uint32_t kStepA = MODE == kGU ? 32 >> 4 : 2048 >> 4, kStepB = 32 >> 4;
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA,
+                                                         p.k.limit_ns)) != 0;
+      };
+      Ring rg;
+      bool ok = true, issued = false;
+      int n32 = 0;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        if ((i & 31) == 0) n32 = decode(i + lane).N;
+        const int N = at_tile(n32, i);
+        const int acc = i & 1;
+        const uint32_t ap = (uint32_t)(i >> 1) & 1u;
+        if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (elect_one()) {
-          umma_bf16(d, da, db, kIdesc, kb ? 1u : 0u);
+        const uint32_t d = tmem_base + (uint32_t)(acc * kMaxN);
+        const uint32_t idesc = kIdesc | (uint32_t)(N >> 3) << 17;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          const uint32_t sa = base_u32 + rg.s * kStageBytes;
+          const uint64_t da = MODE == kGU ? sw128_kmajor_desc(sa) : sw128_mnmajor_desc(sa);
+          const uint64_t db = sw128_kmajor_desc(sa + kABytes);
+          if (!wait_all(full_bar(rg.s), rg.ph)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            umma_bf16_pair(d, da, db, idesc, kb ? 1u : 0u);
 #pragma unroll
-          for (int k = 1; k < kBK / 16; ++k) umma_bf16(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
-          umma_commit(empty_bar(rg.s));
+            for (int k = 1; k < kBK / 16; ++k) umma_bf16_pair(d, da + k * kStepA, db + k * kStepB, idesc, 1u);
+            umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
+          }
+          __syncwarp();
+          issued = true;
+          rg.next(kStages);
         }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), kPairMask);
         __syncwarp();
-        issued = true;
-        rg.next(NS);
       }
-      if (!ok) break;
-      if (elect_one()) umma_commit(tfull_bar(acc));
-      __syncwarp();
-    }
-    if (!ok && issued && lane == 0) {  // wait for every issued MMA before TMEM is freed
-      umma_commit(drain_bar);
-      drain_wait(drain_bar, 0, 100000000ull);
+      if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
+        umma_commit_pair(drain_bar);
+        drain_wait(drain_bar, 0, 200000000ull);
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
-    uint8_t* stg = epi_stage + q * Gm::EPI_WARP;
-    int local = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++local) {
-      const int acc = local & 1;
-      const uint32_t ap = (uint32_t)(local >> 1) & 1u;
+    Tile mine = {};
+    bool odd = false;
+    for (int i = 0; i < my_tiles; ++i) {
+      if ((i & 31) == 0) mine = decode(i + lane);
+      const int wt = at_tile(mine.wt, i), count = at_tile(mine.count, i), N = at_tile(mine.N, i);
+      const int row = at_tile(mine.row, i), prow = at_tile(mine.prow, i);
+      int npad = at_tile(mine.npad, i);
+      if (prow < 0 || npad > p.prows - prow) npad = 0;  // (offsets that decrease: no store outside)
+      const int acc = i & 1;
+      const uint32_t ap = (uint32_t)(i >> 1) & 1u;
       int ok = 1;
       if (lane == 0)
         ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (MODE == kGU) ok = agree(1 + (q & 1), 64, ok != 0);  // partners leave together
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      const TileInfo ti = decode_tile_s<128>(G, tile_start, row_start, tile);
-      grad_epilogue<MODE>(p, ti, pad_start[ti.g], tb, q, lane, stg, &m.out);
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxN);
+      if (MODE == kGU) {
+        const int f0 = wt * kTileM + (int)rank * 64 + (q & 1) * 32;  // (32 features: all inside I or none)
+        const bool gate_warp = q < 2;
+        const int j0 = gate_warp ? 0 : 16;  // the 16 tokens of a block that this warp finishes
+        float* mine_ex = exchange + q * 1024 + lane;
+        const float* other_ex = exchange + (q ^ 2) * 1024 + lane;
+        if (f0 < p.I) {
+          const float* qp = p.q + (size_t)row * p.I + f0 + lane;
+          float nq[16];  // q of the block's 16 tokens, loaded one block ahead
+          auto load_q = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) nq[j] = c + j0 + j < count ? qp[(size_t)(c + j0 + j) * p.I] : 0.0f;
+          };
+          load_q(0);
+          int buf = 0;
+#pragma unroll 1
+          for (int c = 0; c < N; c += 32, buf ^= 512) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tb + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) mine_ex[buf + j * 32] = __uint_as_float(gate_warp ? v[16 + j] : v[j]);
+            named_sync(1 + (q & 1), 64);  // (the buffer after next is free: both have read it)
+            float qv[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) qv[j] = nq[j];
+            if (c + 32 < N) load_q(c + 32);
+            const size_t at = (size_t)(prow + c + j0) * p.I + f0 + lane;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float mine_v = __uint_as_float(gate_warp ? v[j] : v[16 + j]), other_v = other_ex[buf + j * 32];
+              const float gt = gate_warp ? mine_v : other_v, up = gate_warp ? other_v : mine_v;
+              const int t = c + j0 + j;
+              if (t < npad) {
+                const float sg = __fdividef(1.0f, 1.0f + __expf(-gt));
+                const float act = gt * sg;
+                const bool live = t < count;
+                // An infinity or NaN in the row of a or of dy leaves none of its
+                // gate values, or of its q values, finite.
+                odd = odd || (live && !(finite(gt) && finite(qv[j])));
+                const size_t o = at + (size_t)j * p.I;
+                p.h[o] = __float2bfloat16_rn(live ? act * up : 0.0f);
+                p.du[o] = __float2bfloat16_rn(live ? qv[j] * act : 0.0f);
+                p.dg[o] = __float2bfloat16_rn(live ? qv[j] * up * sg * fmaf(gt, 1.0f - sg, 1.0f) : 0.0f);
+              }
+            }
+          }
+        }
+      } else {
+        const int cols = MODE == kQ ? p.I : p.H;
+        const int f0 = wt * kTileM + (int)rank * 128 + q * 32;  // (32 features: all inside or none)
+        if (f0 < cols) {
+          const size_t at = (size_t)row * cols + f0 + lane;
+#pragma unroll 1
+          for (int c = 0; c < N; c += 32) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tb + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (c + j < count) {
+                const size_t o = at + (size_t)(c + j) * cols;
+                if (MODE == kQ) p.q[o] = __uint_as_float(v[j]);
+                else p.da[o] = __float2bfloat16_rn(__uint_as_float(v[j]));
+              }
+            }
+          }
+        }
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(acc));
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(tempty_bar(acc));
+        else mbar_arrive_remote(mapa_shared(tempty_bar(acc), 0));
+      }
     }
-    if (lane == 0) bulk_wait_group0();  // this warp's bulk stores are complete
+    if (MODE == kGU && odd) *p.odd = 1;
   }
 
+  // Both CTAs arrive here only when their roles are done (every wait is
+  // bounded), so neither frees TMEM or leaves while the other may still touch
+  // its shared memory or barriers.
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();
   if (warp == 1) {
-    __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
+// row_chunks: an upper bound on the groups' chunks.
 template <int MODE>
-cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long max_tiles, int num_sms, cudaStream_t s) {
-  using Gm = GradGeo<MODE>;
-  if (max_tiles <= 0) return cudaSuccess;
-  const int grid = (int)(max_tiles < num_sms ? max_tiles : num_sms);
+cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long row_chunks, int num_sms, cudaStream_t s) {
+  constexpr int kTileM = MODE == kGU ? 128 : 256;
+  const long long tiles = row_chunks * ((p.k.N + kTileM - 1) / kTileM);
+  const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  if (pairs < 1) return cudaErrorInvalidValue;
   // Q starts after everything before it; the others' prologues may overlap the
   // end of the launch before them (its offsets were there before Q).
-  return launch_dependent(grouped_grad_kernel<MODE>, grid, Gm::THREADS, Gm::SMEM, s, MODE != kQ, /*cluster=*/1, m, p);
+  return launch_dependent(grouped_grad_kernel<MODE>, 2 * pairs, kThreads, kSmem, s, MODE != kQ, /*cluster=*/2, m, p);
 }
 
 template <int MODE>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(grouped_grad_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              GradGeo<MODE>::SMEM);
+  return cudaFuncSetAttribute(grouped_grad_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
+// The maps of a [rows, cols] tensor in boxes of 64, 32 and 16 rows.
+bool row_maps(CUtensorMap (&m)[3], const void* ptr, uint64_t cols, uint64_t rows) {
+  for (int i = 0; i < 3; ++i)
+    if (!make_tmap_bf16(&m[i], ptr, cols, rows, 64u >> i)) return false;
+  return true;
 }
 
 }  // namespace
@@ -513,39 +518,33 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
   p.prows = (int)padded_rows(a.rows, G);
   p.odd = a.odd;
   p.da = static_cast<__nv_bfloat16*>(a.da);
-  const uint64_t R = a.rows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
-  const long long row_tiles = (a.rows + 127) / 128 + (long long)G;  // at most: one ragged tile per group
-  auto ceil_div = [](long long v, long long d) { return (v + d - 1) / d; };
+  const uint64_t R = a.rows, P = p.prows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
+  const long long row_chunks = (a.rows + kMaxN - 1) / kMaxN + (long long)G;  // at most: one short chunk per group
   cudaError_t e = cudaSuccess;
-  bool maps = true;
   {
     GradMaps m = {};
-    maps = make_tmap_bf16(&m.a, a.dy, H, R, 128) && make_tmap_bf16(&m.b0, a.w_down, I, GH, 64) &&
-           make_tmap_f32_store(&m.out, a.q, I, R);
-    if (!maps) return cudaErrorInvalidValue;
+    if (!make_tmap_bf16(&m.a0, a.w_down, I, GH, 64) || !row_maps(m.b0, a.dy, H, R)) return cudaErrorInvalidValue;
     p.k.N = I;
     p.num_kb = H / kBK;
-    e = run_mode<kQ>(m, p, row_tiles * ceil_div(I, 256), a.num_sms, s);
+    e = run_mode<kQ>(m, p, row_chunks, a.num_sms, s);
   }
   if (e == cudaSuccess) {
     GradMaps m = {};
-    maps = make_tmap_bf16(&m.a, a.a, H, R, 128) && make_tmap_bf16(&m.b0, a.w_gate, H, GI, 128) &&
-           make_tmap_bf16(&m.b1, a.w_up, H, GI, 128);
-    if (!maps) return cudaErrorInvalidValue;
+    if (!make_tmap_bf16(&m.a0, a.w_gate, H, GI, 64) || !make_tmap_bf16(&m.a1, a.w_up, H, GI, 64) ||
+        !row_maps(m.b0, a.a, H, R))
+      return cudaErrorInvalidValue;
     p.k.N = I;
     p.num_kb = H / kBK;
-    e = run_mode<kGU>(m, p, row_tiles * ceil_div(I, 128), a.num_sms, s);
+    e = run_mode<kGU>(m, p, row_chunks, a.num_sms, s);
   }
   if (e == cudaSuccess && a.da) {
     GradMaps m = {};
-    const uint64_t P = p.prows;
-    maps = make_tmap_bf16(&m.a, a.dg, I, P, 128) && make_tmap_bf16(&m.a2, a.du, I, P, 128) &&
-           make_tmap_bf16(&m.b0, a.w_gate, H, GI, 64) && make_tmap_bf16(&m.b1, a.w_up, H, GI, 64) &&
-           make_tmap_bf16(&m.out, a.da, H, R, 32);
-    if (!maps) return cudaErrorInvalidValue;
+    if (!make_tmap_bf16(&m.a0, a.w_gate, H, GI, 64) || !make_tmap_bf16(&m.a1, a.w_up, H, GI, 64) ||
+        !row_maps(m.b0, a.dg, I, P) || !row_maps(m.b1, a.du, I, P))
+      return cudaErrorInvalidValue;
     p.k.N = H;
     p.num_kb = 2 * (I / kBK);
-    e = run_mode<kDX>(m, p, row_tiles * ceil_div(H, 256), a.num_sms, s);
+    e = run_mode<kDX>(m, p, row_chunks, a.num_sms, s);
   }
   if (e == cudaSuccess && want_dw) e = launch_grouped_weight_grad(a, s);
   return e;

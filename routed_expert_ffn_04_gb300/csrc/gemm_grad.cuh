@@ -48,6 +48,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A copy into this CTA that completes on a barrier of either CTA of the pair
+// (`bar` from mapa_shared, or this CTA's own).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 // h, dg and du keep a group's rows together with zero rows up to the next
 // multiple of 16, the tensor cores' step along the rows: row r of group g is
 // row pad_start[g] + r of them. The rows they need for at most `rows` rows in G

@@ -98,15 +98,6 @@ __device__ __forceinline__ DwTile dw_tile(const DwParams& p, const uint16_t* ord
   return t;
 }
 
-// A copy into this CTA that completes on a barrier of either CTA of the pair
-// (`bar` from mapa_shared, or this CTA's own).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
 // Arrive on a barrier of another CTA of the cluster, releasing this CTA's
 // writes, and the wait's other half (the phase has been seen complete).
 __device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
