@@ -36,10 +36,12 @@
 //   GU    64 Wg rows, 64 Wu rows, K-major  a rows, K-major            H
 //   DX    Wg, then Wu columns, MN-major    dg rows, then du rows      I, twice
 //
-// Roles per CTA (7 warps, each walking its tiles in step with warp-uniform
+// Roles per CTA (8 warps, each walking its tiles in step with warp-uniform
 // values and one elected lane issuing): 0 loads A's boxes and arms the stage,
-// 6 loads B's, 1 (of the even CTA, the leader) issues the pair's MMAs, 2-5 are
-// the epilogue, 32 accumulator lanes each. Both CTAs' copies of a stage complete
+// 6 loads B's boxes of 64 rows and 7 its lower ones (a box costs its issuer 100
+// to 150 cycles, a stage's MMAs take 330 at 341 rows per group), 1 (of the
+// even CTA, the leader) issues the pair's MMAs, 2-5 are the epilogue, 32
+// accumulator lanes each. Both CTAs' copies of a stage complete
 // on the leader's full barrier. In GU lanes 0-63 hold the gates and 64-127 the
 // ups of the same 64 features: warps q and q + 2 exchange half of each block
 // of 32 tokens through shared memory and finish 16 tokens each. A warp's store
@@ -71,7 +73,7 @@ constexpr int kABytes = 128 * 128;         // 128 weight rows (or columns) x 64
 constexpr int kBBytes = kMaxN / 2 * 128;   // half of the tokens x 64
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kStages = 6;
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kExchange = 4 * 2 * 2048;  // GU: per epilogue warp two buffers of 16 tokens x 32 features
 constexpr int kBarBytes = 8 * (2 * kStages + 5) + 24;
 constexpr int kTableBytes = (kMaxGroups + 8) * (4 + 4 + 2);  // tile starts, row starts, padding before a group
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto at_tile = [&](int v, int i) { return __shfl_sync(0xFFFFFFFFu, v, i & 31); };
 
-  if (warp == 0 || warp == 6) {
+  if (warp == 0 || warp >= 6) {
     // ------------------------------------------------------------ producers
     const bool is_a = warp == 0;
     const uint32_t bar_base = rank == 0 ? bar0 : mapa_shared(bar0, 0);  // the leader's full barriers
@@ -248,6 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((i & 31) == 0) mine = decode(i + lane);
       const int g = at_tile(mine.g, i), wt = at_tile(mine.wt, i), half = at_tile(mine.N, i) >> 1;
       const int row = at_tile(MODE == kDX ? mine.prow : mine.row, i) + (int)rank * half;
+      // B's `half` rows (a multiple of 16, at most 128): boxes of 64 by warp 6,
+      // then one of 32 and one of 16 by warp 7.
+      const bool b64 = half >= 64, b128 = half == 128, b32 = (half & 32) != 0, b16 = (half & 16) != 0;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
                                                        MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
@@ -274,15 +279,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d_pair(sa + kChunk, map, bar, f + 64, krow);
             }
           } else {
-            // `half` rows (a multiple of 16) in boxes of 64, 32 and 16.
             const CUtensorMap* map = second ? m.b1 : m.b0;
-            int at = 0;
-            for (; half - at >= 64; at += 64) tma_load_2d_pair(sb + at * 128, map, bar, kx, row + at);
-            if (half - at >= 32) {
-              tma_load_2d_pair(sb + at * 128, map + 1, bar, kx, row + at);
-              at += 32;
+            if (warp == 6) {
+              if (b64) tma_load_2d_pair(sb, map, bar, kx, row);
+              if (b128) tma_load_2d_pair(sb + 64 * 128, map, bar, kx, row + 64);
+            } else {
+              const int at = half & 64;
+              if (b32) tma_load_2d_pair(sb + at * 128, map + 1, bar, kx, row + at);
+              if (b16) tma_load_2d_pair(sb + (half - 16) * 128, map + 2, bar, kx, row + half - 16);
             }
-            if (half - at >= 16) tma_load_2d_pair(sb + at * 128, map + 2, bar, kx, row + at);
           }
         }
         __syncwarp();
@@ -395,25 +400,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) qv[j] = nq[j];
             if (c + 32 < N) load_q(c + 32);
-            const size_t at = (size_t)(prow + c + j0) * p.I + f0 + lane;
+            // The 16 x 32 results of h and dg, then of du, go out through this
+            // warp's other exchange buffer (its last reader is done): 64-byte
+            // rows, eight tokens per store instruction.
+            uint16_t* stg = reinterpret_cast<uint16_t*>(exchange + q * 1024 + (buf ^ 512));
+            __nv_bfloat16 du[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float mine_v = __uint_as_float(gate_warp ? v[j] : v[16 + j]), other_v = other_ex[buf + j * 32];
               const float gt = gate_warp ? mine_v : other_v, up = gate_warp ? other_v : mine_v;
-              const int t = c + j0 + j;
-              if (t < npad) {
-                const float sg = __fdividef(1.0f, 1.0f + __expf(-gt));
-                const float act = gt * sg;
-                const bool live = t < count;
-                // An infinity or NaN in the row of a or of dy leaves none of its
-                // gate values, or of its q values, finite.
-                odd = odd || (live && !(finite(gt) && finite(qv[j])));
-                const size_t o = at + (size_t)j * p.I;
-                p.h[o] = __float2bfloat16_rn(live ? act * up : 0.0f);
-                p.du[o] = __float2bfloat16_rn(live ? qv[j] * act : 0.0f);
-                p.dg[o] = __float2bfloat16_rn(live ? qv[j] * up * sg * fmaf(gt, 1.0f - sg, 1.0f) : 0.0f);
-              }
+              const bool live = c + j0 + j < count;
+              const float sg = __fdividef(1.0f, 1.0f + __expf(-gt));
+              const float act = gt * sg;
+              // An infinity or NaN in the row of a or of dy leaves none of its
+              // gate values, or of its q values, finite.
+              odd = odd || (live && !(finite(gt) && finite(qv[j])));
+              const __nv_bfloat16 h = __float2bfloat16_rn(live ? act * up : 0.0f);
+              const __nv_bfloat16 dg = __float2bfloat16_rn(live ? qv[j] * up * sg * fmaf(gt, 1.0f - sg, 1.0f) : 0.0f);
+              du[j] = __float2bfloat16_rn(live ? qv[j] * act : 0.0f);
+              stg[j * 32 + lane] = __bfloat16_as_ushort(h);
+              stg[512 + j * 32 + lane] = __bfloat16_as_ushort(dg);
             }
+            const size_t at = (size_t)(prow + c + j0) * p.I + f0 + (lane & 3) * 8;
+            auto put = [&](__nv_bfloat16* dst, const uint16_t* src) {
+#pragma unroll
+              for (int t = lane >> 2; t < 16; t += 8)
+                if (c + j0 + t < npad)
+                  *reinterpret_cast<uint4*>(dst + at + (size_t)t * p.I) =
+                      *reinterpret_cast<const uint4*>(src + t * 32 + (lane & 3) * 8);
+            };
+            __syncwarp();
+            put(p.h, stg);
+            put(p.dg, stg + 512);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) stg[j * 32 + lane] = __bfloat16_as_ushort(du[j]);
+            __syncwarp();
+            put(p.du, stg);
+            __syncwarp();
           }
         }
       } else {
