@@ -76,7 +76,7 @@ constexpr int kStages = 6;
 constexpr int kThreads = 256;
 constexpr int kExchange = 4 * 2 * 2048;  // GU: per epilogue warp two buffers of 16 tokens x 32 features
 constexpr int kBarBytes = 8 * (2 * kStages + 5) + 24;
-constexpr int kTableBytes = (kMaxGroups + 8) * (4 + 4 + 2);  // tile starts, row starts, padding before a group
+constexpr int kTableBytes = (kMaxGroups + 8) * (4 + 4 + 2 + 2);  // tile starts, row starts, padding, order
 constexpr int kSmem = 1024 + kStages * kStageBytes + kExchange + kBarBytes + kTableBytes;
 constexpr uint16_t kPairMask = 0x3;
 static_assert(kBarBytes % 16 == 0 && kSmem <= kMaxSmem, "shared memory");
@@ -150,6 +150,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Group g's first row in h, dg and du (gemm_grad.cuh) is row_start[g] -
   // row_start[0] + pad_extra[g].
   uint16_t* pad_extra = reinterpret_cast<uint16_t*>(row_start + kMaxGroups + 8);
+  // Groups by the size of their chunks, largest first; tile_start is in that
+  // order. Tiles are dealt to the pairs forwards and backwards in turn, which
+  // keeps the pairs' shares of unequal tiles within a fraction of a tile.
+  uint16_t* order = pad_extra + kMaxGroups + 8;
   int32_t* pads = reinterpret_cast<int32_t*>(base);  // until the loop starts
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };                       // leader: both CTAs' stage s
@@ -167,11 +171,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
   fill_row_start(p.k, row_start, threadIdx.x, kThreads);
   const int n_wt = (p.k.N + kTileM - 1) / kTileM;
+  __syncthreads();
+  auto rows_of = [&](int g) {
+    const int n = row_start[g + 1] - row_start[g];
+    return n > 0 ? n : 0;
+  };
+  int32_t* sizes = pads + kMaxGroups + 8;  // until the loop starts
   for (int g = threadIdx.x; g < G; g += kThreads) {
-    int r0, nr;
-    group_rows(p.k, g, r0, nr);
-    tile_start[g] = n_wt * ((nr + kMaxN - 1) / kMaxN);
-    pads[g] = pad16(nr) - nr;
+    const int n = rows_of(g);
+    pads[g] = pad16(n) - n;
+    sizes[g] = n > 0 ? chunk_of(n, 0).N : 0;
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += kThreads) {
+    const int size = sizes[g];
+    int at = 0;
+    for (int j = 0; j < G; ++j) {
+      const int o = sizes[j];
+      at += (o > size || (o == size && j < g)) ? 1 : 0;
+    }
+    order[at] = (uint16_t)g;
+    tile_start[at] = n_wt * ((rows_of(g) + kMaxN - 1) / kMaxN);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -209,7 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (MODE == kQ && blockIdx.x == 0 && threadIdx.x == 0) *p.odd = 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[G];
-  const int my_tiles = total > pair ? (total - pair + npairs - 1) / npairs : 0;
+  auto tile_of = [&](int i) { return i * npairs + ((i & 1) ? npairs - 1 - pair : pair); };
+  const int rounds = (total + npairs - 1) / npairs;
+  const int my_tiles = rounds > 0 && tile_of(rounds - 1) >= total ? rounds - 1 : rounds;  // the last round may be short
 
   // This pair's tiles, decoded 32 at a time, one by each lane of a role's warp,
   // and read back by shuffles.
@@ -219,14 +241,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto decode = [&](int i) {
     Tile t = {};
     if (i >= my_tiles) return t;
-    const int tile = pair + i * npairs;
+    const int tile = tile_of(i);
     int lo = 0, hi = G;  // tile_start[lo] <= tile < tile_start[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (tile_start[mid] <= tile) lo = mid; else hi = mid;
     }
-    const int n = row_start[lo + 1] - row_start[lo], chunks = (n + kMaxN - 1) / kMaxN;
     const int local = tile - tile_start[lo];
+    lo = order[lo];
+    const int n = rows_of(lo), chunks = (n + kMaxN - 1) / kMaxN;
     t.g = lo;
     t.wt = local / chunks;
     const Chunk c = chunk_of(n, local - t.wt * chunks);
