@@ -36,16 +36,16 @@
 //   GU    64 Wg rows, 64 Wu rows, K-major  a rows, K-major            H
 //   DX    Wg, then Wu columns, MN-major    dg rows, then du rows      I, twice
 //
-// Roles per CTA (8 warps, each walking its tiles in step with warp-uniform
+// Roles per CTA (12 warps, each walking its tiles in step with warp-uniform
 // values and one elected lane issuing): 0 loads A's boxes and arms the stage,
 // 6 loads B's boxes of 64 rows and 7 its lower ones (a box costs its issuer 100
 // to 150 cycles, a stage's MMAs take 330 at 341 rows per group), 1 (of the
-// even CTA, the leader) issues the pair's MMAs, 2-5 are the epilogue, 32
-// accumulator lanes each. Both CTAs' copies of a stage complete
-// on the leader's full barrier. In GU lanes 0-63 hold the gates and 64-127 the
-// ups of the same 64 features: warps q and q + 2 exchange half of each block
-// of 32 tokens through shared memory and finish 16 tokens each. A warp's store
-// of one token is 32 neighbouring features.
+// even CTA, the leader) issues the pair's MMAs, 2-5 and 8-11 are the epilogue,
+// 32 accumulator lanes and every other block of 32 tokens each. Both CTAs'
+// copies of a stage complete on the leader's full barrier. In GU lanes 0-63
+// hold the gates and 64-127 the ups of the same 64 features: the warps of lane
+// quarters q and q + 2 exchange half of each block through shared memory and
+// finish 16 tokens each.
 //
 // Every wait is bounded; on expiry the CTA records an error code in the status
 // word, lets its in-flight copies and MMAs end, frees TMEM and exits.
@@ -73,8 +73,9 @@ constexpr int kABytes = 128 * 128;         // 128 weight rows (or columns) x 64
 constexpr int kBBytes = kMaxN / 2 * 128;   // half of the tokens x 64
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kStages = 6;
-constexpr int kThreads = 256;
-constexpr int kExchange = 4 * 2 * 2048;  // GU: per epilogue warp two buffers of 16 tokens x 32 features
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kExchange = kEpiWarps * 2048;  // GU: per epilogue warp 16 tokens x 32 features
 constexpr int kBarBytes = 8 * (2 * kStages + 5) + 24;
 constexpr int kTableBytes = (kMaxGroups + 8) * (4 + 4 + 2 + 2);  // tile starts, row starts, padding, order
 constexpr int kSmem = 1024 + kStages * kStageBytes + kExchange + kBarBytes + kTableBytes;
@@ -129,7 +130,6 @@ __device__ __forceinline__ bool agree(int id, int threads, bool mine) {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 8);
+      mbar_init(tempty_bar(a), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto at_tile = [&](int v, int i) { return __shfl_sync(0xFFFFFFFFu, v, i & 31); };
 
-  if (warp == 0 || warp >= 6) {
+  if (warp == 0 || warp == 6 || warp == 7) {
     // ------------------------------------------------------------ producers
     const bool is_a = warp == 0;
     const uint32_t bar_base = rank == 0 ? bar0 : mapa_shared(bar0, 0);  // the leader's full barriers
@@ -377,9 +377,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
+    const int q = warp & 3;             // this warp may access TMEM lanes 32q .. 32q+31
+    const int half = warp >= 8 ? 1 : 0;  // its blocks of 32 tokens: every other one
+    const int partners = 1 + (q & 1) + 2 * half;  // named barrier of warps q and q ^ 2
     Tile mine = {};
-    bool odd = false;
+    float odd = 0.0f;  // GU: turns NaN where a gate or q is not finite
     for (int i = 0; i < my_tiles; ++i) {
       if ((i & 31) == 0) mine = decode(i + lane);
       const int wt = at_tile(mine.wt, i), count = at_tile(mine.count, i), N = at_tile(mine.N, i);
@@ -388,76 +390,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (prow < 0 || npad > p.prows - prow) npad = 0;  // (offsets that decrease: no store outside)
       const int acc = i & 1;
       const uint32_t ap = (uint32_t)(i >> 1) & 1u;
+      const int gu_f0 = wt * kTileM + (int)rank * 64;
+      if (MODE == kGU && gu_f0 < p.I) {
+        // This CTA's q of the tile (256 bytes a token) into L2 while the tile's
+        // MMAs run: q is larger than L2, and from HBM a block's loads took 5000
+        // cycles under load, longer than everything else here.
+        const char* qt = reinterpret_cast<const char*>(p.q + (size_t)row * p.I + gu_f0);
+        for (int x = (half * 4 + q) * 32 + lane; x < 2 * count; x += 32 * kEpiWarps)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(qt + (size_t)(x >> 1) * p.I * 4 + (x & 1) * 128));
+      }
       int ok = 1;
       if (lane == 0)
         ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (MODE == kGU) ok = agree(1 + (q & 1), 64, ok != 0);  // partners leave together
+      if (MODE == kGU) ok = agree(partners, 64, ok != 0);  // partners leave together
       if (!ok) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxN);
       if (MODE == kGU) {
-        const int f0 = wt * kTileM + (int)rank * 64 + (q & 1) * 32;  // (32 features: all inside I or none)
+        const int f0 = gu_f0 + (q & 1) * 32;  // (64 features: all inside I or none)
         const bool gate_warp = q < 2;
         const int j0 = gate_warp ? 0 : 16;  // the 16 tokens of a block that this warp finishes
-        float* mine_ex = exchange + q * 1024 + lane;
-        const float* other_ex = exchange + (q ^ 2) * 1024 + lane;
+        float* mine_ex = exchange + (half * 4 + q) * 512;
+        const float* other_ex = exchange + (half * 4 + (q ^ 2)) * 512 + lane;
+        uint16_t* stg = reinterpret_cast<uint16_t*>(mine_ex);
         if (f0 < p.I) {
-          const float* qp = p.q + (size_t)row * p.I + f0 + lane;
-          float nq[16];  // q of the block's 16 tokens, loaded one block ahead
+          const float* qp = p.q + (size_t)(row + j0) * p.I + f0 + lane;
+          float nq[16];  // q of the next block's 16 tokens
           auto load_q = [&](int c) {
+            const float* at = qp + (size_t)c * p.I;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) nq[j] = c + j0 + j < count ? qp[(size_t)(c + j0 + j) * p.I] : 0.0f;
+            for (int j = 0; j < 16; ++j, at += p.I) nq[j] = c + j0 + j < count ? *at : 0.0f;
           };
-          load_q(0);
-          int buf = 0;
+          load_q(32 * half);
 #pragma unroll 1
-          for (int c = 0; c < N; c += 32, buf ^= 512) {
+          for (int c = 32 * half; c < N; c += 64) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(tb + c, v);
             tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) mine_ex[buf + j * 32] = __uint_as_float(gate_warp ? v[16 + j] : v[j]);
-            named_sync(1 + (q & 1), 64);  // (the buffer after next is free: both have read it)
-            float qv[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) qv[j] = nq[j];
-            if (c + 32 < N) load_q(c + 32);
-            // The 16 x 32 results of h and dg, then of du, go out through this
-            // warp's other exchange buffer (its last reader is done): 64-byte
-            // rows, eight tokens per store instruction.
-            uint16_t* stg = reinterpret_cast<uint16_t*>(exchange + q * 1024 + (buf ^ 512));
-            __nv_bfloat16 du[16];
+            float own[16], other[16], qv[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float mine_v = __uint_as_float(gate_warp ? v[j] : v[16 + j]), other_v = other_ex[buf + j * 32];
-              const float gt = gate_warp ? mine_v : other_v, up = gate_warp ? other_v : mine_v;
-              const bool live = c + j0 + j < count;
+              own[j] = __uint_as_float(gate_warp ? v[j] : v[16 + j]);
+              mine_ex[j * 32 + lane] = __uint_as_float(gate_warp ? v[16 + j] : v[j]);
+              qv[j] = nq[j];
+            }
+            if (c + 64 < N) load_q(c + 64);
+            named_sync(partners, 64);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) other[j] = other_ex[j * 32];
+            named_sync(partners, 64);  // both have read: each buffer is its warp's own again
+            // The 16 x 32 results of h and dg, then of du, go out through that
+            // buffer: 64-byte rows, eight tokens per store instruction.
+            const int live = count - (c + j0);  // tokens of the group among the 16
+            uint32_t du[8];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float gt = gate_warp ? own[j] : other[j], up = gate_warp ? other[j] : own[j];
               const float sg = __fdividef(1.0f, 1.0f + __expf(-gt));
-              const float act = gt * sg;
+              const float act = gt * sg, qs = qv[j] * sg;
               // An infinity or NaN in the row of a or of dy leaves none of its
-              // gate values, or of its q values, finite.
-              odd = odd || (live && !(finite(gt) && finite(qv[j])));
-              const __nv_bfloat16 h = __float2bfloat16_rn(live ? act * up : 0.0f);
-              const __nv_bfloat16 dg = __float2bfloat16_rn(live ? qv[j] * up * sg * fmaf(gt, 1.0f - sg, 1.0f) : 0.0f);
-              du[j] = __float2bfloat16_rn(live ? qv[j] * act : 0.0f);
-              stg[j * 32 + lane] = __bfloat16_as_ushort(h);
-              stg[512 + j * 32 + lane] = __bfloat16_as_ushort(dg);
+              // gate values, or of its q values, finite. (One of the next
+              // group's, in a token past this one's, does no harm.)
+              odd = fmaf(0.0f, gt, fmaf(0.0f, qv[j], odd));
+              uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(act * up));
+              uint16_t dg = __bfloat16_as_ushort(__float2bfloat16_rn(qs * up * fmaf(gt, 1.0f - sg, 1.0f)));
+              uint16_t d = __bfloat16_as_ushort(__float2bfloat16_rn(qs * gt));
+              if (j >= live) h = dg = d = 0;
+              stg[j * 32 + lane] = h;
+              stg[512 + j * 32 + lane] = dg;
+              du[j >> 1] = j & 1 ? du[j >> 1] | (uint32_t)d << 16 : (uint32_t)d;
             }
             const size_t at = (size_t)(prow + c + j0) * p.I + f0 + (lane & 3) * 8;
             auto put = [&](__nv_bfloat16* dst, const uint16_t* src) {
 #pragma unroll
-              for (int t = lane >> 2; t < 16; t += 8)
+              for (int u = 0; u < 2; ++u) {
+                const int t = (lane >> 2) + 8 * u;
                 if (c + j0 + t < npad)
                   *reinterpret_cast<uint4*>(dst + at + (size_t)t * p.I) =
                       *reinterpret_cast<const uint4*>(src + t * 32 + (lane & 3) * 8);
+              }
             };
             __syncwarp();
             put(p.h, stg);
             put(p.dg, stg + 512);
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) stg[j * 32 + lane] = __bfloat16_as_ushort(du[j]);
+            for (int j = 0; j < 16; ++j) stg[j * 32 + lane] = (uint16_t)(du[j >> 1] >> (16 * (j & 1)));
             __syncwarp();
             put(p.du, stg);
             __syncwarp();
@@ -468,18 +487,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int f0 = wt * kTileM + (int)rank * 128 + q * 32;  // (32 features: all inside or none)
         if (f0 < cols) {
           const size_t at = (size_t)row * cols + f0 + lane;
+          auto put = [&](size_t o, uint32_t v) {
+            if (MODE == kQ) p.q[o] = __uint_as_float(v);
+            else p.da[o] = __float2bfloat16_rn(__uint_as_float(v));
+          };
 #pragma unroll 1
-          for (int c = 0; c < N; c += 32) {
+          for (int c = 32 * half; c < count; c += 64) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(tb + c, v);
             tmem_ld_wait();
+            size_t o = at + (size_t)c * cols;
+            if (c + 32 <= count) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (c + j < count) {
-                const size_t o = at + (size_t)(c + j) * cols;
-                if (MODE == kQ) p.q[o] = __uint_as_float(v[j]);
-                else p.da[o] = __float2bfloat16_rn(__uint_as_float(v[j]));
-              }
+              for (int j = 0; j < 32; ++j, o += cols) put(o, v[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j, o += cols)
+                if (c + j < count) put(o, v[j]);
             }
           }
         }
@@ -491,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive_remote(mapa_shared(tempty_bar(acc), 0));
       }
     }
-    if (MODE == kGU && odd) *p.odd = 1;
+    if (MODE == kGU && odd != 0.0f) *p.odd = 1;
   }
 
   // Both CTAs arrive here only when their roles are done (every wait is
