@@ -537,3 +537,11 @@ class MoELayer:
         layer_forward(self.handle, self.cfg, self.weights, x, logits, out, self.ws, main=main, side=self.side,
                       x_scale=x_scale)
         return out
+
+
+def __getattr__(name):
+    if name == "MoEBlock":  # block.py uses this module
+        from .block import MoEBlock
+
+        return MoEBlock
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
