@@ -13,7 +13,16 @@
 // and a result tile is short here (rows per expert / 16 MMAs). A 128 x 256 tile
 // on one SM costs 48 KB of loads per 64 rows, which with the result's 64 KB
 // outlasts its MMAs; the pair's tile costs each SM 32 KB for the same MMAs.
-// 192 experts x 341 rows, H = 4096, I = 1536: one SM per tile 2.45 ms.
+//
+// Work is dealt in strips: up to four tiles of one group side by side, which
+// share their A columns. A group of up to 64 rows per stage of the A ring (384)
+// keeps A in shared memory for the whole strip, and its later tiles load only
+// B: 16 KB per 64 rows. Longer groups, which are bound by their MMAs, have
+// strips of one tile; so do all when there are few (fewer than eight strips per
+// pair), to keep the pairs' shares even.
+//
+// Measured at 192 experts x 341 rows, H = 4096, I = 1536 (short runs): one SM
+// per tile 2.45 ms, pairs 2.30, tiles decoded by lanes 2.22, no clearing 1.96.
 //
 // A group's rows end anywhere; the MMA runs in steps of 16 rows. One operand of
 // each product is h, dg or du, whose groups are followed by zero rows up to a
@@ -47,19 +56,19 @@ namespace {
 constexpr int kBK = 64;  // rows per stage
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSmem = 232448;       // 227 KB dynamic shared memory per CTA
-constexpr int kStageBytes = 4 * kChunk;  // A: two chunks of 64 columns; B: two
+constexpr int kHalfBytes = 2 * kChunk;  // a stage of A, or of B: two chunks of 64 columns
 constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 384;
 constexpr int kEpiBytes = kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
-constexpr int kBarBytes = 8 * (3 * kMaxStages + 5) + 8;
+constexpr int kBarBytes = 8 * (6 * kMaxStages + 5) + 8;
 constexpr uint16_t kPairMask = 0x3;
 
 constexpr int table_bytes(int G) { return ((G + 1) * 4 + 2 * G + 2 * G + 15) / 16 * 16; }
 constexpr int smem_bytes(int G, int stages) {
-  return 1024 + stages * kStageBytes + kEpiBytes + kBarBytes + table_bytes(G);
+  return 1024 + 2 * stages * kHalfBytes + kEpiBytes + kBarBytes + table_bytes(G);
 }
-// Six stages, or five when the tables of many groups (more than 229) need the room.
+// Six stages, or five when the tables of many groups (more than 211) need the room.
 constexpr int ring_stages(int G) { return smem_bytes(G, kMaxStages) <= kMaxSmem ? kMaxStages : kMaxStages - 1; }
 static_assert(kBarBytes % 16 == 0, "the tables follow the barriers");
 static_assert(smem_bytes(kMaxGroups, kMaxStages - 1) <= kMaxSmem, "shared memory");
@@ -69,8 +78,14 @@ struct DwParams {
   int H, I;
   int stages;
   const int* odd;              // not 0: a row of a or dy may hold an infinity or NaN
-  int nd, ng, nc_d, nc_g;      // tiles of dWd and of dWg (= of dWu) per group; per row of tiles
-  uint32_t r_group, r_d, r_g;  // floor(2^32 / d) of nd + 2 ng, nc_d, nc_g (div_by)
+  // Strips: [0] of groups longer than the ring, one tile each; [1] of the others.
+  struct Cut {
+    int per_group;        // strips of a group: nd of dWd, then ng of dWg, then ng of dWu
+    int nd, ng;
+    int parts_d, parts_g;  // strips per row of tiles
+    int len_d, len_g;      // tiles per strip
+    uint32_t r_group, r_d, r_g;  // floor(2^32 / d) of per_group, parts_d, parts_g (div_by)
+  } cut[2];
 };
 
 // A = dy, dg, du; B = h, then a twice. Three box heights each (64, 32 and 16
@@ -79,24 +94,6 @@ struct DwMaps {
   CUtensorMap dy[3], dg[3], du[3], h[3], a[3];
   CUtensorMap dw[3];  // dWd, dWg, dWu
 };
-
-// One tile: its group, which of the three products, and its corner. The groups
-// come in `order`: longest first.
-struct DwTile {
-  int g, which, m0, n0;  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
-};
-__device__ __forceinline__ DwTile dw_tile(const DwParams& p, const uint16_t* order, int tile) {
-  DwTile t;
-  const int per = p.nd + 2 * p.ng, slot = div_by(tile, per, p.r_group);
-  t.g = order[slot];
-  int l = tile - slot * per;
-  t.which = l < p.nd ? 0 : (l < p.nd + p.ng ? 1 : 2);
-  l -= t.which == 0 ? 0 : (t.which == 1 ? p.nd : p.nd + p.ng);
-  const int nc = t.which == 0 ? p.nc_d : p.nc_g, row = div_by(l, nc, t.which == 0 ? p.r_d : p.r_g);
-  t.m0 = row * 256;
-  t.n0 = (l - row * nc) * 256;
-  return t;
-}
 
 // Arrive on a barrier of another CTA of the cluster, releasing this CTA's
 // writes, and the wait's other half (the phase has been seen complete).
@@ -123,10 +120,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
   uint8_t* base = smem_raw + pad;
   const uint32_t base_u32 = raw_addr + pad;
-  // Shared memory (the same in both CTAs): ring | epilogue staging | barriers | tables.
-  uint8_t* epi_stage = base + NS * kStageBytes;
+  // Shared memory (the same in both CTAs): A ring | B ring | epilogue staging | barriers | tables.
+  const uint32_t b_ring = base_u32 + NS * kHalfBytes;
+  uint8_t* epi_stage = base + 2 * NS * kHalfBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi_stage + kEpiBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 * kMaxStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* row_start = reinterpret_cast<int32_t*>(epi_stage + kEpiBytes + kBarBytes);
   // Group g's first row in h, dg and du (gemm_grad.cuh) is row_start[g] -
@@ -135,12 +133,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint16_t* order = pad_extra + G;
   int32_t* pads = reinterpret_cast<int32_t*>(epi_stage);  // until the loop starts
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };                         // leader: both CTAs' stage s
-  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };         // each CTA
-  auto tail_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };      // each CTA: a ragged stage
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * kMaxStages + a); };     // each CTA
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * kMaxStages + 2 + a); };  // leader
-  const uint32_t drain_bar = bar0 + 8u * (3 * kMaxStages + 4);
+  // Of A's ring (ab = 0) and B's (ab = 1).
+  auto full_bar = [&](int ab, int s) { return bar0 + 8u * (ab * kMaxStages + s); };        // leader: both CTAs' stage s
+  auto empty_bar = [&](int ab, int s) { return bar0 + 8u * ((2 + ab) * kMaxStages + s); };  // each CTA
+  auto tail_bar = [&](int ab, int s) { return bar0 + 8u * ((4 + ab) * kMaxStages + s); };   // each CTA: a ragged stage
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (6 * kMaxStages + a); };                 // each CTA
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (6 * kMaxStages + 2 + a); };            // leader
+  const uint32_t drain_bar = bar0 + 8u * (6 * kMaxStages + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: leader
@@ -148,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   allow_next_launch();
 
   fill_row_start(p.k, row_start, threadIdx.x, kThreads);
+  int* longs = reinterpret_cast<int*>(epi_stage) + kMaxGroups + 8;  // until the loop starts
+  if (threadIdx.x == 0) *longs = 0;
   __syncthreads();
   // order[rank] = group, by length, longest first (equal lengths by number).
   // Tiles are dealt to the pairs in that order, forwards and backwards in turn,
@@ -161,13 +162,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     order[at] = (uint16_t)g;
     pads[g] = n > 0 ? pad16(n) - n : 0;
+    if (n > NS * kBK) atomicAdd(longs, 1);
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(full_bar(s), 2);
-      mbar_init(empty_bar(s), 1);
-      mbar_init(tail_bar(s), 1);
-    }
+    for (int ab = 0; ab < 2; ++ab)
+      for (int s = 0; s < NS; ++s) {
+        mbar_init(full_bar(ab, s), 2);
+        mbar_init(empty_bar(ab, s), 1);
+        mbar_init(tail_bar(ab, s), 1);
+      }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 2 * kEpiWarps);
@@ -194,71 +197,87 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_previous_launch();
   const bool careful = *static_cast<const volatile int*>(p.odd) != 0;
   const uint32_t tmem_base = *tmem_slot;
-  const int total = G * (p.nd + 2 * p.ng);
+  const int n_long = *longs, long_strips = n_long * p.cut[0].per_group;
+  __syncthreads();  // the epilogue's staging overwrites longs
+  const int total = long_strips + (G - n_long) * p.cut[1].per_group;
   const int rounds = (total + npairs - 1) / npairs;
-  auto tile_of = [&](int r) { return r * npairs + ((r & 1) ? npairs - 1 - pair : pair); };
-  auto rows_of = [&](int g) {
+  auto strip_of = [&](int r) { return r * npairs + ((r & 1) ? npairs - 1 - pair : pair); };
+  const int my_rounds = rounds > 0 && strip_of(rounds - 1) >= total ? rounds - 1 : rounds;  // the last may be short
+  // Strips are decoded 32 rounds at a time, one by each lane of a role's warp,
+  // and read back by shuffles: decoding alone cost a role's thread 1000 to 1500
+  // cycles, as long as half a tile's MMAs.
+  struct Strip {
+    int rows, row0, prow0, m0, n0, len, g_which;  // prow0: in h, dg, du; len: tiles; g * 4 + which
+  };
+  auto decode = [&](int r) {  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
+    Strip t = {};
+    if (r >= my_rounds) return t;
+    int at = strip_of(r);
+    const bool is_long = at < long_strips;
+    const DwParams::Cut& c = p.cut[is_long ? 0 : 1];
+    if (!is_long) at -= long_strips;
+    const int slot = div_by(at, c.per_group, c.r_group);
+    const int g = order[slot + (is_long ? 0 : n_long)];
+    at -= slot * c.per_group;
+    const int which = at < c.nd ? 0 : (at < c.nd + c.ng ? 1 : 2);
+    at -= which == 0 ? 0 : (which == 1 ? c.nd : c.nd + c.ng);
+    const int parts = which == 0 ? c.parts_d : c.parts_g, len = which == 0 ? c.len_d : c.len_g;
+    const int row = div_by(at, parts, which == 0 ? c.r_d : c.r_g), n_tile = (at - row * parts) * len;
+    const int n_tiles = ((which == 0 ? p.I : p.H) + 255) / 256;
     const int n = row_start[g + 1] - row_start[g];
-    return n > 0 ? n : 0;
-  };
-  // Tiles are decoded 32 rounds at a time, one by each lane of a role's warp,
-  // and read back by shuffles: decoding a tile alone cost a role's thread 1000
-  // to 1500 cycles, as long as half the tile's MMAs.
-  struct Tile {
-    int rows, row0, prow0, m0, n0, g_which;  // prow0: in h, dg, du; g * 4 + which
-  };
-  auto decode = [&](int r) {
-    Tile t = {};
-    const int tile = tile_of(r);
-    if (r < rounds && tile < total) {
-      const DwTile d = dw_tile(p, order, tile);
-      t = {rows_of(d.g), row_start[d.g], row_start[d.g] - row_start[0] + pad_extra[d.g], d.m0, d.n0, d.g * 4 + d.which};
-    }
+    t = {n > 0 ? n : 0, row_start[g], row_start[g] - row_start[0] + pad_extra[g], row * 256, n_tile * 256,
+         n_tiles - n_tile < len ? n_tiles - n_tile : len, g * 4 + which};
     return t;
   };
   auto at_round = [&](int v, int r) { return __shfl_sync(0xFFFFFFFFu, v, r & 31); };
-  const int my_rounds = total > tile_of(rounds - 1) ? rounds : rounds - 1;  // the last round may be short
   // A stage with `left` rows of the group from its first row on needs clearing
   // when the group ends inside one of its steps.
   auto ragged = [&](int left) { return careful && left < kBK && (left & 15) != 0; };
 
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers
-    // The whole warp walks the loop in step; one elected lane issues.
-    const bool is_a = warp == 0;
+    // The whole warp walks the loop in step; one elected lane issues. A once per
+    // strip, B once per tile.
+    const int ab = warp == 0 ? 0 : 1;
     Ring rg;
     bool ok = true;
-    Tile mine = {};
+    Strip mine = {};
     for (int r = 0; ok && r < my_rounds; ++r) {
       if ((r & 31) == 0) mine = decode(r + lane);
       const int nrows = at_round(mine.rows, r), which = at_round(mine.g_which, r) & 3;
       // A: dy (rows as given), dg, du; B: h, then a (rows as given).
-      int krow = at_round(is_a == (which == 0) ? mine.row0 : mine.prow0, r);
-      const int x = at_round(is_a ? mine.m0 : mine.n0, r) + (int)rank * 128;
-      const CUtensorMap* maps = is_a ? (which == 0 ? m.dy : (which == 1 ? m.dg : m.du)) : (which == 0 ? m.h : m.a);
-      for (int left = nrows; left > 0; left -= kBK, krow += kBK) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
-                                                       MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
-          ok = false;
-          break;
-        }
-        const int low = left <= 16 ? 2 : (left <= 32 ? 1 : 0);  // box height 64 >> low
-        const CUtensorMap* map = maps + low;
-        const uint32_t dst = base_u32 + rg.s * kStageBytes + (is_a ? 0 : 2 * kChunk);
-        const bool own = ragged(left);  // completes on this CTA's tail barrier
-        const uint32_t bar = own ? tail_bar(rg.s) : (rank == 0 ? full_bar(rg.s) : mapa_shared(full_bar(rg.s), 0));
-        if (elect_one()) {
-          if (is_a && own) {
-            mbar_arrive_expect_tx(bar, (uint32_t)kStageBytes >> low);
-          } else if (is_a && rank == 0) {  // both CTAs' bytes (the other's may land first)
-            mbar_arrive_expect_tx(bar, 2u * ((uint32_t)kStageBytes >> low));
-            mbar_arrive(bar);
+      const int row0 = at_round((ab == 0) == (which == 0) ? mine.row0 : mine.prow0, r);
+      const int tiles = ab == 0 ? 1 : at_round(mine.len, r);
+      const int x0 = at_round(ab == 0 ? mine.m0 : mine.n0, r) + (int)rank * 128;
+      const CUtensorMap* maps = ab == 0 ? (which == 0 ? m.dy : (which == 1 ? m.dg : m.du)) : (which == 0 ? m.h : m.a);
+      for (int t = 0; ok && t < tiles; ++t) {
+        const int x = x0 + t * 256;
+        int krow = row0;
+        for (int left = nrows; left > 0; left -= kBK, krow += kBK) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(ab, rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
+                                                         MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
+            ok = false;
+            break;
           }
-          tma_load_2d_pair(dst, map, bar, x, krow);
-          tma_load_2d_pair(dst + kChunk, map, bar, x + 64, krow);
+          const int low = left <= 16 ? 2 : (left <= 32 ? 1 : 0);  // box height 64 >> low
+          const CUtensorMap* map = maps + low;
+          const uint32_t dst = (ab == 0 ? base_u32 : b_ring) + rg.s * kHalfBytes;
+          const bool own = ragged(left);  // completes on this CTA's tail barrier
+          const uint32_t full = full_bar(ab, rg.s);
+          const uint32_t bar = own ? tail_bar(ab, rg.s) : (rank == 0 ? full : mapa_shared(full, 0));
+          if (elect_one()) {
+            if (own) {
+              mbar_arrive_expect_tx(bar, (uint32_t)kHalfBytes >> low);
+            } else if (rank == 0) {  // both CTAs' bytes (the other's may land first)
+              mbar_arrive_expect_tx(bar, 2u * ((uint32_t)kHalfBytes >> low));
+              mbar_arrive(bar);
+            }
+            tma_load_2d_pair(dst, map, bar, x, krow);
+            tma_load_2d_pair(dst + kChunk, map, bar, x + 64, krow);
+          }
+          __syncwarp();
+          rg.next(NS);
         }
-        __syncwarp();
-        rg.next(NS);
       }
     }
     if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
@@ -278,53 +297,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.k.status, MOE_DEV_TIMEOUT_MMA,
                                                          p.k.limit_ns)) != 0;
       };
-      Ring rg;
+      Ring ra, rb;
       bool ok = true, issued = false;
-      int rows32 = 0;
+      Strip mine = {};
+      int tile = 0;
       for (int r = 0; ok && r < my_rounds; ++r) {
-        if ((r & 31) == 0) rows32 = decode(r + lane).rows;
-        const int acc = r & 1;
-        const uint32_t ap = (uint32_t)(r >> 1) & 1u;
-        const int nrows = at_round(rows32, r);
-        if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-        uint32_t accumulate = 0;
-        for (int left = nrows; left > 0; left -= kBK) {
-          const uint32_t sa = base_u32 + rg.s * kStageBytes;
-          const uint64_t da = sw128_mnmajor_desc(sa), db = sw128_mnmajor_desc(sa + 2 * kChunk);
-          if (!wait_all(full_bar(rg.s), rg.ph)) {
+        if ((r & 31) == 0) mine = decode(r + lane);
+        const int nrows = at_round(mine.rows, r), len = at_round(mine.len, r);
+        const Ring strip = ra;  // where the strip's A starts
+        for (int t = 0; ok && t < len; ++t, ++tile) {
+          const int acc = tile & 1;
+          const uint32_t ap = (uint32_t)(tile >> 1) & 1u;
+          if (!wait_all(tempty_bar(acc), ap ^ 1u)) {
             ok = false;
             break;
           }
-          if (ragged(left)) mbar_acquire_cluster(full_bar(rg.s), rg.ph);  // the other CTA's cleared rows
           tc_fence_after();
-          if (left >= kBK) {
+          const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+          ra = strip;
+          uint32_t accumulate = 0;
+          for (int left = nrows; left > 0; left -= kBK) {
+            const uint64_t da = sw128_mnmajor_desc(base_u32 + ra.s * kHalfBytes);
+            const uint64_t db = sw128_mnmajor_desc(b_ring + rb.s * kHalfBytes);
+            if ((t == 0 && !wait_all(full_bar(0, ra.s), ra.ph)) || !wait_all(full_bar(1, rb.s), rb.ph)) {
+              ok = false;
+              break;
+            }
+            if (ragged(left)) {  // the other CTA's cleared rows
+              if (t == 0) mbar_acquire_cluster(full_bar(0, ra.s), ra.ph);
+              mbar_acquire_cluster(full_bar(1, rb.s), rb.ph);
+            }
+            tc_fence_after();
             if (elect_one()) {
-              umma_bf16_pair(d, da, db, kIdesc, accumulate);
+              if (left >= kBK) {
+                umma_bf16_pair(d, da, db, kIdesc, accumulate);
 #pragma unroll
-              for (int k = 1; k < kBK / 16; ++k) umma_bf16_pair(d, da + k * kStep, db + k * kStep, kIdesc, 1u);
-              umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
+                for (int k = 1; k < kBK / 16; ++k) umma_bf16_pair(d, da + k * kStep, db + k * kStep, kIdesc, 1u);
+              } else {
+                const int steps = (left + 15) >> 4;
+                for (int k = 0; k < steps; ++k)
+                  umma_bf16_pair(d, da + (uint64_t)k * kStep, db + (uint64_t)k * kStep, kIdesc,
+                                 accumulate | (k ? 1u : 0u));
+              }
+              umma_commit_pair_mc(empty_bar(1, rb.s), kPairMask);
+              if (t == len - 1) umma_commit_pair_mc(empty_bar(0, ra.s), kPairMask);
             }
-          } else {
-            const int steps = (left + 15) >> 4;
-            if (elect_one()) {
-              for (int k = 0; k < steps; ++k)
-                umma_bf16_pair(d, da + (uint64_t)k * kStep, db + (uint64_t)k * kStep, kIdesc, accumulate | (k ? 1u : 0u));
-              umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
-            }
+            __syncwarp();
+            accumulate = 1u;
+            issued = true;
+            ra.next(NS);
+            rb.next(NS);
           }
+          if (!ok) break;
+          if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), kPairMask);
           __syncwarp();
-          accumulate = 1u;
-          issued = true;
-          rg.next(NS);
         }
-        if (!ok) break;
-        if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), kPairMask);
-        __syncwarp();
       }
       if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
         umma_commit_pair(drain_bar);
@@ -333,87 +360,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 11) {
     // ------------------------------------------------------------ clearing
-    // A ragged stage, once this CTA's copies of it have landed: clear the rows
-    // from the group's end to the step's end in both operands, and hand the
-    // stage to the leader. A stage's tail barrier has one phase per ragged use.
-    Ring rg;
-    uint32_t phase = 0;
-    int rows32 = 0;
-    for (int r = 0; r < my_rounds; ++r) {
-      if ((r & 31) == 0) rows32 = decode(r + lane).rows;
-      bool ok = true;
-      for (int left = at_round(rows32, r); left > 0; left -= kBK) {
+    // A ragged stage of a ring, once this CTA's copies of it have landed: clear
+    // the rows from the group's end to the step's end, and hand the stage to
+    // the leader. A stage's tail barrier has one phase per ragged use.
+    Ring rg[2];
+    uint32_t phase[2] = {0, 0};
+    Strip mine = {};
+    bool ok = true;
+    auto pass = [&](int ab, int nrows) {  // one tile's stages of a ring
+      for (int left = nrows; ok && left > 0; left -= kBK) {
+        const int st = rg[ab].s;
         if (ragged(left)) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail_bar(rg.s), (phase >> rg.s) & 1u, abort_flag, p.k.status,
-                                                         MOE_DEV_TIMEOUT_MMA, p.k.limit_ns));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail_bar(ab, st), (phase[ab] >> st) & 1u, abort_flag,
+                                                         p.k.status, MOE_DEV_TIMEOUT_MMA, p.k.limit_ns));
           if (!ok) break;
-          phase ^= 1u << rg.s;
+          phase[ab] ^= 1u << st;
           // Eight lanes clear one 128-byte row (a row's swizzle stays inside it).
-          uint8_t* st = base + rg.s * kStageBytes + (lane & 7) * 16;
+          uint8_t* at = base + (ab * NS + st) * kHalfBytes + (lane & 7) * 16;
           for (int i = left + (lane >> 3); i < ((left + 15) & ~15); i += 4) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(st + c * kChunk + i * 128) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(at + i * 128) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(at + kChunk + i * 128) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (rank == 0) mbar_arrive(full_bar(rg.s));
-            else mbar_arrive_remote_release(mapa_shared(full_bar(rg.s), 0));
+            if (rank == 0) mbar_arrive(full_bar(ab, st));
+            else mbar_arrive_remote_release(mapa_shared(full_bar(ab, st), 0));
           }
         }
-        rg.next(NS);
+        rg[ab].next(NS);
       }
-      if (!ok) break;
-    }
+    };
+    if (careful)
+      for (int r = 0; ok && r < my_rounds; ++r) {
+        if ((r & 31) == 0) mine = decode(r + lane);
+        const int nrows = at_round(mine.rows, r), len = at_round(mine.len, r);
+        pass(0, nrows);
+        for (int t = 0; t < len; ++t) pass(1, nrows);
+      }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;             // this warp may access TMEM lanes 32q .. 32q+31
     const int half = warp > 6 ? 1 : 0;  // its 128 columns
     uint8_t* stg = epi_stage + (half * 4 + q) * 4096;
-    Tile mine = {};
-    for (int r = 0; r < my_rounds; ++r) {
+    Strip mine = {};
+    int tile = 0, ok = 1;
+    for (int r = 0; ok && r < my_rounds; ++r) {
       if ((r & 31) == 0) mine = decode(r + lane);
-      const int acc = r & 1;
-      const uint32_t ap = (uint32_t)(r >> 1) & 1u;
       const int which = at_round(mine.g_which, r) & 3, g = at_round(mine.g_which, r) >> 2;
-      const int m0 = at_round(mine.m0, r) + (int)rank * 128 + q * 32, n0 = at_round(mine.n0, r) + half * 128;
+      const int m0 = at_round(mine.m0, r) + (int)rank * 128 + q * 32, len = at_round(mine.len, r);
+      int n0 = at_round(mine.n0, r) + half * 128;
       const bool empty = at_round(mine.rows, r) == 0;
-      int ok = 1;
-      if (lane == 0)
-        ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256 + half * 128);
-      // 32 x 64 blocks by TMA. (Stores from registers are 32 lines per warp
-      // instruction, and the queue they form delays the loads: one SM per tile
-      // 2.70 ms against 2.45.) H and I are multiples of 64, so a block is all
-      // inside the group's matrix or all outside.
-      const int M = which == 0 ? p.H : p.I, N = which == 0 ? p.I : p.H;
-      if (m0 < M) {
+      for (int t = 0; t < len; ++t, ++tile, n0 += 256) {
+        const int acc = tile & 1;
+        const uint32_t ap = (uint32_t)(tile >> 1) & 1u;
+        if (lane == 0)
+          ok = mbar_wait_bounded(tfull_bar(acc), ap, abort_flag, p.k.status, MOE_DEV_TIMEOUT_EPILOGUE, p.k.limit_ns) ? 1 : 0;
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256 + half * 128);
+        // 32 x 64 blocks by TMA. (Stores from registers are 32 lines per warp
+        // instruction, and the queue they form delays the loads: one SM per tile
+        // 2.70 ms against 2.45.) H and I are multiples of 64, so a block is all
+        // inside the group's matrix or all outside.
+        const int M = which == 0 ? p.H : p.I, N = which == 0 ? p.I : p.H;
+        if (m0 < M) {
 #pragma unroll 1
-        for (int c = 0; c < 128 && n0 + c < N; c += 64) {
-          if (empty) {
-            if (lane == 0) bulk_wait_group_read0();
-            __syncwarp();
+          for (int c = 0; c < 128 && n0 + c < N; c += 64) {
+            if (empty) {
+              if (lane == 0) bulk_wait_group_read0();
+              __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-          } else {
-            stage_bf16_block(tb + c, stg, lane);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&m.dw[which], smem_u32(stg), n0 + c, g * M + m0);
-            bulk_commit_group();
+              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+            } else {
+              stage_bf16_block(tb + c, stg, lane);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&m.dw[which], smem_u32(stg), n0 + c, g * M + m0);
+              bulk_commit_group();
+            }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive(tempty_bar(acc));
-        else mbar_arrive_remote(mapa_shared(tempty_bar(acc), 0));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(tempty_bar(acc));
+          else mbar_arrive_remote(mapa_shared(tempty_bar(acc), 0));
+        }
       }
     }
     if (lane == 0) bulk_wait_group0();  // this warp's bulk stores are complete
@@ -461,16 +497,29 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s)
   p.I = I;
   p.stages = ring_stages(G);
   p.odd = a.odd;
-  p.nc_d = (I + 255) / 256;
-  p.nc_g = (H + 255) / 256;
-  p.nd = ((H + 255) / 256) * p.nc_d;
-  p.ng = ((I + 255) / 256) * p.nc_g;
   auto recip = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d) : 0xFFFFFFFFu; };
-  p.r_group = recip(p.nd + 2 * p.ng);
-  p.r_d = recip(p.nc_d);
-  p.r_g = recip(p.nc_g);
-  const long long tiles = (long long)G * (p.nd + 2 * p.ng);
-  const int pairs = (int)(tiles < a.num_sms / 2 ? tiles : a.num_sms / 2);
+  const int tiles_h = (H + 255) / 256, tiles_i = (I + 255) / 256;
+  auto cut = [&](int most) {
+    DwParams::Cut c = {};
+    c.parts_d = (tiles_i + most - 1) / most;
+    c.parts_g = (tiles_h + most - 1) / most;
+    c.len_d = (tiles_i + c.parts_d - 1) / c.parts_d;
+    c.len_g = (tiles_h + c.parts_g - 1) / c.parts_g;
+    c.nd = tiles_h * c.parts_d;
+    c.ng = tiles_i * c.parts_g;
+    c.per_group = c.nd + 2 * c.ng;
+    c.r_group = recip(c.per_group);
+    c.r_d = recip(c.parts_d);
+    c.r_g = recip(c.parts_g);
+    return c;
+  };
+  const long long max_pairs = a.num_sms / 2;
+  p.cut[0] = cut(1);
+  int most = 4;
+  while (most > 1 && (long long)G * cut(most).per_group < 8 * max_pairs) most >>= 1;
+  p.cut[1] = cut(most);
+  const long long tiles = (long long)G * p.cut[0].per_group;
+  const int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
   if (pairs < 1) return cudaErrorInvalidValue;
   return launch_dependent(grouped_weight_grad_kernel, 2 * pairs, kThreads, smem_bytes(G, p.stages), s, true, /*cluster=*/2, m,
                           p);
