@@ -26,7 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxK = 32;
-constexpr int kBatch = 8;  // slots whose rows one pass over the columns holds in flight
+constexpr int kBatch = 8;  // permutation: rows a thread holds in flight
 
 __device__ __forceinline__ void unpack8(const uint4& a, float (&f)[8]) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -46,24 +46,31 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// dlogits[0..E-1] of one token, by one warp; lane k holds slot k's dw. The
-// row has been zeroed before (and that is visible to this warp).
-__device__ __forceinline__ void route_grad_warp(const float* __restrict__ logits, const int32_t* __restrict__ idx,
-                                                float dw, int E, int K, float scaling, int route_norm, float* dlogits,
-                                                int* status) {
+// Slot k's expert and its logit, in lane k of a warp (-1 and 0 in the others,
+// and for an id out of range).
+struct SlotLogit {
+  int e;
+  float l;
+};
+__device__ __forceinline__ SlotLogit load_slot(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                                               int E, int K, int* status) {
   const int lane = threadIdx.x & 31;
-  int e = -1;
-  float sg = 0.0f, om = 0.0f;  // sigma and 1 - sigma
+  SlotLogit s = {-1, 0.0f};
   if (lane < K) {
-    e = idx[lane];
-    if ((unsigned)e < (unsigned)E) {
-      const float l = logits[e];
-      sg = 1.0f / (1.0f + expf(-l));
-      om = 1.0f / (1.0f + expf(l));
-    } else {
-      atomicCAS(status, 0, MOE_DEV_BAD_EXPERT_ID);
-      e = -1;
-    }
+    const int e = idx[lane];
+    if ((unsigned)e < (unsigned)E) s = {e, logits[e]};
+    else atomicCAS(status, 0, MOE_DEV_BAD_EXPERT_ID);
+  }
+  return s;
+}
+// The chosen experts' dlogits of one token, by one warp; lane k holds slot k's
+// dw. The row has been zeroed before (and that is visible to this warp).
+__device__ __forceinline__ void route_grad_warp(SlotLogit s, float dw, int K, float scaling, int route_norm,
+                                                float* dlogits) {
+  float sg = 0.0f, om = 0.0f;  // sigma and 1 - sigma
+  if (s.e >= 0) {
+    sg = 1.0f / (1.0f + expf(-s.l));
+    om = 1.0f / (1.0f + expf(s.l));
   }
   float d = dw;
   if (route_norm) {
@@ -75,32 +82,35 @@ __device__ __forceinline__ void route_grad_warp(const float* __restrict__ logits
     }
     d = a / S / S;
   }
-  if (e >= 0) dlogits[e] = scaling * sg * om * d;
+  if (s.e >= 0) dlogits[s.e] = scaling * sg * om * d;
 }
 
-// One warp per (token, slot, part): it reads its share of the token's dout and
-// of one y row, writes the same share of the dy row and keeps the dot product;
-// nothing is exchanged until the end, so every warp's loads stay in flight.
-// dout[t] comes from L1 for the token's other warps.
-//   parts    1, or 4 when the tokens are too few to fill the SMs: part q takes
-//            every fourth run of 256 columns
-//   tokens   per block so that it has at least 8 warps (few slots per token)
-constexpr int kUnroll = 4;      // 256-column runs a warp has in flight
-constexpr int kMaxWarps = 16;   // per block
+// One warp per (token, slot): it reads the token's dout and one y row, writes
+// the dy row and keeps the dot product; nothing is exchanged until the end, so
+// every warp's loads stay in flight. dout[t] comes from L1 for the token's
+// other warps. A block has one token's slots, or several tokens' when a token
+// has few. 8192 tokens x 8 slots x 4096: 257 us (6.56 TB/s), with four runs of
+// 256 columns per iteration 281 (fewer blocks fit an SM); one block per token
+// whose threads hold all eight rows' columns 367.
+constexpr int kUnroll = 2;     // 256-column runs a warp has in flight
+constexpr int kMaxWarps = 16;  // per block
 
 __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
     const __nv_bfloat16* __restrict__ dout, const float* __restrict__ y, const float* __restrict__ topk_w,
-    const int32_t* __restrict__ f2p, int T, int K, int H, int E, int parts, int slot_warps, int tokens, float scaling,
+    const int32_t* __restrict__ f2p, int T, int K, int H, int E, int slot_warps, int tokens, float scaling,
     int route_norm, const int32_t* __restrict__ topk_idx, const float* __restrict__ logits,
     __nv_bfloat16* __restrict__ dy, float* __restrict__ dtopk_w, float* __restrict__ dlogits, int* status) {
-  __shared__ float dots[4 * kMaxK];  // [token][slot][part]
+  __shared__ float dots[kMaxK];  // [token][slot]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = warp % parts, sw = (warp / parts) % slot_warps, tok = warp / (parts * slot_warps);
+  const int sw = warp % slot_warps, tok = warp / slot_warps;
   const int t = blockIdx.x * tokens + tok;
   const int H8 = H >> 3;
+  SlotLogit slot = {-1, 0.0f};
   if (t < T) {
-    if (dlogits)
-      for (int e = (sw * parts + part) * 32 + lane; e < E; e += 32 * parts * slot_warps) dlogits[(size_t)t * E + e] = 0.0f;
+    if (dlogits) {
+      if (sw == 0) slot = load_slot(logits + (size_t)t * E, topk_idx + (size_t)t * K, E, K, status);
+      for (int e = sw * 32 + lane; e < E; e += 32 * slot_warps) dlogits[(size_t)t * E + e] = 0.0f;
+    }
     const uint4* drow = reinterpret_cast<const uint4*>(dout + (size_t)t * H);
     for (int k = sw; k < K; k += slot_warps) {
       const size_t f = (size_t)t * K + k;
@@ -115,13 +125,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
       if (p >= 0) {
         const float4* yr = reinterpret_cast<const float4*>(y + (size_t)p * H);
         uint4* dyr = reinterpret_cast<uint4*>(dy + (size_t)p * H);
-        const int step = 32 * parts;
-        for (int c = part * 32 + lane; c < H8; c += step * kUnroll) {
+        for (int c = lane; c < H8; c += 32 * kUnroll) {
           uint4 d[kUnroll];
           float4 v[kUnroll][2];
 #pragma unroll
           for (int u = 0; u < kUnroll; ++u) {
-            const int cc = c + u * step;
+            const int cc = c + u * 32;
             if (cc < H8) {
               d[u] = __ldg(drow + cc);
               v[u][0] = __ldcs(yr + 2 * cc);
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
           }
 #pragma unroll
           for (int u = 0; u < kUnroll; ++u) {
-            const int cc = c + u * step;
+            const int cc = c + u * 32;
             if (cc >= H8) break;
             float g[8], o[8];
             unpack8(d[u], g);
@@ -150,20 +159,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, off);
-      if (lane == 0) dots[(tok * K + k) * parts + part] = acc;
+      if (lane == 0) dots[tok * K + k] = acc;
     }
   }
   __syncthreads();
-  // One warp per token: lane k adds slot k's parts in order.
-  if (part != 0 || sw != 0 || t >= T) return;
-  float dw = 0.0f;
-  if (lane < K) {
-    for (int q = 0; q < parts; ++q) dw += dots[(tok * K + lane) * parts + q];
-    dtopk_w[(size_t)t * K + lane] = dw;
-  }
-  if (dlogits)
-    route_grad_warp(logits + (size_t)t * E, topk_idx + (size_t)t * K, dw, E, K, scaling, route_norm,
-                    dlogits + (size_t)t * E, status);
+  if (sw != 0 || t >= T) return;  // one warp per token
+  const float dw = lane < K ? dots[tok * K + lane] : 0.0f;
+  if (lane < K) dtopk_w[(size_t)t * K + lane] = dw;
+  if (dlogits) route_grad_warp(slot, dw, K, scaling, route_norm, dlogits + (size_t)t * E);
 }
 
 // The routing's gradient alone: one warp per token.
@@ -177,8 +180,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
   float* dl = dlogits + (size_t)t * E;
   for (int e = lane; e < E; e += 32) dl[e] = 0.0f;
   __syncwarp();
-  route_grad_warp(logits + (size_t)t * E, topk_idx + (size_t)t * K, lane < K ? dtopk_w[(size_t)t * K + lane] : 0.0f, E,
-                  K, scaling, route_norm, dl, status);
+  const SlotLogit slot = load_slot(logits + (size_t)t * E, topk_idx + (size_t)t * K, E, K, status);
+  route_grad_warp(slot, lane < K ? dtopk_w[(size_t)t * K + lane] : 0.0f, K, scaling, route_norm, dl);
 }
 
 // dx: a work unit is one token's chunk of 8 * blockDim columns; a thread adds
@@ -232,15 +235,10 @@ __global__ void __launch_bounds__(256) permute_bwd_kernel(const __nv_bfloat16* _
 
 cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  // Four parts while the (token, slot) rows alone are fewer than 16 warps for
-  // each of 152 SMs (61 tokens x 8 slots: 3.9 us with four, 5.6 with one).
-  const int parts = (long long)a.T * a.K < 152 * 16 && a.H >= 1024 ? 4 : 1;
-  const int most = kMaxWarps / parts;
-  const int slot_warps = a.K < most ? a.K : most;
-  const int tokens = parts == 1 && slot_warps <= 4 ? 8 / slot_warps : 1;
-  const int threads = 32 * parts * slot_warps * tokens;
-  combine_bwd_kernel<<<(a.T + tokens - 1) / tokens, threads, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w, a.flat_to_perm, a.T, a.K, a.H, a.E, parts,
+  const int slot_warps = a.K < kMaxWarps ? a.K : kMaxWarps;
+  const int tokens = slot_warps <= 4 ? 8 / slot_warps : 1;
+  combine_bwd_kernel<<<(a.T + tokens - 1) / tokens, 32 * slot_warps * tokens, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w, a.flat_to_perm, a.T, a.K, a.H, a.E,
       slot_warps, tokens, a.scaling, a.route_norm, a.topk_idx, a.logits, static_cast<__nv_bfloat16*>(a.dy_perm),
       a.dtopk_w, a.dlogits, a.status);
   return cudaGetLastError();
