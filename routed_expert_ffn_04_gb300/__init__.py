@@ -171,6 +171,7 @@ class Handle:
         h = ctypes.c_void_p()
         _check(lib.moe_create(self.device, ctypes.byref(h)), "moe_create")
         self._h = h
+        self.address = h.value  # None once closed
 
     @property
     def ptr(self):
@@ -179,7 +180,7 @@ class Handle:
     def close(self):
         if self._h:
             load().moe_destroy(self._h)
-            self._h = None
+            self._h = self.address = None
 
     def __del__(self):
         try:
@@ -341,43 +342,36 @@ def layer_forward_gated(h: Handle, cfg: Config, weights: Weights, w_router, x, o
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _arg(h: Handle, what: str, name: str, t, dtype, numel: int, optional: bool = False):
-    """Pointer of a dense tensor of `numel` elements on the handle's device; MoEError otherwise."""
+def _bad_arg(what: str, name: str, t, dtype, numel: int, device: int):
+    """Raises the refusal of a tensor by the binding (numel < 0: of its shape or of any size)."""
     if t is None:
-        if optional:
-            return None
         raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: {name} is missing")
-    if t.dtype is not dtype or t.numel() != numel or t.get_device() != h.device or not t.is_contiguous():
-        raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: {name} must be a dense {dtype} tensor of {numel} elements on "
-                       f"cuda:{h.device}, got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device}")
-    return t.data_ptr()
-
-
-# The current stream's address without building a Stream object (3 us of a small call).
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(h: Handle, s) -> int:
-    """cudaStream_t of s, or of the current stream of the handle's device."""
-    if s is not None:
-        return s.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(h.device)
-    return torch.cuda.current_stream(h.device).cuda_stream
-
-
-def _res_type(what: str, dtype) -> int:
-    if dtype == _BF16:
-        return MOE_RES_BF16
-    if dtype == _F32:
-        return MOE_RES_F32
-    raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: the residual stream is bfloat16 or float32, got {dtype}")
-
-
-def _rows_cols(what: str, name: str, t) -> tuple[int, int]:
-    if t is None or t.dim() < 1 or t.shape[-1] == 0:
+    if device < 0:
         raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: {name} needs a last axis of at least one column")
-    return t.numel() // t.shape[-1], t.shape[-1]
+    size = f" of {numel} elements" if numel >= 0 else ""
+    raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: {name} must be a dense {dtype or ''} tensor{size} on cuda:{device}, "
+                   f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device}")
+
+
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_native_module = None
+
+
+def _native():
+    """The compiled binding: the tensors' checks and the call in one step."""
+    global _native_module
+    if _native_module is None:
+        load()
+        from . import _binding
+
+        # the current stream's address without building a Stream object (3 us of a small call), where torch has that
+        _binding.setup(_bad_arg, _check, getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream), _BF16, _F32,
+                       _I32, _U8)
+        _native_module = _binding
+    return _native_module
 
 
 def add_rmsnorm(h: Handle, x, weight, eps: float, residual=None, h_out=None, out=None, q=None, q_scale=None,
@@ -387,17 +381,7 @@ def add_rmsnorm(h: Handle, x, weight, eps: float, residual=None, h_out=None, out
     x [..., H] bf16, weight [H] bf16; residual and h_out both bf16 or both fp32; q uint8 codes and q_scale [..., H/32]
     uint8 as quantize_mxfp8 writes them (the MX layers' x and x_scale); rstd [rows] fp32 for the backward pass. h_out
     may be residual, and out may be x."""
-    what = "moe_add_rmsnorm"
-    rows, H = _rows_cols(what, "x", x)
-    n = rows * H
-    res = residual if residual is not None else h_out
-    rt = _BF16 if res is None else res.dtype
-    _check(load().moe_add_rmsnorm(
-        h.ptr, rows, H, _res_type(what, rt), _arg(h, what, "x", x, _BF16, n),
-        _arg(h, what, "residual", residual, rt, n, True), _arg(h, what, "weight", weight, _BF16, H), float(eps),
-        _arg(h, what, "h_out", h_out, rt, n, True), _arg(h, what, "out", out, _BF16, n, True),
-        _arg(h, what, "q", q, _U8, n, True), _arg(h, what, "q_scale", q_scale, _U8, n // 32, True),
-        _arg(h, what, "rstd", rstd, _F32, rows, True), _stream_of(h, stream)), what)
+    _native().add_rmsnorm(h.address, h.device, x, weight, eps, residual, h_out, out, q, q_scale, rstd, stream)
 
 
 def add_rmsnorm_backward_workspace_size(rows: int, H: int) -> int:
@@ -411,51 +395,25 @@ def add_rmsnorm_backward(h: Handle, dout, h_res, weight, rstd, dh, ws=None, dh_i
                          stream=None):
     """Gradient of add_rmsnorm at its h_out and rstd: dh (of x and of residual; the stream's type), dx (the same in
     bf16) and dweight [H] fp32 (needs ws). dh_in is the gradient that reaches h_out on its own path."""
-    what = "moe_add_rmsnorm_backward"
-    rows, H = _rows_cols(what, "h_res", h_res)
-    n, rt = rows * H, h_res.dtype
-    _check(load().moe_add_rmsnorm_backward(
-        h.ptr, rows, H, _res_type(what, rt), _arg(h, what, "dout", dout, _BF16, n),
-        _arg(h, what, "dh_in", dh_in, rt, n, True), _arg(h, what, "h_res", h_res, rt, n),
-        _arg(h, what, "weight", weight, _BF16, H), _arg(h, what, "rstd", rstd, _F32, rows),
-        _arg(h, what, "dh", dh, rt, n), _arg(h, what, "dx", dx, _BF16, n, True),
-        _arg(h, what, "dweight", dweight, _F32, H, True), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-        _stream_of(h, stream)), what)
+    _native().add_rmsnorm_backward(h.address, h.device, dout, h_res, weight, rstd, dh, ws, dh_in, dx, dweight, stream)
 
 
 def combine_backward(h: Handle, cfg: Config, dout, y_perm, topk_w, flat_to_perm, dy_perm, dtopk_w, topk_idx=None,
                      logits=None, dlogits=None, stream=None):
     """Gradient of combine (dy_perm [T*K, H] bf16, dtopk_w [T, K] fp32) and, given topk_idx, logits and dlogits, of the
     routing weights (dlogits [T, E] fp32). The shared expert's gradient is dout itself."""
-    what = "moe_combine_backward"
-    T, K, H, E = cfg.T, cfg.K, cfg.H, cfg.E
-    _check(load().moe_combine_backward(
-        h.ptr, ctypes.byref(cfg), _arg(h, what, "dout", dout, _BF16, T * H),
-        _arg(h, what, "y_perm", y_perm, _F32, T * K * H), _arg(h, what, "topk_w", topk_w, _F32, T * K),
-        _arg(h, what, "flat_to_perm", flat_to_perm, _I32, T * K),
-        _arg(h, what, "topk_idx", topk_idx, _I32, T * K, True), _arg(h, what, "logits", logits, _F32, T * E, True),
-        _arg(h, what, "dy_perm", dy_perm, _BF16, T * K * H), _arg(h, what, "dtopk_w", dtopk_w, _F32, T * K),
-        _arg(h, what, "dlogits", dlogits, _F32, T * E, True), _stream_of(h, stream)), what)
+    _native().combine_backward(h.address, h.device, cfg, dout, y_perm, topk_w, flat_to_perm, dy_perm, dtopk_w, topk_idx,
+                               logits, dlogits, stream)
 
 
 def route_backward(h: Handle, cfg: Config, logits, topk_idx, dtopk_w, dlogits, stream=None):
     """Gradient of route at the chosen experts: dlogits [T, E] fp32, 0 for the others."""
-    what = "moe_route_backward"
-    T, K, E = cfg.T, cfg.K, cfg.E
-    _check(load().moe_route_backward(
-        h.ptr, ctypes.byref(cfg), _arg(h, what, "logits", logits, _F32, T * E),
-        _arg(h, what, "topk_idx", topk_idx, _I32, T * K), _arg(h, what, "dtopk_w", dtopk_w, _F32, T * K),
-        _arg(h, what, "dlogits", dlogits, _F32, T * E), _stream_of(h, stream)), what)
+    _native().route_backward(h.address, h.device, cfg, logits, topk_idx, dtopk_w, dlogits, stream)
 
 
 def permute_backward(h: Handle, cfg: Config, dx_perm, flat_to_perm, dx, dx_add=None, stream=None):
     """Gradient of permute's row gather: dx[t] = sum_k dx_perm[flat_to_perm[t*K+k]] (+ dx_add[t]), bf16."""
-    what = "moe_permute_backward"
-    T, K, H = cfg.T, cfg.K, cfg.H
-    _check(load().moe_permute_backward(
-        h.ptr, ctypes.byref(cfg), _arg(h, what, "dx_perm", dx_perm, _BF16, T * K * H),
-        _arg(h, what, "flat_to_perm", flat_to_perm, _I32, T * K), _arg(h, what, "dx_add", dx_add, _BF16, T * H, True),
-        _arg(h, what, "dx", dx, _BF16, T * H), _stream_of(h, stream)), what)
+    _native().permute_backward(h.address, h.device, cfg, dx_perm, flat_to_perm, dx, dx_add, stream)
 
 
 def grouped_gemm_backward_workspace_size(rows: int, H: int, I: int, dtype: int = MOE_BF16, num_groups: int = 1) -> int:
@@ -469,19 +427,8 @@ def grouped_swiglu_backward(h: Handle, a, dy, offsets, w_gate, w_up, w_down, da,
                             num_groups: int, H: int, I: int, dtype: int = MOE_BF16, stream=None):
     """Gradient of grouped_swiglu_gemm (bf16): da [rows, H] (or None) and dw_gate, dw_up, dw_down in the weights'
     shapes (or None, all three), from the forward's inputs and dy [rows, H], all bf16."""
-    what = "moe_grouped_swiglu_backward"
-    rows, cols = _rows_cols(what, "a", a)
-    if cols != H:
-        raise MoEError(MOE_ERR_INVALID_ARG, f"{what}: a has {cols} columns, H is {H}")
-    n, m = rows * H, num_groups * H * I
-    _check(load().moe_grouped_swiglu_backward(
-        h.ptr, int(num_groups), rows, int(H), int(I), int(dtype), _arg(h, what, "a", a, _BF16, n),
-        _arg(h, what, "dy", dy, _BF16, n), _arg(h, what, "offsets", offsets, _I32, num_groups + 1, num_groups == 1),
-        _arg(h, what, "w_gate", w_gate, _BF16, m), _arg(h, what, "w_up", w_up, _BF16, m),
-        _arg(h, what, "w_down", w_down, _BF16, m), _arg(h, what, "da", da, _BF16, n, True),
-        _arg(h, what, "dw_gate", dw_gate, _BF16, m, True), _arg(h, what, "dw_up", dw_up, _BF16, m, True),
-        _arg(h, what, "dw_down", dw_down, _BF16, m, True), _p(ws), ws.numel() * ws.element_size(), _stream_of(h, stream)),
-        what)
+    _native().grouped_swiglu_backward(h.address, h.device, a, dy, offsets, w_gate, w_up, w_down, da, dw_gate, dw_up,
+                                      dw_down, ws, num_groups, H, I, dtype, stream)
 
 
 def make_weights(w: dict) -> Weights:
