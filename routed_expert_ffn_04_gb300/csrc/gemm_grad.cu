@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();  // 0: leader
   const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
   const int G = p.k.G;
-  allow_next_launch();
+  if (MODE != kDX) allow_next_launch();
 
   // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
   fill_row_start(p.k, row_start, threadIdx.x, kThreads);
@@ -223,9 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
-  // Up to here nothing was read that the launch before this one writes (its
-  // blocks may still be running: programmatic dependent launch).
-  wait_for_previous_launch();
+  // Blocks of the launch before may still be running (programmatic dependent
+  // launch): each role waits for its end where it first needs its results, or
+  // where it would start to wait for a role that does. GU's operands do not
+  // come from Q, only its epilogue's q does: two tiles of MMAs fit before it.
+  // In DX a ring of weights does. Every CTA waits, so a launch's end is the end
+  // of all before it. (128 tokens, 2 of 8 experts, H = 1024, I = 512: 44.4 us
+  // when all waited here and the weight gradients for DX, 40.0 so.)
   if (MODE == kQ && blockIdx.x == 0 && threadIdx.x == 0) *p.odd = 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[G];
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Tile mine = {};
     for (int i = 0; ok && i < my_tiles; ++i) {
+      if (MODE == kDX ? i == 0 && !is_a : MODE == kGU && i == 2) wait_for_previous_launch();
       if ((i & 31) == 0) mine = decode(i + lane);
       const int g = at_tile(mine.g, i), wt = at_tile(mine.wt, i), half = at_tile(mine.N, i) >> 1;
       const int row = at_tile(MODE == kDX ? mine.prow : mine.row, i) + (int)rank * half;
@@ -277,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // then one of 32 and one of 16 by warp 7.
       const bool b64 = half >= 64, b128 = half == 128, b32 = (half & 32) != 0, b16 = (half & 16) != 0;
       for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (MODE == kDX && is_a && i * p.num_kb + kb == kStages) wait_for_previous_launch();
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
                                                        MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
           ok = false;
@@ -336,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, issued = false;
       int n32 = 0;
       for (int i = 0; ok && i < my_tiles; ++i) {
+        if (i == (MODE == kGU ? 2 : 0)) wait_for_previous_launch();
         if ((i & 31) == 0) n32 = decode(i + lane).N;
         const int N = at_tile(n32, i);
         const int acc = i & 1;
@@ -382,6 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int partners = 1 + (q & 1) + 2 * half;  // named barrier of warps q and q ^ 2
     Tile mine = {};
     float odd = 0.0f;  // GU: turns NaN where a gate or q is not finite
+    wait_for_previous_launch();
+    // The weight gradients need GU's results, not DX's: they may start now.
+    if (MODE == kDX) allow_next_launch();
     for (int i = 0; i < my_tiles; ++i) {
       if ((i & 31) == 0) mine = decode(i + lane);
       const int wt = at_tile(mine.wt, i), count = at_tile(mine.count, i), N = at_tile(mine.N, i);

@@ -77,6 +77,7 @@ struct DwParams {
   KParams k;  // offsets, G, rows, status, limit_ns
   int H, I;
   int stages;
+  bool after_dx;               // the launch before is DX, else GU
   const int* odd;              // not 0: a row of a or dy may hold an infinity or NaN
   // Strips: [0] of groups longer than the ring, one tile each; [1] of the others.
   struct Cut {
@@ -193,8 +194,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
-  // Up to here nothing was read that the launch before this one writes.
-  wait_for_previous_launch();
+  // DX lets this launch start once GU is done, whose results are all that is
+  // read here; its own end is waited for last, so that this launch's end is the
+  // end of both.
+  if (p.after_dx) {
+    __threadfence();
+    asm volatile("fence.proxy.async;" ::: "memory");
+  } else {
+    wait_for_previous_launch();
+  }
   const bool careful = *static_cast<const volatile int*>(p.odd) != 0;
   const uint32_t tmem_base = *tmem_slot;
   const int n_long = *longs, long_strips = n_long * p.cut[0].per_group;
@@ -458,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Both CTAs arrive here only when their roles are done (every wait is
   // bounded), so neither frees TMEM or leaves while the other may still touch
   // its shared memory or barriers.
+  if (p.after_dx) wait_for_previous_launch();
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
@@ -496,6 +505,7 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s)
   p.H = H;
   p.I = I;
   p.stages = ring_stages(G);
+  p.after_dx = a.da != nullptr;
   p.odd = a.odd;
   auto recip = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d) : 0xFFFFFFFFu; };
   const int tiles_h = (H + 255) / 256, tiles_i = (I + 255) / 256;
