@@ -38,8 +38,8 @@
 //
 // Roles per CTA (12 warps, each walking its tiles in step with warp-uniform
 // values and one elected lane issuing): 0 loads A's boxes and arms the stage,
-// 6 loads B's boxes of 64 rows and 7 its lower ones (a box costs its issuer 100
-// to 150 cycles, a stage's MMAs take 330 at 341 rows per group), 1 (of the
+// 6 and 7 load B's (a box costs its issuer 100 to 150 cycles, a stage's MMAs
+// take 330 at 341 rows per group), 1 (of the
 // even CTA, the leader) issues the pair's MMAs, 2-5 and 8-11 are the epilogue,
 // 32 accumulator lanes and every other block of 32 tokens each. Both CTAs'
 // copies of a stage complete on the leader's full barrier. In GU lanes 0-63
@@ -93,11 +93,13 @@ struct GradParams {
   __nv_bfloat16* da;      // [rows, H]
 };
 
-// a0 / a1: the weights; b0 / b1: the rows, in boxes of 64, 32 and 16 rows.
+// a0 / a1: the weights; b0 / b1: the rows, in boxes of 64, 32, 16 and 8 rows.
 // Q: Wd; dy. GU: Wg, Wu; a. DX: Wg, Wu; dg, du.
 struct GradMaps {
-  CUtensorMap a0, a1, b0[3], b1[3];
+  CUtensorMap a0, a1, b0[4], b1[4];
 };
+__device__ __forceinline__ int pow2_below(int n) { return 1 << (31 - __clz(n - 1)); }  // the largest, n >= 2
+__device__ __forceinline__ int box_map(int rows) { return __clz(rows) - 25; }
 
 // Tokens of chunk c of a group of n rows: [first, first + count), and the MMA's
 // N. (A chunk is at most 256, so the last one is never empty.)
@@ -278,9 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((i & 31) == 0) mine = decode(i + lane);
       const int g = at_tile(mine.g, i), wt = at_tile(mine.wt, i), half = at_tile(mine.N, i) >> 1;
       const int row = at_tile(MODE == kDX ? mine.prow : mine.row, i) + (int)rank * half;
-      // B's `half` rows (a multiple of 16, at most 128): boxes of 64 by warp 6,
-      // then one of 32 and one of 16 by warp 7.
-      const bool b64 = half >= 64, b128 = half == 128, b32 = (half & 32) != 0, b16 = (half & 16) != 0;
+      // B's `half` rows (a multiple of 16, at most 128): the largest power of
+      // two below that by warp 6, the rest by warp 7. Both have a box in every
+      // stage: a warp without one could fall behind by two rounds of the ring,
+      // where a wait by parity would miss the phase that it waits for.
+      const int most = pow2_below(half), rest = half - most, second_box = pow2_below(rest + 1);
+      const int at = warp == 6 ? 0 : most, box = warp == 6 ? most : second_box;
+      const int extra = warp == 6 ? 0 : rest - second_box;  // 48 = 32 + 16
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (MODE == kDX && is_a && i * p.num_kb + kb == kStages) wait_for_previous_launch();
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
@@ -309,14 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
             const CUtensorMap* map = second ? m.b1 : m.b0;
-            if (warp == 6) {
-              if (b64) tma_load_2d_pair(sb, map, bar, kx, row);
-              if (b128) tma_load_2d_pair(sb + 64 * 128, map, bar, kx, row + 64);
-            } else {
-              const int at = half & 64;
-              if (b32) tma_load_2d_pair(sb + at * 128, map + 1, bar, kx, row + at);
-              if (b16) tma_load_2d_pair(sb + (half - 16) * 128, map + 2, bar, kx, row + half - 16);
-            }
+            tma_load_2d_pair(sb + at * 128, map + box_map(box), bar, kx, row + at);
+            if (extra) tma_load_2d_pair(sb + (at + box) * 128, map + box_map(extra), bar, kx, row + at + box);
           }
         }
         __syncwarp();
@@ -557,9 +557,9 @@ cudaError_t set_smem() {
   return cudaFuncSetAttribute(grouped_grad_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
 }
 
-// The maps of a [rows, cols] tensor in boxes of 64, 32 and 16 rows.
-bool row_maps(CUtensorMap (&m)[3], const void* ptr, uint64_t cols, uint64_t rows) {
-  for (int i = 0; i < 3; ++i)
+// The maps of a [rows, cols] tensor in boxes of 64, 32, 16 and 8 rows.
+bool row_maps(CUtensorMap (&m)[4], const void* ptr, uint64_t cols, uint64_t rows) {
+  for (int i = 0; i < 4; ++i)
     if (!make_tmap_bf16(&m[i], ptr, cols, rows, 64u >> i)) return false;
   return true;
 }

@@ -193,3 +193,15 @@ def test_refusals(handle):
             call(**kw)
         assert e.value.status == st, kw
     assert handle.device_status() == 0
+
+
+def test_chunks_of_every_height_over_many_launches(handle):
+    """Every multiple of 32 rows as a chunk (alone and beside a larger one), long reductions, many launches: each of the
+    roles that fill a stage has to have a part in it, or it may fall a ring behind."""
+    p = _problem([32, 64, 96, 128, 160, 192, 224, 256, 288, 512, 545, 128, 128], 2048, 1024)
+    o = _run(handle, p)
+    _against_formulas(p, o)
+    for _ in range(40):
+        again = _run(handle, p)
+        for k in o:
+            assert torch.equal(o[k], again[k]), k
