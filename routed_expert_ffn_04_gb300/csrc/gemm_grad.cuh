@@ -94,8 +94,6 @@ __device__ __forceinline__ void stage_bf16_block(uint32_t taddr, uint8_t* stg, i
   tmem_ld_32x32b_x32(taddr, v);
   tmem_ld_32x32b_x32(taddr + 32, u);
   tmem_ld_wait();
-  if (lane == 0) bulk_wait_group_read0();  // the last store has read the buffer
-  __syncwarp();
   uint8_t* row = stg + lane * 128;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -22,15 +22,18 @@
 // pair), to keep the pairs' shares even.
 //
 // Measured at 192 experts x 341 rows, H = 4096, I = 1536 (short runs): one SM
-// per tile 2.45 ms, pairs 2.30, tiles decoded by lanes 2.22, no clearing 1.96.
+// per tile 2.45 ms, pairs 2.30, tiles decoded by lanes 2.22, no clearing 1.96,
+// strips 1.89, stores from the warps instead of by TMA 1.83 (8.9 GB of HBM
+// traffic: 1.32 ms at a copy's rate; 2.47 TFLOP: 1.33 ms at the burst rate of
+// a large bf16 product).
 //
 // A group's rows end anywhere; the MMA runs in steps of 16 rows. One operand of
 // each product is h, dg or du, whose groups are followed by zero rows up to a
 // multiple of 16, so whatever finite rows of the next group the other operand
 // holds there adds nothing. A zero times an infinity or NaN would: when the
 // launch before has met one (p.odd), the rows past the group's end are
-// cleared in shared memory first (the careful way: 0.3 to 0.5 ms more at the
-// size below, as every tile's last stage waits for it). A group without rows
+// cleared in shared memory first (the careful way: 0.26 ms more at the
+// size above, as every tile's last stage waits for it). A group without rows
 // gives zero gradients.
 //
 // Roles per CTA (12 warps): 0 loads A's boxes and arms the stage; 6 loads B's;
@@ -76,6 +79,7 @@ static_assert(smem_bytes(kMaxGroups, kMaxStages - 1) <= kMaxSmem, "shared memory
 struct DwParams {
   KParams k;  // offsets, G, rows, status, limit_ns
   int H, I;
+  __nv_bfloat16* dw[3];  // dWd, dWg, dWu
   int stages;
   bool after_dx;               // the launch before is DX, else GU
   const int* odd;              // not 0: a row of a or dy may hold an infinity or NaN
@@ -93,7 +97,6 @@ struct DwParams {
 // rows): a group's last stage takes the lowest that covers its rows.
 struct DwMaps {
   CUtensorMap dy[3], dg[3], du[3], h[3], a[3];
-  CUtensorMap dw[3];  // dWd, dWg, dWu
 };
 
 // Arrive on a barrier of another CTA of the cluster, releasing this CTA's
@@ -428,27 +431,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256 + half * 128);
-        // 32 x 64 blocks by TMA. (Stores from registers are 32 lines per warp
-        // instruction, and the queue they form delays the loads: one SM per tile
-        // 2.70 ms against 2.45.) H and I are multiples of 64, so a block is all
-        // inside the group's matrix or all outside.
+        // 32 x 64 blocks through the warp's buffer, which is free again as soon
+        // as it has been read. (By TMA from that buffer a block's store kept it
+        // busy for as long as a short tile's whole MMAs: 2048 tokens, 8 of 64
+        // experts, H = 2048, I = 768, uneven loads 199 us against 167. Stores
+        // straight from the accumulators' lanes are 32 lines per instruction,
+        // and the queue they form delays the loads.) H and I are multiples of
+        // 64, so a block is all inside the group's matrix or all outside.
         const int M = which == 0 ? p.H : p.I, N = which == 0 ? p.I : p.H;
         if (m0 < M) {
 #pragma unroll 1
           for (int c = 0; c < 128 && n0 + c < N; c += 64) {
+            // Four rows of 128 bytes per instruction.
+            __nv_bfloat16* at = p.dw[which] + ((size_t)g * M + m0 + (lane >> 3)) * N + n0 + c + (lane & 7) * 8;
             if (empty) {
-              if (lane == 0) bulk_wait_group_read0();
-              __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stg + lane * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at + (size_t)(4 * j) * N) = make_uint4(0, 0, 0, 0);
             } else {
               stage_bf16_block(tb + c, stg, lane);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&m.dw[which], smem_u32(stg), n0 + c, g * M + m0);
-              bulk_commit_group();
+              __syncwarp();
+              uint4 v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int row = 4 * j + (lane >> 3);
+                v[j] = *reinterpret_cast<const uint4*>(stg + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at + (size_t)(4 * j) * N) = v[j];
             }
           }
         }
@@ -460,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_group0();  // this warp's bulk stores are complete
   }
 
   // Both CTAs arrive here only when their roles are done (every wait is
@@ -484,7 +493,7 @@ cudaError_t gemm_grad_dw_prepare_device() {
 
 cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s) {
   const int G = a.offsets ? a.G : 1, H = a.H, I = a.I;
-  const uint64_t R = a.rows, P = padded_rows(a.rows, G), GI = (uint64_t)G * I, GH = (uint64_t)G * H;
+  const uint64_t R = a.rows, P = padded_rows(a.rows, G);
   DwMaps m = {};
   for (int i = 0; i < 3; ++i) {
     const uint32_t box = 64u >> i;
@@ -493,9 +502,6 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s)
         !make_tmap_bf16(&m.a[i], a.a, H, R, box))
       return cudaErrorInvalidValue;
   }
-  if (!make_tmap_bf16(&m.dw[0], a.dw_down, I, GH, 32) || !make_tmap_bf16(&m.dw[1], a.dw_gate, H, GI, 32) ||
-      !make_tmap_bf16(&m.dw[2], a.dw_up, H, GI, 32))
-    return cudaErrorInvalidValue;
   DwParams p = {};
   p.k.offsets = a.offsets;
   p.k.G = G;
@@ -504,6 +510,8 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s)
   p.k.limit_ns = a.wait_limit_ns;
   p.H = H;
   p.I = I;
+  void* dw[] = {a.dw_down, a.dw_gate, a.dw_up};
+  for (int i = 0; i < 3; ++i) p.dw[i] = static_cast<__nv_bfloat16*>(dw[i]);
   p.stages = ring_stages(G);
   p.after_dx = a.da != nullptr;
   p.odd = a.odd;
