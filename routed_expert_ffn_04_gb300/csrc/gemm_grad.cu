@@ -542,10 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // row_chunks: an upper bound on the groups' chunks.
 template <int MODE>
-cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long row_chunks, int num_sms, cudaStream_t s) {
+int pairs_of(const GradParams& p, long long row_chunks, int num_sms) {
   constexpr int kTileM = MODE == kGU ? 128 : 256;
   const long long tiles = row_chunks * ((p.k.N + kTileM - 1) / kTileM);
-  const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  return (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+}
+
+template <int MODE>
+cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long row_chunks, int num_sms, cudaStream_t s) {
+  const int pairs = pairs_of<MODE>(p, row_chunks, num_sms);
   if (pairs < 1) return cudaErrorInvalidValue;
   // Q starts after everything before it; the others' prologues may overlap the
   // end of the launch before them (its offsets were there before Q).
@@ -618,6 +623,7 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
     p.num_kb = H / kBK;
     e = run_mode<kGU>(m, p, row_chunks, a.num_sms, s);
   }
+  int dx_pairs = 0;
   if (e == cudaSuccess && a.da) {
     GradMaps m = {};
     if (!make_tmap_bf16(&m.a0, a.w_gate, H, GI, 64) || !make_tmap_bf16(&m.a1, a.w_up, H, GI, 64) ||
@@ -625,9 +631,10 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
       return cudaErrorInvalidValue;
     p.k.N = H;
     p.num_kb = 2 * (I / kBK);
+    dx_pairs = pairs_of<kDX>(p, row_chunks, a.num_sms);
     e = run_mode<kDX>(m, p, row_chunks, a.num_sms, s);
   }
-  if (e == cudaSuccess && want_dw) e = launch_grouped_weight_grad(a, s);
+  if (e == cudaSuccess && want_dw) e = launch_grouped_weight_grad(a, dx_pairs, s);
   return e;
 }
 

@@ -257,7 +257,7 @@ struct GroupedGradArgs {
 cudaError_t gemm_grad_prepare_device();
 // The weight gradients from a, dy, h, dg, du (gemm_grad_dw.cu).
 cudaError_t gemm_grad_dw_prepare_device();
-cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, int dx_pairs, cudaStream_t s);
 cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_t s);
 
 // ---- MX quantiser (mxquant.cu)
