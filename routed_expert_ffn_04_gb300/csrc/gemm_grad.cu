@@ -47,6 +47,15 @@
 // quarters q and q + 2 exchange half of each block through shared memory and
 // finish 16 tokens each.
 //
+// Measured at 192 experts x 341 rows, H = 4096, I = 1536 (short runs): Q 0.63,
+// GU 1.24, DX 1.18 ms. Alone, their HBM traffic (3.4, 6.4 and 5.8 GB, mostly
+// the weights, once per launch) takes 0.50, 0.94 and 0.85 ms at a copy's rate,
+// and their MMAs 0.38, 0.75 and 0.75. Tiles of two chunks that share a stage of
+// weights read 29% less from L2, but leave no accumulator for the next tile
+// while the epilogue reads theirs: 0.60, 1.29 and 1.08 ms, and 7% more for the
+// pass at uneven loads. A ring of more and smaller stages where the chunks are
+// short changed nothing.
+//
 // Every wait is bounded; on expiry the CTA records an error code in the status
 // word, lets its in-flight copies and MMAs end, frees TMEM and exits.
 #include <cuda.h>

@@ -223,7 +223,9 @@ __global__ void add_rmsnorm_any_kernel(int H, const __nv_bfloat16* x, const RT* 
 // (cp.async) and reads back only what it copied, twice: for the sum and for
 // the outputs. A block is several groups of threads, each with a row of its
 // own and a barrier of its own (a group of 32 needs none); 32 columns per
-// thread keep the groups small and the sum's exchange cheap.
+// thread keep the groups small and the sum's exchange cheap. 8192 x 4096 in
+// bf16: 45 us (5.9 TB/s; 40 us at a copy's rate), the rows of the last round
+// being 13.5 per group, and 3 to 5 us more until the partial sums are added.
 constexpr int kPieces = 3;
 template <typename RT, int NV>
 struct BwdShape {
