@@ -65,11 +65,12 @@ def load(build_if_missing: bool = False):
     global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
+    missing = [p for p in (LIB_PATH, _build.BINDING) if not os.path.exists(p)]
+    if missing:
         if build_if_missing:
             _build.build()
         else:
-            raise ImportError(f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+            raise ImportError(f"{missing[0]} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     PS = ctypes.POINTER(ctypes.c_size_t)
