@@ -122,6 +122,7 @@ MOE_API moe_status_t moe_combine_backward(moe_handle_t h, const moe_config_t* cf
   a.dy_perm = dy_perm;
   a.dtopk_w = dtopk_w;
   a.dlogits = dlogits;
+  a.num_sms = handle_num_sms(h);
   a.status = handle_status_word(h);
   return status_of(launch_combine_backward(a, static_cast<cudaStream_t>(stream)));
 }

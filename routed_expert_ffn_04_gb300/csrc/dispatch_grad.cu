@@ -89,13 +89,21 @@ __device__ __forceinline__ void route_grad_warp(SlotLogit s, float dw, int K, fl
 // the dy row and keeps the dot product; nothing is exchanged until the end, so
 // every warp's loads stay in flight. dout[t] comes from L1 for the token's
 // other warps. A block has one token's slots, or several tokens' when a token
-// has few. 8192 tokens x 8 slots x 4096: 250 us (6.73 TB/s, a copy's rate); before the
-// routing operands were loaded up front 257, with four runs of 256 columns per
-// iteration 281 (fewer blocks fit an SM), and one block per token whose threads
-// hold all eight rows' columns 367.
-constexpr int kUnroll = 2;     // 256-column runs a warp has in flight
+// has few. (One block per token whose threads hold all eight rows' columns took
+// 367 us at 8192 tokens x 8 slots x 4096.)
+//
+// Runs of 256 columns that a warp has in flight: eight where one wave of blocks
+// holds everything, since a row's round trips are then the whole time, and in
+// many waves of long rows; else two, which leaves room for twice the warps.
+//   us for two / eight runs (8 slots, operands from HBM)
+//   H       61 tokens     152            304            608            8192
+//   512     4.1 / 4.2     4.5 / 4.6      5.3 / 5.4      6.3 / 8.6
+//   1024    5.0 / 4.6     5.8 / 5.1      6.7 / 6.3      8.5 / 10.4     74 / 97
+//   4096    9.3 / 6.9     11.0 / 8.9     14.1 / 13.4    23.2 / 23.7    251 / 248
+// 248 us are 6.79 TB/s, a copy's rate.
 constexpr int kMaxWarps = 16;  // per block
 
+template <int kUnroll>  // 256-column runs a warp has in flight
 __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
     const __nv_bfloat16* __restrict__ dout, const float* __restrict__ y, const float* __restrict__ topk_w,
     const int32_t* __restrict__ f2p, int T, int K, int H, int E, int slot_warps, int tokens, float scaling,
@@ -239,7 +247,11 @@ cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
   const int slot_warps = a.K < kMaxWarps ? a.K : kMaxWarps;
   const int tokens = slot_warps <= 4 ? 8 / slot_warps : 1;
-  combine_bwd_kernel<<<(a.T + tokens - 1) / tokens, 32 * slot_warps * tokens, 0, s>>>(
+  const int grid = (a.T + tokens - 1) / tokens;
+  const int threads = 32 * slot_warps * tokens;
+  const double waves = (double)grid * threads / (512.0 * a.num_sms);  // of the wide form: 512 threads per SM
+  const bool wide = waves <= 1 ? a.H > 512 : waves >= 8 && a.H >= 4096;
+  (wide ? combine_bwd_kernel<8> : combine_bwd_kernel<2>)<<<grid, threads, 0, s>>>(
       static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w, a.flat_to_perm, a.T, a.K, a.H, a.E,
       slot_warps, tokens, a.scaling, a.route_norm, a.topk_idx, a.logits, static_cast<__nv_bfloat16*>(a.dy_perm),
       a.dtopk_w, a.dlogits, a.status);

@@ -222,6 +222,7 @@ struct CombineGradArgs {
   void* dy_perm;                // [T*K, H] bf16
   float* dtopk_w;               // [T, K]
   float* dlogits;               // [T, E], or nullptr
+  int num_sms;
   int* status;
 };
 cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s);
