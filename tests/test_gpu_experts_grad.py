@@ -205,3 +205,25 @@ def test_chunks_of_every_height_over_many_launches(handle):
         again = _run(handle, p)
         for k in o:
             assert torch.equal(o[k], again[k]), k
+
+
+def test_two_streams_at_once(handle):
+    """Chains of launches on two streams, with workspaces of their own, share the GPU and keep their results."""
+    ps = [_problem([100, 0, 300, 41], 512, 256, seed=1), _problem([31, 64, 7], 1024, 192, seed=2)]
+    want = [_run(handle, p) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    bufs = []
+    for p in ps:
+        size = moe.grouped_gemm_backward_workspace_size(p["rows"], p["H"], p["I"], num_groups=p["G"])
+        bufs.append([torch.empty_like(p[k]) for k in ("a", "wg", "wu", "wd")] +
+                    [torch.empty(size, dtype=torch.uint8, device="cuda")])
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for p, b, s in zip(ps, bufs, streams):
+            moe.grouped_swiglu_backward(handle, p["a"], p["dy"], p["offsets"], p["wg"], p["wu"], p["wd"], *b,
+                                        num_groups=p["G"], H=p["H"], I=p["I"], stream=s)
+    torch.cuda.synchronize()
+    assert handle.device_status() == 0
+    for w, b in zip(want, bufs):
+        for k, t in zip(("da", "dg", "du", "dd"), b):
+            assert torch.equal(w[k], t), k
