@@ -425,16 +425,17 @@ __global__ void add_rmsnorm_dw_any_kernel(long long rows, int H, const __nv_bflo
 }
 
 // dw[c] = sum of part[0 .. n-1][c] in a fixed order: 32 columns per block, 32
-// threads per column over every 32nd partial, then those 32 in order.
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restrict__ part, int n, int H,
-                                                            float* __restrict__ dw) {
+// threads per column over every 32nd partial, then those 32 in order. (`part` is
+// written while this kernel may already run: no read-only loads of it, which
+// the compiler may move up past the wait.)
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int n, int H, float* dw) {
   __shared__ float s[32][33];
   const int x = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   wait_for_previous_launch();
   float t = 0.0f;
   if (c < H) {
 #pragma unroll 4
-    for (int i = k; i < n; i += 32) t += part[(size_t)i * H + c];
+    for (int i = k; i < n; i += 32) t += __ldcg(part + (size_t)i * H + c);
   }
   s[k][x] = t;
   __syncthreads();
