@@ -21,6 +21,7 @@
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "launch.cuh"
 
 namespace moe {
 namespace {
@@ -52,7 +53,7 @@ struct SlotLogit {
   int e;
   float l;
 };
-__device__ __forceinline__ SlotLogit load_slot(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+__device__ __forceinline__ SlotLogit load_slot(const float* logits, const int32_t* idx,
                                                int E, int K, int* status) {
   const int lane = threadIdx.x & 31;
   SlotLogit s = {-1, 0.0f};
@@ -105,10 +106,11 @@ constexpr int kMaxWarps = 16;  // per block
 
 template <int kUnroll>  // 256-column runs a warp has in flight
 __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
-    const __nv_bfloat16* __restrict__ dout, const float* __restrict__ y, const float* __restrict__ topk_w,
-    const int32_t* __restrict__ f2p, int T, int K, int H, int E, int slot_warps, int tokens, float scaling,
-    int route_norm, const int32_t* __restrict__ topk_idx, const float* __restrict__ logits,
-    __nv_bfloat16* __restrict__ dy, float* __restrict__ dtopk_w, float* __restrict__ dlogits, int* status) {
+    const __nv_bfloat16* dout, const float* y, const float* topk_w, const int32_t* f2p, int T, int K, int H, int E,
+    int slot_warps, int tokens, float scaling, int route_norm, const int32_t* topk_idx, const float* logits,
+    __nv_bfloat16* dy, float* dtopk_w, float* dlogits, int* status) {
+  allow_next_launch();
+  wait_for_previous_launch();
   __shared__ float dots[kMaxK];  // [token][slot]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sw = warp % slot_warps, tok = warp / slot_warps;
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
           for (int u = 0; u < kUnroll; ++u) {
             const int cc = c + u * 32;
             if (cc < H8) {
-              d[u] = __ldg(drow + cc);
+              d[u] = drow[cc];
               v[u][0] = __ldcs(yr + 2 * cc);
               v[u][1] = __ldcs(yr + 2 * cc + 1);
             }
@@ -196,11 +198,12 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
 // dx: a work unit is one token's chunk of 8 * blockDim columns; a thread adds
 // its 8 columns of the K rows (batches of 8 loads in flight), k ascending.
 // 8192 tokens x 8 rows x 4096 with dx_add: 99.6 us (6.74 TB/s, a copy's rate).
-__global__ void __launch_bounds__(256) permute_bwd_kernel(const __nv_bfloat16* __restrict__ dxp,
-                                                          const int32_t* __restrict__ f2p, int T, int K, int H,
-                                                          int chunks, const __nv_bfloat16* add, __nv_bfloat16* dx,
-                                                          int* status) {
+__global__ void __launch_bounds__(256) permute_bwd_kernel(const __nv_bfloat16* dxp, const int32_t* f2p, int T, int K,
+                                                          int H, int chunks, const __nv_bfloat16* add,
+                                                          __nv_bfloat16* dx, int* status) {
   __shared__ int32_t sp[kMaxK];
+  allow_next_launch();
+  wait_for_previous_launch();
   const long long u = blockIdx.x;
   const int t = (int)(u / chunks);
   const int c = (int)(u - (long long)t * chunks) * blockDim.x + threadIdx.x;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(256) permute_bwd_kernel(const __nv_bfloat16* _
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int p = k0 + j < K ? sp[k0 + j] : -1;
-      v[j] = p >= 0 ? __ldg(reinterpret_cast<const uint4*>(dxp + (size_t)p * H) + c) : make_uint4(0u, 0u, 0u, 0u);
+      v[j] = p >= 0 ? reinterpret_cast<const uint4*>(dxp + (size_t)p * H)[c] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -251,11 +254,10 @@ cudaError_t launch_combine_backward(const CombineGradArgs& a, cudaStream_t s) {
   const int threads = 32 * slot_warps * tokens;
   const double waves = (double)grid * threads / (512.0 * a.num_sms);  // of the wide form: 512 threads per SM
   const bool wide = waves <= 1 ? a.H > 512 : waves >= 8 && a.H >= 4096;
-  (wide ? combine_bwd_kernel<8> : combine_bwd_kernel<2>)<<<grid, threads, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w, a.flat_to_perm, a.T, a.K, a.H, a.E,
-      slot_warps, tokens, a.scaling, a.route_norm, a.topk_idx, a.logits, static_cast<__nv_bfloat16*>(a.dy_perm),
-      a.dtopk_w, a.dlogits, a.status);
-  return cudaGetLastError();
+  return launch_dependent(wide ? combine_bwd_kernel<8> : combine_bwd_kernel<2>, grid, threads, 0, s, true, 1,
+                          static_cast<const __nv_bfloat16*>(a.dout), a.y_perm, a.topk_w, a.flat_to_perm, a.T, a.K, a.H,
+                          a.E, slot_warps, tokens, a.scaling, a.route_norm, a.topk_idx, a.logits,
+                          static_cast<__nv_bfloat16*>(a.dy_perm), a.dtopk_w, a.dlogits, a.status);
 }
 
 cudaError_t launch_route_backward(const float* logits, const int32_t* topk_idx, const float* dtopk_w, int T, int E,
@@ -273,10 +275,9 @@ cudaError_t launch_permute_backward(const void* dx_perm, const int32_t* flat_to_
   const int chunks = (H / 8 + threads - 1) / threads;
   const long long grid = (long long)T * chunks;
   if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-  permute_bwd_kernel<<<(unsigned)grid, threads, 0, s>>>(static_cast<const __nv_bfloat16*>(dx_perm), flat_to_perm, T, K,
-                                                        H, chunks, static_cast<const __nv_bfloat16*>(dx_add),
-                                                        static_cast<__nv_bfloat16*>(dx), status);
-  return cudaGetLastError();
+  return launch_dependent(permute_bwd_kernel, (int)grid, threads, 0, s, true, 1,
+                          static_cast<const __nv_bfloat16*>(dx_perm), flat_to_perm, T, K, H, chunks,
+                          static_cast<const __nv_bfloat16*>(dx_add), static_cast<__nv_bfloat16*>(dx), status);
 }
 
 }  // namespace moe

@@ -124,10 +124,11 @@ __device__ __forceinline__ uint2 mx_block(const float (&f)[8], int& scale_code) 
 // ------------------------------------------------------------------ forward
 template <typename RT, int NV, bool WARP_ROW, bool MX>
 __global__ void __launch_bounds__(WARP_ROW ? 32 * kWarpRows : 512) add_rmsnorm_kernel(long long rows, int H, const __nv_bfloat16* x,
-                                   const RT* residual, const __nv_bfloat16* __restrict__ w, float eps, RT* h_out, __nv_bfloat16* out,
-                                   uint8_t* __restrict__ q, uint8_t* __restrict__ q_scale,
-                                   float* __restrict__ rstd_out) {
+                                   const RT* residual, const __nv_bfloat16* w, float eps, RT* h_out, __nv_bfloat16* out,
+                                   uint8_t* q, uint8_t* q_scale, float* rstd_out) {
   __shared__ float part[32];
+  allow_next_launch();
+  wait_for_previous_launch();
   const int tid = WARP_ROW ? (threadIdx.x & 31) : threadIdx.x;
   const int nt = WARP_ROW ? 32 : blockDim.x;
   const long long row = WARP_ROW ? (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : (long long)blockIdx.x;
@@ -253,8 +254,8 @@ __device__ __forceinline__ void copy16(void* smem, const void* g) {
 template <typename RT, int NV, int STAGES>
 __global__ void __launch_bounds__(512)
     add_rmsnorm_bwd_kernel(long long rows, int H, int nt, const __nv_bfloat16* dout, const RT* dh_in, const RT* h,
-                           const __nv_bfloat16* __restrict__ w, const float* __restrict__ rstd, RT* dh,
-                           __nv_bfloat16* dx, float* __restrict__ part_dw) {
+                           const __nv_bfloat16* w, const float* rstd, RT* dh, __nv_bfloat16* dx, float* part_dw) {
+  wait_for_previous_launch();
   using Sh = BwdShape<RT, NV>;
   __shared__ float part[2][16];  // [buffer][warp of the block]
   extern __shared__ uint4 ring[];  // [stage][vector][piece][thread]; at the end the groups' dw
@@ -431,6 +432,7 @@ __global__ void add_rmsnorm_dw_any_kernel(long long rows, int H, const __nv_bflo
 __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int n, int H, float* dw) {
   __shared__ float s[32][33];
   const int x = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+  allow_next_launch();
   wait_for_previous_launch();
   float t = 0.0f;
   if (c < H) {
@@ -468,9 +470,9 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t s) {
     add_rmsnorm_any_kernel<RT><<<(unsigned)a.rows, 256, 0, s>>>(a.H, x, r, w, a.eps, ho, out, a.rstd);
     return cudaGetLastError();
   }
-#define MOE_NORM(NV, WR, GRID, THREADS)                                                                           \
-  add_rmsnorm_kernel<RT, NV, WR, MX><<<(unsigned)(GRID), (THREADS), 0, s>>>(a.rows, a.H, x, r, w, a.eps, ho, out, \
-                                                                          a.q, a.q_scale, a.rstd)
+#define MOE_NORM(NV, WR, GRID, THREADS)                                                                              \
+  return launch_dependent(add_rmsnorm_kernel<RT, NV, WR, MX>, (int)(GRID), (THREADS), 0, s, true, 1, a.rows, a.H, x, r, \
+                          w, a.eps, ho, out, a.q, a.q_scale, a.rstd)
   if (a.H <= kWarpRowCols) {
     const long long grid = (a.rows + kWarpRows - 1) / kWarpRows;
     if (a.H <= 256) MOE_NORM(1, true, grid, 32 * kWarpRows);
@@ -482,7 +484,6 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t s) {
     MOE_NORM(4, false, a.rows, row_threads(a.H, 4));
   }
 #undef MOE_NORM
-  return cudaGetLastError();
 }
 
 template <typename RT>
@@ -495,17 +496,19 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
   auto* dx = static_cast<__nv_bfloat16*>(a.dx);
   float* part = a.dweight ? a.partials : nullptr;
   const int n = norm_grad_blocks(a.rows, a.H, a.res_f32);
+  cudaError_t e = cudaSuccess;
   if (a.H % 8) {
     if (part) add_rmsnorm_dw_any_kernel<RT><<<n, 256, 0, s>>>(a.rows, a.H, dout, h, a.rstd, part);
     add_rmsnorm_bwd_any_kernel<RT><<<n, 256, 0, s>>>(a.rows, a.H, dout, di, h, w, a.rstd, dh, dx);
+    e = cudaGetLastError();
   } else {
     const int nv = norm_grad_vectors(a.H, a.res_f32), nt = row_threads(a.H, nv);
     const int threads = norm_grad_groups(a.rows, a.H, a.res_f32) * nt;
     const int bytes = nv * kPieces * 16, stages = bwd_stages(bytes, threads);
 #define MOE_NORM(NV, ST)                                                                                      \
   if (nv == NV && stages == ST)                                                                               \
-  add_rmsnorm_bwd_kernel<RT, NV, ST>                                                                          \
-      <<<n, threads, (size_t)ST * bytes * threads, s>>>(a.rows, a.H, nt, dout, di, h, w, a.rstd, dh, dx, part)
+  e = launch_dependent(add_rmsnorm_bwd_kernel<RT, NV, ST>, n, threads, (size_t)ST * bytes * threads, s, true, 1, a.rows, \
+                       a.H, nt, dout, di, h, w, a.rstd, dh, dx, part)
     MOE_NORM(1, 4);
     MOE_NORM(2, 4);
     MOE_NORM(4, 4);
@@ -513,7 +516,6 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
     MOE_NORM(4, 2);
 #undef MOE_NORM
   }
-  cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.dweight)
     e = launch_dependent(sum_partials_kernel, (a.H + 31) / 32, 1024, 0, s, true, /*cluster=*/1, part, n, a.H,
                          a.dweight);
