@@ -177,6 +177,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();  // 0: leader
   const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
   const int G = p.k.G;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {  // one warp of each CTA of the pair, together
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  // Q may be on the GPU while the launch that writes its offsets still runs; the
+  // later launches read them at once, and start when Q is past this point.
+  if (MODE == kQ) wait_for_previous_launch();
   if (MODE != kDX) allow_next_launch();
 
   // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
@@ -203,23 +223,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     order[at] = (uint16_t)g;
     tile_start[at] = n_wt * ((rows_of(g) + kMaxN - 1) / kMaxN);
-  }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * kEpiWarps);
-    }
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {  // one warp of each CTA of the pair, together
-    tmem_alloc_pair(smem_u32(tmem_slot), 512);
-    tmem_relinquish_pair();
   }
   __syncthreads();
   if (warp == 0) scan_warp(tile_start, G, lane);
@@ -561,9 +564,7 @@ template <int MODE>
 cudaError_t run_mode(const GradMaps& m, const GradParams& p, long long row_chunks, int num_sms, cudaStream_t s) {
   const int pairs = pairs_of<MODE>(p, row_chunks, num_sms);
   if (pairs < 1) return cudaErrorInvalidValue;
-  // Q starts after everything before it; the others' prologues may overlap the
-  // end of the launch before them (its offsets were there before Q).
-  return launch_dependent(grouped_grad_kernel<MODE>, 2 * pairs, kThreads, kSmem, s, MODE != kQ, /*cluster=*/2, m, p);
+  return launch_dependent(grouped_grad_kernel<MODE>, 2 * pairs, kThreads, kSmem, s, true, /*cluster=*/2, m, p);
 }
 
 template <int MODE>

@@ -3,6 +3,9 @@
 // It must not read (or overwrite) what that launch writes before
 // wait_for_previous_launch returns, which is when that launch has completed
 // and its writes are visible.
+// Such data is not read through the read-only path (__ldg, const __restrict__
+// parameters), whose loads may move up past the wait. Every block waits, so a
+// launch's end is also the end of those before it.
 #pragma once
 
 #include <cuda_runtime.h>
