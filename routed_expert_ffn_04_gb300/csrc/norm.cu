@@ -13,7 +13,7 @@
 //
 // Bound: HBM. One pass: a row's elements stay in the registers of the threads
 // that loaded them (8 consecutive columns per vector), so each input is read
-// once (8192 x 4096 with MXFP8 output: 45 us, 6.7 TB/s, the copy rate). Rows of
+// once (8192 x 4096 with MXFP8 output: 44.9 us, 6.7 TB/s, the copy rate). Rows of
 // at most 1024 columns take one warp each, longer rows (up to
 // 16384) one block each. Every thread reads its elements of a row before it
 // writes them, so the outputs may overwrite the inputs of their own type.
@@ -225,8 +225,7 @@ __global__ void add_rmsnorm_any_kernel(int H, const __nv_bfloat16* x, const RT* 
 // the outputs. A block is several groups of threads, each with a row of its
 // own and a barrier of its own (a group of 32 needs none); 32 columns per
 // thread keep the groups small and the sum's exchange cheap. 8192 x 4096 in
-// bf16: 45 us (5.9 TB/s; 40 us at a copy's rate), the rows of the last round
-// being 13.5 per group, and 3 to 5 us more until the partial sums are added.
+// bf16: 47 us (40 at a copy's rate), 3 of them until the partial sums are added.
 constexpr int kPieces = 3;
 template <typename RT, int NV>
 struct BwdShape {
@@ -237,12 +236,11 @@ struct BwdShape {
   static constexpr bool RING_IN = RP == 1;
   static constexpr int PIECES = kPieces;
 };
-constexpr int kBwdThreads = 256;  // per block, or one group's if that is more
-// Rows a group holds: four or three where that leaves room for two blocks per
-// SM, else two (at most 192 KB: 512 threads of 4 vectors).
-int bwd_stages(int bytes_per_thread, int threads) {
+// Rows a group holds: four or three where they fit in `room` bytes, else two
+// (at most 192 KB: 512 threads of 4 vectors).
+int bwd_stages(int bytes_per_thread, int threads, int room) {
   const int row = bytes_per_thread * threads;
-  return 4 * row <= 112 * 1024 ? 4 : (3 * row <= 112 * 1024 ? 3 : 2);
+  return 4 * row <= room ? 4 : (3 * row <= room ? 3 : 2);
 }
 
 __device__ __forceinline__ void copy16(void* smem, const void* g) {
@@ -449,14 +447,28 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
 int row_threads(int H, int nv) { return ((H + 8 * nv - 1) / (8 * nv) + 31) / 32 * 32; }
 
 // Backward: vectors of 8 columns per thread (an fp32 row of up to 4096 columns
-// takes two, for its wider loads), and row groups per block: one while every
-// row can have a block of its own.
-constexpr int kBwdBlocks = 304;  // two per SM of a GB300 (152)
+// takes two, for its wider loads).
 int norm_grad_vectors(int H, bool f32) { return H <= 256 ? 1 : (H <= 512 || (f32 && H <= 4096) ? 2 : 4); }
-int norm_grad_groups(long long rows, int H, bool f32) {
-  if (H % 8 || rows <= kBwdBlocks) return 1;
-  const int g = kBwdThreads / row_threads(H, norm_grad_vectors(H, f32));
-  return g < 1 ? 1 : g;
+
+// Its blocks and the row groups of each: a block per row while there are no more
+// than two per SM; then one block per SM of 512 threads for bf16 rows, which
+// halves the partial sums (1000 x 4096 13.2 -> 11.8 us, 8192 x 4096 48.7 ->
+// 47.0, 300 to 1000 x 512 4% slower), and two of 256 for fp32 rows (1000 x 512
+// 5.6 us against 6.9, 1000 x 8192 36.7 against 38.3, 8192 x 4096 90.0 against
+// 88.4). A function of the shape alone, so dw's summation order is the same
+// everywhere.
+constexpr int kSms = 152;  // of a GB300
+struct BwdGrid {
+  int blocks, groups, room;  // room: of a block's ring
+};
+BwdGrid norm_grad_grid(long long rows, int H, bool f32) {
+  constexpr int kOne = 192 * 1024, kTwo = 112 * 1024;  // blocks per SM
+  if (rows <= 2 * kSms) return {(int)rows, 1, rows <= kSms ? kOne : kTwo};
+  if (H % 8) return {2 * kSms, 1, 0};  // no ring
+  const int per_sm = f32 ? 2 : 1, g = 512 / per_sm / row_threads(H, norm_grad_vectors(H, f32));
+  const int groups = g < 1 ? 1 : g;
+  const long long units = (rows + groups - 1) / groups;
+  return {(int)(units < per_sm * kSms ? units : per_sm * kSms), groups, f32 ? kTwo : kOne};
 }
 
 template <typename RT, bool MX>
@@ -495,7 +507,8 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
   auto* dh = static_cast<RT*>(a.dh);
   auto* dx = static_cast<__nv_bfloat16*>(a.dx);
   float* part = a.dweight ? a.partials : nullptr;
-  const int n = norm_grad_blocks(a.rows, a.H, a.res_f32);
+  const BwdGrid g = norm_grad_grid(a.rows, a.H, a.res_f32);
+  const int n = g.blocks;
   cudaError_t e = cudaSuccess;
   if (a.H % 8) {
     if (part) add_rmsnorm_dw_any_kernel<RT><<<n, 256, 0, s>>>(a.rows, a.H, dout, h, a.rstd, part);
@@ -503,8 +516,7 @@ cudaError_t run_norm_bwd(const NormGradArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
   } else {
     const int nv = norm_grad_vectors(a.H, a.res_f32), nt = row_threads(a.H, nv);
-    const int threads = norm_grad_groups(a.rows, a.H, a.res_f32) * nt;
-    const int bytes = nv * kPieces * 16, stages = bwd_stages(bytes, threads);
+    const int threads = g.groups * nt, bytes = nv * kPieces * 16, stages = bwd_stages(bytes, threads, g.room);
 #define MOE_NORM(NV, ST)                                                                                      \
   if (nv == NV && stages == ST)                                                                               \
   e = launch_dependent(add_rmsnorm_bwd_kernel<RT, NV, ST>, n, threads, (size_t)ST * bytes * threads, s, true, 1, a.rows, \
@@ -543,13 +555,8 @@ cudaError_t norm_prepare_device() {
   return e != cudaSuccess ? e : set_all_bwd_smem<__nv_bfloat16>();
 }
 
-// Blocks of the backward pass, fewer when the rows are fewer; a function of the
-// shape alone, so dw's summation order is the same everywhere.
-int norm_grad_blocks(long long rows, int H, bool f32) {
-  const int groups = norm_grad_groups(rows, H, f32);
-  const long long units = (rows + groups - 1) / groups;
-  return (int)(units < kBwdBlocks ? units : kBwdBlocks);
-}
+// Blocks of the backward pass: rows of partial sums in its workspace.
+int norm_grad_blocks(long long rows, int H, bool f32) { return norm_grad_grid(rows, H, f32).blocks; }
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
