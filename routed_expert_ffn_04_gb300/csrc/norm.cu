@@ -231,9 +231,10 @@ template <typename RT, int NV>
 struct BwdShape {
   // 16-byte pieces of one vector of 8 columns: dout, h, and a bf16 dh_in. (An
   // fp32 dh_in would take the room of a row more in flight: it is prefetched
-  // into L2 when the row's copies start and loaded while the row is summed.)
+  // into L2 when the row's copies start and loaded a row ahead, or, where that
+  // would take too many registers, while its row is summed.)
   static constexpr int RP = sizeof(RT) / 2;
-  static constexpr bool RING_IN = RP == 1;
+  static constexpr bool RING_IN = RP == 1, AHEAD = !RING_IN && NV <= 2;
   static constexpr int PIECES = kPieces;
 };
 // Rows a group holds: four or three where they fit in `room` bytes, else two
@@ -299,19 +300,27 @@ __global__ void __launch_bounds__(512)
   const float inv_h = 1.0f / (float)H;
   int buf = 0, st = 0;
   float rs = first < rows ? rstd[first] : 0.0f;
+  Vec8<RT> vi[Sh::RING_IN ? 1 : NV], vi_next[Sh::AHEAD ? NV : 1];
+  auto load_in = [&](Vec8<RT>* to, long long row) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * nt + tid) * 8;
+      to[v].zero();
+      if (dh_in && c < H && row < rows) to[v].load(dh_in + (size_t)row * H + c);
+    }
+  };
+  if (Sh::AHEAD) load_in(vi_next, first);
   for (long long row = first; row < rows; row += step, buf ^= 1) {
     const float rs_next = row + step < rows ? rstd[row + step] : 0.0f;  // a row ahead, like the copies
     fetch(st == 0 ? STAGES - 1 : st - 1, row + (STAGES - 1) * step);
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
     const size_t at = (size_t)row * H;
-    Vec8<RT> vi[Sh::RING_IN ? 1 : NV];
-    if (!Sh::RING_IN) {
+    if (Sh::AHEAD) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int c = (v * nt + tid) * 8;
-        vi[v].zero();
-        if (dh_in && c < H) vi[v].load(dh_in + at + c);
-      }
+      for (int v = 0; v < NV; ++v) vi[v] = vi_next[Sh::AHEAD ? v : 0];
+      load_in(vi_next, row + step);
+    } else if (!Sh::RING_IN) {
+      load_in(vi, row);
     }
     float dot = 0.0f;
 #pragma unroll
@@ -446,29 +455,30 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
 // Threads of a block that holds one row in NV vectors of 8 per thread.
 int row_threads(int H, int nv) { return ((H + 8 * nv - 1) / (8 * nv) + 31) / 32 * 32; }
 
-// Backward: vectors of 8 columns per thread (an fp32 row of up to 4096 columns
+// Backward: vectors of 8 columns per thread (an fp32 row of up to 8192 columns
 // takes two, for its wider loads).
-int norm_grad_vectors(int H, bool f32) { return H <= 256 ? 1 : (H <= 512 || (f32 && H <= 4096) ? 2 : 4); }
+int norm_grad_vectors(int H, bool f32) { return H <= 256 ? 1 : (H <= 512 || (f32 && H <= 8192) ? 2 : 4); }
 
 // Its blocks and the row groups of each: a block per row while there are no more
 // than two per SM; then one block per SM of 512 threads for bf16 rows, which
 // halves the partial sums (1000 x 4096 13.2 -> 11.8 us, 8192 x 4096 48.7 ->
-// 47.0, 300 to 1000 x 512 4% slower), and two of 256 for fp32 rows (1000 x 512
-// 5.6 us against 6.9, 1000 x 8192 36.7 against 38.3, 8192 x 4096 90.0 against
-// 88.4). A function of the shape alone, so dw's summation order is the same
-// everywhere.
+// 47.0, 300 to 1000 x 512 4% slower), and two of 256 for fp32 rows of up to 4096
+// columns (1000 x 512 5.6 us against 6.9, 8192 x 4096 90.0 against 88.4). Longer
+// fp32 rows have a block of up to 512 threads: 3000 x 8192 69 us, with four
+// vectors in each of 256 threads 77. A function of the shape alone, so dw's
+// summation order is the same everywhere.
 constexpr int kSms = 152;  // of a GB300
 struct BwdGrid {
   int blocks, groups, room;  // room: of a block's ring
 };
 BwdGrid norm_grad_grid(long long rows, int H, bool f32) {
   constexpr int kOne = 192 * 1024, kTwo = 112 * 1024;  // blocks per SM
-  if (rows <= 2 * kSms) return {(int)rows, 1, rows <= kSms ? kOne : kTwo};
+  const int nt = row_threads(H, norm_grad_vectors(H, f32)), per_sm = f32 && nt <= 256 ? 2 : 1;
+  if (rows <= 2 * kSms) return {(int)rows, 1, rows <= kSms || nt > 256 ? kOne : kTwo};
   if (H % 8) return {2 * kSms, 1, 0};  // no ring
-  const int per_sm = f32 ? 2 : 1, g = 512 / per_sm / row_threads(H, norm_grad_vectors(H, f32));
-  const int groups = g < 1 ? 1 : g;
+  const int g = 512 / per_sm / nt, groups = g < 1 ? 1 : g;
   const long long units = (rows + groups - 1) / groups;
-  return {(int)(units < per_sm * kSms ? units : per_sm * kSms), groups, f32 ? kTwo : kOne};
+  return {(int)(units < per_sm * kSms ? units : per_sm * kSms), groups, per_sm == 2 ? kTwo : kOne};
 }
 
 template <typename RT, bool MX>
