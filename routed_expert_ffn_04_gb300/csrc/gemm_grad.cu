@@ -98,6 +98,7 @@ struct GradParams {
   float* q;               // [rows, I]
   __nv_bfloat16 *h, *dg, *du;  // [prows, I], padded (padded_rows)
   int prows;
+  bool after_dw;          // DX: the launch before is the weight gradients', else GU
   int* odd;               // set where gate or q is not finite
   __nv_bfloat16* da;      // [rows, H]
 };
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Q may be on the GPU while the launch that writes its offsets still runs; the
   // later launches read them at once, and start when Q is past this point.
   if (MODE == kQ) wait_for_previous_launch();
-  if (MODE != kDX) allow_next_launch();
+  allow_next_launch();
 
   // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
   fill_row_start(p.k, row_start, threadIdx.x, kThreads);
@@ -241,9 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // launch): each role waits for its end where it first needs its results, or
   // where it would start to wait for a role that does. GU's operands do not
   // come from Q, only its epilogue's q does: two tiles of MMAs fit before it.
-  // In DX a ring of weights does. Every CTA waits, so a launch's end is the end
-  // of all before it. (128 tokens, 2 of 8 experts, H = 1024, I = 512: 44.4 us
-  // when all waited here and the weight gradients for DX, 40.0 so.)
+  // In DX a ring of weights does; after the weight gradients, which let it start
+  // when GU is done, DX waits for nothing but, at the end, for them. Every CTA
+  // waits, so a launch's end is the end of all before it. (128 tokens, 2 of 8
+  // experts, H = 1024, I = 512: 44.4 us when all waited here, 40.0 so; 33.9 with
+  // DX before the weight gradients and 31.5 after them, whose set-up is then
+  // hidden too. 40 tokens, 3 of 20 experts, H = 1600, I = 1024 lose 2%: DX finds
+  // less of Wg and Wu in L2.)
+  const bool at_once = MODE == kDX && p.after_dw;
+  if (at_once) fence_previous_results();
   if (MODE == kQ && blockIdx.x == 0 && threadIdx.x == 0) *p.odd = 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[G];
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Tile mine = {};
     for (int i = 0; ok && i < my_tiles; ++i) {
-      if (MODE == kDX ? i == 0 && !is_a : MODE == kGU && i == 2) wait_for_previous_launch();
+      if (MODE == kDX ? i == 0 && !is_a && !at_once : MODE == kGU && i == 2) wait_for_previous_launch();
       if ((i & 31) == 0) mine = decode(i + lane);
       const int g = at_tile(mine.g, i), wt = at_tile(mine.wt, i), half = at_tile(mine.N, i) >> 1;
       const int row = at_tile(MODE == kDX ? mine.prow : mine.row, i) + (int)rank * half;
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = warp == 6 ? 0 : most, box = warp == 6 ? most : second_box;
       const int extra = warp == 6 ? 0 : rest - second_box;  // 48 = 32 + 16
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (MODE == kDX && is_a && i * p.num_kb + kb == kStages) wait_for_previous_launch();
+        if (MODE == kDX && is_a && !at_once && i * p.num_kb + kb == kStages) wait_for_previous_launch();
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.k.status,
                                                        MOE_DEV_TIMEOUT_PRODUCER, p.k.limit_ns))) {
           ok = false;
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, issued = false;
       int n32 = 0;
       for (int i = 0; ok && i < my_tiles; ++i) {
-        if (i == (MODE == kGU ? 2 : 0)) wait_for_previous_launch();
+        if (i == (MODE == kGU ? 2 : 0) && !at_once) wait_for_previous_launch();
         if ((i & 31) == 0) n32 = decode(i + lane).N;
         const int N = at_tile(n32, i);
         const int acc = i & 1;
@@ -401,9 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int partners = 1 + (q & 1) + 2 * half;  // named barrier of warps q and q ^ 2
     Tile mine = {};
     float odd = 0.0f;  // GU: turns NaN where a gate or q is not finite
-    wait_for_previous_launch();
-    // The weight gradients need GU's results, not DX's: they may start now.
-    if (MODE == kDX) allow_next_launch();
+    if (!at_once) wait_for_previous_launch();
     for (int i = 0; i < my_tiles; ++i) {
       if ((i & 31) == 0) mine = decode(i + lane);
       const int wt = at_tile(mine.wt, i), count = at_tile(mine.count, i), N = at_tile(mine.N, i);
@@ -540,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MODE == kGU && odd != 0.0f) *p.odd = 1;
   }
 
+  if (at_once) wait_for_previous_launch();
   // Both CTAs arrive here only when their roles are done (every wait is
   // bounded), so neither frees TMEM or leaves while the other may still touch
   // its shared memory or barriers.
@@ -633,18 +639,18 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
     p.num_kb = H / kBK;
     e = run_mode<kGU>(m, p, row_chunks, a.num_sms, s);
   }
-  int dx_pairs = 0;
+  p.k.N = H;
+  p.num_kb = 2 * (I / kBK);
+  p.after_dw = want_dw;
+  if (e == cudaSuccess && want_dw)
+    e = launch_grouped_weight_grad(a, a.da ? pairs_of<kDX>(p, row_chunks, a.num_sms) : 0, s);
   if (e == cudaSuccess && a.da) {
     GradMaps m = {};
     if (!make_tmap_bf16(&m.a0, a.w_gate, H, GI, 64) || !make_tmap_bf16(&m.a1, a.w_up, H, GI, 64) ||
         !row_maps(m.b0, a.dg, I, P) || !row_maps(m.b1, a.du, I, P))
       return cudaErrorInvalidValue;
-    p.k.N = H;
-    p.num_kb = 2 * (I / kBK);
-    dx_pairs = pairs_of<kDX>(p, row_chunks, a.num_sms);
     e = run_mode<kDX>(m, p, row_chunks, a.num_sms, s);
   }
-  if (e == cudaSuccess && want_dw) e = launch_grouped_weight_grad(a, dx_pairs, s);
   return e;
 }
 

@@ -81,7 +81,6 @@ struct DwParams {
   int H, I;
   __nv_bfloat16* dw[3];  // dWd, dWg, dWu
   int stages;
-  bool after_dx;               // the launch before is DX, else GU
   const int* odd;              // not 0: a row of a or dy may hold an infinity or NaN
   // Strips: [0] of groups longer than the ring, one tile each; [1] of the others.
   struct Cut {
@@ -148,7 +147,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: leader
   const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
-  allow_next_launch();
 
   fill_row_start(p.k, row_start, threadIdx.x, kThreads);
   int* longs = reinterpret_cast<int*>(epi_stage) + kMaxGroups + 8;  // until the loop starts
@@ -197,15 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
-  // DX lets this launch start once GU is done, whose results are all that is
-  // read here; its own end is waited for last, so that this launch's end is the
-  // end of both.
-  if (p.after_dx) {
-    __threadfence();
-    asm volatile("fence.proxy.async;" ::: "memory");
-  } else {
-    wait_for_previous_launch();
-  }
+  // DX, the next launch, needs GU's results and not these: it may start now.
+  wait_for_previous_launch();
+  allow_next_launch();
   const bool careful = *static_cast<const volatile int*>(p.odd) != 0;
   const uint32_t tmem_base = *tmem_slot;
   const int n_long = *longs, long_strips = n_long * p.cut[0].per_group;
@@ -442,11 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m0 < M) {
 #pragma unroll 1
           for (int c = 0; c < 128 && n0 + c < N; c += 64) {
-            // Four rows of 128 bytes per instruction.
+            // Four rows of 128 bytes per instruction, first out of L2 again: DX
+            // still needs the weights that are there.
             __nv_bfloat16* at = p.dw[which] + ((size_t)g * M + m0 + (lane >> 3)) * N + n0 + c + (lane & 7) * 8;
             if (empty) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at + (size_t)(4 * j) * N) = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < 8; ++j) __stcs(reinterpret_cast<uint4*>(at + (size_t)(4 * j) * N), make_uint4(0, 0, 0, 0));
             } else {
               stage_bf16_block(tb + c, stg, lane);
               __syncwarp();
@@ -458,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at + (size_t)(4 * j) * N) = v[j];
+              for (int j = 0; j < 8; ++j) __stcs(reinterpret_cast<uint4*>(at + (size_t)(4 * j) * N), v[j]);
             }
           }
         }
@@ -475,7 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Both CTAs arrive here only when their roles are done (every wait is
   // bounded), so neither frees TMEM or leaves while the other may still touch
   // its shared memory or barriers.
-  if (p.after_dx) wait_for_previous_launch();
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
@@ -513,7 +505,6 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, int dx_pairs, c
   void* dw[] = {a.dw_down, a.dw_gate, a.dw_up};
   for (int i = 0; i < 3; ++i) p.dw[i] = static_cast<__nv_bfloat16*>(dw[i]);
   p.stages = ring_stages(G);
-  p.after_dx = a.da != nullptr;
   p.odd = a.odd;
   auto recip = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d) : 0xFFFFFFFFu; };
   const int tiles_h = (H + 255) / 256, tiles_i = (I + 255) / 256;
@@ -538,11 +529,10 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, int dx_pairs, c
   p.cut[1] = cut(most);
   const long long tiles = (long long)G * p.cut[0].per_group;
   int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
-  // The pairs that DX leaves free start at once, the others when it ends, some
-  // 10 us later (128 tokens, 2 of 8 experts, H = 1024, I = 512), and the work is
-  // dealt beforehand: the free ones alone, if that costs few more rounds of
-  // short tiles (about 1 us each): 38.9 us for the pass became 36.8, 64 tokens,
-  // 2 of 16 experts, H = 512, I = 256 34.7 us 30.7.
+  // DX, which may run beside this launch, starts where a pair is free. Leave it
+  // its pairs, if that costs few more rounds of short tiles (about 1 us each; DX
+  // would otherwise start 8 us later at 128 tokens, 2 of 8 experts, H = 1024, I =
+  // 512: 2.1 us of the pass's 38.9, with the two in the other order).
   const long long strips = (long long)G * p.cut[1].per_group, spare = max_pairs - dx_pairs;
   auto rounds = [&](long long n) { return (strips + n - 1) / n; };
   if (spare > 0 && spare < pairs && rounds(spare) <= rounds(pairs) + (a.rows <= 256ll * G ? 4 : 0)) pairs = (int)spare;

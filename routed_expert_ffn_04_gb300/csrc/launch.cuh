@@ -13,6 +13,12 @@
 namespace moe {
 
 __device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// For a launch that the one before it let start after its own wait: what came
+// before that one is done, and its writes are seen from here on (TMA too).
+__device__ __forceinline__ void fence_previous_results() {
+  __threadfence();
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 // Lets the next launch of the chain be scheduled once every block is here.
 __device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
