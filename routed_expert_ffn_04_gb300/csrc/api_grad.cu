@@ -2,6 +2,8 @@
 // workspace carving (kernels in norm.cu, dispatch_grad.cu and gemm_grad.cu).
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 
@@ -32,7 +34,7 @@ size_t norm_grad_ws(int64_t rows, int H) {
   return align_up((size_t)(a > b ? a : b) * H * 4 + 1, 256);
 }
 
-// moe_grouped_swiglu_backward workspace: a flag, q fp32, then h, dgate and dup
+// moe_grouped_swiglu_backward workspace: a flag and two words (256 bytes), q fp32, then h, dgate and dup
 // bf16 with each group's rows padded to a multiple of 16.
 struct GradWs {
   size_t q, h, dg, du, total;
@@ -46,6 +48,13 @@ GradWs grad_ws(int rows, int G, int I) {
   L.du = L.dg + align_up(np * 2 + 1, 256);
   L.total = L.du + align_up(np * 2 + 1, 256);
   return L;
+}
+
+// A number that no other call has, in this process or (nearly surely) in one
+// that used the same memory before.
+uint64_t next_call() {
+  static std::atomic<uint64_t> n{(uint64_t)std::chrono::system_clock::now().time_since_epoch().count() | 1};
+  return n.fetch_add(1, std::memory_order_relaxed);
 }
 
 bool grad_shape_ok(int num_groups, int rows, int H, int I) {
@@ -190,6 +199,7 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
   g.w_up = w_up;
   g.w_down = w_down;
   g.odd = reinterpret_cast<int*>(w);
+  g.chain = {reinterpret_cast<uint64_t*>(w + 64), reinterpret_cast<uint64_t*>(w + 128), next_call()};
   g.q = reinterpret_cast<float*>(w + L.q);
   g.h = w + L.h;
   g.dg = w + L.dg;

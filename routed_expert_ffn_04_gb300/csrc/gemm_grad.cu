@@ -99,6 +99,7 @@ struct GradParams {
   __nv_bfloat16 *h, *dg, *du;  // [prows, I], padded (padded_rows)
   int prows;
   bool after_dw;          // DX: the launch before is the weight gradients', else GU
+  ChainWords chain;
   int* odd;               // set where gate or q is not finite
   __nv_bfloat16* da;      // [rows, H]
 };
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + kStages * kStageBytes + kExchange);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* early_flag = abort_flag + 1;
   int32_t* tile_start = reinterpret_cast<int32_t*>(base + kStages * kStageBytes + kExchange + kBarBytes);
   int32_t* row_start = tile_start + kMaxGroups + 8;
   // Group g's first row in h, dg and du (gemm_grad.cuh) is row_start[g] -
@@ -195,9 +197,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tmem_relinquish_pair();
   }
-  // Q may be on the GPU while the launch that writes its offsets still runs; the
-  // later launches read them at once, and start when Q is past this point.
-  if (MODE == kQ) wait_for_previous_launch();
+  // Blocks of the launch before may still be running (programmatic dependent
+  // launch). Q waits for its end, here, and publishes that it has: the caller's
+  // operands are complete. GU and DX need no more than that to begin; DX after
+  // the weight gradients finds the word that those publish, and with it GU's
+  // results.
+  if (MODE == kQ) {
+    wait_for_previous_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      *p.odd = 0;
+      *p.chain.gu_done = 0;
+      publish(p.chain.inputs_ready, p.chain.call);
+    }
+  } else {
+    wait_until_published(MODE == kDX && p.after_dw ? p.chain.gu_done : p.chain.inputs_ready, p.chain.call, early_flag);
+  }
   allow_next_launch();
 
   // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
@@ -238,20 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
-  // Blocks of the launch before may still be running (programmatic dependent
-  // launch): each role waits for its end where it first needs its results, or
-  // where it would start to wait for a role that does. GU's operands do not
-  // come from Q, only its epilogue's q does: two tiles of MMAs fit before it.
-  // In DX a ring of weights does; after the weight gradients, which let it start
-  // when GU is done, DX waits for nothing but, at the end, for them. Every CTA
-  // waits, so a launch's end is the end of all before it. (128 tokens, 2 of 8
-  // experts, H = 1024, I = 512: 44.4 us when all waited here, 40.0 so; 33.9 with
-  // DX before the weight gradients and 31.5 after them, whose set-up is then
-  // hidden too. 40 tokens, 3 of 20 experts, H = 1600, I = 1024 lose 2%: DX finds
-  // less of Wg and Wu in L2.)
+  // Each role waits for the end of the launch before where it first needs its
+  // results, or where it would start to wait for a role that does. GU's operands
+  // do not come from Q, only its epilogue's q does: two tiles of MMAs fit before
+  // it. In DX a ring of weights does; after the weight gradients, which let it
+  // start when GU is done, DX waits for nothing but, at the end, for them. Every
+  // CTA waits, so a launch's end is the end of all before it. Against every
+  // thread of every launch waiting for the launch before at its top (us): 128
+  // tokens, 2 of 8 experts, H = 1024, I = 512 44.5 -> 31.6; 64 tokens, 2 of 16,
+  // H = 512, I = 256 35.5 -> 23.5; 40 tokens, 3 of 20, H = 1600, I = 1024 130 ->
+  // 116; 2048 tokens, 4 of 64, H = 4096, I = 1536 1210 -> 1140; 341 rows for each
+  // of 192 experts the same.
   const bool at_once = MODE == kDX && p.after_dw;
-  if (at_once) fence_previous_results();
-  if (MODE == kQ && blockIdx.x == 0 && threadIdx.x == 0) *p.odd = 0;
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[G];
   auto tile_of = [&](int i) { return i * npairs + ((i & 1) ? npairs - 1 - pair : pair); };
@@ -546,6 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (at_once) wait_for_previous_launch();
+  // DX ends the chain. (A thread that has waited; a block of DX that finds the
+  // word cleared waits itself.)
+  if (MODE == kDX && blockIdx.x == 0 && warp == 2 && lane == 0) *p.chain.inputs_ready = 0;
   // Both CTAs arrive here only when their roles are done (every wait is
   // bounded), so neither frees TMEM or leaves while the other may still touch
   // its shared memory or barriers.
@@ -619,6 +634,7 @@ cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_
   p.du = static_cast<__nv_bfloat16*>(a.du);
   p.prows = (int)padded_rows(a.rows, G);
   p.odd = a.odd;
+  p.chain = a.chain;
   p.da = static_cast<__nv_bfloat16*>(a.da);
   const uint64_t R = a.rows, P = p.prows, GI = (uint64_t)G * I, GH = (uint64_t)G * H;
   const long long row_chunks = (a.rows + kMaxN - 1) / kMaxN + (long long)G;  // at most: one short chunk per group

@@ -64,7 +64,7 @@ constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 384;
 constexpr int kEpiBytes = kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
-constexpr int kBarBytes = 8 * (6 * kMaxStages + 5) + 8;
+constexpr int kBarBytes = 8 * (6 * kMaxStages + 5) + 24;  // and the TMEM address and two flags
 constexpr uint16_t kPairMask = 0x3;
 
 constexpr int table_bytes(int G) { return ((G + 1) * 4 + 2 * G + 2 * G + 15) / 16 * 16; }
@@ -82,6 +82,8 @@ struct DwParams {
   __nv_bfloat16* dw[3];  // dWd, dWg, dWu
   int stages;
   const int* odd;              // not 0: a row of a or dy may hold an infinity or NaN
+  ChainWords chain;
+  bool last;                   // of the chain: no DX follows
   // Strips: [0] of groups longer than the ring, one tile each; [1] of the others.
   struct Cut {
     int per_group;        // strips of a group: nd of dWd, then ng of dWg, then ng of dWu
@@ -148,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();  // 0: leader
   const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
 
+  wait_until_published(p.chain.inputs_ready, p.chain.call, abort_flag + 1);
   fill_row_start(p.k, row_start, threadIdx.x, kThreads);
   int* longs = reinterpret_cast<int*>(epi_stage) + kMaxGroups + 8;  // until the loop starts
   if (threadIdx.x == 0) *longs = 0;
@@ -197,6 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   // DX, the next launch, needs GU's results and not these: it may start now.
   wait_for_previous_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    publish(p.chain.gu_done, p.chain.call);
+    if (p.last) *p.chain.inputs_ready = 0;
+  }
   allow_next_launch();
   const bool careful = *static_cast<const volatile int*>(p.odd) != 0;
   const uint32_t tmem_base = *tmem_slot;
@@ -506,6 +513,8 @@ cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, int dx_pairs, c
   for (int i = 0; i < 3; ++i) p.dw[i] = static_cast<__nv_bfloat16*>(dw[i]);
   p.stages = ring_stages(G);
   p.odd = a.odd;
+  p.chain = a.chain;
+  p.last = a.da == nullptr;
   auto recip = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d) : 0xFFFFFFFFu; };
   const int tiles_h = (H + 255) / 256, tiles_i = (I + 255) / 256;
   auto cut = [&](int most) {

@@ -233,6 +233,12 @@ cudaError_t launch_permute_backward(const void* dx_perm, const int32_t* flat_to_
                                     const void* dx_add, void* dx, int* status, cudaStream_t s);
 
 // ---- gradient of the grouped SwiGLU GEMM (gemm_grad.cu)
+// Words by which the chain's launches tell that they have waited (launch.cuh).
+struct ChainWords {
+  uint64_t* inputs_ready;  // Q: what the caller passed is complete
+  uint64_t* gu_done;       // the weight gradients: h, dg and du are
+  uint64_t call;           // this call's number
+};
 struct GroupedGradArgs {
   int G;                   // number of groups
   const int32_t* offsets;  // [G+1] device, or nullptr: one group of `rows`
@@ -247,6 +253,7 @@ struct GroupedGradArgs {
   void* dg;                // the same
   void* du;                // the same
   int* odd;                // one word of scratch
+  ChainWords chain;        // two words of scratch
   void* da;                // [rows, H] bf16, or nullptr
   void* dw_gate;           // [G, I, H] bf16, or nullptr (all three)
   void* dw_up;             // [G, I, H] bf16

@@ -227,3 +227,29 @@ def test_two_streams_at_once(handle):
     for w, b in zip(want, bufs):
         for k, t in zip(("da", "dg", "du", "dd"), b):
             assert torch.equal(w[k], t), k
+
+
+def test_operands_written_by_the_launch_just_before(handle):
+    """The chained launches read nothing before the launch ahead of them has ended: each operand in turn is the last one
+    written, `a` by one of the library's own dependent launches."""
+    ps = [_problem([100, 0, 300, 41], 512, 256, seed=1), _problem([7, 250, 3, 181], 512, 256, seed=2)]
+    rows, names = ps[0]["rows"], ["offsets", "a", "dy", "wg", "wu", "wd"]
+    want = [_run(handle, p) for p in ps]
+    b = {k: ps[0][k].clone() for k in names}
+    out = [torch.empty_like(ps[0][k]) for k in ("a", "wg", "wu", "wd")]
+    ws = torch.empty(moe.grouped_gemm_backward_workspace_size(rows, 512, 256, num_groups=4), dtype=torch.uint8, device="cuda")
+    cfg, same = moe.make_config(rows, 512, 4, 1, 64, 0, 1.0), torch.arange(rows, dtype=torch.int32, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(48):
+        p = ps[i & 1]
+        at = (i >> 1) % len(names)
+        for k in names[at + 1:] + names[:at + 1]:
+            if k == "a":  # one row per token: a copy
+                moe.permute_backward(handle, cfg, p["a"], same, b["a"])
+            else:
+                torch.mul(p[k], 1, out=b[k])
+        moe.grouped_swiglu_backward(handle, *[b[k] for k in ("a", "dy", "offsets", "wg", "wu", "wd")], *out, ws,
+                                    num_groups=4, H=512, I=256)
+        for k, t in zip(("da", "dg", "du", "dd"), out):
+            wrong += (t != want[i & 1][k]).sum()
+    assert wrong.item() == 0 and handle.device_status() == 0
