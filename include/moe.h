@@ -533,7 +533,8 @@ MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_
  * fp32 accumulation; h, dgate and dup are rounded to bf16 once (as the tensor
  * cores take them), and so is each output.
  * a, dy (device): [rows, H] bf16. Outputs (device): da [rows, H] bf16
- * (nullable; rows outside every group are not written); dw_gate, dw_up
+ * (nullable; rows outside every group are not written, and such rows of a and
+ * dy may hold anything, NaN too); dw_gate, dw_up
  * [num_groups, I, H] and dw_down [num_groups, H, I] bf16 (all three or none;
  * overwritten; a group without rows gets zeros). At least one of da and the
  * dw's. No output overlaps an input. dtype: MOE_BF16 (else

@@ -33,8 +33,10 @@
 // holds there adds nothing. A zero times an infinity or NaN would: when the
 // launch before has met one (p.odd), the rows past the group's end are
 // cleared in shared memory first (the careful way: 0.26 ms more at the
-// size above, as every tile's last stage waits for it). A group without rows
-// gives zero gradients.
+// size above, as every tile's last stage waits for it). The launch before looks
+// at groups' rows alone, and rows after the last group may hold anything: a
+// group whose last step reaches one of them always goes the careful way. A
+// group without rows gives zero gradients.
 //
 // Roles per CTA (12 warps): 0 loads A's boxes and arms the stage; 6 loads B's;
 // 1 (of the even CTA, the leader) issues the pair's MMAs; 11 clears ragged
@@ -217,9 +219,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // and read back by shuffles: decoding alone cost a role's thread 1000 to 1500
   // cycles, as long as half a tile's MMAs.
   struct Strip {
-    int rows, row0, prow0, m0, n0, len, g_which;  // prow0: in h, dg, du; len: tiles; g * 4 + which
+    int rows, row0, prow0, m0, n0, len, g_which;  // prow0: in h, dg, du; len: tiles; g * 8 + open * 4 + which
   };
-  auto decode = [&](int r) {  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]
+  // which: 0 dWd [H, I], 1 dWg [I, H], 2 dWu [I, H]; open: the group's last step
+  // reaches rows after the last group.
+  const int end = row_start[G];
+  auto decode = [&](int r) {
     Strip t = {};
     if (r >= my_rounds) return t;
     int at = strip_of(r);
@@ -235,14 +240,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = div_by(at, parts, which == 0 ? c.r_d : c.r_g), n_tile = (at - row * parts) * len;
     const int n_tiles = ((which == 0 ? p.I : p.H) + 255) / 256;
     const int n = row_start[g + 1] - row_start[g];
+    const int open = n > 0 && end < p.k.rows && row_start[g] + pad16(n) > end ? 4 : 0;
     t = {n > 0 ? n : 0, row_start[g], row_start[g] - row_start[0] + pad_extra[g], row * 256, n_tile * 256,
-         n_tiles - n_tile < len ? n_tiles - n_tile : len, g * 4 + which};
+         n_tiles - n_tile < len ? n_tiles - n_tile : len, g * 8 + open + which};
     return t;
   };
   auto at_round = [&](int v, int r) { return __shfl_sync(0xFFFFFFFFu, v, r & 31); };
   // A stage with `left` rows of the group from its first row on needs clearing
   // when the group ends inside one of its steps.
-  auto ragged = [&](int left) { return careful && left < kBK && (left & 15) != 0; };
+  auto ragged = [&](int left, bool open) { return (careful || open) && left < kBK && (left & 15) != 0; };
 
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers
@@ -254,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Strip mine = {};
     for (int r = 0; ok && r < my_rounds; ++r) {
       if ((r & 31) == 0) mine = decode(r + lane);
-      const int nrows = at_round(mine.rows, r), which = at_round(mine.g_which, r) & 3;
+      const int nrows = at_round(mine.rows, r), g_which = at_round(mine.g_which, r), which = g_which & 3;
+      const bool open = (g_which & 4) != 0;
       // A: dy (rows as given), dg, du; B: h, then a (rows as given).
       const int row0 = at_round((ab == 0) == (which == 0) ? mine.row0 : mine.prow0, r);
       const int tiles = ab == 0 ? 1 : at_round(mine.len, r);
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int low = left <= 16 ? 2 : (left <= 32 ? 1 : 0);  // box height 64 >> low
           const CUtensorMap* map = maps + low;
           const uint32_t dst = (ab == 0 ? base_u32 : b_ring) + rg.s * kHalfBytes;
-          const bool own = ragged(left);  // completes on this CTA's tail barrier
+          const bool own = ragged(left, open);  // completes on this CTA's tail barrier
           const uint32_t full = full_bar(ab, rg.s);
           const uint32_t bar = own ? tail_bar(ab, rg.s) : (rank == 0 ? full : mapa_shared(full, 0));
           if (elect_one()) {
@@ -314,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; ok && r < my_rounds; ++r) {
         if ((r & 31) == 0) mine = decode(r + lane);
         const int nrows = at_round(mine.rows, r), len = at_round(mine.len, r);
+        const bool open = (at_round(mine.g_which, r) & 4) != 0;
         const Ring strip = ra;  // where the strip's A starts
         for (int t = 0; ok && t < len; ++t, ++tile) {
           const int acc = tile & 1;
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            if (ragged(left)) {  // the other CTA's cleared rows
+            if (ragged(left, open)) {  // the other CTA's cleared rows
               if (t == 0) mbar_acquire_cluster(full_bar(0, ra.s), ra.ph);
               mbar_acquire_cluster(full_bar(1, rb.s), rb.ph);
             }
@@ -377,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase[2] = {0, 0};
     Strip mine = {};
     bool ok = true;
-    auto pass = [&](int ab, int nrows) {  // one tile's stages of a ring
+    auto pass = [&](int ab, int nrows, bool open) {  // one tile's stages of a ring
       for (int left = nrows; ok && left > 0; left -= kBK) {
         const int st = rg[ab].s;
-        if (ragged(left)) {
+        if (ragged(left, open)) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail_bar(ab, st), (phase[ab] >> st) & 1u, abort_flag,
                                                          p.k.status, MOE_DEV_TIMEOUT_MMA, p.k.limit_ns));
           if (!ok) break;
@@ -401,12 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         rg[ab].next(NS);
       }
     };
-    if (careful)
+    if (careful || end < p.k.rows)
       for (int r = 0; ok && r < my_rounds; ++r) {
         if ((r & 31) == 0) mine = decode(r + lane);
         const int nrows = at_round(mine.rows, r), len = at_round(mine.len, r);
-        pass(0, nrows);
-        for (int t = 0; t < len; ++t) pass(1, nrows);
+        const bool open = (at_round(mine.g_which, r) & 4) != 0;
+        pass(0, nrows, open);
+        for (int t = 0; t < len; ++t) pass(1, nrows, open);
       }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile = 0, ok = 1;
     for (int r = 0; ok && r < my_rounds; ++r) {
       if ((r & 31) == 0) mine = decode(r + lane);
-      const int which = at_round(mine.g_which, r) & 3, g = at_round(mine.g_which, r) >> 2;
+      const int which = at_round(mine.g_which, r) & 3, g = at_round(mine.g_which, r) >> 3;
       const int m0 = at_round(mine.m0, r) + (int)rank * 128 + q * 32, len = at_round(mine.len, r);
       int n0 = at_round(mine.n0, r) + half * 128;
       const bool empty = at_round(mine.rows, r) == 0;

@@ -253,3 +253,56 @@ def test_operands_written_by_the_launch_just_before(handle):
         for k, t in zip(("da", "dg", "du", "dd"), out):
             wrong += (t != want[i & 1][k]).sum()
     assert wrong.item() == 0 and handle.device_status() == 0
+
+
+@pytest.mark.parametrize("counts,H,I,groups", [
+    ([37, 3], 192, 128, (0, 1)), ([17, 3], 128, 64, (0, 1)), ([5, 90, 0, 0], 640, 320, (1,)), ([16, 32, 1, 1, 1], 64, 192, (2, 3, 4)),
+    ([401], 320, 576, (0,)), ([1], 64, 64, (0,)),
+])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", [("dy",), ("a",), ("a", "dy")])
+def test_rows_of_no_group_stay_out(handle, counts, H, I, groups, bad, where):
+    """Rows before the first group and after the last one may hold anything. `groups`: those whose last step of 16 rows
+    reaches past the last group's end."""
+    p = _problem(counts, H, I, lead=4, trail=20)
+    assert all((p["off"][e] + (counts[e] + 15) // 16 * 16 > p["off"][-1]) == (e in groups) for e in range(len(counts)) if counts[e])
+    clean = _run(handle, p)
+    _against_formulas(p, clean)
+    q = dict(p)
+    for k in where:
+        q[k] = p[k].clone()
+        q[k][:4] = bad
+        q[k][p["off"][-1]:] = bad
+    o = _run(handle, q)
+    for k in o:
+        assert torch.equal(o[k], clean[k]), k
+
+
+def test_dropped_pairs_leave_nothing_in_the_weights(handle):
+    """The rows of dropped pairs, which the combine's gradient does not write, lie after the last group."""
+    T, H, E, K, I = 50, 128, 6, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cfg = moe.make_config(T, H, E, K, I, 0, 1.5)
+    logits = torch.randn((T, E), device="cuda", generator=g)
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    idx, tw = i32((T, K)), torch.empty((T, K), device="cuda")
+    moe.route(handle, cfg, logits, idx, tw)
+    sent = idx.clone()
+    sent.view(-1)[torch.randperm(T * K, device="cuda", generator=g)[:21]] = E + 5
+    counts, offsets, perm, f2p = i32(E), i32(E + 1), i32(T * K), i32(T * K)
+    x, xp = _randn(g, (T, H)), torch.zeros((T * K, H), dtype=BF, device="cuda")
+    ws = torch.empty(moe.permute_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    moe.permute(handle, cfg, x, sent, counts, offsets, perm, f2p, xp, ws)
+    assert handle.device_status() != 0  # the dropped pairs are reported
+    off = offsets.tolist()
+    assert off[-1] == T * K - 21
+    y, dout = torch.randn((T * K, H), device="cuda", generator=g), _randn(g, (T, H))
+    p = dict(off=off, offsets=offsets, a=xp, wg=_randn(g, (E, I, H), 0.1), wu=_randn(g, (E, I, H), 0.1),
+             wd=_randn(g, (E, H, I), 0.1), H=H, I=I, G=E, rows=T * K)
+    got = []
+    for fill in (0.0, float("nan")):
+        dy, dtw = torch.full((T * K, H), fill, dtype=BF, device="cuda"), torch.empty((T, K), device="cuda")
+        moe.combine_backward(handle, cfg, dout, y, tw, f2p, dy, dtw)
+        got.append(_run(handle, dict(p, dy=dy)))
+    for k in got[0]:
+        assert torch.equal(got[0][k], got[1][k]), k
