@@ -5,11 +5,12 @@
 //   combine: out[t] = sum_k w[t,k] y[p(t,k)] + shared[t]
 //     dy[p(t,k)] = w[t,k] * dout[t];  dw[t,k] = <dout[t], y[p(t,k)]>;  dshared = dout
 //   routing: w_k = scaling * sigma_k / S, S = sum_j sigma_j (route_norm), or scaling * sigma_k
-//     dl_k = scaling * sigma_k (1 - sigma_k) * sum_j sigma_j (dw_k - dw_j) / S^2   (route_norm)
-//     dl_k = scaling * sigma_k (1 - sigma_k) * dw_k                                (else)
+//     dl_k = scaling * r_k (1 - sigma_k) * sum_j r_j (dw_k - dw_j),  r_k = sigma_k / S   (route_norm)
+//     dl_k = scaling * sigma_k (1 - sigma_k) * dw_k                                      (else)
 //     and 0 for the experts that were not chosen. The differences dw_k - dw_j
 //     are taken before the sum, which keeps the digits that dw_k S - sum_j
-//     sigma_j dw_j would cancel.
+//     sigma_j dw_j would cancel; the sigmoids are divided by S one by one, since
+//     1 / S^2 passes fp32's range where they are small (logits near -88).
 //   permutation: x_perm[p(t,k)] = x[t]
 //     dx[t] = sum_k dx_perm[p(t,k)] + dx_add[t]
 //
@@ -47,8 +48,8 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Slot k's expert and its logit, in lane k of a warp (-1 and 0 in the others,
-// and for an id out of range).
+// Slot k's expert in lane k of a warp (-1 in the others, and for an id out of
+// range), with its logit.
 struct SlotLogit {
   int e;
   float l;
@@ -64,26 +65,31 @@ __device__ __forceinline__ SlotLogit load_slot(const float* logits, const int32_
   }
   return s;
 }
+// r_k, or sigma_k without route_norm, and 1 - sigma_k (0 where there is no expert).
+struct SlotWeight {
+  float r, om;
+};
+__device__ __forceinline__ SlotWeight slot_weight(SlotLogit s, int route_norm) {
+  SlotWeight w = {0.0f, 0.0f};
+  if (s.e >= 0) w = {1.0f / (1.0f + expf(-s.l)), 1.0f / (1.0f + expf(s.l))};
+  if (route_norm) {
+    float S = w.r;  // summed as the forward does
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
+    w.r /= S;
+  }
+  return w;
+}
 // The chosen experts' dlogits of one token, by one warp; lane k holds slot k's
 // dw. The row has been zeroed before (and that is visible to this warp).
-__device__ __forceinline__ void route_grad_warp(SlotLogit s, float dw, int K, float scaling, int route_norm,
+__device__ __forceinline__ void route_grad_warp(int e, SlotWeight w, float dw, int K, float scaling, int route_norm,
                                                 float* dlogits) {
-  float sg = 0.0f, om = 0.0f;  // sigma and 1 - sigma
-  if (s.e >= 0) {
-    sg = 1.0f / (1.0f + expf(-s.l));
-    om = 1.0f / (1.0f + expf(s.l));
-  }
   float d = dw;
   if (route_norm) {
-    float S = 0.0f, a = 0.0f;
-    for (int j = 0; j < K; ++j) {
-      const float sj = __shfl_sync(0xFFFFFFFFu, sg, j), dj = __shfl_sync(0xFFFFFFFFu, dw, j);
-      S += sj;
-      a = fmaf(sj, dw - dj, a);
-    }
-    d = a / S / S;
+    d = 0.0f;
+    for (int j = 0; j < K; ++j) d = fmaf(__shfl_sync(0xFFFFFFFFu, w.r, j), dw - __shfl_sync(0xFFFFFFFFu, dw, j), d);
   }
-  if (s.e >= 0) dlogits[s.e] = scaling * sg * om * d;
+  if (e >= 0) dlogits[e] = scaling * w.r * w.om * d;
 }
 
 // One warp per (token, slot): it reads the token's dout and one y row, writes
@@ -173,11 +179,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps) combine_bwd_kernel(
       if (lane == 0) dots[tok * K + k] = acc;
     }
   }
+  SlotWeight weight = {0.0f, 0.0f};
+  if (dlogits && sw == 0) weight = slot_weight(slot, route_norm);  // while the token's other warps finish
   __syncthreads();
   if (sw != 0 || t >= T) return;  // one warp per token
   const float dw = lane < K ? dots[tok * K + lane] : 0.0f;
   if (lane < K) dtopk_w[(size_t)t * K + lane] = dw;
-  if (dlogits) route_grad_warp(slot, dw, K, scaling, route_norm, dlogits + (size_t)t * E);
+  if (dlogits) route_grad_warp(slot.e, weight, dw, K, scaling, route_norm, dlogits + (size_t)t * E);
 }
 
 // The routing's gradient alone: one warp per token.
@@ -192,7 +200,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
   for (int e = lane; e < E; e += 32) dl[e] = 0.0f;
   __syncwarp();
   const SlotLogit slot = load_slot(logits + (size_t)t * E, topk_idx + (size_t)t * K, E, K, status);
-  route_grad_warp(slot, lane < K ? dtopk_w[(size_t)t * K + lane] : 0.0f, K, scaling, route_norm, dl);
+  route_grad_warp(slot.e, slot_weight(slot, route_norm), lane < K ? dtopk_w[(size_t)t * K + lane] : 0.0f, K, scaling,
+                  route_norm, dl);
 }
 
 // dx: a work unit is one token's chunk of 8 * blockDim columns; a thread adds

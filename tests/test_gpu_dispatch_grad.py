@@ -207,3 +207,37 @@ def test_no_tokens_bad_indices_and_refusals(handle):
     with pytest.raises(moe.MoEError):
         moe.route_backward(handle, cfg, logits, idx, dtw, logits)
     assert handle.device_status() == 0
+
+
+@pytest.mark.parametrize("lo,hi,std", [(-88.6, -86.0, 1.0), (-88.6, -88.0, 300.0), (-60.0, -40.0, 1.0), (20.0, 90.0, 1.0)])
+def test_routing_weights_of_far_logits(handle, lo, hi, std):
+    """Weights divided by their sum stay of order one however small the sigmoids are, and so does their gradient.
+    Down to 1e-39, where fp32 has 2^-150 of absolute rounding left, a sigmoid is good to 4 u, so a weight to (K + 18) u
+    and the gradient, two weights and a sum of K terms, to (2 K + 48) u of its absolute sum; 1 - sigma is good to 4 u or, below
+    fp32's normal numbers, to 2^-126."""
+    T, H, E, K = 70, 64, 24, 6
+    g = torch.Generator(device="cuda").manual_seed(11)
+    cfg = moe.make_config(T, H, E, K, 64, 0, 2.826, True)
+    logits = torch.rand((T, E), device="cuda", generator=g) * (hi - lo) + lo
+    idx, tw = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    moe.route(handle, cfg, logits, idx, tw)
+    assert tw.isfinite().all()
+    dw, dl = torch.randn((T, K), device="cuda", generator=g) * std, torch.empty((T, E), device="cuda")
+    moe.route_backward(handle, cfg, logits, idx, dw, dl)
+    l = torch.gather(logits, 1, idx.long()).double()
+    sg, om = torch.sigmoid(l), torch.sigmoid(-l)
+    r = sg / sg.sum(1, keepdim=True)
+    diff = dw.double()[:, :, None] - dw.double()[:, None, :]
+    want = 2.826 * r * om * (r[:, None, :] * diff).sum(2)
+    size = 2.826 * r * om * (r[:, None, :] * diff.abs()).sum(2)
+    got = torch.gather(dl, 1, idx.long()).double()
+    assert ((got - want).abs() <= ((2 * K + 48) * U + 2.0 ** -126 / om) * size + 2.0 ** -149).all()
+    rest = dl.clone().scatter_(1, idx.long(), 0.0)
+    assert (rest == 0).all()
+    # with the combine's gradient in front: y such that dtopk_w is dw, exactly
+    f2p = torch.arange(T * K, dtype=torch.int32, device="cuda")
+    y, dout = torch.zeros((T * K, H), device="cuda"), torch.zeros((T, H), dtype=BF, device="cuda")
+    y[:, 3], dout[:, 3] = dw.view(-1), 1.0
+    dl2, dtw, dy = torch.empty_like(dl), torch.empty_like(dw), torch.empty((T * K, H), dtype=BF, device="cuda")
+    moe.combine_backward(handle, cfg, dout, y, tw, f2p, dy, dtw, topk_idx=idx, logits=logits, dlogits=dl2)
+    assert torch.equal(dtw, dw) and torch.equal(dl2, dl)
