@@ -536,8 +536,8 @@ MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_
  * (nullable; rows outside every group are not written, and such rows of a and
  * dy may hold anything, NaN too); dw_gate, dw_up
  * [num_groups, I, H] and dw_down [num_groups, H, I] bf16 (all three or none;
- * overwritten; a group without rows gets zeros). At least one of da and the
- * dw's. No output overlaps an input. dtype: MOE_BF16 (else
+ * overwritten; a group without rows gets zeros). With rows, at least one of
+ * da and the dw's. No output overlaps an input. dtype: MOE_BF16 (else
  * MOE_ERR_UNSUPPORTED). offsets, limits: as moe_grouped_swiglu_gemm, and H,
  * I <= 65536. */
 MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups, int rows, int H, int I,

@@ -179,7 +179,7 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
   if (dtype != MOE_BF16) return is_mx_dtype(dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
   if (offsets == nullptr && num_groups != 1) return MOE_ERR_INVALID_ARG;
   const int dws = (dw_gate != nullptr) + (dw_up != nullptr) + (dw_down != nullptr);
-  if ((dws != 0 && dws != 3) || (dws == 0 && !da)) return MOE_ERR_INVALID_ARG;
+  if ((dws != 0 && dws != 3) || (rows > 0 && dws == 0 && !da)) return MOE_ERR_INVALID_ARG;
   if (!w_gate || !w_up || !w_down || !ws || (rows > 0 && (!a || !dy))) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(a, dy, offsets, w_gate, w_up, w_down, da, dw_gate, dw_up, dw_down, ws)) return MOE_ERR_INVALID_ARG;
   const GradWs L = grad_ws(rows, num_groups, I);

@@ -306,3 +306,11 @@ def test_dropped_pairs_leave_nothing_in_the_weights(handle):
         got.append(_run(handle, dict(p, dy=dy)))
     for k in got[0]:
         assert torch.equal(got[0][k], got[1][k]), k
+
+
+@pytest.mark.parametrize("groups,offsets", [(2, True), (1, True), (1, False)])
+def test_no_rows_and_no_weight_gradients(handle, groups, offsets):
+    """A step without rows under frozen weights: the only output asked for has no elements."""
+    p = _problem([0] * groups, 64, 128)
+    o = _run(handle, p, want=("da",), offsets=offsets)
+    assert o["da"].shape == (0, 64) and all((o[k] == 7.0).all() for k in ("dg", "du", "dd"))
