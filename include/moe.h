@@ -537,9 +537,9 @@ MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_
  * dy may hold anything, NaN too); dw_gate, dw_up
  * [num_groups, I, H] and dw_down [num_groups, H, I] bf16 (all three or none;
  * overwritten; a group without rows gets zeros). With rows, at least one of
- * da and the dw's. No output overlaps an input. dtype: MOE_BF16 (else
- * MOE_ERR_UNSUPPORTED). offsets, limits: as moe_grouped_swiglu_gemm, and H,
- * I <= 65536. */
+ * da and the dw's. No output, nor ws, overlaps an input or another output
+ * (MOE_ERR_INVALID_ARG). dtype: MOE_BF16 (else MOE_ERR_UNSUPPORTED). offsets,
+ * limits: as moe_grouped_swiglu_gemm, and H, I <= 65536. */
 MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups, int rows, int H, int I,
                                                  moe_dtype_t dtype, const void* a, const void* dy,
                                                  const int32_t* offsets, const void* w_gate, const void* w_up,

@@ -23,6 +23,15 @@ bool all_aligned(P... p) {
   return (ptr_aligned16(p) && ...);
 }
 
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+
 bool norm_shape_ok(int64_t rows, int H, int res_type) {
   return rows >= 0 && rows < (1ll << 31) && H >= 1 && H <= kMaxNormCols &&
          (res_type == MOE_RES_BF16 || res_type == MOE_RES_F32);
@@ -184,6 +193,17 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
   if (!all_aligned(a, dy, offsets, w_gate, w_up, w_down, da, dw_gate, dw_up, dw_down, ws)) return MOE_ERR_INVALID_ARG;
   const GradWs L = grad_ws(rows, num_groups, I);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  // da is written while the weight gradients still read a and dy.
+  const size_t row_bytes = (size_t)rows * H * 2, w_bytes = (size_t)num_groups * H * I * 2;
+  const Span written[] = {{da, row_bytes}, {dw_gate, w_bytes}, {dw_up, w_bytes}, {dw_down, w_bytes}, {ws, L.total}};
+  const Span read[] = {{a, row_bytes},       {dy, row_bytes},   {offsets, 4 * ((size_t)num_groups + 1)},
+                       {w_gate, w_bytes}, {w_up, w_bytes}, {w_down, w_bytes}};
+  for (const Span& w : written) {
+    for (const Span& r : read)
+      if (overlap(w, r)) return MOE_ERR_INVALID_ARG;
+    for (const Span& o : written)
+      if (&o != &w && overlap(w, o)) return MOE_ERR_INVALID_ARG;
+  }
   const moe_status_t st = bind_handle(h);
   if (st != MOE_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);

@@ -314,3 +314,38 @@ def test_no_rows_and_no_weight_gradients(handle, groups, offsets):
     p = _problem([0] * groups, 64, 128)
     o = _run(handle, p, want=("da",), offsets=offsets)
     assert o["da"].shape == (0, 64) and all((o[k] == 7.0).all() for k in ("dg", "du", "dd"))
+
+
+def test_overlaps_are_refused(handle):
+    """Outputs and the workspace are apart from the inputs and from each other; neighbours may touch."""
+    rows, H, I, G = 32, 128, 64, 2
+    p = _problem([20, 12], H, I)
+    size = moe.grouped_gemm_backward_workspace_size(rows, H, I, num_groups=G)
+    two = torch.empty((2 * rows, H), dtype=BF, device="cuda")
+    two[:rows] = p["a"]
+    a, wdn = two[:rows], G * H * I
+    weights = torch.empty((2 * wdn,), dtype=BF, device="cuda")
+    wg, dg = weights[:wdn].view(G, I, H), weights[wdn:].view(G, I, H)
+    wg.copy_(p["wg"])
+    ws = torch.empty(2 * size, dtype=torch.uint8, device="cuda")
+
+    def call(**kw):
+        d = dict(a=a, dy=p["dy"], offsets=p["offsets"], wg=wg, wu=p["wu"], wd=p["wd"], da=two[rows:], dg=dg,
+                 du=torch.empty_like(wg), dd=torch.empty_like(p["wd"]), ws=ws[:size])
+        d.update(kw)
+        moe.grouped_swiglu_backward(handle, d["a"], d["dy"], d["offsets"], d["wg"], d["wu"], d["wd"], d["da"], d["dg"],
+                                    d["du"], d["dd"], d["ws"], num_groups=G, H=H, I=I)
+        return d
+
+    o = call()
+    _against_formulas(p, dict(o, da=o["da"]))
+    inside = ws[:rows * H * 2].view(BF).view(rows, H)
+    for kw in (dict(da=a), dict(da=p["dy"]), dict(da=two[rows // 2:rows // 2 + rows]), dict(da=two[rows - 1:2 * rows - 1]),
+               dict(dg=wg), dict(dg=weights[64:64 + wdn].view(G, I, H)), dict(du=p["wu"]), dict(dd=p["wd"]), dict(du=dg),
+               dict(dd=dg.view(G, H, I)), dict(da=dg.view(-1)[:rows * H].view(rows, H)), dict(da=inside), dict(a=inside),
+               dict(dy=inside), dict(offsets=ws[256:268].view(torch.int32))):
+        with pytest.raises(moe.MoEError) as e:
+            call(**kw)
+        assert e.value.status == moe.MOE_ERR_INVALID_ARG, list(kw)
+    call(wu=wg)  # inputs may be one tensor
+    assert handle.device_status() == 0
