@@ -60,17 +60,19 @@ def exported_names() -> list[str]:
     return re.findall(r"MOE_API\s+[\w\s\*]+?\b(moe_\w+)\s*\(", text)
 
 
+def _missing(path: str) -> str:
+    return f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')"
+
+
 def load(build_if_missing: bool = False):
     """Load the compiled library; raise if it is not built."""
     global _lib
     if _lib is not None:
         return _lib
-    missing = [p for p in (LIB_PATH, _build.BINDING) if not os.path.exists(p)]
-    if missing:
-        if build_if_missing:
-            _build.build()
-        else:
-            raise ImportError(f"{missing[0]} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+    if build_if_missing and not (os.path.exists(LIB_PATH) and os.path.exists(_build.BINDING)):
+        _build.build()
+    if not os.path.exists(LIB_PATH):
+        raise ImportError(_missing(LIB_PATH))
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     PS = ctypes.POINTER(ctypes.c_size_t)
@@ -362,10 +364,13 @@ _native_module = None
 
 
 def _native():
-    """The compiled binding: the tensors' checks and the call in one step."""
+    """The compiled binding: the tensors' checks and the call in one step. Of this interpreter, and only for the entry
+    points around the layer: the layer's own go through load()."""
     global _native_module
     if _native_module is None:
         load()
+        if not os.path.exists(_build.BINDING):
+            raise ImportError(_missing(_build.BINDING))
         from . import _binding
 
         # the current stream's address without building a Stream object (3 us of a small call), where torch has that

@@ -3,7 +3,9 @@
 Each translation unit compiles in parallel (a few seconds each), then nvcc
 links the shared library. Host code is compiled with hidden visibility so only
 the MOE_API entry points of include/moe.h are exported. csrc/binding.c becomes
-the CPython module _binding beside the library that it is linked to.
+the CPython module _binding beside the library that it is linked to; where it
+does not compile (no Python.h), the library alone is built, with a warning, and
+the Python functions around the layer raise ImportError.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -42,16 +45,22 @@ def _deps() -> list[str]:
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def up_to_date(target: str = LIB) -> bool:
+    if not os.path.exists(target):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = os.path.getmtime(target)
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and up_to_date():
-        return LIB
+    if force or not up_to_date():
+        _build_library(verbose, extra)
+    if force or not up_to_date(BINDING):
+        _build_binding()
+    return LIB
+
+
+def _build_library(verbose: bool, extra: list[str] | None) -> None:
     os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()
     extra = extra or []
@@ -77,15 +86,25 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def _build_binding() -> None:
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden", "-I",
            sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.c"), "-o", tmp, "-L", PKG,
            "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"compiling the binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return LIB
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.returncode != 0 and f"{r.stdout}\n{r.stderr}"
+    except OSError as e:  # no compiler
+        failed = str(e)
+    if not failed:
+        os.replace(tmp, BINDING)
+        return
+    if os.path.exists(BINDING):  # of an older source
+        os.remove(BINDING)
+    warnings.warn(f"_binding is not built: the functions around the layer and of its gradient will raise ImportError\n{failed}",
+                  stacklevel=3)
 
 
 if __name__ == "__main__":

@@ -1,4 +1,5 @@
 """The compiled binding's refusals of tensors (no GPU, no launch)."""
+import os
 import types
 
 import pytest
@@ -51,3 +52,34 @@ def test_arguments_of_other_kinds():
         moe.permute_backward(H, None, X, X, X)  # not a Config
     with pytest.raises(AttributeError):
         moe.add_rmsnorm(H, [1.0], X[0], 1e-5)
+
+
+def test_the_layer_loads_without_the_binding(monkeypatch, tmp_path):
+    monkeypatch.setattr(moe, "_lib", None)
+    monkeypatch.setattr(moe, "_native_module", None)
+    monkeypatch.setattr(moe._build, "BINDING", str(tmp_path / "_binding.so"))
+    assert moe.load() is not None and moe.status_string(0) == "ok"
+    assert moe.workspace_size(moe.make_config(4, 64, 8, 2, 64, 64, 1.0)) > 0
+    with pytest.raises(ImportError, match="_binding.so is missing"):
+        moe.add_rmsnorm(H, X, X[0], 1e-5, out=X)
+
+
+def test_the_library_builds_without_python_headers(monkeypatch, tmp_path):
+    target = tmp_path / "_binding.so"
+    target.write_bytes(b"of an older source")
+    os.utime(target, (0, 0))
+    monkeypatch.setattr(moe._build, "BINDING", str(target))
+    monkeypatch.setattr(moe._build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    before = os.path.getmtime(moe._build.LIB)
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert moe._build.build() == moe._build.LIB
+    assert not target.exists() and os.path.getmtime(moe._build.LIB) == before
+
+
+def test_the_binding_builds_alone(monkeypatch, tmp_path):
+    """For another interpreter beside a library that is there."""
+    target = tmp_path / "_binding.so"
+    monkeypatch.setattr(moe._build, "BINDING", str(target))
+    before = os.path.getmtime(moe._build.LIB)
+    moe._build.build()
+    assert target.exists() and os.path.getmtime(moe._build.LIB) == before
