@@ -122,3 +122,15 @@ def test_the_example_trains_and_serves():
     # Codes from the fp32 norm against codes from its bf16 rounding: 2^-8 / sqrt(3) into a 3-bit mantissa's
     # quantiser moves an element by at most one step now and then; the layer's output by a few 1e-2 at most.
     assert ((out.float() - inside.float()).norm() / inside.float().norm()).item() < 5e-2
+
+
+def test_a_block_of_one_token():
+    shape = synth.MoEShape("one", T=1, H=128, E=8, K=2, I=64, I_shared=64)
+    b = _block(shape, BF)
+    x, r, dout = (torch.randn((1, shape.H), device="cuda").to(BF) for _ in range(3))
+    b.forward(x, r)
+    grads = b.backward(dout, r)
+    _, _, want = _autograd(b, x, r, dout, r, b.topk_idx)
+    for k, v in want.items():
+        assert (grads[k].double() - v).norm() <= 2e-2 * v.norm(), k
+    assert b.handle.device_status() == 0

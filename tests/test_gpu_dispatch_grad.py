@@ -241,3 +241,10 @@ def test_routing_weights_of_far_logits(handle, lo, hi, std):
     dl2, dtw, dy = torch.empty_like(dl), torch.empty_like(dw), torch.empty((T * K, H), dtype=BF, device="cuda")
     moe.combine_backward(handle, cfg, dout, y, tw, f2p, dy, dtw, topk_idx=idx, logits=logits, dlogits=dl2)
     assert torch.equal(dtw, dw) and torch.equal(dl2, dl)
+
+
+@pytest.mark.parametrize("T,H,E,K,norm,drop", [
+    (700, 4096, 192, 8, True, 40), (1021, 1088, 64, 5, False, 7), (2600, 4096, 192, 8, True, 0),  # passes, waves of blocks
+    (5000, 512, 64, 4, True, 3), (900, 2112, 40, 20, True, 11)])
+def test_batches(handle, T, H, E, K, norm, drop):
+    test_against_formulas(handle, T, H, E, K, norm, drop)

@@ -349,3 +349,40 @@ def test_overlaps_are_refused(handle):
         assert e.value.status == moe.MOE_ERR_INVALID_ARG, list(kw)
     call(wu=wg)  # inputs may be one tensor
     assert handle.device_status() == 0
+
+
+@pytest.mark.parametrize("G,H,I", [(64, 1024, 768), (220, 512, 320), (220, 1024, 768)])
+def test_strips_of_several_tiles(handle, G, H, I):
+    """Many groups: strips of two, three and four tiles that share their A columns, groups longer than the ring beside
+    them, with six stages and with five. Every group's results are, bit for bit, those of a call with few groups, whose
+    strips are single tiles; then the same where rows past a group's end have to be cleared."""
+    g = torch.Generator().manual_seed(G + H)
+    counts = torch.randint(0, 70, (G,), generator=g).tolist()
+    counts[3], counts[10], counts[20], counts[30], counts[40], counts[G - 1] = 0, 401, 384, 385, 320, 333
+    p = _problem(counts, H, I, lead=2, trail=9, seed=G)
+    clean = _run(handle, p)
+    for e in range(0, G, 8):
+        n = min(8, G - e)
+        b, end = p["off"][e], p["off"][e + n]
+        part = dict(p, off=[o - b for o in p["off"][e:e + n + 1]], a=p["a"][b:end].contiguous(), dy=p["dy"][b:end].contiguous(),
+                    offsets=p["offsets"][e:e + n + 1] - b, wg=p["wg"][e:e + n].contiguous(), wu=p["wu"][e:e + n].contiguous(),
+                    wd=p["wd"][e:e + n].contiguous(), G=n, rows=end - b)
+        few = _run(handle, part)
+        assert torch.equal(few["da"], clean["da"][b:end])
+        assert all(torch.equal(few[k], clean[k][e:e + n]) for k in ("dg", "du", "dd")), e
+    for where in ("outside", "inside"):
+        q = dict(p, a=p["a"].clone(), dy=p["dy"].clone())
+        q["dy"][p["off"][-1]:] = float("nan")
+        hit = []
+        if where == "inside":
+            hit = [11, 21, 31]
+            for e in hit:
+                q["dy"][p["off"][e]:p["off"][e + 1]] = float("nan")
+                q["a"][p["off"][e]:p["off"][e + 1]] = float("inf")
+            assert all(counts[e] for e in hit)
+        o = _run(handle, q)
+        for e in range(G):
+            if e not in hit:
+                assert torch.equal(o["da"][p["off"][e]:p["off"][e + 1]], clean["da"][p["off"][e]:p["off"][e + 1]])
+                assert all(torch.equal(o[k][e], clean[k][e]) for k in ("dg", "du", "dd")), (where, e)
+        assert all(o["dd"][e].isnan().any() for e in hit)

@@ -237,3 +237,27 @@ def test_refusals(handle):
         moe.add_rmsnorm_backward(handle, x, x, w, rstd, out, torch.empty(16, dtype=torch.uint8, device="cuda"), dweight=dw)
     assert e.value.status == moe.MOE_ERR_WORKSPACE
     assert handle.device_status() == 0
+
+
+LONG = [  # rows, H, residual: every group walks its ring at least twice over
+    (4000, 4096, "f32"), (6000, 1024, "f32"), (3000, 8192, "f32"), (1500, 8200, "f32"), (1500, 16384, "f32"),
+    (30000, 256, "f32"), (30000, 256, "bf16"), (30000, 512, "bf16"), (8000, 4096, "bf16"), (1500, 9216, "bf16"),
+    (1500, 16384, "bf16"), (5003, 1000, "bf16"),
+]
+
+
+@pytest.mark.parametrize("has_in", [True, False])
+@pytest.mark.parametrize("rows,H,res", LONG)
+def test_backward_over_many_rows(handle, rows, H, res, has_in):
+    test_backward(handle, rows, H, res, has_in)
+    rt = F32 if res == "f32" else BF
+    h, dout = _randn((rows, H), rt, 5, 3.0), _randn((rows, H), BF, 6, 0.02)
+    w = (1 + 0.2 * _randn((H,), F32, 7)).to(BF)
+    dh_in = _randn((rows, H), rt, 8, 0.02) if has_in else None
+    rstd = torch.rsqrt(h.float().square().mean(1) + EPS)
+    ws = torch.empty(moe.add_rmsnorm_backward_workspace_size(rows, H), dtype=torch.uint8, device="cuda")
+    dh, dx, dw = torch.empty_like(h), torch.empty_like(dout), torch.empty(H, device="cuda")
+    moe.add_rmsnorm_backward(handle, dout, h, w, rstd, dh, ws, dh_in=dh_in, dx=dx, dweight=dw)
+    h2, d2, dw2 = h.clone(), dout.clone(), torch.empty_like(dw)  # dh over h, dx over dout
+    moe.add_rmsnorm_backward(handle, d2, h2, w, rstd, h2, ws, dh_in=dh_in, dx=d2, dweight=dw2)
+    assert torch.equal(h2, dh) and torch.equal(d2, dx) and torch.equal(dw2, dw)
