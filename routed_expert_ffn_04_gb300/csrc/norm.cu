@@ -463,9 +463,11 @@ int norm_grad_vectors(int H, bool f32) { return H <= 256 ? 1 : (H <= 512 || (f32
 // than two per SM; then one block per SM of 512 threads for bf16 rows, which
 // halves the partial sums (1000 x 4096 13.2 -> 11.8 us, 8192 x 4096 48.7 ->
 // 47.0, 300 to 1000 x 512 4% slower), and two of 256 for fp32 rows of up to 4096
-// columns (1000 x 512 5.6 us against 6.9, 8192 x 4096 90.0 against 88.4). Longer
-// fp32 rows have a block of up to 512 threads: 3000 x 8192 69 us, with four
-// vectors in each of 256 threads 77. A function of the shape alone, so dw's
+// columns, which is within 5% of one either way (us, two / one: 1000 x 512 6.7 /
+// 6.6, 8192 x 512 16.8 / 17.3, 1000 x 2048 11.2 / 10.6, 8192 x 2048 49.3 / 48.3,
+// 1000 x 4096 19.6 / 20.2, 3000 x 4096 38.8 / 39.1, 8192 x 4096 89.9 / 88.4).
+// Longer fp32 rows have a block of up to 512 threads: 3000 x 8192 69 us, with
+// four vectors in each of 256 threads 77. A function of the shape alone, so dw's
 // summation order is the same everywhere.
 constexpr int kSms = 152;  // of a GB300
 struct BwdGrid {
