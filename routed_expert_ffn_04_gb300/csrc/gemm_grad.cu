@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   allow_next_launch();
 
   // ---- tables: row starts; tile_start[g] = tiles of groups before g; padding.
-  fill_row_start(p.k, row_start, threadIdx.x, kThreads);
+  fill_row_start_coherent(p.k, row_start, threadIdx.x, kThreads);
   const int n_wt = (p.k.N + kTileM - 1) / kTileM;
   __syncthreads();
   auto rows_of = [&](int g) {

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "gemm_sched.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -63,6 +64,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 // groups:
 __host__ __device__ inline long long padded_rows(int rows, int G) { return (long long)rows + 15ll * G; }
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
+
+// fill_row_start for launches that may begin before the one that writes the
+// offsets has ended: coherent loads, which stay behind the wait (launch.cuh).
+__device__ __forceinline__ void fill_row_start_coherent(const KParams& p, int32_t* row_start, int tid, int nthreads) {
+  for (int g = tid; g <= p.G; g += nthreads) {
+    const int v = p.offsets ? __ldcg(p.offsets + g) : (g == 0 ? 0 : p.rows);
+    row_start[g] = v < 0 ? 0 : (v > p.rows ? p.rows : v);
+  }
+}
 
 // v[0..G-1] to their exclusive sums, v[G] the total, by one warp.
 __device__ __forceinline__ void scan_warp(int32_t* v, int G, int lane) {

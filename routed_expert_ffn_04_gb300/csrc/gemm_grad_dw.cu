@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
 
   wait_until_published(p.chain.inputs_ready, p.chain.call, abort_flag + 1);
-  fill_row_start(p.k, row_start, threadIdx.x, kThreads);
+  fill_row_start_coherent(p.k, row_start, threadIdx.x, kThreads);
   int* longs = reinterpret_cast<int*>(epi_stage) + kMaxGroups + 8;  // until the loop starts
   if (threadIdx.x == 0) *longs = 0;
   __syncthreads();

@@ -102,11 +102,10 @@ __device__ __forceinline__ TileInfo decode_tile_s(int G, const int32_t* tile_sta
 
 // row_start[g] for g = 0..G (executed by all `nthreads` threads of the CTA
 // before a __syncthreads): rows [row_start[g], row_start[g+1]) are group g,
-// as group_rows clamps them. A coherent load, which stays behind a wait for the
-// launch that writes the offsets (launch.cuh).
+// as group_rows clamps them.
 __device__ __forceinline__ void fill_row_start(const KParams& p, int32_t* row_start, int tid, int nthreads) {
   for (int g = tid; g <= p.G; g += nthreads) {
-    int v = p.offsets ? __ldcg(p.offsets + g) : (g == 0 ? 0 : p.rows);
+    int v = p.offsets ? __ldg(p.offsets + g) : (g == 0 ? 0 : p.rows);
     row_start[g] = v < 0 ? 0 : (v > p.rows ? p.rows : v);
   }
 }
