@@ -65,6 +65,7 @@ def test_the_layer_loads_without_the_binding(monkeypatch, tmp_path):
 
 
 def test_the_library_builds_without_python_headers(monkeypatch, tmp_path):
+    moe._build.build()  # the library is of these sources
     target = tmp_path / "_binding.so"
     target.write_bytes(b"of an older source")
     os.utime(target, (0, 0))
@@ -78,6 +79,7 @@ def test_the_library_builds_without_python_headers(monkeypatch, tmp_path):
 
 def test_the_binding_builds_alone(monkeypatch, tmp_path):
     """For another interpreter beside a library that is there."""
+    moe._build.build()
     target = tmp_path / "_binding.so"
     monkeypatch.setattr(moe._build, "BINDING", str(target))
     before = os.path.getmtime(moe._build.LIB)
