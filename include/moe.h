@@ -546,6 +546,130 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
                                                  const void* w_down, void* da, void* dw_gate, void* dw_up,
                                                  void* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Scores whose shares the balance loss takes. */
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score_t;
+
+/* Scratch bytes moe_balance_loss needs (host-only). */
+MOE_API moe_status_t moe_balance_loss_workspace_size(const moe_config_t* cfg, int num_seqs, size_t* bytes);
+
+/* Balance loss of the router, per sequence, with the per-expert counts. With
+ * s_te = sigma(logits[t,e]) or exp(logits[t,e]) by `score`, p_te = s_te /
+ * sum_j s_tj, and sequence b of n tokens (seq_offsets[b] ..
+ * seq_offsets[b+1]-1):
+ *   counts[b,e] = #{(t,k): topk_idx[t,k] = e}      prob[b,e] = mean_t p_te
+ *   loss[b] = coef sum_e (counts[b,e] E / (K n)) prob[b,e]
+ * An even load with even scores gives loss = coef. A sequence without tokens
+ * gets zeros. Sums are fp32, in a fixed order.
+ * logits (device): [T, E] fp32; topk_idx [T, K]; seq_offsets (device): [num_seqs
+ * + 1] int32, non-decreasing, seq_offsets[num_seqs] <= T; NULL means one
+ * sequence of all tokens. Tokens of no sequence are not read. Outputs
+ * (device): counts [num_seqs, E] int32, prob [num_seqs, E] fp32, loss
+ * [num_seqs] fp32. Scores that underflow keep their ratios (the shares are
+ * those of exp(logit) then); a token whose logits are all -infinity adds
+ * nothing to prob; a NaN logit makes its sequence's prob and loss NaN. An id
+ * outside [0, E) is not counted and records MOE_DEV_BAD_EXPERT_ID. No output,
+ * nor ws, overlaps an input or another output (MOE_ERR_INVALID_ARG). Limits:
+ * num_seqs <= 2^20, coef finite. cfg->H, I, scaling and dtype are not looked
+ * at beyond their checks. */
+MOE_API moe_status_t moe_balance_loss(moe_handle_t h, const moe_config_t* cfg, moe_score_t score, float coef,
+                                      const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                                      int num_seqs, int32_t* counts, float* prob, float* loss, void* ws,
+                                      size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of moe_balance_loss (the counts have none): with f_be = counts[b,e]
+ * E / (K n), for the tokens t of sequence b
+ *   dlogits[t,e] = dloss[b] coef / n (f_be - sum_j f_bj p_tj) p_te (1 - sigma(logits[t,e]))
+ *                  + dlogits_add[t,e]
+ * without the factor (1 - sigma) for MOE_SCORE_SOFTMAX. dloss (device):
+ * [num_seqs] fp32. dlogits_add (device, nullable): [T, E] fp32, for example
+ * moe_route_backward's result. dlogits (device): [T, E] fp32 out, may be
+ * dlogits_add; no other overlap (MOE_ERR_INVALID_ARG). Rows of no sequence are
+ * not written. The rest as moe_balance_loss. */
+MOE_API moe_status_t moe_balance_loss_backward(moe_handle_t h, const moe_config_t* cfg, moe_score_t score, float coef,
+                                               const float* logits, const int32_t* counts, const int32_t* seq_offsets,
+                                               int num_seqs, const float* dloss, const float* dlogits_add,
+                                               float* dlogits, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Products in 8-bit floating point with one fp32 scale per block of 128:
+ * E4M3 codes q (uint8) and scales s, standing for q * s. Python: quantize_fp8,
+ * grouped_gemm_fp8 and so on.
+ *   rows:    a scale per row and 128 columns        [rows, ceil(cols/128)]
+ *   squares: a scale per 128 rows x 128 columns     [ceil(rows/128), ceil(cols/128)]
+ *   columns: a scale per column and 128 rows of a group (below)
+ * A last block may be shorter. Column counts are multiples of 16.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of a plain operand or result. */
+typedef enum { MOE_FLOAT_BF16 = 0, MOE_FLOAT_F32 = 1 } moe_float_t;
+
+/* Quantise `batch` matrices x [rows, cols] to rows (squares == 0) or squares:
+ * scale = max(amax / 448, 2^-126), q = E4M3(x / scale) rounded to nearest even.
+ * A block that holds an infinity or NaN gets that (or NaN) as its scale and
+ * codes of NaN. x (device): bf16 or fp32. q (device): [batch, rows, cols]
+ * uint8; scale (device): [batch, rows, ceil(cols/128)] or [batch,
+ * ceil(rows/128), ceil(cols/128)] fp32. q and scale overlap neither x nor each
+ * other. Limits: cols % 16 == 0, batch * rows * cols <= 2^40. */
+MOE_API moe_status_t moe_quantize_fp8(moe_handle_t h, const void* x, moe_float_t x_type, int64_t batch, int rows,
+                                      int cols, int squares, uint8_t* q, float* scale, moe_stream_t stream);
+
+/* Rows that any `rows` rows in num_groups groups take with each group padded
+ * to a multiple of 128 (host-only): 128 (rows / 128 + num_groups). */
+MOE_API moe_status_t moe_fp8_padded_rows(int rows, int num_groups, int64_t* padded);
+
+/* Quantise x [rows, cols] along its rows, group by group, for
+ * moe_grouped_weight_grad_fp8. Group g (rows offsets[g] .. offsets[g+1]-1)
+ * takes the padded rows from 128 sum_{j<g} ceil(n_j / 128) on, n_j the rows of
+ * group j; block i of 128 padded rows and column c have scale[i, c]; the rows
+ * that pad a group's last block have codes 0. The rule is moe_quantize_fp8's.
+ * x, offsets (device) as the products take them. q (device): [padded, cols],
+ * scale (device): [padded / 128, cols], padded = moe_fp8_padded_rows(rows,
+ * num_groups); blocks behind the last group's are left as they are. Limits as
+ * moe_grouped_gemm_fp8. */
+MOE_API moe_status_t moe_quantize_fp8_columns(moe_handle_t h, const void* x, moe_float_t x_type, int num_groups,
+                                              int rows, int cols, const int32_t* offsets, uint8_t* q, float* scale,
+                                              moe_stream_t stream);
+
+/* out[r] = sum_k a[r,k] w[g][n,k] for the rows r of each group g; with
+ * `transposed`, sum_k a[r,k] w[g][k,n] (the gradient of an input from the
+ * forward's weights as they are). fp32 accumulation, each block's exact
+ * products times its two scales.
+ * a (device): [rows, K] codes, a_scale [rows, ceil(K/128)] (rows). w (device):
+ * [num_groups, N, K] codes (transposed: [num_groups, K, N]), w_scale
+ * [num_groups] x squares of them. offsets (device): as
+ * moe_grouped_swiglu_gemm; NULL means one group of all rows (a dense product).
+ * out (device): [rows, N] bf16 or fp32, rounded once; rows of no group are
+ * not written, and such rows of a may hold anything. No overlap of out with an
+ * input (MOE_ERR_INVALID_ARG). Limits: num_groups <= 1024, N and K multiples
+ * of 16 up to 65536, rows * max(N, K) < 2^40. */
+MOE_API moe_status_t moe_grouped_gemm_fp8(moe_handle_t h, int num_groups, int rows, int N, int K, int transposed,
+                                          const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                                          const uint8_t* w, const float* w_scale, moe_float_t out_type, void* out,
+                                          moe_stream_t stream);
+
+/* The first half of the SwiGLU experts: h = silu(a W_gate^T) * (a W_up^T) per
+ * group, quantised to rows of E4M3 in the same pass (the fp32 h, by the rule of
+ * moe_quantize_fp8): the next moe_grouped_gemm_fp8's a.
+ * a [rows, H] codes with a_scale [rows, ceil(H/128)]; w_gate, w_up
+ * [num_groups, I, H] codes with s_gate, s_up, their squares' scales; q
+ * [rows, I] and scale [rows, ceil(I/128)] out (all device). The rest as
+ * moe_grouped_gemm_fp8. */
+MOE_API moe_status_t moe_grouped_gate_up_fp8(moe_handle_t h, int num_groups, int rows, int H, int I, const uint8_t* a,
+                                             const float* a_scale, const int32_t* offsets, const uint8_t* w_gate,
+                                             const float* s_gate, const uint8_t* w_up, const float* s_up, uint8_t* q,
+                                             float* scale, moe_stream_t stream);
+
+/* Gradient of the weights of out = a w^T: dw[g] = dy^T a over the rows of each
+ * group, from operands that moe_quantize_fp8_columns wrote with the same rows
+ * and offsets: dy [padded, N], dy_scale [padded / 128, N], a [padded, K],
+ * a_scale [padded / 128, K]. dw (device): [num_groups, N, K] bf16 or fp32,
+ * overwritten; a group without rows gets zeros. The rest as
+ * moe_grouped_gemm_fp8. */
+MOE_API moe_status_t moe_grouped_weight_grad_fp8(moe_handle_t h, int num_groups, int rows, int N, int K,
+                                                 const uint8_t* dy, const float* dy_scale, const uint8_t* a,
+                                                 const float* a_scale, const int32_t* offsets, moe_float_t out_type,
+                                                 void* dw, moe_stream_t stream);
+
 /* Launch one block whose thread waits on an mbarrier that nothing ever
  * arrives on, with the handle's wait limit; the wait gives up, records
  * MOE_DEV_TIMEOUT_SELFTEST in the status word and the kernel returns. Used to

@@ -7,8 +7,10 @@ refuses to run when the compiled library is missing; there is no CPU path.
 Names follow the C ABI: route, permute, grouped_swiglu_gemm, combine,
 quantize_mxfp8, quantize_mxfp4, pack_mx_scales, layer_forward, layer_forward_host;
 around the layer and its gradient: add_rmsnorm, add_rmsnorm_backward, combine_backward,
-route_backward, permute_backward, grouped_swiglu_backward. These check their tensors'
-types, sizes, device and layout (dense row-major) and raise MoEError.
+route_backward, permute_backward, grouped_swiglu_backward, balance_loss, balance_loss_backward; products in E4M3
+with one fp32 scale per block of 128: quantize_fp8, quantize_fp8_columns, grouped_gemm_fp8, grouped_gate_up_fp8,
+grouped_weight_grad_fp8. These check their tensors' types, sizes, device and layout (dense row-major) and raise
+MoEError.
 """
 from __future__ import annotations
 
@@ -31,6 +33,8 @@ DTYPES = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8_E4M3, "mxfp4": MOE_MXFP4_W4A8}
  MOE_OPT_GATHER_A, MOE_OPT_MX_TILE) = 0, 1, 2, 3, 4, 5, 6
 STAGES = ["route", "permute", "gemm_gate_up", "gemm_down", "combine", "shared", "total"]
 MOE_RES_BF16, MOE_RES_F32 = 0, 1
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_FLOAT_BF16, MOE_FLOAT_F32 = 0, 1
 DEV_TIMEOUT_SELFTEST = 4
 
 _lib = None
@@ -107,6 +111,15 @@ def load(build_if_missing: bool = False):
         "moe_permute_backward": [P, P, P, P, P, P, P],
         "moe_grouped_gemm_backward_workspace_size": [I, I, I, I, I, PS],
         "moe_grouped_swiglu_backward": [P, I, I, I, I, I, P, P, P, P, P, P, P, P, P, P, P, S, P],
+        "moe_balance_loss_workspace_size": [P, I, PS],
+        "moe_balance_loss": [P, P, I, F, P, P, P, I, P, P, P, P, S, P],
+        "moe_balance_loss_backward": [P, P, I, F, P, P, P, I, P, P, P, P],
+        "moe_quantize_fp8": [P, P, I, ctypes.c_int64, I, I, I, P, P, P],
+        "moe_fp8_padded_rows": [I, I, ctypes.POINTER(ctypes.c_int64)],
+        "moe_quantize_fp8_columns": [P, P, I, I, I, I, P, P, P, P],
+        "moe_grouped_gemm_fp8": [P, I, I, I, I, I, P, P, P, P, P, I, P, P],
+        "moe_grouped_gate_up_fp8": [P, I, I, I, I, P, P, P, P, P, P, P, P, P, P],
+        "moe_grouped_weight_grad_fp8": [P, I, I, I, I, P, P, P, P, P, I, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -435,6 +448,76 @@ def grouped_swiglu_backward(h: Handle, a, dy, offsets, w_gate, w_up, w_down, da,
     shapes (or None, all three), from the forward's inputs and dy [rows, H], all bf16."""
     _native().grouped_swiglu_backward(h.address, h.device, a, dy, offsets, w_gate, w_up, w_down, da, dw_gate, dw_up,
                                       dw_down, ws, num_groups, H, I, dtype, stream)
+
+
+def balance_loss_workspace_size(cfg: Config, num_seqs: int = 1) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_balance_loss_workspace_size(ctypes.byref(cfg), int(num_seqs), ctypes.byref(n)),
+           "moe_balance_loss_workspace_size")
+    return n.value
+
+
+def balance_loss(h: Handle, cfg: Config, logits, topk_idx, counts, prob, loss, ws, *, coef: float = 1.0,
+                 score: int = MOE_SCORE_SIGMOID, seq_offsets=None, stream=None):
+    """Balance loss of the router per sequence: counts [B, E] int32 (pairs that chose an expert), prob [B, E] fp32 (mean
+    share of its score) and loss [B] fp32 = coef sum_e counts E / (K n) prob, from logits [T, E] fp32 and topk_idx
+    [T, K]. seq_offsets [B + 1] int32 on the device, or None: one sequence of all tokens (B = 1)."""
+    _native().balance_loss(h.address, h.device, cfg, logits, topk_idx, counts, prob, loss, ws, coef, score, seq_offsets,
+                           stream)
+
+
+def balance_loss_backward(h: Handle, cfg: Config, logits, counts, dloss, dlogits, *, coef: float = 1.0,
+                          score: int = MOE_SCORE_SIGMOID, seq_offsets=None, dlogits_add=None, stream=None):
+    """Gradient of balance_loss: dlogits [T, E] fp32 from its counts and dloss [B] fp32, plus dlogits_add (for example
+    route_backward's result; may be dlogits itself). Rows of no sequence are left as they are."""
+    _native().balance_loss_backward(h.address, h.device, cfg, logits, counts, dloss, dlogits, coef, score, seq_offsets,
+                                    dlogits_add, stream)
+
+
+# ---- products in E4M3 with one fp32 scale per block of 128
+
+
+def fp8_padded_rows(rows: int, num_groups: int = 1) -> int:
+    """Rows that any `rows` rows in num_groups groups take with each group padded to a multiple of 128."""
+    n = ctypes.c_int64(0)
+    _check(load().moe_fp8_padded_rows(int(rows), int(num_groups), ctypes.byref(n)), "moe_fp8_padded_rows")
+    return n.value
+
+
+def quantize_fp8(h: Handle, x, q, scale, *, squares: bool = False, stream=None):
+    """x [..., rows, cols] bf16 or fp32 -> codes q (uint8, same shape) and fp32 scales: one per 128 columns of a row
+    ([..., rows, ceil(cols/128)]) or, with `squares`, per 128 x 128 of each matrix."""
+    rows = x.shape[-2] if x is not None and x.dim() > 1 else 1
+    _native().quantize_fp8(h.address, h.device, x, q, scale, squares, rows, stream)
+
+
+def quantize_fp8_columns(h: Handle, x, offsets, q, scale, *, num_groups: int, stream=None):
+    """x [rows, cols] -> codes and scales per column and 128 rows of a group, each group's rows from a multiple of 128
+    on: q [fp8_padded_rows(rows, num_groups), cols] uint8, scale [that / 128, cols] fp32 (grouped_weight_grad_fp8)."""
+    _native().quantize_fp8_columns(h.address, h.device, x, offsets, q, scale, num_groups, stream)
+
+
+def grouped_gemm_fp8(h: Handle, a, a_scale, offsets, w, w_scale, out, *, num_groups: int, N: int, K: int,
+                     transposed: bool = False, stream=None):
+    """out [rows, N] (bf16 or fp32) = a w^T per group: a [rows, K] codes with scales per row, w [G, N, K] codes with
+    scales per square; with `transposed`, w is [G, K, N] and out = a w. offsets None: one group."""
+    _native().grouped_gemm_fp8(h.address, h.device, a, a_scale, offsets, w, w_scale, out, num_groups, N, K, transposed,
+                               stream)
+
+
+def grouped_gate_up_fp8(h: Handle, a, a_scale, offsets, w_gate, s_gate, w_up, s_up, q, scale, *, num_groups: int, H: int,
+                        I: int, stream=None):
+    """h = silu(a w_gate^T) (a w_up^T) per group, as codes q [rows, I] and scales [rows, ceil(I/128)]."""
+    _native().grouped_gate_up_fp8(h.address, h.device, a, a_scale, offsets, w_gate, s_gate, w_up, s_up, q, scale,
+                                  num_groups, H, I, stream)
+
+
+def grouped_weight_grad_fp8(h: Handle, dy, dy_scale, a, a_scale, offsets, dw, *, rows: int, num_groups: int, N: int,
+                            K: int, stream=None):
+    """dw [G, N, K] (bf16 or fp32) = dy^T a over each group's rows, of quantize_fp8_columns' results for the same `rows`
+    and offsets."""
+    _native().grouped_weight_grad_fp8(h.address, h.device, dy, dy_scale, a, a_scale, offsets, dw, rows, num_groups, N, K,
+                                      stream)
 
 
 def make_weights(w: dict) -> Weights:

@@ -274,7 +274,8 @@ MOE_API moe_status_t moe_create(int device, moe_handle_t* out) {
   h->num_sms = sms;
   if (gemm_prepare_device() != cudaSuccess || gemm_mx_prepare_device() != cudaSuccess ||
       permute_prepare_device() != cudaSuccess || gemm_grad_prepare_device() != cudaSuccess ||
-      norm_prepare_device() != cudaSuccess ||
+      norm_prepare_device() != cudaSuccess || gemm_fp8_prepare_device() != cudaSuccess ||
+      balance_prepare_device() != cudaSuccess ||
       gate_small_prepare_device() != cudaSuccess ||
       cudaMalloc(&h->status, 64) != cudaSuccess ||
       cudaMemset(h->status, 0, 64) != cudaSuccess ||

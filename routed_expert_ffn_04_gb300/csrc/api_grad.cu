@@ -1,5 +1,5 @@
 // C-ABI entry points around the layer and of its gradient: argument checks and
-// workspace carving (kernels in norm.cu, dispatch_grad.cu and gemm_grad.cu).
+// workspace carving (kernels in norm.cu, dispatch_grad.cu, balance.cu and gemm_grad.cu).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -64,6 +64,26 @@ GradWs grad_ws(int rows, int G, int I) {
 uint64_t next_call() {
   static std::atomic<uint64_t> n{(uint64_t)std::chrono::system_clock::now().time_since_epoch().count() | 1};
   return n.fetch_add(1, std::memory_order_relaxed);
+}
+
+constexpr int kMaxSequences = 1 << 20;
+bool balance_shape_ok(int score, float coef, const int32_t* seq_offsets, int num_seqs) {
+  return (score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX) && std::isfinite(coef) && num_seqs >= 1 &&
+         num_seqs <= kMaxSequences && (seq_offsets || num_seqs == 1);
+}
+BalanceArgs balance_args(moe_handle_t h, const moe_config_t* cfg, int score, float coef, const float* logits,
+                         const int32_t* seq_offsets, int num_seqs) {
+  BalanceArgs a = {};
+  a.T = cfg->T;
+  a.E = cfg->E;
+  a.K = cfg->K;
+  a.B = num_seqs;
+  a.softmax = score == MOE_SCORE_SOFTMAX;
+  a.coef = coef;
+  a.logits = logits;
+  a.seq = seq_offsets;
+  a.status = handle_status_word(h);
+  return a;
 }
 
 bool grad_shape_ok(int num_groups, int rows, int H, int I) {
@@ -157,6 +177,69 @@ MOE_API moe_status_t moe_route_backward(moe_handle_t h, const moe_config_t* cfg,
   return status_of(launch_route_backward(logits, topk_idx, dtopk_w, cfg->T, cfg->E, cfg->K, cfg->scaling,
                                          cfg->route_norm, dlogits, handle_status_word(h),
                                          static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API moe_status_t moe_balance_loss_workspace_size(const moe_config_t* cfg, int num_seqs, size_t* bytes) {
+  const moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!bytes || num_seqs < 1 || num_seqs > kMaxSequences) return MOE_ERR_INVALID_ARG;
+  *bytes = align_up(balance_scratch_bytes(cfg->T, cfg->E, num_seqs), 256);
+  return MOE_OK;
+}
+
+MOE_API moe_status_t moe_balance_loss(moe_handle_t h, const moe_config_t* cfg, moe_score_t score, float coef,
+                                      const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                                      int num_seqs, int32_t* counts, float* prob, float* loss, void* ws,
+                                      size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!balance_shape_ok(score, coef, seq_offsets, num_seqs) || !counts || !prob || !loss || !ws) return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned(logits, topk_idx, seq_offsets, counts, prob, loss, ws)) return MOE_ERR_INVALID_ARG;
+  const size_t need = align_up(balance_scratch_bytes(cfg->T, cfg->E, num_seqs), 256);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const size_t out = (size_t)num_seqs * cfg->E * 4;
+  const Span written[] = {{counts, out}, {prob, out}, {loss, (size_t)num_seqs * 4}, {ws, need}};
+  const Span read[] = {{logits, (size_t)cfg->T * cfg->E * 4}, {topk_idx, (size_t)cfg->T * cfg->K * 4},
+                       {seq_offsets, 4 * ((size_t)num_seqs + 1)}};
+  for (const Span& w : written) {
+    for (const Span& r : read)
+      if (overlap(w, r)) return MOE_ERR_INVALID_ARG;
+    for (const Span& o : written)
+      if (&o != &w && overlap(w, o)) return MOE_ERR_INVALID_ARG;
+  }
+  if ((st = bind_handle(h)) != MOE_OK) return st;
+  BalanceArgs a = balance_args(h, cfg, score, coef, logits, seq_offsets, num_seqs);
+  a.topk_idx = topk_idx;
+  a.counts = counts;
+  a.prob = prob;
+  a.loss = loss;
+  a.scratch = ws;
+  return status_of(launch_balance_loss(a, static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API moe_status_t moe_balance_loss_backward(moe_handle_t h, const moe_config_t* cfg, moe_score_t score, float coef,
+                                               const float* logits, const int32_t* counts, const int32_t* seq_offsets,
+                                               int num_seqs, const float* dloss, const float* dlogits_add,
+                                               float* dlogits, moe_stream_t stream) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!balance_shape_ok(score, coef, seq_offsets, num_seqs)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && (!logits || !counts || !dloss || !dlogits)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned(logits, counts, seq_offsets, dloss, dlogits_add, dlogits)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)cfg->T * cfg->E * 4;
+  const Span out = {dlogits, n};
+  if (overlap(out, {logits, n}) || overlap(out, {counts, (size_t)num_seqs * cfg->E * 4}) ||
+      overlap(out, {seq_offsets, 4 * ((size_t)num_seqs + 1)}) || overlap(out, {dloss, (size_t)num_seqs * 4}) ||
+      (dlogits_add != dlogits && overlap(out, {dlogits_add, n})))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = bind_handle(h)) != MOE_OK) return st;
+  BalanceArgs a = balance_args(h, cfg, score, coef, logits, seq_offsets, num_seqs);
+  a.counts = const_cast<int32_t*>(counts);
+  a.dloss = dloss;
+  a.add = dlogits_add;
+  a.dlogits = dlogits;
+  return status_of(launch_balance_loss_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 MOE_API moe_status_t moe_permute_backward(moe_handle_t h, const moe_config_t* cfg, const void* dx_perm,

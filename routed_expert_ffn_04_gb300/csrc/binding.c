@@ -289,6 +289,196 @@ static PyObject* grouped_swiglu_backward(PyObject* self, PyObject* const* a, Py_
                                           w[2], da, dw[0], dw[1], dw[2], ws, ws_bytes, st), what);
 }
 
+/* Type of a plain operand by its tensor's dtype. */
+static int float_type(PyObject* t, PyObject** dtype, moe_float_t* ft) {
+  PyObject* d = t == Py_None ? NULL : PyObject_GetAttr(t, s_dtype);
+  if (!d && t != Py_None) return 0;
+  *dtype = d == f32 ? f32 : bf16; /* another one fails at its own check */
+  *ft = d == f32 ? MOE_FLOAT_F32 : MOE_FLOAT_BF16;
+  Py_XDECREF(d);
+  return 1;
+}
+static int64_t blocks_of(int64_t n) { return n / 128 + (n % 128 != 0); }
+/* `n` integers of the arguments, each in [0, 2^31). */
+static int ints_of(PyObject* const* a, int n, int* out, const char* what) {
+  for (int i = 0; i < n; ++i) {
+    const long v = PyLong_AsLong(a[i]);
+    if (PyErr_Occurred()) return 0;
+    if (v < 0 || v >= INT32_MAX) {
+      PyObject* r = done(MOE_ERR_INVALID_ARG, what);
+      Py_XDECREF(r);
+      return 0;
+    }
+    out[i] = (int)v;
+  }
+  return 1;
+}
+/* The rows of a tensor [rows, cols], which the call's `cols` has to be. */
+static int rows_of(PyObject* t, const char* what, const char* name, int cols, int* rows) {
+  int64_t r, c;
+  if (!rows_cols(t, what, name, &r, &c)) return 0;
+  if (c != cols || r > INT32_MAX) {
+    PyObject* v = done(MOE_ERR_INVALID_ARG, what);
+    Py_XDECREF(v);
+    return 0;
+  }
+  *rows = (int)r;
+  return 1;
+}
+
+/* The sequences of a batch: offsets [B+1] or None. */
+static int sequences(PyObject* t, const char* what, int device, void** out, int* num) {
+  int64_t n;
+  *num = 1;
+  if (!tensor(t, what, "seq_offsets", i32, -1, device, 1, out)) return 0;
+  if (!*out) return t == Py_None ? 1 : (done(MOE_ERR_INVALID_ARG, what), 0);
+  if (!as_int64(PyObject_CallMethodNoArgs(t, s_numel), &n)) return 0;
+  *num = n - 1 > INT32_MAX ? INT32_MAX : (int)(n - 1);
+  return 1;
+}
+
+/* handle, device, cfg, logits, topk_idx, counts, prob, loss, ws, coef, score, seq_offsets, stream */
+static PyObject* balance_loss(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_balance_loss";
+  moe_handle_t h;
+  int dev, B, score;
+  moe_config_t c;
+  void *l, *idx, *cnt, *prob, *loss, *ws, *seq, *st;
+  size_t ws_bytes;
+  if (!count_is(n, 13) || !handle_of(a[0], a[1], &h, &dev) || !config_of(a[2], &c)) return NULL;
+  const double coef = PyFloat_AsDouble(a[9]);
+  if (PyErr_Occurred() || !ints_of(a + 10, 1, &score, what) || !sequences(a[11], what, dev, &seq, &B)) return NULL;
+  const int64_t T = c.T, BE = product(B, c.E, 1);
+  if (!tensor(a[3], what, "logits", f32, T * c.E, dev, 0, &l) || !tensor(a[4], what, "topk_idx", i32, T * c.K, dev, 0, &idx) ||
+      !tensor(a[5], what, "counts", i32, BE, dev, 0, &cnt) || !tensor(a[6], what, "prob", f32, BE, dev, 0, &prob) ||
+      !tensor(a[7], what, "loss", f32, B, dev, 0, &loss) || !workspace(a[8], what, dev, &ws, &ws_bytes) ||
+      !stream_of(a[12], a[1], &st))
+    return NULL;
+  CALL(moe_balance_loss(h, &c, (moe_score_t)score, (float)coef, l, idx, seq, B, cnt, prob, loss, ws, ws_bytes, st), what);
+}
+
+/* handle, device, cfg, logits, counts, dloss, dlogits, coef, score, seq_offsets, dlogits_add, stream */
+static PyObject* balance_loss_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_balance_loss_backward";
+  moe_handle_t h;
+  int dev, B, score;
+  moe_config_t c;
+  void *l, *cnt, *dloss, *dl, *seq, *add, *st;
+  if (!count_is(n, 12) || !handle_of(a[0], a[1], &h, &dev) || !config_of(a[2], &c)) return NULL;
+  const double coef = PyFloat_AsDouble(a[7]);
+  if (PyErr_Occurred() || !ints_of(a + 8, 1, &score, what) || !sequences(a[9], what, dev, &seq, &B)) return NULL;
+  const int64_t T = c.T;
+  if (!tensor(a[3], what, "logits", f32, T * c.E, dev, 0, &l) ||
+      !tensor(a[4], what, "counts", i32, product(B, c.E, 1), dev, 0, &cnt) ||
+      !tensor(a[5], what, "dloss", f32, B, dev, 0, &dloss) || !tensor(a[6], what, "dlogits", f32, T * c.E, dev, 0, &dl) ||
+      !tensor(a[10], what, "dlogits_add", f32, T * c.E, dev, 1, &add) || !stream_of(a[11], a[1], &st))
+    return NULL;
+  CALL(moe_balance_loss_backward(h, &c, (moe_score_t)score, (float)coef, l, cnt, seq, B, dloss, add, dl, st), what);
+}
+
+/* handle, device, x, q, scale, squares, rows (of a matrix), stream */
+static PyObject* quantize_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_quantize_fp8";
+  moe_handle_t h;
+  int dev, rows;
+  int64_t all, cols;
+  void *x, *q, *sc, *st;
+  PyObject* dt;
+  moe_float_t ft;
+  if (!count_is(n, 8) || !handle_of(a[0], a[1], &h, &dev) || !rows_cols(a[2], what, "x", &all, &cols) ||
+      !float_type(a[2], &dt, &ft) || !ints_of(a + 6, 1, &rows, what))
+    return NULL;
+  const int squares = PyObject_IsTrue(a[5]);
+  if (squares < 0) return NULL;
+  const int64_t batch = rows ? all / rows : 0;
+  const int64_t m = squares ? batch * blocks_of(rows) * blocks_of(cols) : all * blocks_of(cols);
+  if (!tensor(a[2], what, "x", dt, all * cols, dev, 0, &x) || !tensor(a[3], what, "q", u8, all * cols, dev, 0, &q) ||
+      !tensor(a[4], what, "scale", f32, m, dev, 0, &sc) || !stream_of(a[7], a[1], &st))
+    return NULL;
+  CALL(moe_quantize_fp8(h, x, ft, batch, rows, (int)cols, squares, q, sc, st), what);
+}
+
+/* handle, device, x, offsets, q, scale, num_groups, stream */
+static PyObject* quantize_fp8_columns(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_quantize_fp8_columns";
+  moe_handle_t h;
+  int dev, G;
+  int64_t rows, cols, padded;
+  void *x, *off, *q, *sc, *st;
+  PyObject* dt;
+  moe_float_t ft;
+  if (!count_is(n, 8) || !handle_of(a[0], a[1], &h, &dev) || !rows_cols(a[2], what, "x", &rows, &cols) ||
+      !float_type(a[2], &dt, &ft) || !ints_of(a + 6, 1, &G, what))
+    return NULL;
+  if (rows > INT32_MAX || moe_fp8_padded_rows((int)rows, G, &padded) != MOE_OK) return done(MOE_ERR_INVALID_ARG, what);
+  if (!tensor(a[2], what, "x", dt, rows * cols, dev, 0, &x) || !tensor(a[3], what, "offsets", i32, (int64_t)G + 1, dev, G == 1, &off) ||
+      !tensor(a[4], what, "q", u8, padded * cols, dev, 0, &q) || !tensor(a[5], what, "scale", f32, padded / 128 * cols, dev, 0, &sc) ||
+      !stream_of(a[7], a[1], &st))
+    return NULL;
+  CALL(moe_quantize_fp8_columns(h, x, ft, G, (int)rows, (int)cols, off, q, sc, st), what);
+}
+
+/* handle, device, a, a_scale, offsets, w, w_scale, out, num_groups, N, K, transposed, stream */
+static PyObject* grouped_gemm_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_grouped_gemm_fp8";
+  moe_handle_t h;
+  int dev, v[3], rows;
+  void *in, *as, *off, *w, *ws, *out, *st;
+  PyObject* dt;
+  moe_float_t ft;
+  if (!count_is(n, 13) || !handle_of(a[0], a[1], &h, &dev) || !ints_of(a + 8, 3, v, what)) return NULL;
+  const int G = v[0], N = v[1], K = v[2], transposed = PyObject_IsTrue(a[11]);
+  if (transposed < 0 || !rows_of(a[2], what, "a", K, &rows) || !float_type(a[7], &dt, &ft)) return NULL;
+  if (!tensor(a[2], what, "a", u8, (int64_t)rows * K, dev, 0, &in) ||
+      !tensor(a[3], what, "a_scale", f32, rows * blocks_of(K), dev, 0, &as) ||
+      !tensor(a[4], what, "offsets", i32, (int64_t)G + 1, dev, G == 1, &off) || !tensor(a[5], what, "w", u8, product(G, N, K), dev, 0, &w) ||
+      !tensor(a[6], what, "w_scale", f32, product(G, (int)blocks_of(N), (int)blocks_of(K)), dev, 0, &ws) ||
+      !tensor(a[7], what, "out", dt, (int64_t)rows * N, dev, 0, &out) || !stream_of(a[12], a[1], &st))
+    return NULL;
+  CALL(moe_grouped_gemm_fp8(h, G, rows, N, K, transposed, in, as, off, w, ws, ft, out, st), what);
+}
+
+/* handle, device, a, a_scale, offsets, w_gate, s_gate, w_up, s_up, q, scale, num_groups, H, I, stream */
+static PyObject* grouped_gate_up_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_grouped_gate_up_fp8";
+  moe_handle_t h;
+  int dev, v[3], rows;
+  void *in, *as, *off, *wg, *sg, *wu, *su, *q, *sc, *st;
+  if (!count_is(n, 15) || !handle_of(a[0], a[1], &h, &dev) || !ints_of(a + 11, 3, v, what)) return NULL;
+  const int G = v[0], H = v[1], I = v[2];
+  const int64_t m = product(G, H, I), ms = product(G, (int)blocks_of(H), (int)blocks_of(I));
+  if (!rows_of(a[2], what, "a", H, &rows)) return NULL;
+  if (!tensor(a[2], what, "a", u8, (int64_t)rows * H, dev, 0, &in) ||
+      !tensor(a[3], what, "a_scale", f32, rows * blocks_of(H), dev, 0, &as) ||
+      !tensor(a[4], what, "offsets", i32, (int64_t)G + 1, dev, G == 1, &off) || !tensor(a[5], what, "w_gate", u8, m, dev, 0, &wg) ||
+      !tensor(a[6], what, "s_gate", f32, ms, dev, 0, &sg) || !tensor(a[7], what, "w_up", u8, m, dev, 0, &wu) ||
+      !tensor(a[8], what, "s_up", f32, ms, dev, 0, &su) || !tensor(a[9], what, "q", u8, (int64_t)rows * I, dev, 0, &q) ||
+      !tensor(a[10], what, "scale", f32, rows * blocks_of(I), dev, 0, &sc) || !stream_of(a[14], a[1], &st))
+    return NULL;
+  CALL(moe_grouped_gate_up_fp8(h, G, rows, H, I, in, as, off, wg, sg, wu, su, q, sc, st), what);
+}
+
+/* handle, device, dy, dy_scale, a, a_scale, offsets, dw, rows, num_groups, N, K, stream */
+static PyObject* grouped_weight_grad_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char what[] = "moe_grouped_weight_grad_fp8";
+  moe_handle_t h;
+  int dev, v[4];
+  int64_t P;
+  void *dy, *ds, *in, *as, *off, *dw, *st;
+  PyObject* dt;
+  moe_float_t ft;
+  if (!count_is(n, 13) || !handle_of(a[0], a[1], &h, &dev) || !ints_of(a + 8, 4, v, what) || !float_type(a[7], &dt, &ft))
+    return NULL;
+  const int rows = v[0], G = v[1], N = v[2], K = v[3];
+  if (moe_fp8_padded_rows(rows, G, &P) != MOE_OK) return done(MOE_ERR_INVALID_ARG, what);
+  if (!tensor(a[2], what, "dy", u8, P * N, dev, 0, &dy) || !tensor(a[3], what, "dy_scale", f32, P / 128 * N, dev, 0, &ds) ||
+      !tensor(a[4], what, "a", u8, P * K, dev, 0, &in) || !tensor(a[5], what, "a_scale", f32, P / 128 * K, dev, 0, &as) ||
+      !tensor(a[6], what, "offsets", i32, (int64_t)G + 1, dev, G == 1, &off) || !tensor(a[7], what, "dw", dt, product(G, N, K), dev, 0, &dw) ||
+      !stream_of(a[12], a[1], &st))
+    return NULL;
+  CALL(moe_grouped_weight_grad_fp8(h, G, rows, N, K, dy, ds, in, as, off, ft, dw, st), what);
+}
+
 /* bad_arg, bad_status, current_stream, bfloat16, float32, int32, uint8 */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject** to[] = {&bad_arg, &bad_status, &current_stream, &bf16, &f32, &i32, &u8};
@@ -303,7 +493,9 @@ static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {FAST(setup), FAST(add_rmsnorm), FAST(add_rmsnorm_backward), FAST(combine_backward),
                                 FAST(route_backward), FAST(permute_backward), FAST(grouped_swiglu_backward),
-                                {NULL, NULL, 0, NULL}};
+                                FAST(balance_loss), FAST(balance_loss_backward), FAST(quantize_fp8),
+                                FAST(quantize_fp8_columns), FAST(grouped_gemm_fp8), FAST(grouped_gate_up_fp8),
+                                FAST(grouped_weight_grad_fp8), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__binding(void) {

@@ -1,0 +1,288 @@
+// Quantisers to E4M3 with one fp32 scale per block of 128 (fp8.cuh has the rule),
+// of bf16 or fp32 matrices:
+//   rows     128 values of a row share a scale      (a product's activations)
+//   squares  128 rows x 128 columns share a scale   (weights)
+//   columns  128 rows of a group, one column        (the weight gradient's
+//            operands: the reduction runs over the rows; each group starts at a
+//            multiple of 128 rows of the result, and zero rows fill its last block)
+// One pass: a block's values stay in registers between its maximum and its
+// codes. Bound by HBM: 2 (4) bytes in and 1 out per value.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fp8.cuh"
+#include "internal.h"
+#include "launch.cuh"
+
+namespace moe {
+namespace {
+
+// 16 bytes of input: eight bf16 or four fp32 values.
+template <bool F32>
+struct Vec {
+  static constexpr int kN = F32 ? 4 : 8;
+  uint4 raw;
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = F32 ? (&raw.x)[i] : (&raw.x)[i >> 1];
+    return __uint_as_float(F32 ? w : ((i & 1) ? (w & 0xFFFF0000u) : (w << 16)));
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t a = fp8_abs_bits(at(i));
+      t = a > t ? a : t;
+    }
+    return t;
+  }
+  __device__ __forceinline__ void store(uint8_t* q, const Fp8Block& b) const {
+    const uint32_t lo = b.code4(at(0), at(1), at(2), at(3));
+    if (F32) *reinterpret_cast<uint32_t*>(q) = lo;
+    else *reinterpret_cast<uint2*>(q) = make_uint2(lo, b.code4(at(4 & (kN - 1)), at(5 & (kN - 1)), at(6 & (kN - 1)), at(7 & (kN - 1))));
+  }
+};
+
+// ---------------------------------------------------------------- rows
+// A block of a row per 16 lanes (bf16) or warp (fp32), kBlocksInFlight of them at
+// a time.
+constexpr int kRowThreads = 256;
+constexpr int kInFlight = 4;
+
+template <bool F32>
+__global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const uint8_t* x, long long rows, int cols, int nb,
+                                                                    uint8_t* q, float* scale) {
+  constexpr int kN = Vec<F32>::kN, kLanes = 128 / kN, kEsize = F32 ? 4 : 2;
+  constexpr int kGroups = kRowThreads / kLanes;  // blocks that the thread block works on at a time
+  wait_for_previous_launch();
+  allow_next_launch();
+  const long long blocks = rows * nb;
+  const int sub = threadIdx.x % kLanes;
+  const long long first = (long long)blockIdx.x * (kGroups * kInFlight) + threadIdx.x / kLanes;
+  Vec<F32> v[kInFlight];
+  long long at[kInFlight];
+#pragma unroll
+  for (int j = 0; j < kInFlight; ++j) {
+    const long long b = first + (long long)j * kGroups;
+    v[j].raw = make_uint4(0, 0, 0, 0);
+    at[j] = -1;
+    if (b < blocks) {
+      const long long row = b / nb;
+      const int col = (int)(b - row * nb) * 128 + sub * kN;
+      if (col < cols) {
+        at[j] = row * cols + col;
+        v[j].raw = __ldcs(reinterpret_cast<const uint4*>(x + at[j] * kEsize));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kInFlight; ++j) {
+    uint32_t top = v[j].amax_bits();
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+      top = u > top ? u : top;
+    }
+    const Fp8Block blk(fp8_scale(top));
+    if (at[j] >= 0) {
+      v[j].store(q + at[j], blk);
+      if (sub == 0) scale[first + (long long)j * kGroups] = blk.scale;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- 128 x 128 tiles
+// A thread block holds a tile, 64 values per thread: rows a 16th (bf16) or an 8th
+// (fp32) of the tile apart.
+constexpr int kTileThreads = 256;
+
+template <bool F32>
+struct TileRegs {
+  static constexpr int kN = Vec<F32>::kN, kLanes = 128 / kN, kStep = kTileThreads / kLanes, kRows = 128 / kStep;
+  Vec<F32> v[kRows];
+  int col, row;  // of this thread's first value in the tile
+  __device__ __forceinline__ TileRegs() : col(threadIdx.x % kLanes * kN), row(threadIdx.x / kLanes) {}
+  // x: the tile's first element; rows and columns past `nr`, `nc` are zeros.
+  __device__ __forceinline__ void load(const uint8_t* x, long long ld, int nr, int nc) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row + i * kStep;
+      v[i].raw = make_uint4(0, 0, 0, 0);
+      if (r < nr && col < nc) v[i].raw = __ldcs(reinterpret_cast<const uint4*>(x + (r * ld + col) * (F32 ? 4 : 2)));
+    }
+  }
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(kTileThreads)
+    quantize_squares_kernel(const uint8_t* x, int rows, int cols, int row_blocks, int col_blocks, uint8_t* q, float* scale) {
+  __shared__ uint32_t tops[kTileThreads / 32];
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int cb = blockIdx.x % col_blocks;
+  const long long rb_all = blockIdx.x / col_blocks;  // of all matrices
+  const long long mat = rb_all / row_blocks;
+  const int rb = (int)(rb_all - mat * row_blocks);
+  const long long at = (mat * rows + rb * 128ll) * cols + cb * 128;
+  const int nr = rows - rb * 128, nc = cols - cb * 128;
+  TileRegs<F32> t;
+  t.load(x + at * (F32 ? 4 : 2), cols, nr, nc);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < TileRegs<F32>::kRows; ++i) {
+    const uint32_t a = t.v[i].amax_bits();
+    top = a > top ? a : top;
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = tops[threadIdx.x & 7];
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  const Fp8Block blk(fp8_scale(top));
+  if (threadIdx.x == 0) scale[blockIdx.x] = blk.scale;
+#pragma unroll
+  for (int i = 0; i < TileRegs<F32>::kRows; ++i) {
+    const int r = t.row + i * TileRegs<F32>::kStep;
+    if (r < nr && t.col < nc) t.v[i].store(q + at + (long long)r * cols + t.col, blk);
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kTileThreads)
+    quantize_columns_kernel(const uint8_t* x, int rows, int cols, const int32_t* offsets, int G, uint8_t* q, float* scale) {
+  using T = TileRegs<F32>;
+  __shared__ uint32_t part[T::kStep][128];
+  __shared__ float scales[128];
+  __shared__ int where[3];
+  wait_for_previous_launch();
+  allow_next_launch();
+  // The group whose blocks of 128 rows this one is of: every lane of a warp takes
+  // some groups, and the one whose blocks end past blockIdx.y looks for it.
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (G + 31) / 32, b = lane * per < G ? lane * per : G, e = b + per < G ? b + per : G;
+    auto start = [&](int g) {
+      const int v = offsets ? __ldcg(offsets + g) : (g == 0 ? 0 : rows);
+      return v < 0 ? 0 : (v > rows ? rows : v);
+    };
+    int mine = 0;
+    for (int g = b, r = e > b ? start(b) : 0; g < e; ++g) {
+      const int s = start(g + 1);
+      if (s > r) mine += (s - r + 127) / 128;
+      r = s;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const int want = blockIdx.x;
+    if (lane == 31 && want >= incl) where[1] = -1;
+    if (want < incl && want >= incl - mine) {
+      int at = incl - mine;
+      for (int g = b; g < e; ++g) {
+        const int r = start(g), s = start(g + 1), n = s > r ? (s - r + 127) / 128 : 0;
+        if (want < at + n) {
+          where[0] = r + (want - at) * 128;
+          where[1] = s - where[0];
+          break;
+        }
+        at += n;
+      }
+    }
+  }
+  __syncthreads();
+  const int row0 = where[0], nr = where[1];
+  if (nr < 0) return;  // behind the last group
+  for (int cb = blockIdx.y; cb * 128 < cols; cb += gridDim.y) {
+    const int nc = cols - cb * 128;
+    T t;
+    t.load(x + ((long long)row0 * cols + cb * 128) * (F32 ? 4 : 2), cols, nr, nc);
+    uint32_t top[T::kN];
+#pragma unroll
+    for (int j = 0; j < T::kN; ++j) {
+      top[j] = 0;
+#pragma unroll
+      for (int i = 0; i < T::kRows; ++i) {
+        const uint32_t a = fp8_abs_bits(t.v[i].at(j));
+        top[j] = a > top[j] ? a : top[j];
+      }
+      part[t.row][t.col + j] = top[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < T::kStep; ++i) {
+        const uint32_t a = part[i][threadIdx.x];
+        m = a > m ? a : m;
+      }
+      const float s = fp8_scale(m);
+      scales[threadIdx.x] = s;
+      if ((int)threadIdx.x < nc) scale[(long long)blockIdx.x * cols + cb * 128 + threadIdx.x] = s;
+    }
+    __syncthreads();
+    if (t.col < nc) {
+      uint8_t* at = q + ((long long)blockIdx.x * 128 + t.row) * cols + cb * 128 + t.col;
+      uint32_t w[T::kRows][T::kN / 4];
+#pragma unroll
+      for (int j = 0; j < T::kN; ++j) {
+        const Fp8Block blk(scales[t.col + j]);
+#pragma unroll
+        for (int i = 0; i < T::kRows; ++i) {
+          const uint32_t c = __nv_cvt_float_to_fp8(blk.over(t.v[i].at(j)), __NV_SATFINITE, __NV_E4M3);
+          w[i][j / 4] = (j & 3) ? (w[i][j / 4] | c << (8 * (j & 3))) : c;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < T::kRows; ++i) {
+        uint8_t* d = at + (long long)i * T::kStep * cols;
+        if (F32) *reinterpret_cast<uint32_t*>(d) = w[i][0];
+        else *reinterpret_cast<uint2*>(d) = make_uint2(w[i][0], w[i][T::kN / 4 - 1]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize_rows(const void* x, bool f32, int64_t rows, int cols, uint8_t* q, float* scale,
+                                     cudaStream_t s) {
+  const int nb = fp8_blocks(cols);
+  if (rows == 0) return cudaSuccess;
+  const long long per = (long long)kRowThreads / (f32 ? 32 : 16) * kInFlight, grid = (rows * nb + per - 1) / per;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  const uint8_t* in = static_cast<const uint8_t*>(x);
+  return f32 ? launch_dependent(quantize_rows_kernel<true>, (int)grid, kRowThreads, 0, s, true, 1, in, rows, cols, nb, q, scale)
+             : launch_dependent(quantize_rows_kernel<false>, (int)grid, kRowThreads, 0, s, true, 1, in, rows, cols, nb, q, scale);
+}
+
+cudaError_t launch_fp8_quantize_squares(const void* x, bool f32, int64_t batch, int rows, int cols, uint8_t* q,
+                                        float* scale, cudaStream_t s) {
+  const int rb = fp8_blocks(rows), cb = fp8_blocks(cols);
+  const long long grid = batch * rb * cb;
+  if (grid == 0) return cudaSuccess;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  const uint8_t* in = static_cast<const uint8_t*>(x);
+  return f32 ? launch_dependent(quantize_squares_kernel<true>, (int)grid, kTileThreads, 0, s, true, 1, in, rows, cols, rb, cb, q, scale)
+             : launch_dependent(quantize_squares_kernel<false>, (int)grid, kTileThreads, 0, s, true, 1, in, rows, cols, rb, cb, q, scale);
+}
+
+cudaError_t launch_fp8_quantize_columns(const void* x, bool f32, int rows, int cols, const int32_t* offsets, int G,
+                                        uint8_t* q, float* scale, cudaStream_t s) {
+  if (rows == 0) return cudaSuccess;
+  const int blocks = (int)(fp8_padded_rows(rows, G) / 128), cb = fp8_blocks(cols);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)(cb < 65535 ? cb : 65535), 1);
+  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const uint8_t* in = static_cast<const uint8_t*>(x);
+  return f32 ? cudaLaunchKernelEx(&cfg, quantize_columns_kernel<true>, in, rows, cols, offsets, G, q, scale)
+             : cudaLaunchKernelEx(&cfg, quantize_columns_kernel<false>, in, rows, cols, offsets, G, q, scale);
+}
+
+}  // namespace moe

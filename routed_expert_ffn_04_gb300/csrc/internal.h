@@ -268,6 +268,63 @@ cudaError_t gemm_grad_dw_prepare_device();
 cudaError_t launch_grouped_weight_grad(const GroupedGradArgs& a, int dx_pairs, cudaStream_t s);
 cudaError_t launch_grouped_swiglu_backward(const GroupedGradArgs& a, cudaStream_t s);
 
+// ---- E4M3 with one fp32 scale per block of 128 (fp8.cuh): products (gemm_fp8.cu)
+enum Fp8Mode { kFp8Forward = 0, kFp8Transposed = 1, kFp8GateUp = 2, kFp8WeightGrad = 3 };
+struct Fp8GemmArgs {
+  int G;                   // number of groups
+  const int32_t* offsets;  // [G+1] device, or nullptr: one group of `rows`
+  int rows, N, K;          // GATE_UP: N = I, K = H
+  const void* a;           // [rows, K] codes; WEIGHT_GRAD: dy [fp8_padded_rows, N]
+  const float* a_scale;    // [rows, K/128]; WEIGHT_GRAD: [padded / 128, N]
+  const void *w0, *w1;     // [G, N, K] ([G, K, N] transposed); GATE_UP: gate, up; WEIGHT_GRAD: w0 = a [padded, K]
+  const float *s0, *s1;    // their scales per 128 x 128; WEIGHT_GRAD: [padded / 128, K]
+  void* out;               // [rows, N] bf16 or fp32; GATE_UP: codes; WEIGHT_GRAD: [G, N, K]
+  int out_f32;
+  float* out_scale;        // GATE_UP: [rows, N/128]
+  int num_sms;
+  int* status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t gemm_fp8_prepare_device();
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, int mode, cudaStream_t s);
+// Rows that hold any `rows` rows in G groups with each group's padded to a multiple of 128.
+inline int64_t fp8_padded_rows(int64_t rows, int64_t G) { return (rows / 128 + G) * 128; }
+// 3-D uint8 tensor map [groups, outer, inner], box {128 bytes, box_rows, 1}, 128-byte swizzle: rows past a
+// group's `outer` read as 0, not as the next group's.
+bool make_tmap_u8_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t groups,
+                     uint32_t box_rows);
+
+// Quantisers (fp8_quant.cu): x [rows, cols] bf16 or fp32, cols % 16 == 0. columns: q [fp8_padded_rows, cols],
+// scale [padded / 128, cols]; blocks behind the last group are left as they are.
+cudaError_t launch_fp8_quantize_rows(const void* x, bool f32, int64_t rows, int cols, uint8_t* q, float* scale,
+                                     cudaStream_t s);
+cudaError_t launch_fp8_quantize_squares(const void* x, bool f32, int64_t batch, int rows, int cols, uint8_t* q,
+                                        float* scale, cudaStream_t s);
+cudaError_t launch_fp8_quantize_columns(const void* x, bool f32, int rows, int cols, const int32_t* offsets, int G,
+                                        uint8_t* q, float* scale, cudaStream_t s);
+
+// ---- balance loss of the router (balance.cu)
+struct BalanceArgs {
+  int T, E, K, B;
+  bool softmax;
+  float coef;
+  const float* logits;      // [T, E]
+  const int32_t* topk_idx;  // [T, K]
+  const int32_t* seq;       // [B+1], or nullptr: one sequence of all tokens
+  int32_t* counts;          // [B, E]; the gradient reads it
+  float* prob;              // [B, E]
+  float* loss;              // [B]
+  void* scratch;            // balance_scratch_bytes
+  int* status;
+  const float* dloss;       // [B]
+  const float* add;         // [T, E] or nullptr
+  float* dlogits;           // [T, E]
+};
+cudaError_t balance_prepare_device();
+size_t balance_scratch_bytes(int T, int E, int B);
+cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s);
+cudaError_t launch_balance_loss_backward(const BalanceArgs& a, cudaStream_t s);
+
 // ---- MX quantiser (mxquant.cu)
 // q / scale / atoms may each be null. scale: row-major [rows, cols/32];
 // atoms: the scale atoms of the rows as one group (cols % 128 == 0; the rows
