@@ -30,7 +30,8 @@
 // 128 swizzled bytes, 8 rows (1024 bytes) per step of the layout, 32 rows per MMA.
 //
 // Roles per CTA (12 warps, each walking its tiles in step): 0 loads, 1 (of the
-// even CTA, the leader) issues the pair's MMAs, 4-11 are the epilogue: TMEM lanes
+// even CTA, the leader) issues the pair's MMAs, 2 and 3 multiply each block's
+// scales into factors ahead of the epilogue, 4-11 are the epilogue: TMEM lanes
 // 32 (w % 4) .., columns 128 ((w - 4) / 4) ... Both CTAs' copies of a stage
 // complete on the leader's full barrier. Every wait is bounded; on expiry the
 // CTA records a code in the status word, lets its copies and MMAs end, frees
@@ -53,17 +54,22 @@ namespace {
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSmem = 232448;  // 227 KB dynamic shared memory per CTA
 constexpr int kHalf = 128 * 128;  // a CTA's A, or B, of a stage
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 // Registers per thread: 168 at launch (three warps in each quarter of the SM),
-// then a first warpgroup of loads and MMAs hands most of its own to the two of
-// the epilogue, whose accumulators take 128: 128 x 56 + 256 x 224 = 384 x 168.
-constexpr int kRegsFew = 56, kRegsMany = 224;
-static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsMany == kThreads * 168, "registers");
-constexpr int kStgBytes = kEpiWarps * 4096;   // staging: 32 rows of 128 bytes per warp
-constexpr int kColBytes = kEpiWarps * 2 * 512;  // WEIGHT_GRAD: column factors of a block, twice; GATE_UP: row maxima
+// then a first warpgroup of loads, MMAs and scales hands most of its own to the
+// two of the epilogue, whose accumulators take 128: 128 x 56 + 256 x 224 = 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
+static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsMany == kThreads * kRegsLaunch, "registers");
+constexpr int kStgBlock = 4096;               // staging: 32 rows of 128 bytes, two of them per warp
+constexpr int kStgWarp = 2 * kStgBlock;
+constexpr int kStgBytes = kEpiWarps * kStgWarp;
+constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
+constexpr int kFactorSlots = 4;               // blocks whose factors are kept
+constexpr int kFactors = 384;                 // of a block: rows' (twice, or once and 256 columns')
+constexpr int kColBytes = kFactorSlots * kFactors * 4 + 2048;  // and GATE_UP's row maxima
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kBarBytes = 8 * kBars + 8;  // and the TMEM address and the abort flag
 constexpr int kTableBytes = (kMaxGroups + 8) * 4 * 2;
@@ -84,9 +90,10 @@ struct Fp8Params {
   uint64_t limit_ns;
 };
 
-// a: boxes of 128, 64, 32 and 16 rows (WEIGHT_GRAD: a[0] alone, of dy).
+// a: boxes of 128, 64, 32 and 16 rows (WEIGHT_GRAD: a[0] alone, of dy). out: 32
+// rows of 128 bytes (GATE_UP: of 64).
 struct Fp8Maps {
-  CUtensorMap a[4], b0, b1;
+  CUtensorMap a[4], b0, b1, out;
 };
 
 // D (+)= A B over the CTA pair, E4M3 inputs, fp32 accumulator (M = 256, K = 32).
@@ -125,29 +132,35 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Two fp32 at a time. volatile: they stay behind the wait for their TMEM load.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
+// Loads of the scales that stay where they are written: the compiler moves
+// others down to their use, a tile or four blocks later, and waits there.
+__device__ __forceinline__ float load_now(const float* p) {
+  float v;
+  asm volatile("ld.global.ca.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
 }
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
+__device__ __forceinline__ float4 load_now(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.ca.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
 }
-__device__ __forceinline__ void add_scaled(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t factor) {
-  asm volatile(
-      "{\n\t.reg .b64 p;\n\t"
-      "mov.b64 p, {%1, %2};\n\t"
-      "fma.rn.f32x2 %0, p, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(lo), "r"(hi), "l"(factor));
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+
+// x sigma(x), 2 ulp: the approximate quotient, which is 0 past 2^126 as it should be here.
+__device__ __forceinline__ float silu_fast(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+
+// Bounded wait by a whole warp. The waits suspend (polling took issue slots from
+// the epilogue: 1053 -> 946 us for gate and up at 192 x 341 rows).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int code,
+                                          uint64_t limit_ns) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, code, limit_ns)) != 0;
 }
 
 // A tile: group, its first row (WEIGHT_GRAD: of the padded rows), the rows it
@@ -156,7 +169,8 @@ struct Tile {
   int g, row0, nrows, m0, n0, kb;
 };
 
-template <int MODE>
+// VEC: a's scales of a row start at multiples of 16 bytes.
+template <int MODE, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_fp8_kernel(const __grid_constant__ Fp8Maps m, const Fp8Params p) {
   constexpr bool kA_MN = MODE == kFp8WeightGrad, kB_MN = MODE == kFp8WeightGrad || MODE == kFp8Transposed;
@@ -169,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Shared memory (the same in both CTAs): A ring | B ring | staging | column factors | barriers | tables.
   const uint32_t b_ring = sm0 + kStages * kHalf;
   uint8_t* staging = base + 2 * kStages * kHalf;
-  float* cols = reinterpret_cast<float*>(staging + kStgBytes);
+  float* factors = reinterpret_cast<float*>(staging + kStgBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStgBytes + kColBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
+      mbar_init(tfull_bar(a), 1 + kScaleWarps);
       mbar_init(tempty_bar(a), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
@@ -309,9 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdesc = idesc_e4m3(256, 256, kA_MN, kB_MN);
       constexpr uint32_t kStepA = kA_MN ? 4096 >> 4 : 32 >> 4, kStepB = kB_MN ? 4096 >> 4 : 32 >> 4;  // 32 of k
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.status, MOE_DEV_TIMEOUT_MMA,
-                                                         p.limit_ns)) != 0;
+        return warp_wait(bar, parity, abort_flag, p.status, MOE_DEV_TIMEOUT_MMA, p.limit_ns);
       };
       Ring rg;
       Ring acc;  // TMEM buffer of the block
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < t.kb; ++kb) {
           const uint64_t da = kA_MN ? mn_desc(sm0 + rg.s * kHalf) : sw128_kmajor_desc(sm0 + rg.s * kHalf);
           const uint64_t db = kB_MN ? mn_desc(b_ring + rg.s * kHalf) : sw128_kmajor_desc(b_ring + rg.s * kHalf);
-          if (!wait_all(tempty_bar(acc.s), acc.ph ^ 1u) || !wait_all(full_bar(rg.s), rg.ph)) {
+          if (!wait_all(full_bar(rg.s), rg.ph) || !wait_all(tempty_bar(acc.s), acc.ph ^ 1u)) {
             ok = false;
             break;
           }
@@ -345,17 +357,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         drain_wait(drain_bar, 0, 200000000ull);
       }
     }
+  } else {
+    // ------------------------------------------------------------ scales
+    // The factors of each block for the epilogue: rows' for columns 0-127 and
+    // 128-255 (GATE_UP: gates, ups), or rows' and columns' (WEIGHT_GRAD). A
+    // block's factors complete its phase of tfull together with its MMAs. Slot
+    // j % 4 is free when block j - 2 is complete: its MMAs waited for the
+    // epilogue to be done with block j - 4. Loads run four blocks (WEIGHT_GRAD:
+    // one) ahead.
+    const int kbs = fp8_blocks(p.K), nbs = fp8_blocks(p.N);  // scales per row of a; blocks of w's columns
+    const int s0 = (warp - kScaleWarp0) * 64 + lane;          // rows s0 and s0 + 32 of this CTA's 128
+    Ring acc;
+    int slot = 0;
+    bool ok = true;
+    auto hand_over = [&](auto&& write) {
+      ok = warp_wait(tfull_bar(acc.s), acc.ph ^ 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+      if (!ok) return;
+      write(factors + slot * kFactors);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tfull_bar(acc.s));
+      slot = (slot + 1) % kFactorSlots;
+      acc.next(2);
+    };
+    for (int tile = pair; ok && tile < total; tile += npairs) {
+      const Tile t = decode(tile);
+      if (MODE == kFp8WeightGrad) {
+        const int n0 = t.m0 + (int)rank * 128 + s0, n1 = n0 + 32, c0 = t.n0 + (warp - kScaleWarp0) * 128 + 4 * lane;
+        const int c = c0 < p.K ? c0 : p.K - 4;
+        const int r0 = n0 < p.N ? n0 : p.N - 1, r1 = n1 < p.N ? n1 : p.N - 1;
+        struct Block {
+          float a, b;
+          float4 c;
+        };
+        auto load = [&](int kb) {
+          const size_t blk = (size_t)(t.row0 / 128 + (kb < t.kb ? kb : t.kb - 1));
+          return Block{load_now(p.sa + blk * p.N + r0), load_now(p.sa + blk * p.N + r1),
+                       load_now(reinterpret_cast<const float4*>(p.sb + blk * p.K + c))};
+        };
+        if (t.kb == 0) continue;
+        Block next = load(0);
+        for (int kb = 0; ok && kb < t.kb; ++kb) {
+          const Block cur = next;
+          next = load(kb + 1);
+          hand_over([&](float* f) {
+            f[s0] = cur.a;
+            f[s0 + 32] = cur.b;
+            *reinterpret_cast<float4*>(f + 128 + (warp - kScaleWarp0) * 128 + 4 * lane) = cur.c;
+          });
+        }
+      } else {
+        // Rows past the group's end take its last row's scales: their results are not stored.
+        const int last = t.nrows - 1, a0 = (int)rank * 128 + s0;
+        const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs;
+        const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs;
+        auto load_a = [&](const float* sa, int kb) {
+          if (VEC) return load_now(reinterpret_cast<const float4*>(sa + (kb < kbs ? kb : kbs - 4)));
+          const int e = kbs - 1;
+          return make_float4(load_now(sa + (kb < e ? kb : e)), load_now(sa + (kb + 1 < e ? kb + 1 : e)),
+                             load_now(sa + (kb + 2 < e ? kb + 2 : e)), load_now(sa + (kb + 3 < e ? kb + 3 : e)));
+        };
+        const int nb = t.n0 / 128, nb1 = MODE == kFp8GateUp || nb + 1 == nbs ? nb : nb + 1;
+        auto load_w = [&](const float* sb, int n, int kb) {  // a lane each for 32 blocks
+          const int k = kb + lane < kbs ? kb + lane : kbs - 1;
+          return load_now(sb + (MODE == kFp8Transposed ? ((size_t)t.g * kbs + k) * nbs + n : ((size_t)t.g * nbs + n) * kbs + k));
+        };
+        const float* sb1 = MODE == kFp8GateUp ? p.sb1 : p.sb;
+        float4 n0 = load_a(sa0, 0), n1 = load_a(sa1, 0);
+        float w = 0.f, w1 = 0.f, w_next = load_w(p.sb, nb, 0), w1_next = load_w(sb1, nb1, 0);
+        for (int kb0 = 0; ok && kb0 < t.kb; kb0 += 4) {
+          if ((kb0 & 31) == 0) {
+            w = w_next;
+            w1 = w1_next;
+            w_next = load_w(p.sb, nb, kb0 + 32);
+            w1_next = load_w(sb1, nb1, kb0 + 32);
+          }
+          float4 c0 = n0, c1 = n1;
+          n0 = load_a(sa0, kb0 + 4);
+          n1 = load_a(sa1, kb0 + 4);
+          const int stop = t.kb - kb0 < 4 ? t.kb : kb0 + 4;
+          for (int kb = kb0; ok && kb < stop; ++kb) {
+            const float x = __shfl_sync(0xFFFFFFFFu, w, kb & 31), y = __shfl_sync(0xFFFFFFFFu, w1, kb & 31);
+            hand_over([&](float* f) {
+              f[s0] = c0.x * x;
+              f[s0 + 32] = c1.x * x;
+              f[128 + s0] = c0.x * y;
+              f[128 + s0 + 32] = c1.x * y;
+            });
+            c0 = make_float4(c0.y, c0.z, c0.w, 0.f);
+            c1 = make_float4(c1.y, c1.z, c1.w, 0.f);
+          }
+        }
+      }
+    }
   }
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     const int q = warp & 3;                      // this warp may access TMEM lanes 32q .. 32q+31
     const int half = (warp - kEpiWarp0) >> 2;    // its 128 columns (GATE_UP: 64 of gate, 64 of up)
-    uint8_t* stg = staging + (half * 4 + q) * 4096;
-    float* colf = cols + (half * 4 + q) * 256;   // WEIGHT_GRAD: two blocks' factors
-    const int kbs = fp8_blocks(p.K);             // a's scales per row
-    const int nbs = fp8_blocks(p.N);
-    const bool vec = (kbs & 3) == 0;
+    uint8_t* stg = staging + (warp - kEpiWarp0) * kStgWarp;
     const uint32_t tempty0 = rank == 0 ? tempty_bar(0) : mapa_shared(tempty_bar(0), 0);
     auto release = [&](int buf) {
       tc_fence_before();
@@ -365,206 +465,182 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive_remote(tempty0 + 8u * buf);
       }
     };
+    const int r = (int)rank * 128 + q * 32 + lane;  // row of the tile
     Ring acc;
-    int ok = 1, seq = 0;
+    bool ok = true;
+    int seq = 0, slot = 0;
     for (int tile = pair; ok && tile < total; tile += npairs, ++seq) {
-      const Tile t = decode(tile);
-      const int r = (int)rank * 128 + q * 32 + lane;  // row of the tile
-      uint64_t sum[64];
+      const Tile c_t = decode(tile);
+      if (MODE != kFp8WeightGrad && c_t.nrows <= (int)rank * 128 + q * 32) {  // none of this warp's rows: keep step
+        for (int kb = 0; ok && kb < c_t.kb; ++kb) {
+          ok = warp_wait(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+          if (ok) release(acc.s);
+          acc.next(2);
+          slot = (slot + 1) % kFactorSlots;
+        }
+        continue;
+      }
+      // The accumulators live in this loop: nothing but its end and the results
+      // below read them, so that no copies join them with another path's.
+      float sum[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = 0;
-      // One block: wait, take the partial sums out, 32 columns loading while 32 are added.
-      auto block = [&](auto&& factor) {
-        if (lane == 0)
-          ok = mbar_wait_bounded(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns) ? 1 : 0;
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) return;
+      for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+      // 32 columns of a block's partial sums on their way while the 32 before are
+      // added, over the blocks' borders too: the next block's wait and its first
+      // load come before this one's last additions.
+      uint32_t v0[32], v1[32];
+      uint32_t tb = 0;
+      auto at = [&](int c) { return tb + (MODE == kFp8GateUp ? (c & 1) * 32 + (c >> 1) * 128 : 32 * c); };
+      auto begin = [&] {  // wait for a block and load its first columns
+        if (!warp_wait(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return false;
         tc_fence_after();
-        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 256);
-        // GATE_UP: columns 64 half .. of the gates (0-127) and of the ups (128-255).
-        auto at = [&](int c) { return MODE == kFp8GateUp ? tb + 64 * half + (c & 1) * 32 + (c >> 1) * 128 : tb + 128 * half + 32 * c; };
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(at(0), v[0]);
+        tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 256) + (MODE == kFp8GateUp ? 64 : 128) * half;
+        tmem_ld_32x32b_x32(at(0), v0);
+        return true;
+      };
+      auto arrived = [&](uint32_t (&x)[32]) {  // used behind the wait only
         tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) tmem_ld_32x32b_x32(at(c + 1), v[(c + 1) & 1]);
-          else release(acc.s);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) add_scaled(sum[16 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], factor(c, i));
-          if (c < 3) tmem_ld_wait();
-        }
-        acc.next(2);
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(x[i]));
       };
-      if (MODE != kFp8WeightGrad) {
-        const bool live = r < t.nrows;
-        if (t.nrows <= (int)rank * 128 + q * 32) {  // none of this warp's rows: keep step
-          for (int kb = 0; ok && kb < t.kb; ++kb) {
-            if (lane == 0)
-              ok = mbar_wait_bounded(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns) ? 1 : 0;
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (ok) release(acc.s);
-            acc.next(2);
-          }
-          continue;
-        } else {
-          const float* sa = p.sa + (size_t)(t.row0 + r) * kbs;
-          auto load4 = [&](int kb) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!live || kb >= kbs) return v;
-            if (vec) return __ldca(reinterpret_cast<const float4*>(sa + kb));
-            v.x = __ldca(sa + kb);
-            if (kb + 1 < kbs) v.y = __ldca(sa + kb + 1);
-            if (kb + 2 < kbs) v.z = __ldca(sa + kb + 2);
-            if (kb + 3 < kbs) v.w = __ldca(sa + kb + 3);
-            return v;
-          };
-          // w's scales of this warp's 128 columns: block nb, every kb.
-          const int nb0 = t.n0 / 128 + (MODE == kFp8GateUp ? 0 : half), nb = nb0 < nbs ? nb0 : nbs - 1;
-          const size_t step = MODE == kFp8Transposed ? nbs : 1;
-          const size_t first = MODE == kFp8Transposed ? (size_t)t.g * kbs * nbs + nb : ((size_t)t.g * nbs + nb) * kbs;
-          float4 next = load4(0);
-          float wl = 0.f, wl1 = 0.f;
-          for (int kb0 = 0; ok && kb0 < t.kb; kb0 += 4) {
-            if ((kb0 & 31) == 0) {  // a lane each for the next 32 blocks
-              const int kb = kb0 + lane;
-              wl = kb < t.kb ? __ldca(p.sb + first + kb * step) : 0.f;
-              if (MODE == kFp8GateUp) wl1 = kb < t.kb ? __ldca(p.sb1 + first + kb * step) : 0.f;
-            }
-            float4 cur = next;
-            next = load4(kb0 + 4);
-            const int stop = t.kb - kb0 < 4 ? t.kb : kb0 + 4;
+      if (c_t.kb > 0 && !begin()) goto done;
 #pragma unroll 1
-            for (int kb = kb0; ok && kb < stop; ++kb) {
-              const float f0 = cur.x * __shfl_sync(0xFFFFFFFFu, wl, kb & 31);
-              const uint64_t g0 = pack2(f0, f0);
-              if (MODE == kFp8GateUp) {
-                const float f1 = cur.x * __shfl_sync(0xFFFFFFFFu, wl1, kb & 31);
-                const uint64_t g1 = pack2(f1, f1);
-                block([&](int c, int) { return c < 2 ? g0 : g1; });
-              } else {
-                block([&](int, int) { return g0; });
-              }
-              cur = make_float4(cur.y, cur.z, cur.w, 0.f);
+      for (int kb = 0; kb < c_t.kb; ++kb) {
+        const float* f = factors + slot * kFactors;
+        slot = (slot + 1) % kFactorSlots;
+        const float f0 = f[(MODE == kFp8GateUp || MODE == kFp8WeightGrad ? 0 : half) * 128 + q * 32 + lane];
+        const float f1 = MODE == kFp8GateUp ? f[128 + q * 32 + lane] : f0;
+        f += 128 + 128 * half;  // WEIGHT_GRAD: the columns'
+        auto add = [&](int c, const uint32_t (&v)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float4 x = make_float4(c < 2 ? f0 : f1, c < 2 ? f0 : f1, c < 2 ? f0 : f1, c < 2 ? f0 : f1);
+            if (MODE == kFp8WeightGrad) {
+              const float4 y = *reinterpret_cast<const float4*>(f + 32 * c + i);
+              x = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
             }
+            sum[32 * c + i] = fmaf(__uint_as_float(v[i]), x.x, sum[32 * c + i]);
+            sum[32 * c + i + 1] = fmaf(__uint_as_float(v[i + 1]), x.y, sum[32 * c + i + 1]);
+            sum[32 * c + i + 2] = fmaf(__uint_as_float(v[i + 2]), x.z, sum[32 * c + i + 2]);
+            sum[32 * c + i + 3] = fmaf(__uint_as_float(v[i + 3]), x.w, sum[32 * c + i + 3]);
           }
-        }
-      } else {
-        const int n = t.m0 + r, c0 = t.n0 + 128 * half;
-        const size_t blk = (size_t)tile_start[t.g];
-        auto load_row = [&](int kb) { return kb < t.kb && n < p.N ? __ldca(p.sa + (blk + kb) * p.N + n) : 0.f; };
-        auto load_col = [&](int kb) {
-          const int c = c0 + 4 * lane;
-          return kb < t.kb && c < p.K ? __ldca(reinterpret_cast<const float4*>(p.sb + (blk + kb) * p.K + c))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        float row = load_row(0);
-        float4 col = load_col(0);
-        for (int kb = 0; ok && kb < t.kb; ++kb) {
-          float* slot = colf + (kb & 1) * 128;
-          *reinterpret_cast<float4*>(slot + 4 * lane) = col;
-          __syncwarp();
-          const uint64_t f = pack2(row, row);
-          row = load_row(kb + 1);
-          col = load_col(kb + 1);
-          block([&](int c, int i) { return mul2(f, *reinterpret_cast<const uint64_t*>(slot + 32 * c + 2 * i)); });
-        }
-        __syncwarp();
+        arrived(v0);
+        tmem_ld_32x32b_x32(at(1), v1);
+        add(0, v0);
+        arrived(v1);
+        tmem_ld_32x32b_x32(at(2), v0);
+        add(1, v1);
+        arrived(v0);
+        tmem_ld_32x32b_x32(at(3), v1);
+        add(2, v0);
+        arrived(v1);
+        if (MODE == kFp8WeightGrad) add(3, v1);  // its column factors are read until the release
+        release(acc.s);
+        acc.next(2);
+        if (kb + 1 < c_t.kb && !begin()) goto done;
+        if (MODE != kFp8WeightGrad) add(3, v1);
       }
-      if (!ok) break;
-
-      const int live_rows = MODE == kFp8WeightGrad ? p.N - t.m0 : t.nrows;
+      // Results go out by TMA from the warp's staging (the tensor maps' swizzles),
+      // while the next tile is summed: stores from the warps held them up for as
+      // long as three blocks (an SM stores 32 bytes a cycle). A group's last rows,
+      // fewer than 32, are stored by the warp; WEIGHT_GRAD's map ends where a
+      // group's matrix does.
       const int r0 = (int)rank * 128 + q * 32;  // this warp's first row of the tile
+      const int live_rows = MODE == kFp8WeightGrad ? p.N - c_t.m0 : c_t.nrows;
+      const bool whole = MODE == kFp8WeightGrad || r0 + 32 <= live_rows;
+      const int width = MODE == kFp8WeightGrad ? p.K : p.N;
+      auto reuse = [&] {  // the staging's last copies have left
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+      };
+      // Block h of the staging: `bytes` (64 or 128) of each row, from column col0 of `esize` bytes on.
+      auto send = [&](int h, int bytes, int esize, int col0) {
+        if (whole) {
+          if (lane == 0 && col0 < width && r0 < live_rows) {
+            const uint32_t src = smem_u32(stg + h * kStgBlock);
+            if (MODE == kFp8WeightGrad) tma_store_3d(&m.out, src, col0, c_t.m0 + r0, c_t.g);
+            else tma_store_3d(&m.out, src, col0, c_t.row0 + r0, 0);
+            bulk_commit_group();
+          }
+          return;
+        }
+        const int per = bytes / 16, col = col0 + 16 / esize * (lane % per);  // 16-byte chunks of a row
+        uint8_t* out = static_cast<uint8_t*>(p.out) + ((size_t)(c_t.row0 + r0) * width + col) * esize;
+        for (int i = lane / per; i < 32; i += 32 / per) {
+          const int chunk = (lane % per) ^ (bytes == 128 ? i & 7 : (i >> 1) & 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(stg + h * kStgBlock + i * bytes + 16 * chunk);
+          if (col < width && r0 + i < live_rows) *reinterpret_cast<uint4*>(out + (size_t)i * width * esize) = v;
+        }
+      };
       if (MODE == kFp8GateUp) {
         // h of 64 columns; the block's largest is the larger of the two halves'.
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 g = unpack2(sum[i]), u = unpack2(sum[32 + i]);
-          const float a = silu_f(g.x) * u.x, b = silu_f(g.y) * u.y;
-          sum[i] = pack2(a, b);
-          const uint32_t x = fp8_abs_bits(a), y = fp8_abs_bits(b);
+        for (int i = 0; i < 64; ++i) {
+          sum[i] = silu_fast(sum[i]) * sum[64 + i];
+          const uint32_t x = fp8_abs_bits(sum[i]);
           top = x > top ? x : top;
-          top = y > top ? y : top;
         }
         // Two slots by turns: the other warp may still read the last tile's.
-        uint32_t* tops = reinterpret_cast<uint32_t*>(cols) + (seq & 1) * 256;
-        tops[half * 128 + q * 32 + lane] = top;
+        uint32_t* tops = reinterpret_cast<uint32_t*>(factors + kFactorSlots * kFactors) + (seq & 1) * 256 + q * 32 + lane;
+        tops[half * 128] = top;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-        const uint32_t other = tops[(half ^ 1) * 128 + q * 32 + lane];
+        const uint32_t other = tops[(half ^ 1) * 128];
         const float scale = fp8_scale(top > other ? top : other);
-        if (half == 0 && r < t.nrows) p.out_scale[(size_t)(t.row0 + r) * nbs + t.n0 / 128] = scale;
+        if (half == 0 && r < c_t.nrows) p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = scale;
         const Fp8Block blk(scale);
+        reuse();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 codes: chunk c of the row's 64 bytes, at c ^ (row / 2) % 4
+        for (int c = 0; c < 4; ++c) {
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 a = unpack2(sum[8 * c + 2 * i]), b = unpack2(sum[8 * c + 2 * i + 1]);
-            w[i] = blk.code4(a.x, a.y, b.x, b.y);
+            const int e = 16 * c + 4 * i;
+            w[i] = blk.code4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
           }
           *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        fence_proxy_async_smem();
         __syncwarp();
-        uint8_t* out = static_cast<uint8_t*>(p.out);
-        const int col = t.n0 + 64 * half + 16 * (lane & 3);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // eight rows' 64 bytes per instruction
-          const int i = 8 * j + (lane >> 2);
-          const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
-          if (r0 + i < t.nrows && col < p.N) *reinterpret_cast<uint4*>(out + (size_t)(t.row0 + r0 + i) * p.N + col) = v;
-        }
-        __syncwarp();
+        send(0, 64, 1, c_t.n0 + 64 * half);
       } else {
-        // Through the warp's staging, 128 bytes of each of 32 rows at a time (16-byte
-        // chunk j of row i at j ^ i % 8), then four whole rows per store instruction.
-        const size_t row_first = MODE == kFp8WeightGrad ? (size_t)t.g * p.N + t.m0 : (size_t)t.row0;
-        const int width = MODE == kFp8WeightGrad ? p.K : p.N;
-        const int c0 = t.n0 + 128 * half;
-        auto flush = [&](uint8_t* at, int esize, int col) {  // at: this lane's column in row row_first + r0
-          __syncwarp();
-          const bool in = col < width;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int i = 4 * j + (lane >> 3);
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
-            if (in && r0 + i < live_rows) *reinterpret_cast<uint4*>(at + (size_t)i * width * esize) = v;
-          }
-          __syncwarp();
-        };
-        uint8_t* srow = stg + lane * 128;
+        const int c0 = c_t.n0 + 128 * half;
         if (p.out_f32) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c0 + 32 * c >= width) break;
+          for (int g = 0; g < 2; ++g) {
+            reuse();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 a = unpack2(sum[16 * c + 2 * j]), b = unpack2(sum[16 * c + 2 * j + 1]);
-              *reinterpret_cast<float4*>(srow + ((j ^ (lane & 7)) << 4)) = make_float4(a.x, a.y, b.x, b.y);
+            for (int j = 0; j < 16; ++j) {
+              const int e = 64 * g + 4 * j;
+              *reinterpret_cast<float4*>(stg + (j >> 3) * kStgBlock + lane * 128 + (((j & 7) ^ (lane & 7)) << 4)) =
+                  make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
             }
-            const int col = c0 + 32 * c + 4 * (lane & 7);
-            flush(static_cast<uint8_t*>(p.out) + ((row_first + r0) * width + col) * 4, 4, col);
+            fence_proxy_async_smem();
+            __syncwarp();
+            send(0, 128, 4, c0 + 64 * g);
+            send(1, 128, 4, c0 + 64 * g + 32);
           }
         } else {
+          reuse();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c0 + 64 * c >= width) break;
+          for (int j = 0; j < 16; ++j) {
+            uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 a = unpack2(sum[32 * c + 4 * j + i]);
-                w[i] = pack_bf16(a.x, a.y);
-              }
-              *reinterpret_cast<uint4*>(srow + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            const int col = c0 + 64 * c + 8 * (lane & 7);
-            flush(static_cast<uint8_t*>(p.out) + ((row_first + r0) * width + col) * 2, 2, col);
+            for (int i = 0; i < 4; ++i) w[i] = pack_bf16(sum[8 * j + 2 * i], sum[8 * j + 2 * i + 1]);
+            *reinterpret_cast<uint4*>(stg + (j >> 3) * kStgBlock + lane * 128 + (((j & 7) ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          send(0, 128, 2, c0);
+          send(1, 128, 2, c0 + 64);
         }
       }
     }
+  done:
+    tmem_ld_wait();
+    bulk_wait_group0();
   }
 
   // Both CTAs arrive here only when their roles are done (every wait is
@@ -595,6 +671,9 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
     if (MODE == kFp8GateUp) ok = ok && make_tmap_u8_3d(&m.b1, a.w1, inner, outer, G, 128);
   }
   if (MODE != kFp8GateUp) m.b1 = m.b0;
+  if (MODE == kFp8GateUp) ok = ok && make_tmap_rows(&m.out, a.out, 1, a.N, a.rows, 1, 64);
+  else if (MODE == kFp8WeightGrad) ok = ok && make_tmap_rows(&m.out, a.out, a.out_f32 ? 4 : 2, a.K, a.N, G, 128);
+  else ok = ok && make_tmap_rows(&m.out, a.out, a.out_f32 ? 4 : 2, a.N, a.rows, 1, 128);
   if (!ok) return cudaErrorInvalidValue;
   Fp8Params p = {};
   p.offsets = a.offsets;
@@ -616,17 +695,25 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
   const long long most = a.num_sms / 2;
   const int pairs = (int)(tiles < most ? tiles : most);
   if (pairs < 1) return cudaErrorInvalidValue;
-  return launch_dependent(grouped_gemm_fp8_kernel<MODE>, 2 * pairs, kThreads, kSmem, s, true, /*cluster=*/2, m, p);
+  const bool vec = MODE == kFp8WeightGrad || fp8_blocks(a.K) % 4 == 0;
+  if (vec) return launch_dependent(grouped_gemm_fp8_kernel<MODE, true>, 2 * pairs, kThreads, kSmem, s, true, /*cluster=*/2, m, p);
+  return launch_dependent(grouped_gemm_fp8_kernel<MODE, MODE == kFp8WeightGrad>, 2 * pairs, kThreads, kSmem, s, true, /*cluster=*/2, m, p);
 }
 
 }  // namespace
 
+namespace {
+template <int MODE, bool VEC>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+}  // namespace
+
 cudaError_t gemm_fp8_prepare_device() {
-  const cudaError_t errs[] = {
-      cudaFuncSetAttribute(grouped_gemm_fp8_kernel<kFp8Forward>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-      cudaFuncSetAttribute(grouped_gemm_fp8_kernel<kFp8Transposed>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-      cudaFuncSetAttribute(grouped_gemm_fp8_kernel<kFp8GateUp>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-      cudaFuncSetAttribute(grouped_gemm_fp8_kernel<kFp8WeightGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)};
+  const cudaError_t errs[] = {allow_smem<kFp8Forward, true>(),    allow_smem<kFp8Forward, false>(),
+                              allow_smem<kFp8Transposed, true>(), allow_smem<kFp8Transposed, false>(),
+                              allow_smem<kFp8GateUp, true>(),     allow_smem<kFp8GateUp, false>(),
+                              allow_smem<kFp8WeightGrad, true>()};
   for (cudaError_t e : errs)
     if (e != cudaSuccess) return e;
   return cudaSuccess;

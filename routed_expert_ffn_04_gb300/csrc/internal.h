@@ -293,6 +293,9 @@ inline int64_t fp8_padded_rows(int64_t rows, int64_t G) { return (rows / 128 + G
 // group's `outer` read as 0, not as the next group's.
 bool make_tmap_u8_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t groups,
                      uint32_t box_rows);
+// 3-D tensor map for stores of 32 rows x row_bytes (64 or 128, the swizzle too), elements of esize
+// bytes (1, 2 bf16, 4 fp32), of [groups, outer, inner] and cut off at a group's `outer`.
+bool make_tmap_rows(CUtensorMap* m, void* ptr, int esize, uint64_t inner, uint64_t outer, uint64_t groups, int row_bytes);
 
 // Quantisers (fp8_quant.cu): x [rows, cols] bf16 or fp32, cols % 16 == 0. columns: q [fp8_padded_rows, cols],
 // scale [padded / 128, cols]; blocks behind the last group are left as they are.
