@@ -67,8 +67,10 @@ typedef enum {
 typedef enum {
   MOE_BF16 = 0,       /* bf16 operands, fp32 accumulation */
   MOE_MXFP8_E4M3 = 1, /* E4M3 elements + one E8M0 scale per 32 along K */
-  MOE_MXFP4_W4A8 = 2  /* W4A8 ([Hy3] section 8.2): routed-expert weights E2M1 +
+  MOE_MXFP4_W4A8 = 2, /* W4A8 ([Hy3] section 8.2): routed-expert weights E2M1 +
                          E8M0/32 (MXFP4), activations MXFP8, shared expert W8A8 */
+  MOE_FP8_BLOCK128 = 3 /* E4M3 elements + one fp32 scale per 128 of an activation's
+                          row, per 128 x 128 of a weight (moe_quantize_fp8) */
 } moe_dtype_t;
 
 /* Layer shape. T tokens, H hidden, E routed experts, K experts per token,
@@ -76,7 +78,7 @@ typedef enum {
  * (0 = no shared expert). scaling = router_scaling_factor ([Hy3] section 一:
  * 2.826); route_norm != 0 divides the K sigmoid scores by their sum.
  * Limits: 1 <= K <= min(E, 32), E <= 1024, H % 64 == 0, I % 64 == 0,
- * I_shared % 64 == 0 (MXFP8: H, I, I_shared % 128 == 0), T * K < 2^31,
+ * I_shared % 64 == 0 (all but bf16: H, I, I_shared % 128 == 0), T * K < 2^31,
  * T*K*max(H,I) < 2^40. */
 typedef struct {
   int T, H, E, K, I, I_shared;
@@ -100,7 +102,10 @@ typedef struct {
  *   tile order: w_gate = moe_tile_mxfp4_weights(gate, up) of the [E*I, H]
  *   gate and up codes together, w_up unused (NULL), w_down =
  *   moe_tile_mxfp4_weights(down, NULL) of [E*H, I]; 32-byte aligned. Their
- *   scales and the shared expert (E4M3 + atoms) are as in MXFP8 mode. */
+ *   scales and the shared expert (E4M3 + atoms) are as in MXFP8 mode.
+ * FP8_BLOCK128 mode: w_* are E4M3 codes (uint8) in the bf16 mode's shapes, and
+ *   all of s_* and ss_* point to fp32 scales per square, as moe_quantize_fp8
+ *   writes them: s_gate, s_up [E, I/128, H/128], s_down [E, H/128, I/128]. */
 typedef struct {
   const void *w_gate, *w_up, *w_down;
   const uint8_t *s_gate, *s_up, *s_down;
@@ -203,7 +208,8 @@ MOE_API moe_status_t moe_permute_workspace_size(const moe_config_t* cfg, size_t*
  * perm_src [T*K] (permuted row -> f), flat_to_perm [T*K] (its inverse),
  * x_perm [T*K, H] = x[perm_src[r] / K]. Rows of one expert keep ascending f.
  * x (device): [T, H] bf16; MXFP8 mode: E4M3 codes with x_scale [T, H/32]
- * and x_perm_scale [T*K, H/32] (else both ignored). An expert id outside
+ * and x_perm_scale [T*K, H/32] (else both ignored); FP8_BLOCK128: the same with
+ * fp32 scales, [T, H/128] and [T*K, H/128]. An expert id outside
  * [0, E) is skipped and recorded in the device status word. */
 MOE_API moe_status_t moe_permute(moe_handle_t h, const moe_config_t* cfg, const void* x,
                                  const uint8_t* x_scale, const int32_t* topk_idx, int32_t* counts,
@@ -236,6 +242,9 @@ MOE_API moe_status_t moe_grouped_gemm_workspace_size(int rows, int num_groups, i
  *   codes of [num_groups*I, H] gate and up weights, w_up unused, w_down =
  *   moe_tile_mxfp4_weights(down, NULL) of [num_groups*H, I]; 32-byte aligned;
  *   scales and a as in MXFP8.
+ * FP8_BLOCK128: a and w_* E4M3 codes, a_scale [rows, H/128] and s_gate, s_up,
+ *   s_down (per square) fp32; h is rounded as moe_grouped_gate_up_fp8 does.
+ *   H % 128 == 0, I % 128 == 0.
  * offsets (device): [num_groups + 1] int32, non-decreasing, offsets[0] = 0,
  *   offsets[num_groups] <= rows; NULL means one group of all rows (a dense
  *   SwiGLU MLP, used for the shared expert).
@@ -333,6 +342,8 @@ MOE_API moe_status_t moe_pack_mx_scales(moe_handle_t h, const uint8_t* scale0,
  *   x_scale_or_null != NULL: x already holds E4M3 codes [T, H] (uint8) and
  *     x_scale_or_null their E8M0 scales [T, H/32], row-major, as
  *     moe_quantize_mxfp8 writes them; nothing is re-quantised.
+ * FP8_BLOCK128: the same with the rule of moe_quantize_fp8 (rows) and fp32 scales
+ *   [T, H/128].
  * bf16 mode: x_scale_or_null must be NULL (MOE_ERR_INVALID_ARG otherwise).
  * logits (device): [T, E] fp32. out (device): [T, H] bf16.
  * ws (device): at least moe_workspace_size bytes. */
@@ -411,7 +422,7 @@ MOE_API moe_status_t moe_read_stage_times(moe_handle_t h, float* ms, int* n_call
  * Limit: E * ceil(T*K / 256) <= MOE_PERMUTE_STATIC_MAX_HIST_INTS (for E = 192
  * and K = 8: T <= 43690); larger sizes return MOE_ERR_WORKSPACE before any
  * launch.
- * MXFP8 and W4A8 configs move the 1-byte E4M3 rows of x and their E8M0
+ * MXFP8, W4A8 and FP8_BLOCK128 configs move the 1-byte E4M3 rows of x and their
  * scales exactly as moe_permute does (same H rule: H % 128 == 0).
  * The first call on a device looks up the array's device address (with that
  * device current) and caches it for the life of the process; make that first

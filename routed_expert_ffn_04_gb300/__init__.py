@@ -27,8 +27,8 @@ LIB_PATH = _build.LIB
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT = range(6)
-MOE_BF16, MOE_MXFP8_E4M3, MOE_MXFP4_W4A8 = 0, 1, 2
-DTYPES = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8_E4M3, "mxfp4": MOE_MXFP4_W4A8}
+MOE_BF16, MOE_MXFP8_E4M3, MOE_MXFP4_W4A8, MOE_FP8_BLOCK128 = 0, 1, 2, 3
+DTYPES = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8_E4M3, "mxfp4": MOE_MXFP4_W4A8, "fp8": MOE_FP8_BLOCK128}
 (MOE_OPT_GEMM_MODE, MOE_OPT_STAGE_TIMING, MOE_OPT_WAIT_LIMIT_US, MOE_OPT_SHARED_FOLD, MOE_OPT_SHARED_SMS,
  MOE_OPT_GATHER_A, MOE_OPT_MX_TILE) = 0, 1, 2, 3, 4, 5, 6
 STAGES = ["route", "permute", "gemm_gate_up", "gemm_down", "combine", "shared", "total"]
@@ -491,6 +491,18 @@ def quantize_fp8(h: Handle, x, q, scale, *, squares: bool = False, stream=None):
     _native().quantize_fp8(h.address, h.device, x, q, scale, squares, rows, stream)
 
 
+def quantize_weights_fp8(h: Handle, w: dict, stream=None) -> dict:
+    """The "fp8" layers' form of a bf16 weight dict: w_* and ws_* -> E4M3 codes, s_* and ss_* -> fp32 scales per square."""
+    out = {}
+    for k, v in w.items():
+        sizes = v.shape[:-2] + (-(-v.shape[-2] // 128), -(-v.shape[-1] // 128))
+        q, sc = torch.empty(v.shape, dtype=_U8, device=v.device), torch.empty(sizes, dtype=_F32, device=v.device)
+        quantize_fp8(h, v, q, sc, squares=True, stream=stream)
+        out[k] = q
+        out[("ss_" + k[3:]) if k.startswith("ws_") else ("s_" + k[2:])] = sc
+    return out
+
+
 def quantize_fp8_columns(h: Handle, x, offsets, q, scale, *, num_groups: int, stream=None):
     """x [rows, cols] -> codes and scales per column and 128 rows of a group, each group's rows from a multiple of 128
     on: q [fp8_padded_rows(rows, num_groups), cols] uint8, scale [that / 128, cols] fp32 (grouped_weight_grad_fp8)."""
@@ -531,7 +543,8 @@ def make_weights(w: dict) -> Weights:
 
 def layer_forward(h: Handle, cfg: Config, weights: Weights, x, logits, out, ws, main=None, side=None,
                   x_scale=None):
-    """x_scale: E8M0 scales [T, H/32] when x already holds MXFP8 E4M3 codes (MX configs only)."""
+    """x_scale: E8M0 scales [T, H/32] when x already holds MXFP8 E4M3 codes (MX configs), or fp32 scales [T, H/128] of
+    FP8_BLOCK128 configs."""
     side_p = ctypes.c_void_p(side.cuda_stream) if side is not None else None
     _check(load().moe_layer_forward(h.ptr, ctypes.byref(cfg), ctypes.byref(weights), _p(x), _p(x_scale), _p(logits),
                                     _p(out), _p(ws), ws.numel() * ws.element_size(), _stream(main), side_p),
@@ -562,12 +575,16 @@ class MoELayer:
             if weights.get("s_up") is not None:  # row-major scales -> scale atoms
                 weights = pack_weights_mx(self.handle, weights)
             torch.cuda.synchronize(self.device)
+        if shape.dtype == "fp8" and weights["w_gate"].dtype != torch.uint8:
+            with torch.cuda.device(self.device):
+                weights = quantize_weights_fp8(self.handle, weights)
+                torch.cuda.synchronize(self.device)
         self.weights_t = weights
         self.weights = make_weights(weights)
         self.side = torch.cuda.Stream(device=self.device) if side_stream else None
 
     def __call__(self, x, logits, out=None, main=None, x_scale=None):
-        """x: [T, H] bf16, or (MX layers, with x_scale) MXFP8 E4M3 codes with their E8M0 scales."""
+        """x: [T, H] bf16, or (with x_scale) E4M3 codes with their scales: E8M0 of MX layers, fp32 [T, H/128] of "fp8" ones."""
         if out is None:
             out = torch.empty((self.shape.T, self.shape.H), dtype=torch.bfloat16, device=self.device)
         layer_forward(self.handle, self.cfg, self.weights, x, logits, out, self.ws, main=main, side=self.side,

@@ -13,9 +13,12 @@ class MoEBlock:
 
     weights: w_gate, w_up [E, I, H], w_down [E, H, I], and with I_shared > 0 ws_gate, ws_up [I_shared, H], ws_down
     [H, I_shared]; w_router [E, H]; norm_weight [H]; all bf16 on the block's device. forward() keeps what backward()
-    needs until the next forward(); the tensors they return are the block's own buffers."""
+    needs until the next forward(); the tensors they return are the block's own buffers. With balance_coef, forward()
+    leaves the router's balance loss in `balance` ([1] fp32; the batch is one sequence) and the pairs that chose each
+    expert in `load` ([1, E]), and backward() adds the loss's gradient."""
 
-    def __init__(self, shape, weights: dict, w_router, norm_weight, eps: float = 1e-5, residual_dtype=torch.bfloat16):
+    def __init__(self, shape, weights: dict, w_router, norm_weight, eps: float = 1e-5, residual_dtype=torch.bfloat16,
+                 balance_coef: float = 0.0):
         if shape.dtype != "bf16":
             raise ValueError("MoEBlock trains bf16 layers")
         self.shape, self.w, self.w_router, self.norm_weight, self.eps = shape, weights, w_router, norm_weight, eps
@@ -44,6 +47,11 @@ class MoEBlock:
         if s.I_shared:
             sizes += [moe.grouped_gemm_workspace_size(T, H, s.I_shared),
                       moe.grouped_gemm_backward_workspace_size(T, H, s.I_shared)]
+        self.balance_coef = balance_coef
+        if balance_coef:
+            self.load, self.prob, self.balance = new(1, E, dt=i32), new(1, E, dt=f32), new(1, dt=f32)
+            self.one = torch.ones(1, device=self.dev)
+            sizes.append(moe.balance_loss_workspace_size(self.cfg))
         self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=self.dev)  # one stream: the calls take turns
 
     def forward(self, x, residual=None, stream=None):
@@ -52,6 +60,9 @@ class MoEBlock:
         moe.add_rmsnorm(h, x, self.norm_weight, self.eps, residual=residual, h_out=self.h, out=self.n, rstd=self.rstd,
                         stream=stream)
         moe.gate_route(h, cfg, self.n, self.w_router, self.topk_idx, self.topk_w, logits_out=self.logits, stream=stream)
+        if self.balance_coef:
+            moe.balance_loss(h, cfg, self.logits, self.topk_idx, self.load, self.prob, self.balance, self.ws,
+                             coef=self.balance_coef, stream=stream)
         moe.permute(h, cfg, self.n, self.topk_idx, self.counts, self.offsets, self.perm_src, self.flat_to_perm,
                     self.x_perm, self.ws, stream=stream)
         moe.grouped_swiglu_gemm(h, self.x_perm, self.offsets, w["w_gate"], w["w_up"], w["w_down"], self.y_perm, self.ws,
@@ -62,12 +73,15 @@ class MoEBlock:
         moe.combine(h, cfg, self.y_perm, self.topk_w, self.flat_to_perm, self.shared, self.out, stream=stream)
         return self.out, self.h
 
-    def backward(self, dout, dh=None, stream=None):
-        """dout [T, H] bf16 (gradient of out), dh (gradient of h on its own path, the stream's type, or None) ->
-        gradients by name: dx and dresidual, norm_weight and w_router (fp32), and the expert weights (bf16)."""
+    def backward(self, dout, dh=None, stream=None, dbalance=None):
+        """dout [T, H] bf16 (gradient of out), dh (gradient of h on its own path, the stream's type, or None), dbalance
+        ([1] fp32, gradient of balance, or None: 1) -> gradients by name: dx and dresidual, norm_weight and w_router (fp32), and the expert weights (bf16)."""
         s, h, cfg, w, g = self.shape, self.handle, self.cfg, self.w, self.grads
         moe.combine_backward(h, cfg, dout, self.y_perm, self.topk_w, self.flat_to_perm, self.dy_perm, self.dtopk_w,
                              topk_idx=self.topk_idx, logits=self.logits, dlogits=self.dlogits, stream=stream)
+        if self.balance_coef:
+            moe.balance_loss_backward(h, cfg, self.logits, self.load, self.one if dbalance is None else dbalance,
+                                      self.dlogits, coef=self.balance_coef, dlogits_add=self.dlogits, stream=stream)
         moe.grouped_swiglu_backward(h, self.x_perm, self.dy_perm, self.offsets, w["w_gate"], w["w_up"], w["w_down"],
                                     self.dx_perm, g["w_gate"], g["w_up"], g["w_down"], self.ws, num_groups=s.E, H=s.H,
                                     I=s.I, stream=stream)

@@ -71,9 +71,9 @@ moe_status_t check_cfg(const moe_config_t* c) {
   if ((long long)c->T * c->K >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
   const long long wide = c->H > c->I ? c->H : c->I;
   if ((long long)c->T * c->K * wide >= (1ll << 40)) return MOE_ERR_INVALID_ARG;
-  if (c->dtype != MOE_BF16 && !is_mx(c->dtype)) return MOE_ERR_INVALID_ARG;
-  // MX: whole scale atoms (128 x 128) along H, I and I_shared.
-  if (is_mx(c->dtype) && (c->H % 128 || c->I % 128 || c->I_shared % 128))
+  if (c->dtype != MOE_BF16 && !is_mx(c->dtype) && !is_fp8_dtype(c->dtype)) return MOE_ERR_INVALID_ARG;
+  // MX: whole scale atoms (128 x 128) along H, I and I_shared; FP8_BLOCK128: whole blocks.
+  if (c->dtype != MOE_BF16 && (c->H % 128 || c->I % 128 || c->I_shared % 128))
     return MOE_ERR_INVALID_ARG;
   if (!(c->scaling == c->scaling)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
@@ -100,8 +100,9 @@ int shared_sm_budget(int num_sms, int option) {
 struct Layout {
   size_t topk_idx, topk_w, counts, offsets, tile_offsets, perm_src, flat_to_perm, perm_scratch, x_perm, h,
       y_perm, s, h_shared, x_stage, logits_stage, out_stage, x_mx, total;
-  // MXFP8 only: E8M0 scales of x (x_mx holds its E4M3 codes) row-major and
-  // as scale atoms; atoms of the permuted x, of h and of the shared expert's h.
+  // Not in bf16: scales of x (x_mx holds its E4M3 codes) row-major and (MX)
+  // as scale atoms; scales of the permuted x, of h and of the shared expert's h:
+  // atoms (MX) or row-major fp32 (FP8_BLOCK128).
   size_t x_mx_s, x_mx_atoms, x_perm_s, h_s, h_shared_s;
 };
 
@@ -122,8 +123,8 @@ Layout layout_of(const moe_config_t* c) {
   L.perm_src = take(TK * 4);
   L.flat_to_perm = take(TK * 4);
   L.perm_scratch = take(permute_scratch_bytes((int)TK, (int)E));
-  const bool mx = is_mx(c->dtype);
-  const size_t eb = mx ? 1 : 2;  // bytes per activation element (E4M3 codes or bf16)
+  const bool mx = is_mx(c->dtype), fp8 = is_fp8_dtype(c->dtype);
+  const size_t eb = mx || fp8 ? 1 : 2;  // bytes per activation element (E4M3 codes or bf16)
   // Foldable layers keep room for the shared expert's T rows after the routed ones.
   const size_t RX = TK + (foldable(c) ? T : 0);
   L.x_perm = take(RX * H * eb);
@@ -134,12 +135,12 @@ Layout layout_of(const moe_config_t* c) {
   L.x_stage = take(T * H * 2);
   L.logits_stage = take(T * E * 4);
   L.out_stage = take(T * H * 2);
-  L.x_mx = take(mx ? T * H : 0);
-  L.x_mx_s = take(mx ? T * H / 32 : 0);
+  L.x_mx = take(mx || fp8 ? T * H : 0);
+  L.x_mx_s = take(mx || fp8 ? T * H / 32 : 0);
   L.x_mx_atoms = take(mx ? scale_atom_bytes(T, 1, (int)H) : 0);
-  L.x_perm_s = take(mx ? scale_atom_bytes(TK, (int)E, (int)H) : 0);
-  L.h_s = take(mx ? scale_atom_bytes(TK, (int)E, (int)I) : 0);
-  L.h_shared_s = take(mx ? scale_atom_bytes(T, 1, (int)Is) : 0);
+  L.x_perm_s = take(mx ? scale_atom_bytes(TK, (int)E, (int)H) : fp8 ? TK * H / 32 : 0);
+  L.h_s = take(mx ? scale_atom_bytes(TK, (int)E, (int)I) : fp8 ? TK * I / 32 : 0);
+  L.h_shared_s = take(mx ? scale_atom_bytes(T, 1, (int)Is) : fp8 ? T * Is / 32 : 0);
   L.total = off;
   return L;
 }
@@ -206,6 +207,44 @@ cudaError_t timing_events(moe_handle_t h) {
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+// The SwiGLU experts in E4M3 with one fp32 scale per block of 128: gate and up
+// with h quantised on the way, then down.
+cudaError_t swiglu_fp8(moe_handle_t h, int G, const int32_t* offsets, int rows, int H, int I, int num_sms, const void* a,
+                       const void* a_scale, const void* wg, const void* wu, const void* wd, const void* sg, const void* su,
+                       const void* sd, void* hbuf, void* h_scale, float* y, cudaStream_t s, cudaEvent_t between) {
+  Fp8GemmArgs g = {};
+  g.G = G;
+  g.offsets = offsets;
+  g.rows = rows;
+  g.num_sms = num_sms;
+  g.status = h->status;
+  g.wait_limit_ns = h->wait_limit_ns;
+  g.N = I;
+  g.K = H;
+  g.a = a;
+  g.a_scale = static_cast<const float*>(a_scale);
+  g.w0 = wg;
+  g.w1 = wu;
+  g.s0 = static_cast<const float*>(sg);
+  g.s1 = static_cast<const float*>(su);
+  g.out = hbuf;
+  g.out_scale = static_cast<float*>(h_scale);
+  cudaError_t e = launch_gemm_fp8(g, kFp8GateUp, s);
+  if (between) cudaEventRecord(between, s);
+  g.N = H;
+  g.K = I;
+  g.a = hbuf;
+  g.a_scale = static_cast<const float*>(h_scale);
+  g.w0 = wd;
+  g.s0 = static_cast<const float*>(sd);
+  g.w1 = nullptr;
+  g.s1 = nullptr;
+  g.out = y;
+  g.out_f32 = 1;
+  g.out_scale = nullptr;
+  return e == cudaSuccess ? launch_gemm_fp8(g, kFp8Forward, s) : e;
 }
 
 // Gating ([Hy3] section 8.5: the main stream runs gating, then the routed
@@ -370,7 +409,7 @@ MOE_API moe_status_t moe_permute(moe_handle_t h, const moe_config_t* cfg, const 
                                  moe_stream_t stream) {
   moe_status_t st = check_cfg(cfg);
   if (st != MOE_OK) return st;
-  const bool mx = is_mx(cfg->dtype);
+  const bool mx = cfg->dtype != MOE_BF16;  // E4M3 codes, H / 32 bytes of scales per row
   const bool any = cfg->T > 0;
   if (!counts || !offsets || !ws) return MOE_ERR_INVALID_ARG;
   if (any && (!x || !topk_idx || !perm_src || !flat_to_perm || !x_perm)) return MOE_ERR_INVALID_ARG;
@@ -395,13 +434,18 @@ MOE_API moe_status_t moe_permute(moe_handle_t h, const moe_config_t* cfg, const 
 }
 
 namespace {
-// moe_grouped_swiglu_gemm workspace: h, then (MXFP8) the scale atoms of h and of a.
+// moe_grouped_swiglu_gemm workspace: h, then (MXFP8) the scale atoms of h and of a, or (FP8_BLOCK128) h's scales.
 struct GemmWs {
   size_t h, h_atoms, a_atoms, total;
 };
-GemmWs gemm_ws(int rows, int groups, int H, int I, bool mx) {
+GemmWs gemm_ws(int rows, int groups, int H, int I, bool mx, bool fp8) {
   GemmWs L;
   L.h = 0;
+  if (fp8) {  // codes of h and their fp32 scales
+    L.h_atoms = align_up((size_t)rows * I + 1, 256);
+    L.a_atoms = L.total = L.h_atoms + align_up((size_t)rows * ((I + 127) / 128) * 4 + 1, 256);
+    return L;
+  }
   L.h_atoms = align_up((size_t)rows * I * (mx ? 1 : 2) + 1, 256);
   L.a_atoms = L.h_atoms + (mx ? align_up(scale_atom_bytes(rows, groups, I) + 1, 256) : 0);
   L.total = L.a_atoms + (mx ? align_up(scale_atom_bytes(rows, groups, H) + 1, 256) : 0);
@@ -412,8 +456,8 @@ GemmWs gemm_ws(int rows, int groups, int H, int I, bool mx) {
 MOE_API moe_status_t moe_grouped_gemm_workspace_size(int rows, int num_groups, int H, int I,
                                                      moe_dtype_t dtype, size_t* bytes) {
   if (!bytes || rows < 0 || num_groups <= 0 || H <= 0 || I <= 0) return MOE_ERR_INVALID_ARG;
-  if (dtype != MOE_BF16 && !is_mx(dtype)) return MOE_ERR_INVALID_ARG;
-  *bytes = gemm_ws(rows, num_groups, H, I, is_mx(dtype)).total;
+  if (dtype != MOE_BF16 && !is_mx(dtype) && !is_fp8_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  *bytes = gemm_ws(rows, num_groups, H, I, is_mx(dtype), is_fp8_dtype(dtype)).total;
   return MOE_OK;
 }
 
@@ -428,22 +472,28 @@ MOE_API moe_status_t moe_grouped_swiglu_gemm(moe_handle_t h, int num_groups, int
     return MOE_ERR_INVALID_ARG;
   if (offsets == nullptr && num_groups != 1) return MOE_ERR_INVALID_ARG;
   if ((long long)rows * (H > I ? H : I) >= (1ll << 40)) return MOE_ERR_INVALID_ARG;
-  if (dtype != MOE_BF16 && !is_mx(dtype)) return MOE_ERR_INVALID_ARG;
-  const bool mx = is_mx(dtype);
+  if (dtype != MOE_BF16 && !is_mx(dtype) && !is_fp8_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  const bool mx = is_mx(dtype), fp8 = is_fp8_dtype(dtype);
   const bool w4 = dtype == MOE_MXFP4_W4A8;
   // W4A8: w_gate holds the gate and up codes together, w_up is unused.
   if (!a || !w_gate || (!w_up && !w4) || !w_down || !y || !ws) return MOE_ERR_INVALID_ARG;
   if (mx && (!a_scale || !s_gate || !s_down || H % 128 || I % 128)) return MOE_ERR_INVALID_ARG;
   if (w4 && !weights_aligned32(w_gate, w_up, w_down)) return MOE_ERR_INVALID_ARG;
-  (void)s_up;  // MXFP8: s_gate holds the gate and up scale atoms together
+  // MXFP8: s_gate holds the gate and up scale atoms together, s_up is unused.
+  if (fp8 && (!a_scale || !s_gate || !s_up || !s_down || H % 128 || I % 128 || H > 65536 || I > 65536))
+    return MOE_ERR_INVALID_ARG;
+  if (fp8 && (!aligned16(a_scale) || !aligned16(s_up))) return MOE_ERR_INVALID_ARG;
   const void* ptrs[] = {a, offsets, w_gate, w_up, w_down, y, ws, s_gate, s_down};
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-  const GemmWs W = gemm_ws(rows, num_groups, H, I, mx);
+  const GemmWs W = gemm_ws(rows, num_groups, H, I, mx, fp8);
   if (ws_bytes < W.total) return MOE_ERR_WORKSPACE;
   moe_status_t st = check_handle(h);
   if (st != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (fp8)
+    return cuda_status(swiglu_fp8(h, num_groups, offsets, rows, H, I, h->num_sms, a, a_scale, w_gate, w_up, w_down, s_gate,
+                                  s_up, s_down, ws, at<void>(ws, W.h_atoms), y, s, nullptr));
   GroupedGemmArgs g = gemm_args(h, num_groups, offsets, rows, H, I, a, w_gate, w_up, w_down, ws, y,
                                 mx ? s_gate : nullptr, mx ? s_down : nullptr);
   g.w4 = w4;
@@ -533,15 +583,21 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
   const bool has_shared = cfg->I_shared > 0;
   if (cfg->T > 0 && (!x || (!logits && !w_router) || !out)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w_router)) return MOE_ERR_INVALID_ARG;
-  const bool mx = is_mx(cfg->dtype);
+  const bool mx = is_mx(cfg->dtype), fp8 = is_fp8_dtype(cfg->dtype);
   const bool w4 = cfg->dtype == MOE_MXFP4_W4A8;  // routed experts E2M1; shared stays E4M3
   // W4A8: w_gate holds the routed gate and up codes together, w_up is unused.
   if (!w->w_gate || (!w->w_up && !w4) || !w->w_down) return MOE_ERR_INVALID_ARG;
   if (has_shared && (!w->ws_gate || !w->ws_up || !w->ws_down)) return MOE_ERR_INVALID_ARG;
-  // Pre-quantised activations: only in MX mode, and only with given logits
+  // Pre-quantised activations: not in bf16 mode, and only with given logits
   // (the router reads bf16 x).
-  if (x_scale && (!mx || w_router)) return MOE_ERR_INVALID_ARG;
+  if (x_scale && ((!mx && !fp8) || w_router)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_scale)) return MOE_ERR_INVALID_ARG;
+  if (fp8) {
+    const uint8_t* scales[] = {w->s_gate, w->s_up, w->s_down, w->ss_gate, w->ss_up, w->ss_down};
+    for (int i = 0; i < (has_shared ? 6 : 3); ++i)
+      if (!scales[i] || !aligned16(scales[i])) return MOE_ERR_INVALID_ARG;
+    if (cfg->H > 65536 || cfg->I > 65536 || cfg->I_shared > 65536) return MOE_ERR_INVALID_ARG;
+  }
   if (mx && (!w->s_gate || !w->s_down)) return MOE_ERR_INVALID_ARG;
   if (w4 && !weights_aligned32(w->w_gate, w->w_up, w->w_down)) return MOE_ERR_INVALID_ARG;
   if (mx && has_shared && (!w->ss_gate || !w->ss_down)) return MOE_ERR_INVALID_ARG;
@@ -588,7 +644,7 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
   cudaError_t e = cudaSuccess;
   mark(0, sm);
   const void* x_gate = x;  // the router reads x as given (bf16)
-  const uint8_t* xq_s = nullptr;  // MX: row-major E8M0 scales of the E4M3 x
+  const uint8_t* xq_s = nullptr;  // row-major scales of the E4M3 x (MX: E8M0, FP8_BLOCK128: fp32)
   if (mx && x_scale) {
     // The caller's E4M3 codes and scales; the shared expert still needs its
     // scales as atoms (one group of T rows).
@@ -602,6 +658,14 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
     e = launch_mx_quantize(x, T, H, static_cast<uint8_t*>(xq), s,
                            has_shared ? at<uint8_t>(ws, L.x_mx_atoms) : nullptr, sm);
     xq_s = s;
+    x = xq;
+  }
+  if (fp8 && x_scale) {
+    xq_s = x_scale;
+  } else if (fp8) {
+    uint8_t* xq = at<uint8_t>(ws, L.x_mx);
+    xq_s = at<uint8_t>(ws, L.x_mx_s);
+    e = launch_fp8_quantize_rows(x, false, T, H, xq, at<float>(ws, L.x_mx_s), sm);
     x = xq;
   }
   cudaStream_t s_sh = ss ? ss : sm;
@@ -631,9 +695,13 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
     // Beside the routed path the shared MLP should finish early rather than
     // use few SMs well: up to 128 tokens its weights fill the MMA rows
     // (more CTAs stream them) unless a tiling is forced.
-    if (!mx && g.mode == kModeAuto && T <= 128) g.mode = kModeWeightsM;
+    if (!mx && !fp8 && g.mode == kModeAuto && T <= 128) g.mode = kModeWeightsM;
     if (k_sh > 0) g.num_sms = k_sh;
-    if (mx) {
+    if (fp8) {
+      if (e == cudaSuccess)
+        e = swiglu_fp8(h, 1, nullptr, T, H, Is, g.num_sms, x, xq_s, w->ws_gate, w->ws_up, w->ws_down, w->ss_gate, w->ss_up,
+                       w->ss_down, h_shared, at<void>(ws, L.h_shared_s), s_out, s_sh, nullptr);
+    } else if (mx) {
       g.a_scale = at<uint8_t>(ws, L.x_mx_atoms);
       g.h_scale = at<uint8_t>(ws, L.h_shared_s);
       if (e == cudaSuccess) e = launch_gemm_mx_gate_up(g, s_sh);
@@ -670,7 +738,7 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
   }
   // bf16, tokens-as-M: GEMM-1 gathers its A rows from x itself (InitRouting's
   // row gather fused into the grouped GMM's load), so x_perm is not written.
-  const bool gather = !mx && !fold && h->gather_a && gemm_pick_mode(g) == kModeTokensM;
+  const bool gather = !mx && !fp8 && !fold && h->gather_a && gemm_pick_mode(g) == kModeTokensM;
   if (gather) {
     g.gather_src = perm_src;
     g.gather_k = K;
@@ -682,7 +750,9 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
                                     topk_idx, offsets, tile_offsets, K, TK, E,
                                     static_cast<uint8_t*>(x_perm), at<uint8_t>(ws, L.x_perm_s),
                                     h->status, sm)
-           : launch_scatter_rows(x, T, H * 2, flat_to_perm, K, TK, x_perm, h->status, sm);
+           : launch_scatter_rows(x, T, fp8 ? H : H * 2, flat_to_perm, K, TK, x_perm, h->status, sm);
+  if (e == cudaSuccess && fp8)
+    e = launch_scatter_rows(xq_s, T, H / 32, flat_to_perm, K, TK, at<void>(ws, L.x_perm_s), h->status, sm);
   if (e == cudaSuccess && fold) {  // group E: x itself, after the routed rows
     set_i32_kernel<<<1, 1, 0, sm>>>(offsets + E + 1, TK + T);
     e = cudaGetLastError();
@@ -691,9 +761,15 @@ static moe_status_t layer_forward_impl(moe_handle_t h, const moe_config_t* cfg,
                           cudaMemcpyDeviceToDevice, sm);
   }
   mark(2, sm);
-  if (e == cudaSuccess) e = mx ? launch_gemm_mx_gate_up(g, sm) : launch_gemm_gate_up(g, sm);
-  mark(3, sm);
-  if (e == cudaSuccess) e = mx ? launch_gemm_mx_down(g, sm) : launch_gemm_down(g, sm);
+  if (fp8) {
+    if (e == cudaSuccess)
+      e = swiglu_fp8(h, E, offsets, TK, H, I, g.num_sms, x_perm, at<void>(ws, L.x_perm_s), w->w_gate, w->w_up, w->w_down,
+                     w->s_gate, w->s_up, w->s_down, hbuf, at<void>(ws, L.h_s), y_perm, sm, ev ? ev[3] : nullptr);
+  } else {
+    if (e == cudaSuccess) e = mx ? launch_gemm_mx_gate_up(g, sm) : launch_gemm_gate_up(g, sm);
+    mark(3, sm);
+    if (e == cudaSuccess) e = mx ? launch_gemm_mx_down(g, sm) : launch_gemm_down(g, sm);
+  }
   mark(4, sm);
   if (e == cudaSuccess && has_shared && ss && !fold) e = cudaStreamWaitEvent(sm, h->ev_sh, 0);
   if (e == cudaSuccess)

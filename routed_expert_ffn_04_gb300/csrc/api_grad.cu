@@ -257,7 +257,7 @@ MOE_API moe_status_t moe_permute_backward(moe_handle_t h, const moe_config_t* cf
 MOE_API moe_status_t moe_grouped_gemm_backward_workspace_size(int rows, int num_groups, int H, int I,
                                                                 moe_dtype_t dtype, size_t* bytes) {
   if (!bytes || !grad_shape_ok(num_groups, rows, H, I)) return MOE_ERR_INVALID_ARG;
-  if (dtype != MOE_BF16) return is_mx_dtype(dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16) return is_mx_dtype(dtype) || is_fp8_dtype(dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
   *bytes = grad_ws(rows, num_groups, I).total;
   return MOE_OK;
 }
@@ -268,7 +268,7 @@ MOE_API moe_status_t moe_grouped_swiglu_backward(moe_handle_t h, int num_groups,
                                                  const void* w_down, void* da, void* dw_gate, void* dw_up,
                                                  void* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream) {
   if (!grad_shape_ok(num_groups, rows, H, I)) return MOE_ERR_INVALID_ARG;
-  if (dtype != MOE_BF16) return is_mx_dtype(dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16) return is_mx_dtype(dtype) || is_fp8_dtype(dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
   if (offsets == nullptr && num_groups != 1) return MOE_ERR_INVALID_ARG;
   const int dws = (dw_gate != nullptr) + (dw_up != nullptr) + (dw_down != nullptr);
   if ((dws != 0 && dws != 3) || (rows > 0 && dws == 0 && !da)) return MOE_ERR_INVALID_ARG;

@@ -649,34 +649,6 @@ bool make_tmap_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t oute
   return make_map(m, ptr, true, inner, outer, box_rows);
 }
 
-bool make_tmap_u8_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t groups,
-                     uint32_t box_rows) {
-  if (!g_encode) return false;
-  const cuuint64_t dims[3] = {inner, outer, groups};
-  const cuuint64_t strides[2] = {inner, inner * outer};
-  const cuuint32_t box[3] = {128, box_rows, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-bool make_tmap_rows(CUtensorMap* m, void* ptr, int esize, uint64_t inner, uint64_t outer, uint64_t groups, int row_bytes) {
-  if (!g_encode) return false;
-  const cuuint64_t dims[3] = {inner, outer, groups};
-  const cuuint64_t strides[2] = {inner * esize, inner * outer * esize};
-  const cuuint32_t box[3] = {(cuuint32_t)(row_bytes / esize), 32, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUtensorMapDataType type = esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  const CUresult r = g_encode(m, type, 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 bool make_tmap_e2m1(CUtensorMap* m, const void* ptr, uint64_t rows64, uint32_t box_rows) {
   if (!g_encode || box_rows == 0 || box_rows > 256 || (reinterpret_cast<uintptr_t>(ptr) & 31)) return false;
   const cuuint64_t dims[2] = {128, rows64};

@@ -163,6 +163,37 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, code, limit_ns)) != 0;
 }
 
+// ---- tensor maps (3-D: a group's matrix is cut off at its own edge)
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiledFn>(f) : nullptr;
+  }();
+  return fn;
+}
+// Boxes of row_bytes (the swizzle too: 64 or 128) x box_rows x 1 of [groups, outer, inner] elements of esize bytes
+// (1, 2 bf16, 4 fp32).
+bool make_map(CUtensorMap* m, const void* ptr, int esize, uint64_t inner, uint64_t outer, uint64_t groups, int row_bytes,
+              uint32_t box_rows) {
+  if (!encode_tiled()) return false;
+  const cuuint64_t dims[3] = {inner, outer, groups};
+  const cuuint64_t strides[2] = {inner * esize, inner * outer * esize};
+  const cuuint32_t box[3] = {(cuuint32_t)(row_bytes / esize), box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType type = esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return encode_tiled()(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A tile: group, its first row (WEIGHT_GRAD: of the padded rows), the rows it
 // has there, first column, blocks of the reduction.
 struct Tile {
@@ -300,10 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(bar, bytes);  // both CTAs' bytes (the other's may land first)
           const uint32_t da = sm0 + rg.s * kHalf, db = b_ring + rg.s * kHalf;
           if (kA_MN) {
-            tma_load_2d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128);
-            tma_load_2d_pair(db, bmap, bar, bn, t.row0 + kb * 128);
+            tma_load_3d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128, 0);
+            tma_load_3d_pair(db, bmap, bar, bn, t.row0 + kb * 128, 0);
           } else {
-            if (box) tma_load_2d_pair(da, amap, bar, kb * 128, t.row0 + (int)rank * 128);
+            if (box) tma_load_3d_pair(da, amap, bar, kb * 128, t.row0 + (int)rank * 128, 0);
             if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, kb * 128, t.g);
             else tma_load_3d_pair(db, bmap, bar, kb * 128, bn, t.g);
           }
@@ -662,18 +693,18 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
   bool ok = true;
   if (MODE == kFp8WeightGrad) {
     const uint64_t P = fp8_padded_rows(a.rows, G);
-    ok = make_tmap_u8(&m.a[0], a.a, a.N, P, 128) && make_tmap_u8(&m.b0, a.w0, a.K, P, 128);
+    ok = make_map(&m.a[0], a.a, 1, a.N, P, 1, 128, 128) && make_map(&m.b0, a.w0, 1, a.K, P, 1, 128, 128);
     for (int i = 1; i < 4; ++i) m.a[i] = m.a[0];
   } else {
-    for (int i = 0; ok && i < 4; ++i) ok = make_tmap_u8(&m.a[i], a.a, a.K, a.rows, 128u >> i);
+    for (int i = 0; ok && i < 4; ++i) ok = make_map(&m.a[i], a.a, 1, a.K, a.rows, 1, 128, 128u >> i);
     const uint64_t inner = MODE == kFp8Transposed ? a.N : a.K, outer = MODE == kFp8Transposed ? a.K : a.N;
-    ok = ok && make_tmap_u8_3d(&m.b0, a.w0, inner, outer, G, 128);
-    if (MODE == kFp8GateUp) ok = ok && make_tmap_u8_3d(&m.b1, a.w1, inner, outer, G, 128);
+    ok = ok && make_map(&m.b0, a.w0, 1, inner, outer, G, 128, 128);
+    if (MODE == kFp8GateUp) ok = ok && make_map(&m.b1, a.w1, 1, inner, outer, G, 128, 128);
   }
   if (MODE != kFp8GateUp) m.b1 = m.b0;
-  if (MODE == kFp8GateUp) ok = ok && make_tmap_rows(&m.out, a.out, 1, a.N, a.rows, 1, 64);
-  else if (MODE == kFp8WeightGrad) ok = ok && make_tmap_rows(&m.out, a.out, a.out_f32 ? 4 : 2, a.K, a.N, G, 128);
-  else ok = ok && make_tmap_rows(&m.out, a.out, a.out_f32 ? 4 : 2, a.N, a.rows, 1, 128);
+  if (MODE == kFp8GateUp) ok = ok && make_map(&m.out, a.out, 1, a.N, a.rows, 1, 64, 32);
+  else if (MODE == kFp8WeightGrad) ok = ok && make_map(&m.out, a.out, a.out_f32 ? 4 : 2, a.K, a.N, G, 128, 32);
+  else ok = ok && make_map(&m.out, a.out, a.out_f32 ? 4 : 2, a.N, a.rows, 1, 128, 32);
   if (!ok) return cudaErrorInvalidValue;
   Fp8Params p = {};
   p.offsets = a.offsets;

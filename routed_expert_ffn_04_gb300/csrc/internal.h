@@ -26,6 +26,10 @@ constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// E4M3 with one fp32 scale per block of 128: activations of 1 byte per element,
+// and per row H / 32 bytes of scales, as the MX dtypes.
+inline bool is_fp8_dtype(int dtype) { return dtype == MOE_FP8_BLOCK128; }
+
 // Both MX dtypes carry E4M3 activations (1 byte per element) with one E8M0
 // scale per 32 elements; they differ only in the routed experts' weights.
 inline bool is_mx_dtype(int dtype) { return dtype == MOE_MXFP8_E4M3 || dtype == MOE_MXFP4_W4A8; }
@@ -289,14 +293,6 @@ cudaError_t gemm_fp8_prepare_device();
 cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, int mode, cudaStream_t s);
 // Rows that hold any `rows` rows in G groups with each group's padded to a multiple of 128.
 inline int64_t fp8_padded_rows(int64_t rows, int64_t G) { return (rows / 128 + G) * 128; }
-// 3-D uint8 tensor map [groups, outer, inner], box {128 bytes, box_rows, 1}, 128-byte swizzle: rows past a
-// group's `outer` read as 0, not as the next group's.
-bool make_tmap_u8_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t groups,
-                     uint32_t box_rows);
-// 3-D tensor map for stores of 32 rows x row_bytes (64 or 128, the swizzle too), elements of esize
-// bytes (1, 2 bf16, 4 fp32), of [groups, outer, inner] and cut off at a group's `outer`.
-bool make_tmap_rows(CUtensorMap* m, void* ptr, int esize, uint64_t inner, uint64_t outer, uint64_t groups, int row_bytes);
-
 // Quantisers (fp8_quant.cu): x [rows, cols] bf16 or fp32, cols % 16 == 0. columns: q [fp8_padded_rows, cols],
 // scale [padded / 128, cols]; blocks behind the last group are left as they are.
 cudaError_t launch_fp8_quantize_rows(const void* x, bool f32, int64_t rows, int cols, uint8_t* q, float* scale,

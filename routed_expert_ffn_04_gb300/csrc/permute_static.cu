@@ -54,8 +54,8 @@ extern "C" MOE_API moe_status_t moe_permute_static_scratch(
   size_t need = 0;
   moe_status_t st = moe_permute_workspace_size(cfg, &need);  // validates cfg
   if (st != MOE_OK) return st;
-  // MXFP8 and W4A8 both move 1-byte E4M3 rows plus their E8M0 scales.
-  const bool mx = moe::is_mx_dtype(cfg->dtype);
+  // MXFP8, W4A8 and FP8_BLOCK128 all move 1-byte E4M3 rows plus H / 32 bytes of scales.
+  const bool mx = moe::is_mx_dtype(cfg->dtype) || moe::is_fp8_dtype(cfg->dtype);
   const bool any = cfg->T > 0;
   if (!counts || !offsets) return MOE_ERR_INVALID_ARG;
   if (any && (!x || !topk_idx || !perm_src || !flat_to_perm || !x_perm)) return MOE_ERR_INVALID_ARG;

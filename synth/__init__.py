@@ -39,7 +39,7 @@ class MoEShape:
     I_shared: int
     scaling: float = SCALING_HY3
     route_norm: bool = True
-    dtype: str = "bf16"  # "bf16", "mxfp8" (W8A8) or "mxfp4" (W4A8: MXFP4 routed weights)
+    dtype: str = "bf16"  # "bf16", "mxfp8" (W8A8), "mxfp4" (W4A8: MXFP4 routed weights) or "fp8" (fp32 scale per 128)
     skew: bool = False
 
     def as_dict(self):
