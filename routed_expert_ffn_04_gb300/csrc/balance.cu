@@ -6,8 +6,8 @@
 //   d loss / d logit_e = coef / n (f_e - sum_j f_j p_j) p_e (1 - sigma(logit_e))
 // (softmax: without the last factor; the counts have no gradient).
 //
-// A warp takes a token: its lanes hold the experts lane, lane + 32, ..., so a
-// lane's sums over the tokens are of fixed experts and stay in registers. A
+// A warp takes a token: its lanes hold the experts lane, lane + 32, ... (or pairs
+// of neighbours), so a lane's sums over the tokens are of fixed experts and stay in registers. A
 // block takes a strip of tokens, and for each sequence in it writes one row of
 // partial sums (row strip + sequence: unique, since both only grow). A second
 // launch adds a sequence's rows in a fixed order, eight blocks of a cluster
@@ -78,61 +78,91 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A token's shares from its logits (in place), lane's experts lane + 32 j; with
-// `slope`, d log(score) / d logit too.
-template <int V, bool SOFTMAX, bool SLOPE>
-__device__ __forceinline__ void shares(float (&x)[V], float (&slope)[V], int E, int lane) {
-  float sum = 0.0f;
-  if (SOFTMAX) {
+// Expert of a lane's value j. FULL (E = 32 V): pairs of neighbours, loaded at
+// once, and no lane's value is of no expert.
+template <bool FULL>
+__device__ __forceinline__ int expert_of(int j, int lane) {
+  return FULL ? 64 * (j >> 1) + 2 * lane + (j & 1) : lane + 32 * j;
+}
+
+// exp(x) and 1 / x to 2 ulp, tiny results as 0: two instructions each, where the
+// forms that keep subnormals take five (with them and the checks of lanes past E
+// a token of 256 experts took 238 instructions).
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A token's scores from its logits (in place), and 1 over their sum: the shares
+// are their products. With SLOPE also d log(score) / d logit.
+template <int V, bool SOFTMAX, bool SLOPE, bool FULL>
+__device__ __forceinline__ float scores(float (&x)[V], float (&slope)[V], int E, int lane) {
+  auto is = [&](int j) { return FULL || expert_of<FULL>(j, lane) < E; };
+  // exp(x - the largest): scores that underflow keep their ratios.
+  auto relative = [&] {
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
     top = warp_max(top);
     if (top == -INFINITY) top = 0.0f;  // all scores 0
+    float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      x[j] = lane + 32 * j < E ? __expf(x[j] - top) : 0.0f;
+      x[j] = is(j) ? exp_fast(x[j] - top) : 0.0f;
       sum += x[j];
     }
-    sum = warp_sum(sum);
+    return warp_sum(sum);
+  };
+  float sum = 0.0f;
+  if (SOFTMAX) {
+    sum = relative();
   } else {
-    float raw[V];
+    float sg[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      raw[j] = x[j];
-      const float a = __expf(-fabsf(x[j])), d = __fdividef(1.0f, 1.0f + a);
-      if (SLOPE) slope[j] = x[j] >= 0.0f ? a * d : d;
-      x[j] = lane + 32 * j < E ? (raw[j] >= 0.0f ? d : a * d) : 0.0f;
-      sum += x[j];
+      const float a = exp_fast(-fabsf(x[j])), d = rcp_fast(1.0f + a), ad = a * d;
+      const bool up = x[j] >= 0.0f;
+      if (SLOPE) slope[j] = up ? ad : d;
+      sg[j] = is(j) ? (up ? d : ad) : 0.0f;
+      sum += sg[j];
     }
     sum = warp_sum(sum);
     if (sum < 1e-30f) {  // sigma(x) = exp(x) here
-      float top = -INFINITY;
+      sum = relative();
+    } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) top = fmaxf(top, raw[j]);
-      top = warp_max(top);
-      if (top == -INFINITY) top = 0.0f;
-      sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[j] = lane + 32 * j < E ? __expf(raw[j] - top) : 0.0f;
-        sum += x[j];
-      }
-      sum = warp_sum(sum);
+      for (int j = 0; j < V; ++j) x[j] = sg[j];
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays
-#pragma unroll
-  for (int j = 0; j < V; ++j) x[j] *= inv;
+  return sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays
 }
 
-template <int V>
+template <int V, bool FULL>
 __device__ __forceinline__ void load_row(float (&x)[V], const float* row, int E, int lane, float fill) {
+  if (FULL) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = lane + 32 * j < E ? __ldcs(row + lane + 32 * j) : fill;
+    for (int j = 0; j < V; j += 2) {
+      const float2 v = __ldcs(reinterpret_cast<const float2*>(row + expert_of<true>(j, lane)));
+      x[j] = v.x;
+      x[j + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = lane + 32 * j < E ? __ldcs(row + lane + 32 * j) : fill;
+  }
 }
 
-template <int V, bool SOFTMAX>
+// Tokens that a warp takes at a time.
+template <int V>
+constexpr int kAtOnce = V <= 8 ? 2 : 1;
+
+template <int V, bool SOFTMAX, bool FULL>
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceParams p) {
   extern __shared__ float smem[];
   float* sums = smem;                                                 // [warps][E]
@@ -156,21 +186,32 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-    for (int t = lo + warp; t < hi; t += kSumWarps) {
-      float x[V], unused[V];
-      load_row<V>(x, p.logits + (size_t)t * E, E, lane, -INFINITY);
-      if (lane < p.K) {
-        const int e = __ldcs(p.topk_idx + (size_t)t * p.K + lane);
-        if (e >= 0 && e < E) atomicAdd(hist + e, 1);
-        else atomicCAS(p.status, 0, MOE_DEV_BAD_EXPERT_ID);
-      }
-      shares<V, SOFTMAX, false>(x, unused, E, lane);
+    for (int t = lo + warp; t < hi; t += kAtOnce<V> * kSumWarps) {
+      float x[kAtOnce<V>][V], unused[V];
+      int id[kAtOnce<V>];
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] += x[j];
+      for (int k = 0; k < kAtOnce<V>; ++k) {
+        const int at = t + k * kSumWarps < hi ? t + k * kSumWarps : t;
+        load_row<V, FULL>(x[k], p.logits + (size_t)at * E, E, lane, -INFINITY);
+        id[k] = lane < p.K ? __ldcs(p.topk_idx + (size_t)at * p.K + lane) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce<V>; ++k) {
+        if (t + k * kSumWarps >= hi) break;
+        if (lane < p.K) {
+          if (id[k] >= 0 && id[k] < E) atomicAdd(hist + id[k], 1);
+          else atomicCAS(p.status, 0, MOE_DEV_BAD_EXPERT_ID);
+        }
+        const float inv = scores<V, SOFTMAX, false, FULL>(x[k], unused, E, lane);
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(x[k][j], inv, acc[j]);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (lane + 32 * j < E) sums[warp * E + lane + 32 * j] = acc[j];
+    for (int j = 0; j < V; ++j) {
+      const int e = expert_of<FULL>(j, lane);
+      if (e < E) sums[warp * E + e] = acc[j];
+    }
     __syncthreads();
     const size_t row = ((size_t)blockIdx.x + b) * E;
     for (int e = threadIdx.x; e < E; e += kSumThreads) {
@@ -243,7 +284,7 @@ __global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(const Bala
   }
 }
 
-template <int V, bool SOFTMAX>
+template <int V, bool SOFTMAX, bool FULL>
 __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const BalanceParams p) {
   __shared__ int first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
@@ -264,53 +305,71 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
     const float w = __ldcg(p.dloss + b) * p.coef * inv_n;
     float f[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = lane + 32 * j < E ? (float)__ldcg(p.counts + (size_t)b * E + lane + 32 * j) * per : 0.0f;
-    for (int t = lo + warp; t < hi; t += kGradWarps) {
-      float x[V], slope[V], add[V];
-      load_row<V>(x, p.logits + (size_t)t * E, E, lane, -INFINITY);
-      if (p.add) load_row<V>(add, p.add + (size_t)t * E, E, lane, 0.0f);
-      shares<V, SOFTMAX, true>(x, slope, E, lane);
-      float c = 0.0f;
+    for (int j = 0; j < V; ++j) {
+      const int e = expert_of<FULL>(j, lane);
+      f[j] = e < E ? (float)__ldcg(p.counts + (size_t)b * E + e) * per : 0.0f;
+    }
+    for (int t0 = lo + warp; t0 < hi; t0 += kAtOnce<V> * kGradWarps) {
+      float x[kAtOnce<V>][V], add[kAtOnce<V>][V], slope[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) c += f[j] * x[j];
-      c = warp_sum(c);
+      for (int k = 0; k < kAtOnce<V>; ++k) {
+        const int at = t0 + k * kGradWarps < hi ? t0 + k * kGradWarps : t0;
+        load_row<V, FULL>(x[k], p.logits + (size_t)at * E, E, lane, -INFINITY);
+        if (p.add) load_row<V, FULL>(add[k], p.add + (size_t)at * E, E, lane, 0.0f);
+      }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float d = w * (f[j] - c) * x[j];
-        if (!SOFTMAX) d *= slope[j];
-        if (p.add) d += add[j];
-        if (lane + 32 * j < E) __stcs(p.dlogits + (size_t)t * E + lane + 32 * j, d);
+      for (int k = 0; k < kAtOnce<V>; ++k) {
+        const int t = t0 + k * kGradWarps;
+        if (t >= hi) break;
+        const float inv = scores<V, SOFTMAX, true, FULL>(x[k], slope, E, lane);
+        float c = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) c = fmaf(f[j], x[k][j], c);
+        c = warp_sum(c) * inv;
+        float* row = p.dlogits + (size_t)t * E;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          float d = w * (f[j] - c) * (x[k][j] * inv);
+          if (!SOFTMAX) d *= slope[j];
+          x[k][j] = p.add ? d + add[k][j] : d;
+        }
+        if (FULL) {
+#pragma unroll
+          for (int j = 0; j < V; j += 2)
+            __stcs(reinterpret_cast<float2*>(row + expert_of<true>(j, lane)), make_float2(x[k][j], x[k][j + 1]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (lane + 32 * j < E) __stcs(row + lane + 32 * j, x[k][j]);
+        }
       }
     }
   }
 }
 
-template <int V, bool SOFTMAX>
-cudaError_t run_sum(const BalanceParams& p, int strips, cudaStream_t s) {
+template <bool GRAD, int V, bool SOFTMAX, bool FULL>
+cudaError_t run(const BalanceParams& p, int strips, cudaStream_t s) {
+  if (GRAD) return launch_dependent(balance_grad_kernel<V, SOFTMAX, FULL>, strips, kGradThreads, 0, s, true, 1, p);
   const size_t smem = (size_t)(kSumWarps + 1) * p.E * 4;
-  return launch_dependent(balance_sum_kernel<V, SOFTMAX>, strips, kSumThreads, smem, s, true, 1, p);
+  return launch_dependent(balance_sum_kernel<V, SOFTMAX, FULL>, strips, kSumThreads, smem, s, true, 1, p);
 }
-template <int V, bool SOFTMAX>
-cudaError_t run_grad(const BalanceParams& p, int strips, cudaStream_t s) {
-  return launch_dependent(balance_grad_kernel<V, SOFTMAX>, strips, kGradThreads, 0, s, true, 1, p);
+// Values per lane: the least that hold E, so that few lanes' loads and exponentials are of no expert.
+template <bool GRAD, bool SOFTMAX, int V>
+cudaError_t fit(const BalanceParams& p, int strips, cudaStream_t s) {
+  return p.E == 32 * V ? run<GRAD, V, SOFTMAX, true>(p, strips, s) : run<GRAD, V, SOFTMAX, false>(p, strips, s);
 }
-template <bool SOFTMAX>
-cudaError_t pick_sum(const BalanceParams& p, int strips, cudaStream_t s) {
-  if (p.E <= 64) return run_sum<2, SOFTMAX>(p, strips, s);
-  if (p.E <= 128) return run_sum<4, SOFTMAX>(p, strips, s);
-  if (p.E <= 192) return run_sum<6, SOFTMAX>(p, strips, s);
-  if (p.E <= 256) return run_sum<8, SOFTMAX>(p, strips, s);
-  if (p.E <= 512) return run_sum<16, SOFTMAX>(p, strips, s);
-  return run_sum<32, SOFTMAX>(p, strips, s);
+template <bool GRAD, bool SOFTMAX>
+cudaError_t pick(const BalanceParams& p, int strips, cudaStream_t s) {
+  if (p.E <= 64) return fit<GRAD, SOFTMAX, 2>(p, strips, s);
+  if (p.E <= 128) return fit<GRAD, SOFTMAX, 4>(p, strips, s);
+  if (p.E <= 192) return fit<GRAD, SOFTMAX, 6>(p, strips, s);
+  if (p.E <= 256) return fit<GRAD, SOFTMAX, 8>(p, strips, s);
+  if (p.E <= 512) return fit<GRAD, SOFTMAX, 16>(p, strips, s);
+  return fit<GRAD, SOFTMAX, 32>(p, strips, s);
 }
-template <bool SOFTMAX>
-cudaError_t pick_grad(const BalanceParams& p, int strips, cudaStream_t s) {
-  if (p.E <= 64) return run_grad<2, SOFTMAX>(p, strips, s);
-  if (p.E <= 128) return run_grad<4, SOFTMAX>(p, strips, s);
-  if (p.E <= 192) return run_grad<6, SOFTMAX>(p, strips, s);
-  if (p.E <= 256) return run_grad<8, SOFTMAX>(p, strips, s);
-  if (p.E <= 512) return run_grad<16, SOFTMAX>(p, strips, s);
-  return run_grad<32, SOFTMAX>(p, strips, s);
+template <bool GRAD>
+cudaError_t pick(const BalanceParams& p, bool softmax, int strips, cudaStream_t s) {
+  return softmax ? pick<GRAD, true>(p, strips, s) : pick<GRAD, false>(p, strips, s);
 }
 
 BalanceParams params_of(const BalanceArgs& a, int strip) {
@@ -347,8 +406,10 @@ int sum_strips(int T) { return (T + sum_strip(T) - 1) / sum_strip(T); }
 cudaError_t balance_prepare_device() {
   const int most = (kSumWarps + 1) * 1024 * 4;
   const cudaError_t errs[] = {
-      cudaFuncSetAttribute(balance_sum_kernel<32, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
-      cudaFuncSetAttribute(balance_sum_kernel<32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)};
+      cudaFuncSetAttribute(balance_sum_kernel<32, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<32, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<32, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<32, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)};
   for (cudaError_t e : errs)
     if (e != cudaSuccess) return e;
   return cudaSuccess;
@@ -362,7 +423,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
   p.part = static_cast<float*>(a.scratch);
   p.part_n = reinterpret_cast<int32_t*>(p.part + ((size_t)strips + a.B) * a.E);
   if (strips > 0) {
-    const cudaError_t e = a.softmax ? pick_sum<true>(p, strips, s) : pick_sum<false>(p, strips, s);
+    const cudaError_t e = pick<false>(p, a.softmax, strips, s);
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(balance_final_kernel, a.B * kFinalCluster, kFinalThreads, 0, s, true, kFinalCluster, p);
@@ -370,10 +431,12 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
 
 cudaError_t launch_balance_loss_backward(const BalanceArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  // Four tokens per warp, so that a lane's f is loaded for a few of them.
-  const int strip = 4 * kGradWarps, strips = (a.T + strip - 1) / strip;
+  // Two tokens per warp, more (so that a lane's f is loaded for several) once two
+  // blocks of each SM are at work.
+  const int per_warp = (a.T + 304 * kGradWarps - 1) / (304 * kGradWarps), strip = kGradWarps * (per_warp > 2 ? per_warp : 2);
+  const int strips = (a.T + strip - 1) / strip;
   const BalanceParams p = params_of(a, strip);
-  return a.softmax ? pick_grad<true>(p, strips, s) : pick_grad<false>(p, strips, s);
+  return pick<true>(p, a.softmax, strips, s);
 }
 
 }  // namespace moe

@@ -27,6 +27,12 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
   return s < kFp8LeastScale ? kFp8LeastScale : s;  // a NaN stays
 }
 
+__device__ __forceinline__ uint32_t fp8_pack2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  return fp8_pack2(a, b) | fp8_pack2(c, d) << 16;
+}
 // v / scale rounded once to fp32, as the division is, by one Newton step on the
 // quotient (P. Markstein, 1990): with inv = 1 / scale rounded to nearest, y0 = v
 // inv is within an ulp and y0 + inv (v - y0 scale) rounds to the quotient. The
@@ -34,15 +40,13 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
 struct Fp8Block {
   float scale, inv;
   __device__ __forceinline__ explicit Fp8Block(float s) : scale(s), inv(1.0f / s) {}
+  __device__ __forceinline__ Fp8Block(float s, float i) : scale(s), inv(i) {}
   __device__ __forceinline__ float over(float v) const {
     const float y0 = v * inv;
     return fmaf(fmaf(-y0, scale, v), inv, y0);
   }
-  __device__ __forceinline__ uint32_t code2(float a, float b) const {
-    return __nv_cvt_float2_to_fp8x2(make_float2(over(a), over(b)), __NV_SATFINITE, __NV_E4M3);
-  }
   __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) const {
-    return code2(a, b) | code2(c, d) << 16;
+    return fp8_pack4(over(a), over(b), over(c), over(d));
   }
 };
 
