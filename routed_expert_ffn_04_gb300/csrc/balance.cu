@@ -431,9 +431,9 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
 
 cudaError_t launch_balance_loss_backward(const BalanceArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  // Two tokens per warp, more (so that a lane's f is loaded for several) once two
+  // Four tokens per warp, more (so that a lane's f is loaded for several) once two
   // blocks of each SM are at work.
-  const int per_warp = (a.T + 304 * kGradWarps - 1) / (304 * kGradWarps), strip = kGradWarps * (per_warp > 2 ? per_warp : 2);
+  const int per_warp = (a.T + 304 * kGradWarps - 1) / (304 * kGradWarps), strip = kGradWarps * (per_warp > 4 ? per_warp : 4);
   const int strips = (a.T + strip - 1) / strip;
   const BalanceParams p = params_of(a, strip);
   return pick<true>(p, a.softmax, strips, s);

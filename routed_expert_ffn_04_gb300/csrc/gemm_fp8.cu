@@ -54,7 +54,6 @@ namespace {
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSmem = 232448;  // 227 KB dynamic shared memory per CTA
 constexpr int kHalf = 128 * 128;  // a CTA's A, or B, of a stage
-constexpr int kStages = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -63,19 +62,25 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 // two of the epilogue, whose accumulators take 128: 128 x 56 + 256 x 224 = 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsMany == kThreads * kRegsLaunch, "registers");
-constexpr int kStgBlock = 4096;               // staging: 32 rows of 128 bytes, two of them per warp
-constexpr int kStgWarp = 2 * kStgBlock;
-constexpr int kStgBytes = kEpiWarps * kStgWarp;
+constexpr int kStgBlock = 4096;  // staging: 32 rows of 128 bytes
+// Stages of the ring, and staging per warp: GATE_UP's rows of a warp are 64 bytes
+// of codes, the others' 256 bytes (two blocks).
+constexpr int stages(int mode) { return mode == kFp8GateUp ? 5 : 4; }
+constexpr int stg_warp(int mode) { return mode == kFp8GateUp ? kStgBlock / 2 : 2 * kStgBlock; }
 constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
 constexpr int kFactorSlots = 4;               // blocks whose factors are kept
 constexpr int kFactors = 384;                 // of a block: rows' (twice, or once and 256 columns')
-constexpr int kColBytes = kFactorSlots * kFactors * 4 + 2048;  // and GATE_UP's row maxima
-constexpr int kBars = 2 * kStages + 5;
-constexpr int kBarBytes = 8 * kBars + 8;  // and the TMEM address and the abort flag
+constexpr int kColBytes = kFactorSlots * kFactors * 4 + 6144;  // and GATE_UP's row maxima: two slots of four parts, two of two
+constexpr int bars_of(int mode) { return 2 * stages(mode) + 9; }
+constexpr int bar_bytes(int mode) { return (8 * bars_of(mode) + 8 + 15) / 16 * 16; }  // and the TMEM address and the abort flag
 constexpr int kTableBytes = (kMaxGroups + 8) * 4 * 2;
-constexpr int kSmem = 1024 + 2 * kStages * kHalf + kStgBytes + kColBytes + kBarBytes + kTableBytes;
+constexpr int smem_of(int mode) {
+  return 1024 + 2 * stages(mode) * kHalf + kEpiWarps * stg_warp(mode) + kColBytes + bar_bytes(mode) + kTableBytes;
+}
+// Groups of up to so many rows have split tiles (Tile).
+constexpr int kSplitRows = 128;
 constexpr uint16_t kPairMask = 0x3;
-static_assert(kSmem <= kMaxSmem && kBarBytes % 16 == 0, "shared memory");
+static_assert(smem_of(kFp8GateUp) <= kMaxSmem && smem_of(kFp8Forward) <= kMaxSmem, "shared memory");
 
 struct Fp8Params {
   const int32_t* offsets;  // [G+1] or nullptr
@@ -194,10 +199,21 @@ bool make_map(CUtensorMap* m, const void* ptr, int esize, uint64_t inner, uint64
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Store to the shared memory of a CTA of the cluster (addresses from mapa_shared)
+// that counts its 4 bytes on a barrier there: no release, which would wait for
+// this SM's other memory traffic (3000 cycles).
+__device__ __forceinline__ void st_async(uint32_t cluster_addr, uint32_t v, uint32_t cluster_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
+               "r"(cluster_bar)
+               : "memory");
+}
+
 // A tile: group, its first row (WEIGHT_GRAD: of the padded rows), the rows it
-// has there, first column, blocks of the reduction.
+// has there, first column, blocks of the reduction; split: both CTAs hold its
+// rows (at most 128), each adds half of its columns.
 struct Tile {
   int g, row0, nrows, m0, n0, kb;
+  bool split;
 };
 
 // VEC: a's scales of a row start at multiples of 16 bytes.
@@ -206,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_fp8_kernel(const __grid_constant__ Fp8Maps m, const Fp8Params p) {
   constexpr bool kA_MN = MODE == kFp8WeightGrad, kB_MN = MODE == kFp8WeightGrad || MODE == kFp8Transposed;
   constexpr int kCols = MODE == kFp8GateUp ? 128 : 256;  // result columns per tile
+  constexpr int kStages = stages(MODE), kStgWarp = stg_warp(MODE), kStgBytes = kEpiWarps * kStgWarp;
+  constexpr int kBars = bars_of(MODE), kBarBytes = bar_bytes(MODE);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
@@ -226,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kStages + a); };   // each CTA
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kStages + 2 + a); };  // leader
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
+  auto tops_bar = [&](int q) { return bar0 + 8u * (2 * kStages + 5 + q); };  // each CTA: GATE_UP's split tiles
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: leader
@@ -241,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(a), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(tops_bar(i), 2);  // this CTA's two warps; the other's come as bytes
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -281,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.row0 = tile_start[t.g] * 128;
       t.nrows = row_start[t.g + 1] - row_start[t.g];
       t.kb = t.nrows > 0 ? (t.nrows + 127) / 128 : 0;
+      t.split = false;
       return t;
     }
     int lo = 0, hi = G;  // tile_start[lo] <= tile < tile_start[hi]
@@ -296,11 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.row0 = row_start[lo] + t.m0;
     t.nrows = n - t.m0;
     t.kb = (p.K + 127) / 128;
+    t.split = n <= kSplitRows;
     return t;
   };
+  auto first_row = [&](const Tile& t) { return t.split ? 0 : (int)rank * 128; };  // of this CTA's A
   // Rows of A that CTA r of the pair has in a tile, and the box that covers them (0: none).
   auto rows_of = [&](const Tile& t, int r) {
-    const int n = t.nrows - 128 * r;
+    const int n = t.nrows - (t.split ? 0 : 128 * r);
     return n < 0 ? 0 : (n > 128 ? 128 : n);
   };
   auto box_of = [&](int n) { return n > 64 ? 128 : (n > 32 ? 64 : (n > 16 ? 32 : (n > 0 ? 16 : 0))); };
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128, 0);
             tma_load_3d_pair(db, bmap, bar, bn, t.row0 + kb * 128, 0);
           } else {
-            if (box) tma_load_3d_pair(da, amap, bar, kb * 128, t.row0 + (int)rank * 128, 0);
+            if (box) tma_load_3d_pair(da, amap, bar, kb * 128, t.row0 + first_row(t), 0);
             if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, kb * 128, t.g);
             else tma_load_3d_pair(db, bmap, bar, kb * 128, bn, t.g);
           }
@@ -438,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // Rows past the group's end take its last row's scales: their results are not stored.
-        const int last = t.nrows - 1, a0 = (int)rank * 128 + s0;
+        const int last = t.nrows - 1, a0 = first_row(t) + s0;
         const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs;
         const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs;
         auto load_a = [&](const float* sa, int kb) {
@@ -496,13 +519,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive_remote(tempty0 + 8u * buf);
       }
     };
-    const int r = (int)rank * 128 + q * 32 + lane;  // row of the tile
     Ring acc;
     bool ok = true;
-    int seq = 0, slot = 0;
-    for (int tile = pair; ok && tile < total; tile += npairs, ++seq) {
+    int slot = 0;
+    uint32_t split_phase = 0, joined = 0;  // GATE_UP: tiles whose maxima were put together, split and not
+    for (int tile = pair; ok && tile < total; tile += npairs) {
       const Tile c_t = decode(tile);
-      if (MODE != kFp8WeightGrad && c_t.nrows <= (int)rank * 128 + q * 32) {  // none of this warp's rows: keep step
+      const int r0 = first_row(c_t) + q * 32;  // this warp's first row of the tile
+      if (MODE != kFp8WeightGrad && c_t.nrows <= r0) {  // none of this warp's rows: keep step
         for (int kb = 0; ok && kb < c_t.kb; ++kb) {
           ok = warp_wait(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
           if (ok) release(acc.s);
@@ -511,8 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      // The accumulators live in this loop: nothing but its end and the results
-      // below read them, so that no copies join them with another path's.
+      // Columns of the tile that this warp adds: `wide` from col0 on (GATE_UP: of the
+      // gates, and as many of the ups), 32 of them at a time.
+      const bool split = MODE != kFp8WeightGrad && c_t.split;
+      const int wide = (MODE == kFp8GateUp ? 64 : 128) >> (split ? 1 : 0);
+      const int col0 = (split ? 2 * (int)rank + half : half) * wide;
+      // The accumulators live in the loops below: nothing but their end and the results
+      // read them, so that no copies join them with another path's.
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
@@ -521,12 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // load come before this one's last additions.
       uint32_t v0[32], v1[32];
       uint32_t tb = 0;
-      auto at = [&](int c) { return tb + (MODE == kFp8GateUp ? (c & 1) * 32 + (c >> 1) * 128 : 32 * c); };
       auto begin = [&] {  // wait for a block and load its first columns
         if (!warp_wait(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return false;
         tc_fence_after();
-        tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 256) + (MODE == kFp8GateUp ? 64 : 128) * half;
-        tmem_ld_32x32b_x32(at(0), v0);
+        tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 256 + col0);
+        tmem_ld_32x32b_x32(tb, v0);
         return true;
       };
       auto arrived = [&](uint32_t (&x)[32]) {  // used behind the wait only
@@ -534,50 +562,72 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(x[i]));
       };
-      if (c_t.kb > 0 && !begin()) goto done;
-#pragma unroll 1
-      for (int kb = 0; kb < c_t.kb; ++kb) {
-        const float* f = factors + slot * kFactors;
+      float f0 = 0.f, f1 = 0.f;  // the row's factors of the block (GATE_UP: the gates', the ups')
+      const float* f = nullptr;
+      auto take_factors = [&] {
+        f = factors + slot * kFactors;
         slot = (slot + 1) % kFactorSlots;
-        const float f0 = f[(MODE == kFp8GateUp || MODE == kFp8WeightGrad ? 0 : half) * 128 + q * 32 + lane];
-        const float f1 = MODE == kFp8GateUp ? f[128 + q * 32 + lane] : f0;
+        const int part = MODE == kFp8GateUp || MODE == kFp8WeightGrad ? 0 : (split ? (int)rank : half);
+        f0 = f[part * 128 + q * 32 + lane];
+        f1 = MODE == kFp8GateUp ? f[128 + q * 32 + lane] : f0;
         f += 128 + 128 * half;  // WEIGHT_GRAD: the columns'
-        auto add = [&](int c, const uint32_t (&v)[32]) {
+      };
+      auto add = [&](int c, float y, const uint32_t (&v)[32]) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 x = make_float4(c < 2 ? f0 : f1, c < 2 ? f0 : f1, c < 2 ? f0 : f1, c < 2 ? f0 : f1);
-            if (MODE == kFp8WeightGrad) {
-              const float4 y = *reinterpret_cast<const float4*>(f + 32 * c + i);
-              x = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
-            }
-            sum[32 * c + i] = fmaf(__uint_as_float(v[i]), x.x, sum[32 * c + i]);
-            sum[32 * c + i + 1] = fmaf(__uint_as_float(v[i + 1]), x.y, sum[32 * c + i + 1]);
-            sum[32 * c + i + 2] = fmaf(__uint_as_float(v[i + 2]), x.z, sum[32 * c + i + 2]);
-            sum[32 * c + i + 3] = fmaf(__uint_as_float(v[i + 3]), x.w, sum[32 * c + i + 3]);
+        for (int i = 0; i < 32; i += 4) {
+          float4 x = make_float4(y, y, y, y);
+          if (MODE == kFp8WeightGrad) {
+            const float4 z = *reinterpret_cast<const float4*>(f + 32 * c + i);
+            x = make_float4(y * z.x, y * z.y, y * z.z, y * z.w);
           }
-        };
-        arrived(v0);
-        tmem_ld_32x32b_x32(at(1), v1);
-        add(0, v0);
-        arrived(v1);
-        tmem_ld_32x32b_x32(at(2), v0);
-        add(1, v1);
-        arrived(v0);
-        tmem_ld_32x32b_x32(at(3), v1);
-        add(2, v0);
-        arrived(v1);
-        if (MODE == kFp8WeightGrad) add(3, v1);  // its column factors are read until the release
-        release(acc.s);
-        acc.next(2);
-        if (kb + 1 < c_t.kb && !begin()) goto done;
-        if (MODE != kFp8WeightGrad) add(3, v1);
+          sum[32 * c + i] = fmaf(__uint_as_float(v[i]), x.x, sum[32 * c + i]);
+          sum[32 * c + i + 1] = fmaf(__uint_as_float(v[i + 1]), x.y, sum[32 * c + i + 1]);
+          sum[32 * c + i + 2] = fmaf(__uint_as_float(v[i + 2]), x.z, sum[32 * c + i + 2]);
+          sum[32 * c + i + 3] = fmaf(__uint_as_float(v[i + 3]), x.w, sum[32 * c + i + 3]);
+        }
+      };
+      if (c_t.kb > 0 && !begin()) goto done;
+      if (split) {
+#pragma unroll 1
+        for (int kb = 0; kb < c_t.kb; ++kb) {
+          take_factors();
+          arrived(v0);
+          tmem_ld_32x32b_x32(tb + (MODE == kFp8GateUp ? 128 : 32), v1);
+          add(0, f0, v0);
+          arrived(v1);
+          release(acc.s);
+          acc.next(2);
+          const float y = f1;
+          if (kb + 1 < c_t.kb && !begin()) goto done;
+          add(1, y, v1);
+        }
+      } else {
+        auto at = [&](int c) { return tb + (MODE == kFp8GateUp ? (c & 1) * 32 + (c >> 1) * 128 : 32 * c); };
+#pragma unroll 1
+        for (int kb = 0; kb < c_t.kb; ++kb) {
+          take_factors();
+          arrived(v0);
+          tmem_ld_32x32b_x32(at(1), v1);
+          add(0, f0, v0);
+          arrived(v1);
+          tmem_ld_32x32b_x32(at(2), v0);
+          add(1, f0, v1);
+          arrived(v0);
+          tmem_ld_32x32b_x32(at(3), v1);
+          add(2, f1, v0);
+          arrived(v1);
+          if (MODE == kFp8WeightGrad) add(3, f1, v1);  // its column factors are read until the release
+          release(acc.s);
+          acc.next(2);
+          if (kb + 1 < c_t.kb && !begin()) goto done;
+          if (MODE != kFp8WeightGrad) add(3, f1, v1);
+        }
       }
       // Results go out by TMA from the warp's staging (the tensor maps' swizzles),
       // while the next tile is summed: stores from the warps held them up for as
       // long as three blocks (an SM stores 32 bytes a cycle). A group's last rows,
       // fewer than 32, are stored by the warp; WEIGHT_GRAD's map ends where a
       // group's matrix does.
-      const int r0 = (int)rank * 128 + q * 32;  // this warp's first row of the tile
       const int live_rows = MODE == kFp8WeightGrad ? p.N - c_t.m0 : c_t.nrows;
       const bool whole = MODE == kFp8WeightGrad || r0 + 32 <= live_rows;
       const int width = MODE == kFp8WeightGrad ? p.K : p.N;
@@ -605,41 +655,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (MODE == kFp8GateUp) {
-        // h of 64 columns; the block's largest is the larger of the two halves'.
+        // h of 64 columns (32 of a split tile); the block's largest is the largest of
+        // the two warps' (four: two in each CTA). Two slots of either kind by turns:
+        // another warp may still read the last such tile's.
         uint32_t top = 0;
+        auto finish = [&](float g, float u) {
+          const float x = silu_fast(g) * u;
+          const uint32_t b = fp8_abs_bits(x);
+          top = b > top ? b : top;
+          return x;
+        };
+        uint32_t* tops = reinterpret_cast<uint32_t*>(factors + kFactorSlots * kFactors) + q * 32 + lane;
+        if (split) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          sum[i] = silu_fast(sum[i]) * sum[64 + i];
-          const uint32_t x = fp8_abs_bits(sum[i]);
-          top = x > top ? x : top;
+          for (int i = 0; i < 32; ++i) sum[i] = finish(sum[i], sum[32 + i]);
+          tops += (split_phase & 1) * 512;
+          uint32_t* mine = tops + (2 * rank + half) * 128;
+          *mine = top;
+          st_async(mapa_shared(smem_u32(mine), rank ^ 1u), top, mapa_shared(tops_bar(q), rank ^ 1u));
+          __syncwarp();
+          if (lane == 0) {
+            if (half == 0) mbar_arrive_expect_tx(tops_bar(q), 2 * 32 * 4);
+            else mbar_arrive(tops_bar(q));
+          }
+          ok = warp_wait(tops_bar(q), split_phase & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+          if (!ok) goto done;
+          ++split_phase;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = *reinterpret_cast<volatile uint32_t*>(tops + i * 128);
+            top = x > top ? x : top;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) sum[i] = finish(sum[i], sum[64 + i]);
+          tops += 1024 + (joined++ & 1) * 256;
+          tops[half * 128] = top;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+          const uint32_t other = tops[(half ^ 1) * 128];
+          top = other > top ? other : top;
         }
-        // Two slots by turns: the other warp may still read the last tile's.
-        uint32_t* tops = reinterpret_cast<uint32_t*>(factors + kFactorSlots * kFactors) + (seq & 1) * 256 + q * 32 + lane;
-        tops[half * 128] = top;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-        const uint32_t other = tops[(half ^ 1) * 128];
-        const float scale = fp8_scale(top > other ? top : other);
-        if (half == 0 && r < c_t.nrows) p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = scale;
+        const float scale = fp8_scale(top);
+        const int r = r0 + lane;
+        if (half == 0 && (!split || rank == 0) && r < c_t.nrows)
+          p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = scale;
         const Fp8Block blk(scale);
-        reuse();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        auto codes = [&](int c) {  // 16 of them
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = 16 * c + 4 * i;
             w[i] = blk.code4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
           }
-          *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        reuse();
+        if (split) {  // 32 bytes of each row, sixteen rows per store: chunk c of row i at c ^ (i / 4) % 2
+#pragma unroll
+          for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(stg + lane * 32 + ((c ^ ((lane >> 2) & 1)) << 4)) = codes(c);
+          __syncwarp();
+          const int col = c_t.n0 + col0 + 16 * (lane & 1);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int i = 16 * j + (lane >> 1);
+            const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 32 + (((lane & 1) ^ ((i >> 2) & 1)) << 4));
+            if (r0 + i < c_t.nrows && col < p.N)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (size_t)(c_t.row0 + r0 + i) * p.N + col) = v;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = codes(c);
+          fence_proxy_async_smem();
+          __syncwarp();
+          send(0, 64, 1, c_t.n0 + col0);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        send(0, 64, 1, c_t.n0 + 64 * half);
       } else {
-        const int c0 = c_t.n0 + 128 * half;
+        const int c0 = c_t.n0 + col0;
         if (p.out_f32) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
+            if (g == 1 && split) break;
             reuse();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -665,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           send(0, 128, 2, c0);
-          send(1, 128, 2, c0 + 64);
+          if (!split) send(1, 128, 2, c0 + 64);
         }
       }
     }
@@ -727,8 +822,8 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
   const int pairs = (int)(tiles < most ? tiles : most);
   if (pairs < 1) return cudaErrorInvalidValue;
   const bool vec = MODE == kFp8WeightGrad || fp8_blocks(a.K) % 4 == 0;
-  if (vec) return launch_dependent(grouped_gemm_fp8_kernel<MODE, true>, 2 * pairs, kThreads, kSmem, s, true, /*cluster=*/2, m, p);
-  return launch_dependent(grouped_gemm_fp8_kernel<MODE, MODE == kFp8WeightGrad>, 2 * pairs, kThreads, kSmem, s, true, /*cluster=*/2, m, p);
+  if (vec) return launch_dependent(grouped_gemm_fp8_kernel<MODE, true>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
+  return launch_dependent(grouped_gemm_fp8_kernel<MODE, MODE == kFp8WeightGrad>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
 }
 
 }  // namespace
@@ -736,7 +831,7 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
 namespace {
 template <int MODE, bool VEC>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(MODE));
 }
 }  // namespace
 
