@@ -6,13 +6,15 @@
 //   d loss / d logit_e = coef / n (f_e - sum_j f_j p_j) p_e (1 - sigma(logit_e))
 // (softmax: without the last factor; the counts have no gradient).
 //
-// A warp takes a token: its lanes hold the experts lane, lane + 32, ... (or pairs
-// of neighbours), so a lane's sums over the tokens are of fixed experts and stay in registers. A
-// block takes a strip of tokens, and for each sequence in it writes one row of
-// partial sums (row strip + sequence: unique, since both only grow). A second
-// launch adds a sequence's rows in a fixed order, eight blocks of a cluster
-// sharing the experts. The logits are read once; what bounds it is HBM for many
-// tokens and the two launches for few.
+// L = 8, 16 (past 128 experts) or 32 lanes (past 256) take a token: a warp up to
+// four at a time, with fewer steps of shuffles for a token's sum, and no idle
+// lanes where E is small (450209 x 8: 61 -> 23 us). A lane's
+// sums over the tokens are of fixed experts and stay in registers. A block takes
+// a strip of tokens, and for each sequence in it writes one row of partial sums
+// (row strip + sequence: unique, since both only grow). A second launch adds a
+// sequence's rows in a fixed order, eight blocks of a cluster sharing the experts.
+// The logits are read once; what bounds it is HBM for many tokens and the two
+// launches for few.
 //
 // Scores that all underflow (every logit far below 0) keep their ratios: the
 // shares are then taken relative to the largest. A token whose scores are all 0
@@ -29,7 +31,9 @@ namespace {
 
 constexpr int kSumWarps = 16, kSumThreads = 32 * kSumWarps;
 constexpr int kGradWarps = 8, kGradThreads = 32 * kGradWarps;
-constexpr int kFinalThreads = 256, kFinalCluster = 8;
+constexpr int kFinalMost = 1024, kFinalCluster = 8;
+constexpr int kIdsAhead = 8;            // ids that a thread loads at a time
+constexpr int kNoId = 1 << 30;          // past the last pair
 
 struct BalanceParams {
   int T, E, K, B, strip;
@@ -67,27 +71,60 @@ __device__ int first_sequence(const BalanceParams& p, int t, int lane) {
   return lo;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum and maximum over the L lanes that hold a token.
+template <int L = 32>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
 
-// Expert of a lane's value j. FULL (E = 32 V): pairs of neighbours, loaded at
-// once, and no lane's value is of no expert.
-template <bool FULL>
-__device__ __forceinline__ int expert_of(int j, int lane) {
-  return FULL ? 64 * (j >> 1) + 2 * lane + (j & 1) : lane + 32 * j;
+// Loads that stay where they are written (a group of tokens ahead of their use).
+__device__ __forceinline__ float load_now(const float* p) {
+  float v;
+  asm volatile("ld.global.cs.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
 }
+__device__ __forceinline__ float4 load_now(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+
+// What a kernel's template holds: L lanes per token with V experts each; FOURS (E
+// a multiple of 4): groups of four neighbours, loaded at once; FULL: E = L V.
+template <int L_, int V_, bool FOURS_, bool FULL_>
+struct Shape {
+  static constexpr int L = L_, V = V_;
+  static constexpr bool FOURS = FOURS_, FULL = FULL_;
+  static constexpr int kTokens = 32 / L;  // of a warp at a time
+  static __device__ __forceinline__ int expert(int j, int sub) { return FOURS ? 4 * (sub + L * (j >> 2)) + (j & 3) : sub + L * j; }
+  static __device__ __forceinline__ bool is(int j, int sub, int E) { return FULL || expert(j, sub) < E; }
+  static __device__ __forceinline__ void load(float (&x)[V], const float* row, int E, int sub, float fill) {
+    if constexpr (FOURS) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float4 v = is(j, sub, E) ? load_now(reinterpret_cast<const float4*>(row + expert(j, sub))) : make_float4(fill, fill, fill, fill);
+        x[j] = v.x;
+        x[j + 1] = v.y;
+        x[j + 2] = v.z;
+        x[j + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = is(j, sub, E) ? load_now(row + expert(j, sub)) : fill;
+    }
+  }
+};
 
 // exp(x) and 1 / x to 2 ulp, tiny results as 0: two instructions each, where the
-// forms that keep subnormals take five (with them and the checks of lanes past E
-// a token of 256 experts took 238 instructions).
+// forms that keep subnormals take five.
 __device__ __forceinline__ float exp_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
@@ -99,81 +136,70 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return r;
 }
 
-// A token's scores from its logits (in place), and 1 over their sum: the shares
-// are their products. With SLOPE also d log(score) / d logit.
-template <int V, bool SOFTMAX, bool SLOPE, bool FULL>
-__device__ __forceinline__ float scores(float (&x)[V], float (&slope)[V], int E, int lane) {
-  auto is = [&](int j) { return FULL || expert_of<FULL>(j, lane) < E; };
+// A token's scores from its logits (in place; `row`: where they came from), and 1
+// over their sum: the shares are their products. With SLOPE also d log(score) / d logit.
+template <class S, bool SOFTMAX, bool SLOPE>
+__device__ __forceinline__ float scores(float (&x)[S::V], float (&slope)[SLOPE ? S::V : 1], const float* row, int E, int sub) {
+  constexpr int V = S::V;
   // exp(x - the largest): scores that underflow keep their ratios.
   auto relative = [&] {
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
-    top = warp_max(top);
+    top = lanes_max<S::L>(top);
     if (top == -INFINITY) top = 0.0f;  // all scores 0
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      x[j] = is(j) ? exp_fast(x[j] - top) : 0.0f;
+      x[j] = S::is(j, sub, E) ? exp_fast(x[j] - top) : 0.0f;
       sum += x[j];
     }
-    return warp_sum(sum);
+    return lanes_sum<S::L>(sum);
   };
   float sum = 0.0f;
   if (SOFTMAX) {
     sum = relative();
   } else {
-    float sg[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float a = exp_fast(-fabsf(x[j])), d = rcp_fast(1.0f + a), ad = a * d;
       const bool up = x[j] >= 0.0f;
-      if (SLOPE) slope[j] = up ? ad : d;
-      sg[j] = is(j) ? (up ? d : ad) : 0.0f;
-      sum += sg[j];
+      if (SLOPE) slope[SLOPE ? j : 0] = up ? ad : d;
+      x[j] = S::is(j, sub, E) ? (up ? d : ad) : 0.0f;
+      sum += x[j];
     }
-    sum = warp_sum(sum);
-    if (sum < 1e-30f) {  // sigma(x) = exp(x) here
-      sum = relative();
-    } else {
+    sum = lanes_sum<S::L>(sum);
+    const bool tiny = sum < 1e-30f;
+    if (__any_sync(0xFFFFFFFFu, tiny)) {  // sigma(x) = exp(x) there: from the logits once more
+      float sg[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = sg[j];
+      for (int j = 0; j < V; ++j) sg[j] = x[j];
+      S::load(x, row, E, sub, -INFINITY);
+      const float sum2 = relative();
+      if (tiny) {
+        sum = sum2;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = sg[j];
+      }
     }
   }
   return sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays
 }
 
-template <int V, bool FULL>
-__device__ __forceinline__ void load_row(float (&x)[V], const float* row, int E, int lane, float fill) {
-  if (FULL) {
-#pragma unroll
-    for (int j = 0; j < V; j += 2) {
-      const float2 v = __ldcs(reinterpret_cast<const float2*>(row + expert_of<true>(j, lane)));
-      x[j] = v.x;
-      x[j + 1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = lane + 32 * j < E ? __ldcs(row + lane + 32 * j) : fill;
-  }
-}
-
-// Tokens that a warp takes at a time.
-template <int V>
-constexpr int kAtOnce = V <= 8 ? 2 : 1;
-
-template <int V, bool SOFTMAX, bool FULL>
-__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceParams p) {
+template <class S, bool SOFTMAX>
+__global__ void __launch_bounds__(kSumThreads, 1) balance_sum_kernel(const BalanceParams p) {
+  constexpr int V = S::V, L = S::L;
   extern __shared__ float smem[];
   float* sums = smem;                                                 // [warps][E]
   int32_t* hist = reinterpret_cast<int32_t*>(smem + kSumWarps * p.E);  // [E]
   __shared__ int first;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, E = p.E;
   wait_for_previous_launch();
   allow_next_launch();
   const int t0 = blockIdx.x * p.strip, t1 = t0 + p.strip < p.T ? t0 + p.strip : p.T;
   if (warp == 0) {
-    const int b = first_sequence(p, t0, lane);
+    const int b = p.seq ? first_sequence(p, t0, lane) : 0;
     if (lane == 0) first = b;
   }
   for (int e = threadIdx.x; e < E; e += kSumThreads) hist[e] = 0;
@@ -183,34 +209,70 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
     if (a >= t1) break;
     const int lo = a > t0 ? a : t0, hi = z < t1 ? z : t1;
     if (lo >= hi) continue;
+    // The counts. Up to 16 experts one ballot each, as their words would be added to
+    // by many lanes at once.
+    const int32_t* ids = p.topk_idx + (size_t)lo * p.K;
+    const long long pairs = (long long)(hi - lo) * p.K;
+    int mine = 0;
+    for (long long i0 = threadIdx.x; i0 - lane < pairs; i0 += kIdsAhead * kSumThreads) {
+      int id[kIdsAhead];
+#pragma unroll
+      for (int k = 0; k < kIdsAhead; ++k) {
+        const long long i = i0 + k * kSumThreads;
+        id[k] = i < pairs ? __ldcs(ids + i) : kNoId;
+      }
+#pragma unroll
+      for (int k = 0; k < kIdsAhead; ++k) {
+        if (i0 + k * kSumThreads < pairs && (id[k] < 0 || id[k] >= E)) atomicCAS(p.status, 0, MOE_DEV_BAD_EXPERT_ID);
+        if (E <= 16) {
+          for (int e = 0; e < E; ++e) {
+            const int n = __popc(__ballot_sync(0xFFFFFFFFu, id[k] == e));
+            if (lane == e) mine += n;
+          }
+        } else if (id[k] >= 0 && id[k] < E) {
+          atomicAdd(hist + id[k], 1);
+        }
+      }
+    }
+    if (E <= 16 && lane < E) atomicAdd(hist + lane, mine);
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-    for (int t = lo + warp; t < hi; t += kAtOnce<V> * kSumWarps) {
-      float x[kAtOnce<V>][V], unused[V];
-      int id[kAtOnce<V>];
+    // U groups of tokens at a time, the next ones' logits on their way meanwhile: 64 KB
+    // per SM in flight (32 KB: 13 of the 22 us of 65536 x 256 were waits).
+    constexpr int U = V <= 4 ? 8 : (V <= 8 ? 4 : (V <= 16 ? 2 : 1)), kStep = kSumWarps * S::kTokens;
+    float next[U][V];
+    auto load = [&](int t) {
 #pragma unroll
-      for (int k = 0; k < kAtOnce<V>; ++k) {
-        const int at = t + k * kSumWarps < hi ? t + k * kSumWarps : t;
-        load_row<V, FULL>(x[k], p.logits + (size_t)at * E, E, lane, -INFINITY);
-        id[k] = lane < p.K ? __ldcs(p.topk_idx + (size_t)at * p.K + lane) : 0;
+      for (int u = 0; u < U; ++u) {
+        if (t + u * kStep >= hi) break;
+        const int at = t + u * kStep + lane / L;
+        S::load(next[u], p.logits + (size_t)(at < hi ? at : lo) * E, E, sub, -INFINITY);
       }
+    };
+    load(lo + warp * S::kTokens);
+    for (int t = lo + warp * S::kTokens; t < hi; t += U * kStep) {
+      float x[U][V], unused[1];
 #pragma unroll
-      for (int k = 0; k < kAtOnce<V>; ++k) {
-        if (t + k * kSumWarps >= hi) break;
-        if (lane < p.K) {
-          if (id[k] >= 0 && id[k] < E) atomicAdd(hist + id[k], 1);
-          else atomicCAS(p.status, 0, MOE_DEV_BAD_EXPERT_ID);
-        }
-        const float inv = scores<V, SOFTMAX, false, FULL>(x[k], unused, E, lane);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = fmaf(x[k][j], inv, acc[j]);
+        for (int j = 0; j < V; ++j) x[u][j] = next[u][j];
+      if (t + U * kStep < hi) load(t + U * kStep);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u * kStep >= hi) break;
+        const bool live = t + u * kStep + lane / L < hi;
+        float inv = scores<S, SOFTMAX, false>(x[u], unused, p.logits + (size_t)(live ? t + u * kStep + lane / L : lo) * E, E, sub);
+        if (!live) inv = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(live ? x[u][j] : 0.0f, inv, acc[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = expert_of<FULL>(j, lane);
-      if (e < E) sums[warp * E + e] = acc[j];
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
+      if (lane < L && S::is(j, sub, E)) sums[warp * E + S::expert(j, sub)] = acc[j];
     }
     __syncthreads();
     const size_t row = ((size_t)blockIdx.x + b) * E;
@@ -226,50 +288,52 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
   }
 }
 
-// A cluster per sequence, each block every eighth run of 32 experts.
-__global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(const BalanceParams p) {
-  __shared__ float ps[kFinalThreads];
-  __shared__ int pn[kFinalThreads];
+// A cluster per sequence, its blocks taking runs of 32 experts by turns.
+__global__ void __launch_bounds__(kFinalMost) balance_final_kernel(const BalanceParams p) {
+  const int kWarps = blockDim.x / 32;  // a power of two
+  __shared__ float ps[kFinalMost];
+  __shared__ int pn[kFinalMost];
   __shared__ float share[kFinalCluster];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
   const uint32_t rank = cluster_ctarank();
-  const int b = (int)cluster_id_x();
+  const int b = (int)cluster_id_x(), nranks = (int)(gridDim.x / ncluster_x());
   wait_for_previous_launch();
   allow_next_launch();
   const int a = seq_start(p, b), z = seq_start(p, b + 1), n = z > a ? z - a : 0;
   const int s0 = n ? a / p.strip : 0, s1 = n ? (z - 1) / p.strip + 1 : 0;
   const float inv_n = n ? 1.0f / (float)n : 0.0f, per = (float)E * inv_n / (float)p.K;
   float loss = 0.0f;
-  for (int e0 = (int)rank * 32; e0 < E; e0 += 32 * kFinalCluster) {
+  for (int e0 = (int)rank * 32; e0 < E; e0 += 32 * nranks) {
     const int e = e0 + lane;
     float s = 0.0f;
     int c = 0;
     if (e < E) {
-#pragma unroll 4
-      for (int i = s0 + warp; i < s1; i += kFinalThreads / 32) {
+#pragma unroll 5
+      for (int i = s0 + warp; i < s1; i += kWarps) {
         s += __ldcg(p.part + ((size_t)i + b) * E + e);
         c += __ldcg(p.part_n + ((size_t)i + b) * E + e);
       }
     }
-    ps[threadIdx.x] = s;
-    pn[threadIdx.x] = c;
-    __syncthreads();
-    if (warp == 0) {
-      for (int w = 1; w < kFinalThreads / 32; ++w) {
-        s += ps[w * 32 + lane];
-        c += pn[w * 32 + lane];
+    // Halves are added until one warp's are left.
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+      ps[threadIdx.x] = s;
+      pn[threadIdx.x] = c;
+      __syncthreads();
+      if (warp < half) {
+        s += ps[threadIdx.x + 32 * half];
+        c += pn[threadIdx.x + 32 * half];
       }
-      if (e < E) {
-        const float prob = s * inv_n;
-        p.counts[(size_t)b * E + e] = c;
-        p.prob[(size_t)b * E + e] = prob;
-        loss += (float)c * per * prob;
-      }
+      __syncthreads();
     }
-    __syncthreads();
+    if (warp == 0 && e < E) {
+      const float prob = s * inv_n;
+      p.counts[(size_t)b * E + e] = c;
+      p.prob[(size_t)b * E + e] = prob;
+      loss += (float)c * per * prob;
+    }
   }
   if (warp == 0) {
-    loss = warp_sum(loss);
+    loss = lanes_sum(loss);
     if (lane == 0) {
       const uint32_t at = mapa_shared(smem_u32(share + rank), 0);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(loss) : "memory");
@@ -279,93 +343,85 @@ __global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(const Bala
   cluster_sync_all();
   if (rank == 0 && threadIdx.x == 0) {
     float l = 0.0f;
-    for (int r = 0; r < kFinalCluster; ++r) l += share[r];
+    for (int r = 0; r < nranks; ++r) l += share[r];
     p.loss[b] = p.coef * l;
   }
 }
 
-template <int V, bool SOFTMAX, bool FULL>
+template <class S, bool SOFTMAX>
 __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const BalanceParams p) {
-  __shared__ int first;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
+  constexpr int V = S::V, L = S::L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, E = p.E;
   wait_for_previous_launch();
   allow_next_launch();
   const int t0 = blockIdx.x * p.strip, t1 = t0 + p.strip < p.T ? t0 + p.strip : p.T;
-  if (warp == 0) {
-    const int b = first_sequence(p, t0, lane);
-    if (lane == 0) first = b;
-  }
-  __syncthreads();
-  for (int b = first; b < p.B; ++b) {
+  for (int b = p.seq ? first_sequence(p, t0, lane) : 0; b < p.B; ++b) {
     const int a = seq_start(p, b), z = seq_start(p, b + 1);
     if (a >= t1) break;
     const int lo = a > t0 ? a : t0, hi = z < t1 ? z : t1;
-    if (lo + warp >= hi) continue;
+    if (lo + warp * S::kTokens >= hi) continue;
     const float inv_n = 1.0f / (float)(z - a), per = (float)E * inv_n / (float)p.K;
     const float w = __ldcg(p.dloss + b) * p.coef * inv_n;
     float f[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = expert_of<FULL>(j, lane);
-      f[j] = e < E ? (float)__ldcg(p.counts + (size_t)b * E + e) * per : 0.0f;
-    }
-    for (int t0 = lo + warp; t0 < hi; t0 += kAtOnce<V> * kGradWarps) {
-      float x[kAtOnce<V>][V], add[kAtOnce<V>][V], slope[V];
+    for (int j = 0; j < V; ++j)
+      f[j] = S::is(j, sub, E) ? (float)__ldcg(p.counts + (size_t)b * E + S::expert(j, sub)) * per : 0.0f;
+    for (int t = lo + warp * S::kTokens; t < hi; t += kGradWarps * S::kTokens) {
+      const bool live = t + lane / L < hi;
+      const size_t at = (size_t)(live ? t + lane / L : t) * E;
+      float x[V], slope[V], add[V];
+      S::load(x, p.logits + at, E, sub, -INFINITY);
+      if (p.add) S::load(add, p.add + at, E, sub, 0.0f);
+      const float inv = scores<S, SOFTMAX, true>(x, slope, p.logits + at, E, sub);
+      float c = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kAtOnce<V>; ++k) {
-        const int at = t0 + k * kGradWarps < hi ? t0 + k * kGradWarps : t0;
-        load_row<V, FULL>(x[k], p.logits + (size_t)at * E, E, lane, -INFINITY);
-        if (p.add) load_row<V, FULL>(add[k], p.add + (size_t)at * E, E, lane, 0.0f);
+      for (int j = 0; j < V; ++j) c = fmaf(f[j], x[j], c);
+      c = lanes_sum<L>(c) * inv;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float d = w * (f[j] - c) * (x[j] * inv);
+        if (!SOFTMAX) d *= slope[j];
+        x[j] = p.add ? d + add[j] : d;
       }
+      float* row = p.dlogits + at;
+      if (!live) {
+      } else if constexpr (S::FOURS) {
 #pragma unroll
-      for (int k = 0; k < kAtOnce<V>; ++k) {
-        const int t = t0 + k * kGradWarps;
-        if (t >= hi) break;
-        const float inv = scores<V, SOFTMAX, true, FULL>(x[k], slope, E, lane);
-        float c = 0.0f;
+        for (int j = 0; j < V; j += 4)
+          if (S::is(j, sub, E)) __stcs(reinterpret_cast<float4*>(row + S::expert(j, sub)), make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]));
+      } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) c = fmaf(f[j], x[k][j], c);
-        c = warp_sum(c) * inv;
-        float* row = p.dlogits + (size_t)t * E;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float d = w * (f[j] - c) * (x[k][j] * inv);
-          if (!SOFTMAX) d *= slope[j];
-          x[k][j] = p.add ? d + add[k][j] : d;
-        }
-        if (FULL) {
-#pragma unroll
-          for (int j = 0; j < V; j += 2)
-            __stcs(reinterpret_cast<float2*>(row + expert_of<true>(j, lane)), make_float2(x[k][j], x[k][j + 1]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (lane + 32 * j < E) __stcs(row + lane + 32 * j, x[k][j]);
-        }
+        for (int j = 0; j < V; ++j)
+          if (S::is(j, sub, E)) __stcs(row + S::expert(j, sub), x[j]);
       }
     }
   }
 }
 
-template <bool GRAD, int V, bool SOFTMAX, bool FULL>
+template <bool GRAD, bool SOFTMAX, class S>
 cudaError_t run(const BalanceParams& p, int strips, cudaStream_t s) {
-  if (GRAD) return launch_dependent(balance_grad_kernel<V, SOFTMAX, FULL>, strips, kGradThreads, 0, s, true, 1, p);
+  if (GRAD) return launch_dependent(balance_grad_kernel<S, SOFTMAX>, strips, kGradThreads, 0, s, true, 1, p);
   const size_t smem = (size_t)(kSumWarps + 1) * p.E * 4;
-  return launch_dependent(balance_sum_kernel<V, SOFTMAX, FULL>, strips, kSumThreads, smem, s, true, 1, p);
+  return launch_dependent(balance_sum_kernel<S, SOFTMAX>, strips, kSumThreads, smem, s, true, 1, p);
 }
-// Values per lane: the least that hold E, so that few lanes' loads and exponentials are of no expert.
-template <bool GRAD, bool SOFTMAX, int V>
+template <bool GRAD, bool SOFTMAX, int L, int V>
 cudaError_t fit(const BalanceParams& p, int strips, cudaStream_t s) {
-  return p.E == 32 * V ? run<GRAD, V, SOFTMAX, true>(p, strips, s) : run<GRAD, V, SOFTMAX, false>(p, strips, s);
+  if (p.E == L * V && V % 4 == 0) return run<GRAD, SOFTMAX, Shape<L, V, V % 4 == 0, V % 4 == 0>>(p, strips, s);
+  if (p.E % 4 == 0 && V % 4 == 0) return run<GRAD, SOFTMAX, Shape<L, V, V % 4 == 0, false>>(p, strips, s);
+  return run<GRAD, SOFTMAX, Shape<L, V, false, false>>(p, strips, s);
 }
+// Values per lane: the least of these that hold E, so that few loads and exponentials are of no expert.
 template <bool GRAD, bool SOFTMAX>
 cudaError_t pick(const BalanceParams& p, int strips, cudaStream_t s) {
-  if (p.E <= 64) return fit<GRAD, SOFTMAX, 2>(p, strips, s);
-  if (p.E <= 128) return fit<GRAD, SOFTMAX, 4>(p, strips, s);
-  if (p.E <= 192) return fit<GRAD, SOFTMAX, 6>(p, strips, s);
-  if (p.E <= 256) return fit<GRAD, SOFTMAX, 8>(p, strips, s);
-  if (p.E <= 512) return fit<GRAD, SOFTMAX, 16>(p, strips, s);
-  return fit<GRAD, SOFTMAX, 32>(p, strips, s);
+  if (p.E <= 8) return fit<GRAD, SOFTMAX, 2, 4>(p, strips, s);
+  if (p.E <= 16) return fit<GRAD, SOFTMAX, 4, 4>(p, strips, s);
+  if (p.E <= 32) return fit<GRAD, SOFTMAX, 8, 4>(p, strips, s);
+  if (p.E <= 64) return fit<GRAD, SOFTMAX, 8, 8>(p, strips, s);
+  if (p.E <= 128) return fit<GRAD, SOFTMAX, 8, 16>(p, strips, s);
+  if (p.E <= 192) return fit<GRAD, SOFTMAX, 16, 12>(p, strips, s);
+  if (p.E <= 256) return fit<GRAD, SOFTMAX, 16, 16>(p, strips, s);
+  if (p.E <= 512) return fit<GRAD, SOFTMAX, 32, 16>(p, strips, s);
+  return fit<GRAD, SOFTMAX, 32, 32>(p, strips, s);
 }
 template <bool GRAD>
 cudaError_t pick(const BalanceParams& p, bool softmax, int strips, cudaStream_t s) {
@@ -393,23 +449,26 @@ BalanceParams params_of(const BalanceArgs& a, int strip) {
   return p;
 }
 
-// Tokens per block of the sums: two per warp at least, and at most about 300
-// blocks, so that the second launch has few rows to add.
+// Tokens per block of the sums: one per warp at least, and at most
+// 152 blocks, one per SM, so that the second launch has few rows to add.
 int sum_strip(int T) {
-  const int n = (T + 303) / 304;
-  return n > 2 * kSumWarps ? n : 2 * kSumWarps;
+  const int n = (T + 151) / 152;
+  return n > kSumWarps ? n : kSumWarps;
 }
 int sum_strips(int T) { return (T + sum_strip(T) - 1) / sum_strip(T); }
 
 }  // namespace
 
 cudaError_t balance_prepare_device() {
+  // Past 512 experts the sums take more shared memory than a launch may without asking.
   const int most = (kSumWarps + 1) * 1024 * 4;
   const cudaError_t errs[] = {
-      cudaFuncSetAttribute(balance_sum_kernel<32, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
-      cudaFuncSetAttribute(balance_sum_kernel<32, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
-      cudaFuncSetAttribute(balance_sum_kernel<32, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
-      cudaFuncSetAttribute(balance_sum_kernel<32, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)};
+      cudaFuncSetAttribute(balance_sum_kernel<Shape<32, 32, true, true>, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<Shape<32, 32, true, true>, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<Shape<32, 32, true, false>, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<Shape<32, 32, true, false>, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<Shape<32, 32, false, false>, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+      cudaFuncSetAttribute(balance_sum_kernel<Shape<32, 32, false, false>, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)};
   for (cudaError_t e : errs)
     if (e != cudaSuccess) return e;
   return cudaSuccess;
@@ -426,14 +485,19 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
     const cudaError_t e = pick<false>(p, a.softmax, strips, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(balance_final_kernel, a.B * kFinalCluster, kFinalThreads, 0, s, true, kFinalCluster, p);
+  // A warp for about five of a sequence's rows (152 for one sequence), a block for 32 experts.
+  int warps = 4, blocks = 1;
+  while (warps < kFinalMost / 32 && warps * 5 < strips / a.B) warps *= 2;
+  while (blocks < kFinalCluster && blocks * 32 < a.E) blocks *= 2;
+  return launch_dependent(balance_final_kernel, a.B * blocks, 32 * warps, 0, s, true, blocks, p);
 }
 
 cudaError_t launch_balance_loss_backward(const BalanceArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  // Four tokens per warp, more (so that a lane's f is loaded for several) once two
-  // blocks of each SM are at work.
-  const int per_warp = (a.T + 304 * kGradWarps - 1) / (304 * kGradWarps), strip = kGradWarps * (per_warp > 4 ? per_warp : 4);
+  // Eight tokens per warp at least, so that a lane's f is loaded for several and a
+  // small batch takes one wave of blocks (8192 x 192: 6.5 us; four 7.9, two 10.5),
+  // more once four blocks of each SM are at work.
+  const int per_warp = (a.T + 608 * kGradWarps - 1) / (608 * kGradWarps), strip = kGradWarps * (per_warp > 8 ? (per_warp + 3) / 4 * 4 : 8);
   const int strips = (a.T + strip - 1) / strip;
   const BalanceParams p = params_of(a, strip);
   return pick<true>(p, a.softmax, strips, s);

@@ -26,14 +26,17 @@ struct Vec {
     const uint32_t w = F32 ? (&raw.x)[i] : (&raw.x)[i >> 1];
     return __uint_as_float(F32 ? w : ((i & 1) ? (w & 0xFFFF0000u) : (w << 16)));
   }
+  // |values| as bits that order as they do, per value: bf16 ones two to a word.
+  static constexpr uint32_t kAbs = F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+  static __device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) { return F32 ? (a > b ? a : b) : __vmaxu2(a, b); }
+  // The largest of a word's values, as fp8_abs_bits.
+  static __device__ __forceinline__ uint32_t whole(uint32_t t) {
+    if (F32) return t;
+    const uint32_t hi = t & 0xFFFF0000u, lo = t << 16;
+    return hi > lo ? hi : lo;
+  }
   __device__ __forceinline__ uint32_t amax_bits() const {
-    uint32_t t = 0;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const uint32_t a = fp8_abs_bits(at(i));
-      t = a > t ? a : t;
-    }
-    return t;
+    return whole(max_of(max_of(raw.x & kAbs, raw.y & kAbs), max_of(raw.z & kAbs, raw.w & kAbs)));
   }
   __device__ __forceinline__ void store(uint8_t* q, const Fp8Block& b) const {
     const uint32_t lo = b.code4(at(0), at(1), at(2), at(3));
@@ -101,6 +104,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const uint8_
 // A thread block holds a tile, 64 values per thread: rows a 16th (bf16) or an 8th
 // (fp32) of the tile apart.
 constexpr int kTileThreads = 256;
+constexpr int kMaxGroups = 1024;
 
 template <bool F32>
 struct TileRegs {
@@ -133,12 +137,14 @@ __global__ void __launch_bounds__(kTileThreads)
   const int nr = rows - rb * 128, nc = cols - cb * 128;
   TileRegs<F32> t;
   t.load(x + at * (F32 ? 4 : 2), cols, nr, nc);
+  using V = Vec<F32>;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < TileRegs<F32>::kRows; ++i) {
-    const uint32_t a = t.v[i].amax_bits();
-    top = a > top ? a : top;
+    const uint4 r = t.v[i].raw;
+    top = V::max_of(top, V::max_of(V::max_of(r.x & V::kAbs, r.y & V::kAbs), V::max_of(r.z & V::kAbs, r.w & V::kAbs)));
   }
+  top = V::whole(top);
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
   __syncthreads();
@@ -157,25 +163,23 @@ template <bool F32>
 __global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
     quantize_columns_kernel(const uint8_t* x, int rows, int cols, const int32_t* offsets, int G, uint8_t* q, float* scale) {
   using T = TileRegs<F32>;
-  __shared__ uint32_t part[T::kStep][128];
+  __shared__ __align__(16) uint32_t part[T::kStep][128];
   __shared__ __align__(16) float scales[128], invs[128];
-  __shared__ int where[3];
+  __shared__ int where[2], starts[kMaxGroups + 1];
   wait_for_previous_launch();
   allow_next_launch();
   // The group whose blocks of 128 rows this one is of: every lane of a warp takes
-  // some groups, and the one whose blocks end past blockIdx.y looks for it.
+  // some groups, and the one whose blocks end past blockIdx.x looks for it.
+  for (int g = threadIdx.x; g <= G; g += kTileThreads) {
+    const int v = offsets ? __ldcg(offsets + g) : (g == 0 ? 0 : rows);
+    starts[g] = v < 0 ? 0 : (v > rows ? rows : v);
+  }
+  __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (G + 31) / 32, b = lane * per < G ? lane * per : G, e = b + per < G ? b + per : G;
-    auto start = [&](int g) {
-      const int v = offsets ? __ldcg(offsets + g) : (g == 0 ? 0 : rows);
-      return v < 0 ? 0 : (v > rows ? rows : v);
-    };
+    auto blocks = [&](int g) { return starts[g + 1] > starts[g] ? (starts[g + 1] - starts[g] + 127) / 128 : 0; };
     int mine = 0;
-    for (int g = b, r = e > b ? start(b) : 0; g < e; ++g) {
-      const int s = start(g + 1);
-      if (s > r) mine += (s - r + 127) / 128;
-      r = s;
-    }
+    for (int g = b; g < e; ++g) mine += blocks(g);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -187,10 +191,10 @@ __global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
     if (want < incl && want >= incl - mine) {
       int at = incl - mine;
       for (int g = b; g < e; ++g) {
-        const int r = start(g), s = start(g + 1), n = s > r ? (s - r + 127) / 128 : 0;
+        const int n = blocks(g);
         if (want < at + n) {
-          where[0] = r + (want - at) * 128;
-          where[1] = s - where[0];
+          where[0] = starts[g] + (want - at) * 128;
+          where[1] = starts[g + 1] - where[0];
           break;
         }
         at += n;
@@ -204,15 +208,20 @@ __global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
     const int nc = cols - cb * 128;
     T t;
     t.load(x + ((long long)row0 * cols + cb * 128) * (F32 ? 4 : 2), cols, nr, nc);
+    using V = Vec<F32>;
+    uint32_t top[4];
 #pragma unroll
-    for (int j = 0; j < T::kN; ++j) {
-      uint32_t top = 0;
+    for (int w = 0; w < 4; ++w) {
+      top[w] = 0;
 #pragma unroll
-      for (int i = 0; i < T::kRows; ++i) {
-        const uint32_t a = fp8_abs_bits(t.v[i].at(j));
-        top = a > top ? a : top;
-      }
-      part[t.row][t.col + j] = top;
+      for (int i = 0; i < T::kRows; ++i) top[w] = V::max_of(top[w], (&t.v[i].raw.x)[w] & V::kAbs);
+    }
+    uint4* mine = reinterpret_cast<uint4*>(&part[t.row][t.col]);
+    if (F32) {
+      mine[0] = make_uint4(top[0], top[1], top[2], top[3]);
+    } else {
+      mine[0] = make_uint4(top[0] << 16, top[0] & 0xFFFF0000u, top[1] << 16, top[1] & 0xFFFF0000u);
+      mine[1] = make_uint4(top[2] << 16, top[2] & 0xFFFF0000u, top[3] << 16, top[3] & 0xFFFF0000u);
     }
     __syncthreads();
     if (threadIdx.x < 128) {
