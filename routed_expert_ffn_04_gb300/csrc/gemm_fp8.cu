@@ -25,6 +25,25 @@
 // rows per group, below that the weights' bytes take longer (16 KB per SM and
 // block: 700 cycles of its share of HBM against 512 of MMAs).
 //
+// A group of up to 128 rows is one tile high and would leave the odd CTA's rows
+// empty, its epilogue idle beside one that is the slower half. Such a tile is
+// split: both CTAs hold all its rows, and each adds half of the columns of every
+// block (192 groups of 4 rows, gate and up of 4096 x 1536: 481 -> 435 us; of 100
+// rows, down: 340 -> 297). GATE_UP's row maxima then cross the pair.
+//
+// What bounds it: with full tiles the epilogue's handshake, about 850 cycles per
+// block against the MMAs' 512 (of them 265 for the additions of a scheduler's two
+// warps and 100-280 for its reads of TMEM, which hardly overlap), then a tile's
+// own epilogue (GATE_UP: 4000 cycles of SwiGLU and codes, half of them waits for
+// exp and the quotient); with few rows HBM and the loads' latency. Measured, H 4096,
+// I 1536, 192 groups:
+//   GATE_UP      341 rows 995 us, 1.66 PFLOP/s; 4 rows 440 us, 5.5 TB/s
+//   FORWARD      341 rows 690 us, 1.2 PFLOP/s (2.4 GB, of them 1.1 of fp32 results)
+//   WEIGHT_GRAD  341 rows 870 us (2.8 GB, of them 2.4 of bf16 results)
+//   FORWARD      dense 8192 x 4096 x 4096 113 us, 2.4 PFLOP/s
+// One half of a block's columns at a time through the handshake (MMAs of 128
+// columns, two barriers) was slower: 1131 and 126 us.
+//
 // TRANSPOSED and WEIGHT_GRAD read operands MN-major from the row-major tensors,
 // with no transposed copy: a box of 128 columns x 128 rows lands as 128 rows of
 // 128 swizzled bytes, 8 rows (1024 bytes) per step of the layout, 32 rows per MMA.
@@ -71,7 +90,7 @@ constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
 constexpr int kFactorSlots = 4;               // blocks whose factors are kept
 constexpr int kFactors = 384;                 // of a block: rows' (twice, or once and 256 columns')
 constexpr int kColBytes = kFactorSlots * kFactors * 4 + 6144;  // and GATE_UP's row maxima: two slots of four parts, two of two
-constexpr int bars_of(int mode) { return 2 * stages(mode) + 9; }
+constexpr int bars_of(int mode) { return 2 * stages(mode) + 17; }
 constexpr int bar_bytes(int mode) { return (8 * bars_of(mode) + 8 + 15) / 16 * 16; }  // and the TMEM address and the abort flag
 constexpr int kTableBytes = (kMaxGroups + 8) * 4 * 2;
 constexpr int smem_of(int mode) {
@@ -244,7 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kStages + a); };   // each CTA
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kStages + 2 + a); };  // leader
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
-  auto tops_bar = [&](int q) { return bar0 + 8u * (2 * kStages + 5 + q); };  // each CTA: GATE_UP's split tiles
+  // Each CTA, GATE_UP: a tile's maxima are there, by q; of split tiles two by turns,
+  // as the other CTA may be a tile ahead.
+  auto join_bar = [&](int q) { return bar0 + 8u * (2 * kStages + 5 + q); };
+  auto split_bar = [&](int q, uint32_t turn) { return bar0 + 8u * (2 * kStages + 9 + 4 * turn + q); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: leader
@@ -260,7 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(a), 2 * kEpiWarps);
     }
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(tops_bar(i), 2);  // this CTA's two warps; the other's come as bytes
+    for (int i = 0; i < 4; ++i) {  // this CTA's two warps; the other's come as bytes
+      mbar_init(join_bar(i), 2);
+      mbar_init(split_bar(i, 0), 2);
+      mbar_init(split_bar(i, 1), 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -329,181 +355,183 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto box_of = [&](int n) { return n > 64 ? 128 : (n > 32 ? 64 : (n > 16 ? 32 : (n > 0 ? 16 : 0))); };
 
   if (warp < kEpiWarp0) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    Ring rg;
-    bool ok = true;
-    for (int tile = pair; ok && tile < total; tile += npairs) {
-      const Tile t = decode(tile);
-      const int box = kA_MN ? 128 : box_of(rows_of(t, (int)rank));
-      const int boxes = kA_MN ? 256 : box_of(rows_of(t, 0)) + box_of(rows_of(t, 1));
-      const uint32_t bytes = (uint32_t)boxes * 128u + 2u * kHalf;
-      const CUtensorMap* amap = &m.a[kA_MN || box == 128 ? 0 : (box == 64 ? 1 : (box == 32 ? 2 : 3))];
-      const CUtensorMap* bmap = MODE == kFp8GateUp && rank == 1 ? &m.b1 : &m.b0;
-      const int bn = t.n0 + (MODE == kFp8GateUp ? 0 : (int)rank * 128);
-      for (int kb = 0; kb < t.kb; ++kb) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.status,
-                                                       MOE_DEV_TIMEOUT_PRODUCER, p.limit_ns))) {
-          ok = false;
-          break;
-        }
-        const uint32_t full = full_bar(rg.s);
-        const uint32_t bar = rank == 0 ? full : mapa_shared(full, 0);
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(bar, bytes);  // both CTAs' bytes (the other's may land first)
-          const uint32_t da = sm0 + rg.s * kHalf, db = b_ring + rg.s * kHalf;
-          if (kA_MN) {
-            tma_load_3d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128, 0);
-            tma_load_3d_pair(db, bmap, bar, bn, t.row0 + kb * 128, 0);
-          } else {
-            if (box) tma_load_3d_pair(da, amap, bar, kb * 128, t.row0 + first_row(t), 0);
-            if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, kb * 128, t.g);
-            else tma_load_3d_pair(db, bmap, bar, kb * 128, bn, t.g);
-          }
-        }
-        __syncwarp();
-        rg.next(kStages);
-      }
-    }
-    if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 5000000ull) {
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (rank == 0) {
-      constexpr uint32_t kIdesc = idesc_e4m3(256, 256, kA_MN, kB_MN);
-      constexpr uint32_t kStepA = kA_MN ? 4096 >> 4 : 32 >> 4, kStepB = kB_MN ? 4096 >> 4 : 32 >> 4;  // 32 of k
-      auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        return warp_wait(bar, parity, abort_flag, p.status, MOE_DEV_TIMEOUT_MMA, p.limit_ns);
-      };
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
       Ring rg;
-      Ring acc;  // TMEM buffer of the block
-      bool ok = true, issued = false;
+      bool ok = true;
       for (int tile = pair; ok && tile < total; tile += npairs) {
         const Tile t = decode(tile);
+        const int box = kA_MN ? 128 : box_of(rows_of(t, (int)rank));
+        const int boxes = kA_MN ? 256 : box_of(rows_of(t, 0)) + box_of(rows_of(t, 1));
+        const uint32_t bytes = (uint32_t)boxes * 128u + 2u * kHalf;
+        const CUtensorMap* amap = &m.a[kA_MN || box == 128 ? 0 : (box == 64 ? 1 : (box == 32 ? 2 : 3))];
+        const CUtensorMap* bmap = MODE == kFp8GateUp && rank == 1 ? &m.b1 : &m.b0;
+        const int bn = t.n0 + (MODE == kFp8GateUp ? 0 : (int)rank * 128);
         for (int kb = 0; kb < t.kb; ++kb) {
-          const uint64_t da = kA_MN ? mn_desc(sm0 + rg.s * kHalf) : sw128_kmajor_desc(sm0 + rg.s * kHalf);
-          const uint64_t db = kB_MN ? mn_desc(b_ring + rg.s * kHalf) : sw128_kmajor_desc(b_ring + rg.s * kHalf);
-          if (!wait_all(full_bar(rg.s), rg.ph) || !wait_all(tempty_bar(acc.s), acc.ph ^ 1u)) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.status,
+                                                         MOE_DEV_TIMEOUT_PRODUCER, p.limit_ns))) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t d = tmem_base + (uint32_t)(acc.s * 256);
+          const uint32_t full = full_bar(rg.s);
+          const uint32_t bar = rank == 0 ? full : mapa_shared(full, 0);
           if (elect_one()) {
-            umma_e4m3_pair(d, da, db, kIdesc, 0u);
-#pragma unroll
-            for (int k = 1; k < 4; ++k) umma_e4m3_pair(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
-            umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
-            umma_commit_pair_mc(tfull_bar(acc.s), kPairMask);
+            if (rank == 0) mbar_arrive_expect_tx(bar, bytes);  // both CTAs' bytes (the other's may land first)
+            const uint32_t da = sm0 + rg.s * kHalf, db = b_ring + rg.s * kHalf;
+            if (kA_MN) {
+              tma_load_3d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128, 0);
+              tma_load_3d_pair(db, bmap, bar, bn, t.row0 + kb * 128, 0);
+            } else {
+              if (box) tma_load_3d_pair(da, amap, bar, kb * 128, t.row0 + first_row(t), 0);
+              if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, kb * 128, t.g);
+              else tma_load_3d_pair(db, bmap, bar, kb * 128, bn, t.g);
+            }
           }
           __syncwarp();
-          issued = true;
           rg.next(kStages);
-          acc.next(2);
         }
       }
-      if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
-        umma_commit_pair(drain_bar);
-        drain_wait(drain_bar, 0, 200000000ull);
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ scales
-    // The factors of each block for the epilogue: rows' for columns 0-127 and
-    // 128-255 (GATE_UP: gates, ups), or rows' and columns' (WEIGHT_GRAD). A
-    // block's factors complete its phase of tfull together with its MMAs. Slot
-    // j % 4 is free when block j - 2 is complete: its MMAs waited for the
-    // epilogue to be done with block j - 4. Loads run four blocks (WEIGHT_GRAD:
-    // one) ahead.
-    const int kbs = fp8_blocks(p.K), nbs = fp8_blocks(p.N);  // scales per row of a; blocks of w's columns
-    const int s0 = (warp - kScaleWarp0) * 64 + lane;          // rows s0 and s0 + 32 of this CTA's 128
-    Ring acc;
-    int slot = 0;
-    bool ok = true;
-    auto hand_over = [&](auto&& write) {
-      ok = warp_wait(tfull_bar(acc.s), acc.ph ^ 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
-      if (!ok) return;
-      write(factors + slot * kFactors);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tfull_bar(acc.s));
-      slot = (slot + 1) % kFactorSlots;
-      acc.next(2);
-    };
-    for (int tile = pair; ok && tile < total; tile += npairs) {
-      const Tile t = decode(tile);
-      if (MODE == kFp8WeightGrad) {
-        const int n0 = t.m0 + (int)rank * 128 + s0, n1 = n0 + 32, c0 = t.n0 + (warp - kScaleWarp0) * 128 + 4 * lane;
-        const int c = c0 < p.K ? c0 : p.K - 4;
-        const int r0 = n0 < p.N ? n0 : p.N - 1, r1 = n1 < p.N ? n1 : p.N - 1;
-        struct Block {
-          float a, b;
-          float4 c;
-        };
-        auto load = [&](int kb) {
-          const size_t blk = (size_t)(t.row0 / 128 + (kb < t.kb ? kb : t.kb - 1));
-          return Block{load_now(p.sa + blk * p.N + r0), load_now(p.sa + blk * p.N + r1),
-                       load_now(reinterpret_cast<const float4*>(p.sb + blk * p.K + c))};
-        };
-        if (t.kb == 0) continue;
-        Block next = load(0);
-        for (int kb = 0; ok && kb < t.kb; ++kb) {
-          const Block cur = next;
-          next = load(kb + 1);
-          hand_over([&](float* f) {
-            f[s0] = cur.a;
-            f[s0 + 32] = cur.b;
-            *reinterpret_cast<float4*>(f + 128 + (warp - kScaleWarp0) * 128 + 4 * lane) = cur.c;
-          });
+      if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 5000000ull) {
         }
-      } else {
-        // Rows past the group's end take its last row's scales: their results are not stored.
-        const int last = t.nrows - 1, a0 = first_row(t) + s0;
-        const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs;
-        const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs;
-        auto load_a = [&](const float* sa, int kb) {
-          if (VEC) return load_now(reinterpret_cast<const float4*>(sa + (kb < kbs ? kb : kbs - 4)));
-          const int e = kbs - 1;
-          return make_float4(load_now(sa + (kb < e ? kb : e)), load_now(sa + (kb + 1 < e ? kb + 1 : e)),
-                             load_now(sa + (kb + 2 < e ? kb + 2 : e)), load_now(sa + (kb + 3 < e ? kb + 3 : e)));
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (rank == 0) {
+        constexpr uint32_t kIdesc = idesc_e4m3(256, 256, kA_MN, kB_MN);
+        constexpr uint32_t kStepA = kA_MN ? 4096 >> 4 : 32 >> 4, kStepB = kB_MN ? 4096 >> 4 : 32 >> 4;  // 32 of k
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+          return warp_wait(bar, parity, abort_flag, p.status, MOE_DEV_TIMEOUT_MMA, p.limit_ns);
         };
-        const int nb = t.n0 / 128, nb1 = MODE == kFp8GateUp || nb + 1 == nbs ? nb : nb + 1;
-        auto load_w = [&](const float* sb, int n, int kb) {  // a lane each for 32 blocks
-          const int k = kb + lane < kbs ? kb + lane : kbs - 1;
-          return load_now(sb + (MODE == kFp8Transposed ? ((size_t)t.g * kbs + k) * nbs + n : ((size_t)t.g * nbs + n) * kbs + k));
-        };
-        const float* sb1 = MODE == kFp8GateUp ? p.sb1 : p.sb;
-        float4 n0 = load_a(sa0, 0), n1 = load_a(sa1, 0);
-        float w = 0.f, w1 = 0.f, w_next = load_w(p.sb, nb, 0), w1_next = load_w(sb1, nb1, 0);
-        for (int kb0 = 0; ok && kb0 < t.kb; kb0 += 4) {
-          if ((kb0 & 31) == 0) {
-            w = w_next;
-            w1 = w1_next;
-            w_next = load_w(p.sb, nb, kb0 + 32);
-            w1_next = load_w(sb1, nb1, kb0 + 32);
+        Ring rg;
+        Ring acc;  // TMEM buffer of the block
+        bool ok = true, issued = false;
+        for (int tile = pair; ok && tile < total; tile += npairs) {
+          const Tile t = decode(tile);
+          for (int kb = 0; kb < t.kb; ++kb) {
+            const uint64_t da = kA_MN ? mn_desc(sm0 + rg.s * kHalf) : sw128_kmajor_desc(sm0 + rg.s * kHalf);
+            const uint64_t db = kB_MN ? mn_desc(b_ring + rg.s * kHalf) : sw128_kmajor_desc(b_ring + rg.s * kHalf);
+            if (!wait_all(full_bar(rg.s), rg.ph) || !wait_all(tempty_bar(acc.s), acc.ph ^ 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(acc.s * 256);
+            if (elect_one()) {
+              umma_e4m3_pair(d, da, db, kIdesc, 0u);
+  #pragma unroll
+              for (int k = 1; k < 4; ++k) umma_e4m3_pair(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
+              umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
+              umma_commit_pair_mc(tfull_bar(acc.s), kPairMask);
+            }
+            __syncwarp();
+            issued = true;
+            rg.next(kStages);
+            acc.next(2);
           }
-          float4 c0 = n0, c1 = n1;
-          n0 = load_a(sa0, kb0 + 4);
-          n1 = load_a(sa1, kb0 + 4);
-          const int stop = t.kb - kb0 < 4 ? t.kb : kb0 + 4;
-          for (int kb = kb0; ok && kb < stop; ++kb) {
-            const float x = __shfl_sync(0xFFFFFFFFu, w, kb & 31), y = __shfl_sync(0xFFFFFFFFu, w1, kb & 31);
+        }
+        if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
+          umma_commit_pair(drain_bar);
+          drain_wait(drain_bar, 0, 200000000ull);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ scales
+      // The factors of each block for the epilogue: rows' for columns 0-127 and
+      // 128-255 (GATE_UP: gates, ups), or rows' and columns' (WEIGHT_GRAD). A
+      // block's factors complete its phase of tfull together with its MMAs. Slot
+      // j % 4 is free when block j - 2 is complete: its MMAs waited for the
+      // epilogue to be done with block j - 4. Loads run four blocks (WEIGHT_GRAD:
+      // one) ahead.
+      const int kbs = fp8_blocks(p.K), nbs = fp8_blocks(p.N);  // scales per row of a; blocks of w's columns
+      const int s0 = (warp - kScaleWarp0) * 64 + lane;          // rows s0 and s0 + 32 of this CTA's 128
+      Ring acc;
+      int slot = 0;
+      bool ok = true;
+      auto hand_over = [&](auto&& write) {
+        ok = warp_wait(tfull_bar(acc.s), acc.ph ^ 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+        if (!ok) return;
+        write(factors + slot * kFactors);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tfull_bar(acc.s));
+        slot = (slot + 1) % kFactorSlots;
+        acc.next(2);
+      };
+      for (int tile = pair; ok && tile < total; tile += npairs) {
+        const Tile t = decode(tile);
+        if (MODE == kFp8WeightGrad) {
+          const int n0 = t.m0 + (int)rank * 128 + s0, n1 = n0 + 32, c0 = t.n0 + (warp - kScaleWarp0) * 128 + 4 * lane;
+          const int c = c0 < p.K ? c0 : p.K - 4;
+          const int r0 = n0 < p.N ? n0 : p.N - 1, r1 = n1 < p.N ? n1 : p.N - 1;
+          const int blocks = p.rows / 128 + G;  // that there are; offsets that fall could ask for more
+          struct Block {
+            float a, b;
+            float4 c;
+          };
+          auto load = [&](int kb) {
+            const int at = t.row0 / 128 + (kb < t.kb ? kb : t.kb - 1);
+            const size_t blk = (size_t)(at < blocks ? at : blocks - 1);
+            return Block{load_now(p.sa + blk * p.N + r0), load_now(p.sa + blk * p.N + r1),
+                         load_now(reinterpret_cast<const float4*>(p.sb + blk * p.K + c))};
+          };
+          if (t.kb == 0) continue;
+          Block next = load(0);
+          for (int kb = 0; ok && kb < t.kb; ++kb) {
+            const Block cur = next;
+            next = load(kb + 1);
             hand_over([&](float* f) {
-              f[s0] = c0.x * x;
-              f[s0 + 32] = c1.x * x;
-              f[128 + s0] = c0.x * y;
-              f[128 + s0 + 32] = c1.x * y;
+              f[s0] = cur.a;
+              f[s0 + 32] = cur.b;
+              *reinterpret_cast<float4*>(f + 128 + (warp - kScaleWarp0) * 128 + 4 * lane) = cur.c;
             });
-            c0 = make_float4(c0.y, c0.z, c0.w, 0.f);
-            c1 = make_float4(c1.y, c1.z, c1.w, 0.f);
+          }
+        } else {
+          // Rows past the group's end take its last row's scales: their results are not stored.
+          const int last = t.nrows - 1, a0 = first_row(t) + s0;
+          const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs;
+          const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs;
+          auto load_a = [&](const float* sa, int kb) {
+            if (VEC) return load_now(reinterpret_cast<const float4*>(sa + (kb < kbs ? kb : kbs - 4)));
+            const int e = kbs - 1;
+            return make_float4(load_now(sa + (kb < e ? kb : e)), load_now(sa + (kb + 1 < e ? kb + 1 : e)),
+                               load_now(sa + (kb + 2 < e ? kb + 2 : e)), load_now(sa + (kb + 3 < e ? kb + 3 : e)));
+          };
+          const int nb = t.n0 / 128, nb1 = MODE == kFp8GateUp || nb + 1 == nbs ? nb : nb + 1;
+          auto load_w = [&](const float* sb, int n, int kb) {  // a lane each for 32 blocks
+            const int k = kb + lane < kbs ? kb + lane : kbs - 1;
+            return load_now(sb + (MODE == kFp8Transposed ? ((size_t)t.g * kbs + k) * nbs + n : ((size_t)t.g * nbs + n) * kbs + k));
+          };
+          const float* sb1 = MODE == kFp8GateUp ? p.sb1 : p.sb;
+          float4 n0 = load_a(sa0, 0), n1 = load_a(sa1, 0);
+          float w = 0.f, w1 = 0.f, w_next = load_w(p.sb, nb, 0), w1_next = load_w(sb1, nb1, 0);
+          for (int kb0 = 0; ok && kb0 < t.kb; kb0 += 4) {
+            if ((kb0 & 31) == 0) {
+              w = w_next;
+              w1 = w1_next;
+              w_next = load_w(p.sb, nb, kb0 + 32);
+              w1_next = load_w(sb1, nb1, kb0 + 32);
+            }
+            float4 c0 = n0, c1 = n1;
+            n0 = load_a(sa0, kb0 + 4);
+            n1 = load_a(sa1, kb0 + 4);
+            const int stop = t.kb - kb0 < 4 ? t.kb : kb0 + 4;
+            for (int kb = kb0; ok && kb < stop; ++kb) {
+              const float x = __shfl_sync(0xFFFFFFFFu, w, kb & 31), y = __shfl_sync(0xFFFFFFFFu, w1, kb & 31);
+              hand_over([&](float* f) {
+                f[s0] = c0.x * x;
+                f[s0 + 32] = c1.x * x;
+                f[128 + s0] = c0.x * y;
+                f[128 + s0 + 32] = c1.x * y;
+              });
+              c0 = make_float4(c0.y, c0.z, c0.w, 0.f);
+              c1 = make_float4(c1.y, c1.z, c1.w, 0.f);
+            }
           }
         }
       }
     }
-  }
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
@@ -669,16 +697,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (split) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[i] = finish(sum[i], sum[32 + i]);
-          tops += (split_phase & 1) * 512;
+          const uint32_t turn = split_phase & 1, bar = split_bar(q, turn);
+          tops += turn * 512;
           uint32_t* mine = tops + (2 * rank + half) * 128;
           *mine = top;
-          st_async(mapa_shared(smem_u32(mine), rank ^ 1u), top, mapa_shared(tops_bar(q), rank ^ 1u));
+          st_async(mapa_shared(smem_u32(mine), rank ^ 1u), top, mapa_shared(bar, rank ^ 1u));
           __syncwarp();
           if (lane == 0) {
-            if (half == 0) mbar_arrive_expect_tx(tops_bar(q), 2 * 32 * 4);
-            else mbar_arrive(tops_bar(q));
+            if (half == 0) mbar_arrive_expect_tx(bar, 2 * 32 * 4);
+            else mbar_arrive(bar);
           }
-          ok = warp_wait(tops_bar(q), split_phase & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+          ok = warp_wait(bar, (split_phase >> 1) & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
           if (!ok) goto done;
           ++split_phase;
 #pragma unroll
@@ -689,10 +718,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 64; ++i) sum[i] = finish(sum[i], sum[64 + i]);
-          tops += 1024 + (joined++ & 1) * 256;
+          tops += 1024 + (joined & 1) * 256;
           tops[half * 128] = top;
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-          const uint32_t other = tops[(half ^ 1) * 128];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(join_bar(q));
+          ok = warp_wait(join_bar(q), joined & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+          if (!ok) goto done;
+          ++joined;
+          const uint32_t other = *reinterpret_cast<volatile uint32_t*>(tops + (half ^ 1) * 128);
           top = other > top ? other : top;
         }
         const float scale = fp8_scale(top);
@@ -775,6 +808,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
+  if (*abort_flag) {  // the other CTA's last stores and arrivals here land: 5 ms
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 5000000ull) {
+    }
+  }
+  __syncwarp();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);

@@ -289,6 +289,11 @@ def test_gate_up(handle, counts, H, I):
         r += n
 
 
+def test_gate_up_small_and_large_groups_in_turn(handle):
+    """Tiles of up to 128 rows and higher ones by turns in the same thread blocks, several of each."""
+    test_gate_up(handle, [20, 200, 128, 129] * 20, 128, 512)
+
+
 # ---------------------------------------------------------------- weights' gradient
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
 @pytest.mark.parametrize("counts, N, K", [([1], 16, 16), ([0, 5, 0], 48, 80), ([128, 1, 300, 0, 129], 272, 400), ([1000], 256, 512),
@@ -313,6 +318,24 @@ def test_weight_grad(handle, counts, N, K, out_dtype):
         x, y = (val(q[at:at + m]) * spread(s[at // 128:(at + m) // 128], m, 0) for q, s in (qs[:2], qs[2:]))
         close(dw[i], x.t() @ y, x.abs().t() @ y.abs(), max(1, nblocks(n)), f"group {i} of {n}")
         at += m
+
+
+def test_offsets_that_fall_stay_inside(handle):
+    """Not allowed, and not refused as the offsets are on the device: the groups ask for more blocks than there are. What
+    is read and written stays inside the tensors."""
+    off, rows, N, K = torch.tensor([0, 300, 0, 300, 0, 300], dtype=torch.int32, device="cuda"), 300, 128, 256
+    P = moe.fp8_padded_rows(rows, 5)
+    assert P // 128 < 3 * nblocks(rows)
+    qs = []
+    for C in (N, K):
+        q, s = torch.full((P + 1, C), 0xA5, dtype=U8, device="cuda"), torch.full((P // 128 + 1, C), -1.0, device="cuda")
+        moe.quantize_fp8_columns(handle, torch.ones((rows, C), dtype=BF16, device="cuda"), off, q[:P], s[:P // 128], num_groups=5)
+        assert (q[P:] == 0xA5).all() and (s[P // 128:] == -1.0).all()
+        qs += [q[:P], s[:P // 128]]
+    dw = torch.full((6, N, K), 7.0, device="cuda")
+    moe.grouped_weight_grad_fp8(handle, *qs, off, dw[:5], rows=rows, num_groups=5, N=N, K=K)
+    torch.cuda.synchronize()
+    assert (dw[5] == 7.0).all() and (dw[1] == 0).all() and (dw[3] == 0).all()
 
 
 def test_gradient_against_differences(handle):
