@@ -580,8 +580,8 @@ MOE_API moe_status_t moe_balance_loss_workspace_size(const moe_config_t* cfg, in
  * nothing to prob; a NaN logit makes its sequence's prob and loss NaN. An id
  * outside [0, E) is not counted and records MOE_DEV_BAD_EXPERT_ID. No output,
  * nor ws, overlaps an input or another output (MOE_ERR_INVALID_ARG). Limits:
- * num_seqs <= 2^20, coef finite. cfg->H, I, scaling and dtype are not looked
- * at beyond their checks. */
+ * num_seqs <= 2^20, T <= 2^30, coef finite. cfg->H, I, scaling and dtype are
+ * not looked at beyond their checks. */
 MOE_API moe_status_t moe_balance_loss(moe_handle_t h, const moe_config_t* cfg, moe_score_t score, float coef,
                                       const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
                                       int num_seqs, int32_t* counts, float* prob, float* loss, void* ws,

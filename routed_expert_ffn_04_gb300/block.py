@@ -75,7 +75,8 @@ class MoEBlock:
 
     def backward(self, dout, dh=None, stream=None, dbalance=None):
         """dout [T, H] bf16 (gradient of out), dh (gradient of h on its own path, the stream's type, or None), dbalance
-        ([1] fp32, gradient of balance, or None: 1) -> gradients by name: dx and dresidual, norm_weight and w_router (fp32), and the expert weights (bf16)."""
+        ([1] fp32, gradient of balance, or None: 1) -> gradients by name: dx and dresidual, norm_weight and w_router
+        (fp32), and the expert weights (bf16)."""
         s, h, cfg, w, g = self.shape, self.handle, self.cfg, self.w, self.grads
         moe.combine_backward(h, cfg, dout, self.y_perm, self.topk_w, self.flat_to_perm, self.dy_perm, self.dtopk_w,
                              topk_idx=self.topk_idx, logits=self.logits, dlogits=self.dlogits, stream=stream)

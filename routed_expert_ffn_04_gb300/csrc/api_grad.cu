@@ -67,8 +67,9 @@ uint64_t next_call() {
 }
 
 constexpr int kMaxSequences = 1 << 20;
-bool balance_shape_ok(int score, float coef, const int32_t* seq_offsets, int num_seqs) {
-  return (score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX) && std::isfinite(coef) && num_seqs >= 1 &&
+constexpr int kMaxBalanceTokens = 1 << 30;
+bool balance_shape_ok(const moe_config_t* cfg, int score, float coef, const int32_t* seq_offsets, int num_seqs) {
+  return cfg->T <= kMaxBalanceTokens && (score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX) && std::isfinite(coef) && num_seqs >= 1 &&
          num_seqs <= kMaxSequences && (seq_offsets || num_seqs == 1);
 }
 BalanceArgs balance_args(moe_handle_t h, const moe_config_t* cfg, int score, float coef, const float* logits,
@@ -182,7 +183,7 @@ MOE_API moe_status_t moe_route_backward(moe_handle_t h, const moe_config_t* cfg,
 MOE_API moe_status_t moe_balance_loss_workspace_size(const moe_config_t* cfg, int num_seqs, size_t* bytes) {
   const moe_status_t st = check_config(cfg);
   if (st != MOE_OK) return st;
-  if (!bytes || num_seqs < 1 || num_seqs > kMaxSequences) return MOE_ERR_INVALID_ARG;
+  if (!bytes || cfg->T > kMaxBalanceTokens || num_seqs < 1 || num_seqs > kMaxSequences) return MOE_ERR_INVALID_ARG;
   *bytes = align_up(balance_scratch_bytes(cfg->T, cfg->E, num_seqs), 256);
   return MOE_OK;
 }
@@ -193,7 +194,7 @@ MOE_API moe_status_t moe_balance_loss(moe_handle_t h, const moe_config_t* cfg, m
                                       size_t ws_bytes, moe_stream_t stream) {
   moe_status_t st = check_config(cfg);
   if (st != MOE_OK) return st;
-  if (!balance_shape_ok(score, coef, seq_offsets, num_seqs) || !counts || !prob || !loss || !ws) return MOE_ERR_INVALID_ARG;
+  if (!balance_shape_ok(cfg, score, coef, seq_offsets, num_seqs) || !counts || !prob || !loss || !ws) return MOE_ERR_INVALID_ARG;
   if (cfg->T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(logits, topk_idx, seq_offsets, counts, prob, loss, ws)) return MOE_ERR_INVALID_ARG;
   const size_t need = align_up(balance_scratch_bytes(cfg->T, cfg->E, num_seqs), 256);
@@ -224,7 +225,7 @@ MOE_API moe_status_t moe_balance_loss_backward(moe_handle_t h, const moe_config_
                                                float* dlogits, moe_stream_t stream) {
   moe_status_t st = check_config(cfg);
   if (st != MOE_OK) return st;
-  if (!balance_shape_ok(score, coef, seq_offsets, num_seqs)) return MOE_ERR_INVALID_ARG;
+  if (!balance_shape_ok(cfg, score, coef, seq_offsets, num_seqs)) return MOE_ERR_INVALID_ARG;
   if (cfg->T > 0 && (!logits || !counts || !dloss || !dlogits)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(logits, counts, seq_offsets, dloss, dlogits_add, dlogits)) return MOE_ERR_INVALID_ARG;
   const size_t n = (size_t)cfg->T * cfg->E * 4;

@@ -288,6 +288,10 @@ __global__ void __launch_bounds__(kSumThreads, 1) balance_sum_kernel(const Balan
   }
 }
 
+// The two halves of a cluster's barrier, for work in between.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // A cluster per sequence, its blocks taking runs of 32 experts by turns.
 __global__ void __launch_bounds__(kFinalMost) balance_final_kernel(const BalanceParams p) {
   const int kWarps = blockDim.x / 32;  // a power of two
@@ -299,6 +303,7 @@ __global__ void __launch_bounds__(kFinalMost) balance_final_kernel(const Balance
   const int b = (int)cluster_id_x(), nranks = (int)(gridDim.x / ncluster_x());
   wait_for_previous_launch();
   allow_next_launch();
+  cluster_arrive();  // waited for before the first block's shared memory is written
   const int a = seq_start(p, b), z = seq_start(p, b + 1), n = z > a ? z - a : 0;
   const int s0 = n ? a / p.strip : 0, s1 = n ? (z - 1) / p.strip + 1 : 0;
   const float inv_n = n ? 1.0f / (float)n : 0.0f, per = (float)E * inv_n / (float)p.K;
@@ -332,6 +337,8 @@ __global__ void __launch_bounds__(kFinalMost) balance_final_kernel(const Balance
       loss += (float)c * per * prob;
     }
   }
+  __syncwarp();
+  cluster_wait();
   if (warp == 0) {
     loss = lanes_sum(loss);
     if (lane == 0) {

@@ -48,6 +48,20 @@ def test_balance_refusals(lib):
         assert grad(**bad) == INVALID
 
 
+def test_balance_token_limit(lib):
+    """T up to 2^30 (token indices are 32 bits, and a block's strip of tokens ends past T)."""
+    n = ctypes.c_size_t(0)
+    for T, ok in ((1 << 30, True), ((1 << 30) + 1, False), ((1 << 31) - 1, False)):
+        c = cfg(T=T, K=1, E=1)
+        assert (lib.moe_balance_loss_workspace_size(c, 1, ctypes.byref(n)) == 0) is ok
+        far = [P(1 << 44), P(1 << 43), *A]
+        # Allowed sizes get as far as the workspace's.
+        st = lib.moe_balance_loss(None, c, 0, 1.0, far[0], far[1], None, 1, A[0], A[1], A[2], A[3], 8, None)
+        assert st == (moe.MOE_ERR_WORKSPACE if ok else INVALID)
+        if not ok:
+            assert lib.moe_balance_loss_backward(None, c, 0, 1.0, far[0], A[0], None, 1, A[1], None, far[1], None) == INVALID
+
+
 def test_padded_rows(lib):
     assert moe.fp8_padded_rows(0, 1) == 128 and moe.fp8_padded_rows(127, 3) == 384 and moe.fp8_padded_rows(128, 1) == 256
     for n, G in ((-1, 1), (1, 0), (1, 1025)):
