@@ -31,6 +31,11 @@
 // block (192 groups of 4 rows, gate and up of 4096 x 1536: 481 -> 435 us; of 100
 // rows, down: 340 -> 297). GATE_UP's row maxima then cross the pair.
 //
+// PARTS: where few tiles leave SMs idle, a cluster of four pairs shares a tile, each
+// pair a quarter of the reduction. Each CTA then takes a quarter of its columns
+// from its counterparts, through the idle ring by asynchronous stores, and adds the
+// parts in their order (7 rows, K 4096, N 1536: 14.5 -> 7.7 us).
+//
 // What bounds it: with full tiles the epilogue's handshake, about 850 cycles per
 // block against the MMAs' 512 (of them 265 for the additions of a scheduler's two
 // warps and 100-280 for its reads of TMEM, which hardly overlap), then a tile's
@@ -58,6 +63,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "fp8.cuh"
@@ -98,6 +105,7 @@ constexpr int smem_of(int mode) {
 }
 // Groups of up to so many rows have split tiles (Tile).
 constexpr int kSplitRows = 128;
+constexpr int kParts = 4;  // PARTS: pairs of a cluster
 constexpr uint16_t kPairMask = 0x3;
 static_assert(smem_of(kFp8GateUp) <= kMaxSmem && smem_of(kFp8Forward) <= kMaxSmem, "shared memory");
 
@@ -227,16 +235,25 @@ __device__ __forceinline__ void st_async(uint32_t cluster_addr, uint32_t v, uint
                : "memory");
 }
 
+__device__ __forceinline__ void st_async4(uint32_t cluster_addr, float4 v, uint32_t cluster_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   cluster_addr),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(cluster_bar)
+               : "memory");
+}
+
 // A tile: group, its first row (WEIGHT_GRAD: of the padded rows), the rows it
-// has there, first column, blocks of the reduction; split: both CTAs hold its
+// has there, first column, blocks of the reduction, the first of them (PARTS:
+// this pair's); split: both CTAs hold its
 // rows (at most 128), each adds half of its columns.
 struct Tile {
-  int g, row0, nrows, m0, n0, kb;
+  int g, row0, nrows, m0, n0, kb, k0;
   bool split;
 };
 
-// VEC: a's scales of a row start at multiples of 16 bytes.
-template <int MODE, bool VEC>
+// VEC: a's scales of a row start at multiples of 16 bytes. PARTS: a cluster's
+// pairs each take a part of the reduction of one tile.
+template <int MODE, bool VEC, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_fp8_kernel(const __grid_constant__ Fp8Maps m, const Fp8Params p) {
   constexpr bool kA_MN = MODE == kFp8WeightGrad, kB_MN = MODE == kFp8WeightGrad || MODE == kFp8Transposed;
@@ -264,12 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kStages + 2 + a); };  // leader
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
   // Each CTA, GATE_UP: a tile's maxima are there, by q; of split tiles two by turns,
-  // as the other CTA may be a tile ahead.
+  // as the other CTA may be a tile ahead. PARTS: a warp's slices (turn: its half).
   auto join_bar = [&](int q) { return bar0 + 8u * (2 * kStages + 5 + q); };
   auto split_bar = [&](int q, uint32_t turn) { return bar0 + 8u * (2 * kStages + 9 + 4 * turn + q); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();  // 0: leader
+  const uint32_t crank = cluster_ctarank(), leader = PARTS ? crank & ~1u : 0u, rank = crank - leader;  // 0: leader
+  const uint16_t pair_mask = (uint16_t)(kPairMask << leader);
+  const int part = (int)leader / 2;
   const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
   const int G = p.G;
   if (threadIdx.x == 0) {
@@ -284,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain_bar, 1);
     for (int i = 0; i < 4; ++i) {  // this CTA's two warps; the other's come as bytes
       mbar_init(join_bar(i), 2);
-      mbar_init(split_bar(i, 0), 2);
-      mbar_init(split_bar(i, 1), 2);
+      mbar_init(split_bar(i, 0), PARTS ? 1 : 2);
+      mbar_init(split_bar(i, 1), PARTS ? 1 : 2);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -314,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // the other CTA's barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = MODE == kFp8WeightGrad ? G * n_wt * n_kt : tile_start[G];
+  // PARTS: at most one tile per cluster.
+  const int all = MODE == kFp8WeightGrad ? G * n_wt * n_kt : tile_start[G], total = PARTS && all > npairs ? npairs : all;
 
   auto decode = [&](int tile) {
     Tile t;
@@ -327,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.row0 = tile_start[t.g] * 128;
       t.nrows = row_start[t.g + 1] - row_start[t.g];
       t.kb = t.nrows > 0 ? (t.nrows + 127) / 128 : 0;
+      t.k0 = 0;
       t.split = false;
       return t;
     }
@@ -342,7 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.n0 = wt * kCols;
     t.row0 = row_start[lo] + t.m0;
     t.nrows = n - t.m0;
+    t.k0 = 0;
     t.kb = (p.K + 127) / 128;
+    if (PARTS) {
+      const int per = (t.kb + kParts - 1) / kParts, left = t.kb - part * per;
+      t.k0 = part * per;
+      t.kb = left < 0 ? 0 : (left < per ? left : per);
+    }
     t.split = n <= kSplitRows;
     return t;
   };
@@ -375,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t full = full_bar(rg.s);
-          const uint32_t bar = rank == 0 ? full : mapa_shared(full, 0);
+          const uint32_t bar = rank == 0 ? full : mapa_shared(full, leader);
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(bar, bytes);  // both CTAs' bytes (the other's may land first)
             const uint32_t da = sm0 + rg.s * kHalf, db = b_ring + rg.s * kHalf;
@@ -383,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128, 0);
               tma_load_3d_pair(db, bmap, bar, bn, t.row0 + kb * 128, 0);
             } else {
-              if (box) tma_load_3d_pair(da, amap, bar, kb * 128, t.row0 + first_row(t), 0);
-              if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, kb * 128, t.g);
-              else tma_load_3d_pair(db, bmap, bar, kb * 128, bn, t.g);
+              if (box) tma_load_3d_pair(da, amap, bar, (t.k0 + kb) * 128, t.row0 + first_row(t), 0);
+              if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, (t.k0 + kb) * 128, t.g);
+              else tma_load_3d_pair(db, bmap, bar, (t.k0 + kb) * 128, bn, t.g);
             }
           }
           __syncwarp();
@@ -423,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_e4m3_pair(d, da, db, kIdesc, 0u);
   #pragma unroll
               for (int k = 1; k < 4; ++k) umma_e4m3_pair(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
-              umma_commit_pair_mc(empty_bar(rg.s), kPairMask);
-              umma_commit_pair_mc(tfull_bar(acc.s), kPairMask);
+              umma_commit_pair_mc(empty_bar(rg.s), pair_mask);
+              umma_commit_pair_mc(tfull_bar(acc.s), pair_mask);
             }
             __syncwarp();
             issued = true;
@@ -490,17 +517,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // Rows past the group's end take its last row's scales: their results are not stored.
           const int last = t.nrows - 1, a0 = first_row(t) + s0;
-          const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs;
-          const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs;
+          if (PARTS && t.kb == 0) continue;
+          const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs + t.k0;
+          const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs + t.k0;
+          const int left = kbs - t.k0;  // blocks from this part's first on
           auto load_a = [&](const float* sa, int kb) {
-            if (VEC) return load_now(reinterpret_cast<const float4*>(sa + (kb < kbs ? kb : kbs - 4)));
-            const int e = kbs - 1;
+            if (VEC) return load_now(reinterpret_cast<const float4*>(sa + (kb < left ? kb : left - 4)));
+            const int e = left - 1;
             return make_float4(load_now(sa + (kb < e ? kb : e)), load_now(sa + (kb + 1 < e ? kb + 1 : e)),
                                load_now(sa + (kb + 2 < e ? kb + 2 : e)), load_now(sa + (kb + 3 < e ? kb + 3 : e)));
           };
           const int nb = t.n0 / 128, nb1 = MODE == kFp8GateUp || nb + 1 == nbs ? nb : nb + 1;
           auto load_w = [&](const float* sb, int n, int kb) {  // a lane each for 32 blocks
-            const int k = kb + lane < kbs ? kb + lane : kbs - 1;
+            const int k = t.k0 + (kb + lane < left ? kb + lane : left - 1);
             return load_now(sb + (MODE == kFp8Transposed ? ((size_t)t.g * kbs + k) * nbs + n : ((size_t)t.g * nbs + n) * kbs + k));
           };
           const float* sb1 = MODE == kFp8GateUp ? p.sb1 : p.sb;
@@ -532,13 +561,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    __syncwarp();
+    if (PARTS && pair < total) cluster_sync_all();
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     const int q = warp & 3;                      // this warp may access TMEM lanes 32q .. 32q+31
     const int half = (warp - kEpiWarp0) >> 2;    // its 128 columns (GATE_UP: 64 of gate, 64 of up)
     uint8_t* stg = staging + (warp - kEpiWarp0) * kStgWarp;
-    const uint32_t tempty0 = rank == 0 ? tempty_bar(0) : mapa_shared(tempty_bar(0), 0);
+    bool idle = false;  // PARTS: the cluster's rings are
+    const uint32_t tempty0 = rank == 0 ? tempty_bar(0) : mapa_shared(tempty_bar(0), leader);
     auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
@@ -650,6 +682,98 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kb + 1 < c_t.kb && !begin()) goto done;
           if (MODE != kFp8WeightGrad) add(3, f1, v1);
         }
+      }
+      if constexpr (PARTS) {
+        // The pairs' sums are put together: each CTA takes a slice of every warp's
+        // columns, a warp's 32 rows of it from the same warp of its counterparts in
+        // the other pairs, through its ring, which is idle by then (16 bytes of 32
+        // rows at a time: 512 bytes in order).
+        cluster_sync_all();
+        idle = true;
+        auto join = [&](auto n) {
+          constexpr int kKinds = MODE == kFp8GateUp ? 2 : 1;  // gates and ups
+          constexpr int kN = n.value / kKinds, kPer = kN / kParts;  // groups of four columns: of the warp, of a slice
+          auto at = [&](int from, int c) { return base + ((from * kEpiWarps + warp - kEpiWarp0) * (kPer * kKinds) + c) * 512 + lane * 16; };
+          const uint32_t bar = split_bar(q, (uint32_t)half);
+          if (lane == 0) mbar_arrive_expect_tx(bar, kParts * kPer * kKinds * 512);
+#pragma unroll
+          for (int c = 0; c < kN * kKinds; ++c) {
+            const int kind = c / kN, to = c % kN / kPer;
+            const uint32_t cta = 2 * to + rank;
+            st_async4(mapa_shared(smem_u32(at(part, kind * kPer + c % kPer)), cta),
+                      make_float4(sum[4 * c], sum[4 * c + 1], sum[4 * c + 2], sum[4 * c + 3]), mapa_shared(bar, cta));
+          }
+          if (!warp_wait(bar, 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return;
+          float x[4 * kPer * kKinds];
+#pragma unroll
+          for (int c = 0; c < kPer * kKinds; ++c) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+              const float4 y = *reinterpret_cast<const float4*>(at(i, c));
+              v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+            }
+            x[4 * c] = v.x;
+            x[4 * c + 1] = v.y;
+            x[4 * c + 2] = v.z;
+            x[4 * c + 3] = v.w;
+          }
+          const int r = r0 + lane, first = c_t.n0 + col0 + part * kPer * 4;
+          const bool live = r < c_t.nrows;
+          const size_t row = (size_t)(c_t.row0 + r) * p.N + first;
+          if constexpr (MODE == kFp8GateUp) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 4 * kPer; ++i) {
+              x[i] = silu_fast(x[i]) * x[4 * kPer + i];
+              const uint32_t b = fp8_abs_bits(x[i]);
+              top = b > top ? b : top;
+            }
+            // The maxima of each CTA's warps, behind the slices, to all CTAs that have these rows.
+            constexpr bool kSplit = n.value == 16;
+            constexpr uint32_t kStep = kSplit ? 1 : 2, kFrom = 2 * kParts / kStep;
+            uint32_t* tops = reinterpret_cast<uint32_t*>(base + 4 * 2 * kHalf) + q * 32 + lane;
+            if (lane == 0) {
+              if (half == 0) mbar_arrive_expect_tx(join_bar(q), kFrom * 2 * 32 * 4);
+              else mbar_arrive(join_bar(q));
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kFrom; ++i) {
+              const uint32_t cta = kSplit ? i : 2 * i + rank;
+              st_async(mapa_shared(smem_u32(tops + (2 * crank + half) * 128), cta), top, mapa_shared(join_bar(q), cta));
+            }
+            if (!warp_wait(join_bar(q), 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return;
+#pragma unroll
+            for (uint32_t i = 0; i < 2 * kFrom; ++i) {
+              const uint32_t from = kSplit ? i / 2 : i / 2 * 2 + rank;
+              const uint32_t t = tops[(2 * from + (i & 1)) * 128];
+              top = t > top ? t : top;
+            }
+            const Fp8Block blk(fp8_scale(top));
+            if (live && half == 0 && part == 0 && (!kSplit || rank == 0))
+              p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = blk.scale;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c)
+              if (live && first + 4 * c < p.N)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row + 4 * c) =
+                    blk.code4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+              if (!live || first + 4 * c >= p.N) break;
+              if (p.out_f32)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row + 4 * c) =
+                    make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+              else
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row + 4 * c) =
+                    make_uint2(pack_bf16(x[4 * c], x[4 * c + 1]), pack_bf16(x[4 * c + 2], x[4 * c + 3]));
+            }
+          }
+        };
+        if (split) join(std::integral_constant<int, 16>());
+        else join(std::integral_constant<int, 32>());
+        __syncwarp();
+        continue;
       }
       // Results go out by TMA from the warp's staging (the tensor maps' swizzles),
       // while the next tile is summed: stores from the warps held them up for as
@@ -800,6 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   done:
     tmem_ld_wait();
     bulk_wait_group0();
+    __syncwarp();
+    if (PARTS && pair < total && !idle) cluster_sync_all();
   }
 
   // Both CTAs arrive here only when their roles are done (every wait is
@@ -818,6 +944,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
   }
+}
+
+// Whether kParts pairs share each tile's reduction. Up to 15 clusters of eight CTAs
+// run at once (7 rows x 3840 x 4096, 15 tiles: 14.6 us, in parts 8.2; 16 tiles take
+// two waves, 15.3). The exchange of the sums costs as much as rows / 8 blocks (10
+// tiles, K = 1024 and 2048: 32 rows 7.1 -> 6.1 and 9.5 -> 6.8 us, 128 rows 7.9 -> 9.3
+// and 10.4 -> 10.0), of tiles higher than 128 rows more (160 rows, K = 2560 and
+// 4096: 13.8 -> 15.4, 18.5 -> 16.5).
+bool in_parts(long long tiles, int rows, int blocks) {
+  const int least = rows > 128 ? 28 : (rows / 8 > 4 ? rows / 8 : 4);
+  return tiles <= 15 && blocks >= least;
 }
 
 template <int MODE>
@@ -860,24 +997,30 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
   const long long most = a.num_sms / 2;
   const int pairs = (int)(tiles < most ? tiles : most);
   if (pairs < 1) return cudaErrorInvalidValue;
+  if constexpr (MODE != kFp8WeightGrad) {
+    const long long filled = n_wt * (a.rows / 256 + (G < a.rows ? G : a.rows));  // tiles of groups that have rows
+    if (in_parts(filled, a.rows, fp8_blocks(a.K)))
+      return launch_dependent(grouped_gemm_fp8_kernel<MODE, false, true>, (int)(2 * kParts * filled), kThreads, smem_of(MODE), s,
+                              true, /*cluster=*/2 * kParts, m, p);
+  }
   const bool vec = MODE == kFp8WeightGrad || fp8_blocks(a.K) % 4 == 0;
-  if (vec) return launch_dependent(grouped_gemm_fp8_kernel<MODE, true>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
-  return launch_dependent(grouped_gemm_fp8_kernel<MODE, MODE == kFp8WeightGrad>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
+  if (vec) return launch_dependent(grouped_gemm_fp8_kernel<MODE, true, false>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
+  return launch_dependent(grouped_gemm_fp8_kernel<MODE, MODE == kFp8WeightGrad, false>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
 }
 
 }  // namespace
 
 namespace {
-template <int MODE, bool VEC>
+template <int MODE, bool VEC, bool PARTS = false>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(MODE));
+  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, VEC, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(MODE));
 }
 }  // namespace
 
 cudaError_t gemm_fp8_prepare_device() {
-  const cudaError_t errs[] = {allow_smem<kFp8Forward, true>(),    allow_smem<kFp8Forward, false>(),
-                              allow_smem<kFp8Transposed, true>(), allow_smem<kFp8Transposed, false>(),
-                              allow_smem<kFp8GateUp, true>(),     allow_smem<kFp8GateUp, false>(),
+  const cudaError_t errs[] = {allow_smem<kFp8Forward, true>(),    allow_smem<kFp8Forward, false>(),    allow_smem<kFp8Forward, false, true>(),
+                              allow_smem<kFp8Transposed, true>(), allow_smem<kFp8Transposed, false>(), allow_smem<kFp8Transposed, false, true>(),
+                              allow_smem<kFp8GateUp, true>(),     allow_smem<kFp8GateUp, false>(),     allow_smem<kFp8GateUp, false, true>(),
                               allow_smem<kFp8WeightGrad, true>()};
   for (cudaError_t e : errs)
     if (e != cudaSuccess) return e;

@@ -217,6 +217,18 @@ def test_dense_product(handle, rows, transposed):
     product(handle, [rows], 512, 1024, transposed, BF16, dense=True)
 
 
+FEW = [([1], 512, 4096), ([33], 272, 1616), ([128], 256, 2048), ([129], 1536, 4096), ([0, 0, 3, 0, 70, 0, 0], 256, 1920),
+       ([296], 400, 3728), ([130, 0, 200], 512, 3600), ([3, 9], 272, 528), ([250, 6, 128], 2064, 2048)]
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("counts, N, K", FEW)
+def test_few_tiles(handle, counts, N, K, out_dtype, transposed):
+    """Few tiles and a long reduction: parts of it on several pairs of SMs, of like and unlike lengths."""
+    product(handle, counts, N, K, transposed, out_dtype)
+
+
 def test_many_groups(handle):
     product(handle, [(i * 7) % 5 for i in range(1024)], 128, 256, False, BF16)
 
@@ -287,6 +299,11 @@ def test_gate_up(handle, counts, H, I):
         tol = dh * (1 + 2.0 ** -4) + 2.0 ** -4 * h.abs() + spread(s[r:r + n], I, 1) * 2.0 ** -10
         assert ((back - h).abs() <= tol).all(), f"group {i}: {float(((back - h).abs() - tol).max())}"
         r += n
+
+
+@pytest.mark.parametrize("counts, I, H", FEW)
+def test_gate_up_few_tiles(handle, counts, I, H):
+    test_gate_up(handle, counts, H, I)
 
 
 def test_gate_up_small_and_large_groups_in_turn(handle):
