@@ -44,7 +44,7 @@
 // I 1536, 192 groups:
 //   GATE_UP      341 rows 995 us, 1.66 PFLOP/s; 4 rows 440 us, 5.5 TB/s
 //   FORWARD      341 rows 690 us, 1.2 PFLOP/s (2.4 GB, of them 1.1 of fp32 results)
-//   WEIGHT_GRAD  341 rows 870 us (2.8 GB, of them 2.4 of bf16 results)
+//   WEIGHT_GRAD  341 rows 788 us (2.8 GB, of them 2.4 of bf16 results)
 //   FORWARD      dense 8192 x 4096 x 4096 113 us, 2.4 PFLOP/s
 // One half of a block's columns at a time through the handshake (MMAs of 128
 // columns, two barriers) was slower: 1131 and 126 us.
@@ -161,6 +161,16 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -609,12 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // added, over the blocks' borders too: the next block's wait and its first
       // load come before this one's last additions.
       uint32_t v0[32], v1[32];
+      uint32_t u[2][16];  // WEIGHT_GRAD: 16 columns at a time
       uint32_t tb = 0;
       auto begin = [&] {  // wait for a block and load its first columns
         if (!warp_wait(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return false;
         tc_fence_after();
         tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 256 + col0);
-        tmem_ld_32x32b_x32(tb, v0);
+        if constexpr (MODE == kFp8WeightGrad) tmem_ld_32x32b_x16(tb, u[0]);
+        else tmem_ld_32x32b_x32(tb, v0);
         return true;
       };
       auto arrived = [&](uint32_t (&x)[32]) {  // used behind the wait only
@@ -634,20 +646,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto add = [&](int c, float y, const uint32_t (&v)[32]) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 x = make_float4(y, y, y, y);
-          if (MODE == kFp8WeightGrad) {
-            const float4 z = *reinterpret_cast<const float4*>(f + 32 * c + i);
-            x = make_float4(y * z.x, y * z.y, y * z.z, y * z.w);
-          }
-          sum[32 * c + i] = fmaf(__uint_as_float(v[i]), x.x, sum[32 * c + i]);
-          sum[32 * c + i + 1] = fmaf(__uint_as_float(v[i + 1]), x.y, sum[32 * c + i + 1]);
-          sum[32 * c + i + 2] = fmaf(__uint_as_float(v[i + 2]), x.z, sum[32 * c + i + 2]);
-          sum[32 * c + i + 3] = fmaf(__uint_as_float(v[i + 3]), x.w, sum[32 * c + i + 3]);
-        }
+        for (int i = 0; i < 32; ++i) sum[32 * c + i] = fmaf(__uint_as_float(v[i]), y, sum[32 * c + i]);
       };
       if (c_t.kb > 0 && !begin()) goto done;
-      if (split) {
+      if constexpr (MODE == kFp8WeightGrad) {
+        // Columns' factors as well. They are read before the wait for their columns
+        // (which the compiler moves no load across): with 32 columns at a time there
+        // were no registers for that, and each read was waited for (192 x 341 rows:
+        // 871 -> 788 us). Every lane reads all 128, which fills the shared memory's
+        // port (648 us without); TMEM loads of 16 lanes x 256 bits, with which a lane
+        // has four rows and a quarter of the columns, were no faster (798, 64 columns
+        // at a time 817).
+#pragma unroll 1
+        for (int kb = 0; kb < c_t.kb; ++kb) {
+          take_factors();
+          const float y = f0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float4 z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = *reinterpret_cast<const float4*>(f + 16 * c + 4 * i);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(u[c & 1][i]));
+            if (c < 7) {
+              tmem_ld_32x32b_x16(tb + 16 * (c + 1), u[(c & 1) ^ 1]);
+            } else {
+              release(acc.s);
+              acc.next(2);
+              if (kb + 1 < c_t.kb && !begin()) goto done;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float* a = sum + 16 * c + 4 * i;
+              const uint32_t* v = u[c & 1] + 4 * i;
+              a[0] = fmaf(__uint_as_float(v[0]), y * z[i].x, a[0]);
+              a[1] = fmaf(__uint_as_float(v[1]), y * z[i].y, a[1]);
+              a[2] = fmaf(__uint_as_float(v[2]), y * z[i].z, a[2]);
+              a[3] = fmaf(__uint_as_float(v[3]), y * z[i].w, a[3]);
+            }
+          }
+        }
+      } else if (split) {
 #pragma unroll 1
         for (int kb = 0; kb < c_t.kb; ++kb) {
           take_factors();
@@ -676,11 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(at(3), v1);
           add(2, f1, v0);
           arrived(v1);
-          if (MODE == kFp8WeightGrad) add(3, f1, v1);  // its column factors are read until the release
           release(acc.s);
           acc.next(2);
           if (kb + 1 < c_t.kb && !begin()) goto done;
-          if (MODE != kFp8WeightGrad) add(3, f1, v1);
+          add(3, f1, v1);
         }
       }
       if constexpr (PARTS) {
