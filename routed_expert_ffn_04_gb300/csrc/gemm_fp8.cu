@@ -15,56 +15,44 @@
 // sums out of TMEM and add them, times the factor, to accumulators in registers.
 // fp32 scales cannot go through the block-scaled kinds, which take powers of two.
 //
-// A tile is 256 rows x 256 columns on a pair of CTAs (the two SMs of a TPC,
-// cta_group::2): each CTA holds 128 rows of A and half of B, 32 KB per block of
-// 128, and its TMEM the partial sums of its 128 rows, double-buffered (2 x 256
-// columns, all of it). A thread's accumulators are 128 columns of one row: its
-// factor is one number per block (two for GATE_UP). Rows (tokens) as M make the
-// factor, SwiGLU and the quantisation of a row of h local to a thread; a group's
-// last tile costs its whole MMAs (341 rows take 512), which matters only past 256
-// rows per group, below that the weights' bytes take longer (16 KB per SM and
-// block: 700 cycles of its share of HBM against 512 of MMAs).
-//
-// A group of up to 128 rows is one tile high and would leave the odd CTA's rows
-// empty, its epilogue idle beside one that is the slower half. Such a tile is
-// split: both CTAs hold all its rows, and each adds half of the columns of every
-// block (192 groups of 4 rows, gate and up of 4096 x 1536: 481 -> 435 us; of 100
-// rows, down: 340 -> 297). GATE_UP's row maxima then cross the pair.
-//
-// PARTS: where few tiles leave SMs idle, a cluster of four pairs shares a tile, each
-// pair a quarter of the reduction. Each CTA then takes a quarter of its columns
-// from its counterparts, through the idle ring by asynchronous stores, and adds the
-// parts in their order (7 rows, K 4096, N 1536: 14.5 -> 7.7 us).
-//
-// What bounds it: with full tiles the epilogue's handshake, about 850 cycles per
-// block against the MMAs' 512 (of them 265 for the additions of a scheduler's two
-// warps and 100-280 for its reads of TMEM, which hardly overlap), then a tile's
-// own epilogue (GATE_UP: 4000 cycles of SwiGLU and codes, half of them waits for
-// exp and the quotient); with few rows HBM and the loads' latency. Measured, H 4096,
-// I 1536, 192 groups:
-//   GATE_UP      341 rows 995 us, 1.66 PFLOP/s; 4 rows 440 us, 5.5 TB/s
-//   FORWARD      341 rows 690 us, 1.2 PFLOP/s (2.4 GB, of them 1.1 of fp32 results)
-//   WEIGHT_GRAD  341 rows 788 us (2.8 GB, of them 2.4 of bf16 results)
-//   FORWARD      dense 8192 x 4096 x 4096 113 us, 2.4 PFLOP/s
-// One half of a block's columns at a time through the handshake (MMAs of 128
-// columns, two barriers) was slower: 1131 and 126 us.
+// A tile is 128 rows x 256 columns on one CTA (cta_group::1): 48 KB of operands per
+// block of 128, and two buffers of 256 columns of TMEM for partial sums. A thread's
+// accumulators are 128 columns of one row: its factor is one number per block (two
+// for GATE_UP). Rows (tokens) as M make the factor, SwiGLU and the quantisation of a
+// row of h local to a thread. Tiles of 256 rows on pairs of CTAs (cta_group::2)
+// load a third less, but each block then waits for the slower CTA's epilogue, a
+// group of 341 rows takes 512 and one of few rows leaves a CTA idle: 192 such
+// groups took 990 us (GATE_UP) and 684 (FORWARD), on single CTAs 809 and 544; 4 rows
+// each, 449 and 361; dense 8192 x 4096 x 4096 113 and 111.
 //
 // TRANSPOSED and WEIGHT_GRAD read operands MN-major from the row-major tensors,
 // with no transposed copy: a box of 128 columns x 128 rows lands as 128 rows of
 // 128 swizzled bytes, 8 rows (1024 bytes) per step of the layout, 32 rows per MMA.
 //
-// Roles per CTA (12 warps, each walking its tiles in step): 0 loads, 1 (of the
-// even CTA, the leader) issues the pair's MMAs, 2 and 3 multiply each block's
-// scales into factors ahead of the epilogue, 4-11 are the epilogue: TMEM lanes
-// 32 (w % 4) .., columns 128 ((w - 4) / 4) ... Both CTAs' copies of a stage
-// complete on the leader's full barrier. Every wait is bounded; on expiry the
-// CTA records a code in the status word, lets its copies and MMAs end, frees
-// TMEM and exits.
+// PARTS: where few tiles leave SMs idle, the four or eight CTAs of a cluster share a
+// tile, each a part of the reduction. Each CTA then takes a slice of the columns
+// from the others, through the idle ring by asynchronous stores, and adds the parts
+// in their order (7 rows, K 4096, N 1536: 15.2 -> 7.5 us). Whole copies of a slice
+// instead were better past 64 rows only (128: 17.3 -> 14.3; 1: 9.0 -> 9.7).
+//
+// What bounds it: of few rows HBM; of many the epilogue, which adds a block in about
+// 700 cycles (265 for the additions of a scheduler's two warps and 100-280 for its
+// reads of TMEM, which hardly overlap, and the barriers) against 512 of MMAs, and the
+// tile's own end (GATE_UP: 4000 cycles of SwiGLU and codes, half of them waits for
+// exp and the quotient). Measured, H 4096, I 1536, 192 groups:
+//   GATE_UP      341 rows 809 us, 2.0 PFLOP/s; 4 rows 361 us, 6.7 TB/s
+//   FORWARD      341 rows 544 us, 1.5 PFLOP/s and 4.4 TB/s (2.4 GB, 1.1 of fp32 results)
+//   WEIGHT_GRAD  341 rows 773 us (2.8 GB, of them 2.4 of bf16 results)
+//   FORWARD      dense 8192 x 4096 x 4096 111 us, 2.5 PFLOP/s
+//
+// Roles (12 warps, each walking its tiles in step): 0 loads, 1 issues the MMAs, 2
+// and 3 multiply each block's scales into factors ahead of the epilogue, 4-11 are
+// the epilogue: TMEM lanes 32 (w % 4) .., columns 128 ((w - 4) / 4) ... Every wait is
+// bounded; on expiry the CTA records a code in the status word, lets its copies and
+// MMAs end, frees TMEM and exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-
-#include <type_traits>
 
 #include "../../include/moe.h"
 #include "fp8.cuh"
@@ -79,7 +67,7 @@ namespace {
 
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSmem = 232448;  // 227 KB dynamic shared memory per CTA
-constexpr int kHalf = 128 * 128;  // a CTA's A, or B, of a stage
+constexpr int kTileBytes = 128 * 128;  // of 128 rows (columns) and a block of 128 of the reduction
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -91,23 +79,30 @@ static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsMany == kThreads * kRegsLau
 constexpr int kStgBlock = 4096;  // staging: 32 rows of 128 bytes
 // Stages of the ring, and staging per warp: GATE_UP's rows of a warp are 64 bytes
 // of codes, the others' 256 bytes (two blocks).
-constexpr int stages(int mode) { return mode == kFp8GateUp ? 5 : 4; }
-constexpr int stg_warp(int mode) { return mode == kFp8GateUp ? kStgBlock / 2 : 2 * kStgBlock; }
+// The ring, of stages of A (128 rows) and B (256), and staging per warp: GATE_UP's
+// rows of a warp are 64 bytes of codes, the others' 256 or 512, 128 at a time. Four
+// stages instead of three: 828 -> 809 us for GATE_UP's 341 rows.
+constexpr int ring_bytes(int mode) { return (mode == kFp8GateUp ? 12 : 10) * kTileBytes; }
+constexpr int stg_warp(int mode) { return mode == kFp8GateUp ? kStgBlock / 2 : kStgBlock; }
+// Rows of A in a stage where no group has more, for one more stage (the MMAs read on
+// past them, rows whose results nobody takes).
+constexpr int kNarrowRows = 32;
+constexpr int stages(int mode, bool narrow) {
+  return ring_bytes(mode) / ((narrow ? kNarrowRows * 128 : kTileBytes) + 2 * kTileBytes);
+}
 constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
 constexpr int kFactorSlots = 4;               // blocks whose factors are kept
 constexpr int kFactors = 384;                 // of a block: rows' (twice, or once and 256 columns')
-constexpr int kColBytes = kFactorSlots * kFactors * 4 + 6144;  // and GATE_UP's row maxima: two slots of four parts, two of two
-constexpr int bars_of(int mode) { return 2 * stages(mode) + 17; }
-constexpr int bar_bytes(int mode) { return (8 * bars_of(mode) + 8 + 15) / 16 * 16; }  // and the TMEM address and the abort flag
+constexpr int kColBytes = kFactorSlots * kFactors * 4 + 2048;  // and GATE_UP's row maxima: two slots of two parts
+constexpr int kMostStages = 5;
+constexpr int kBars = 2 * kMostStages + 5 + 4 + kEpiWarps;
+constexpr int kBarBytes = (8 * kBars + 8 + 15) / 16 * 16;  // and the TMEM address and the abort flag
 constexpr int kTableBytes = (kMaxGroups + 8) * 4 * 2;
 constexpr int smem_of(int mode) {
-  return 1024 + 2 * stages(mode) * kHalf + kEpiWarps * stg_warp(mode) + kColBytes + bar_bytes(mode) + kTableBytes;
+  return 1024 + ring_bytes(mode) + kEpiWarps * stg_warp(mode) + kColBytes + kBarBytes + kTableBytes;
 }
-// Groups of up to so many rows have split tiles (Tile).
-constexpr int kSplitRows = 128;
-constexpr int kParts = 4;  // PARTS: pairs of a cluster
-constexpr uint16_t kPairMask = 0x3;
 static_assert(smem_of(kFp8GateUp) <= kMaxSmem && smem_of(kFp8Forward) <= kMaxSmem, "shared memory");
+static_assert(stages(kFp8GateUp, true) <= kMostStages && stages(kFp8Forward, true) <= kMostStages, "barriers");
 
 struct Fp8Params {
   const int32_t* offsets;  // [G+1] or nullptr
@@ -128,13 +123,13 @@ struct Fp8Maps {
   CUtensorMap a[4], b0, b1, out;
 };
 
-// D (+)= A B over the CTA pair, E4M3 inputs, fp32 accumulator (M = 256, K = 32).
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
+// D (+)= A B, E4M3 inputs, fp32 accumulator (M = 128, K = 32).
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -143,22 +138,21 @@ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-// MN-major operand of 128 columns: rows of the reduction 128 bytes apart, groups
-// of 8 rows 1024 bytes; 32 rows are 4096 bytes.
+// MN-major operand: 128 columns' rows of the reduction 128 bytes apart, groups of 8
+// rows 1024 bytes; 32 rows are 4096 bytes.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
   uint64_t d = 0;
   d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kHalf >> 4) << 16;  // the next 128 columns: there are none
+  d |= (uint64_t)(kTileBytes >> 4) << 16;  // the next 128 columns (of B)
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                                 int z) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
@@ -253,31 +247,27 @@ __device__ __forceinline__ void st_async4(uint32_t cluster_addr, float4 v, uint3
 }
 
 // A tile: group, its first row (WEIGHT_GRAD: of the padded rows), the rows it
-// has there, first column, blocks of the reduction, the first of them (PARTS:
-// this pair's); split: both CTAs hold its
-// rows (at most 128), each adds half of its columns.
+// has there, first row and column, blocks of the reduction and the first of them
+// (PARTS: this CTA's).
 struct Tile {
   int g, row0, nrows, m0, n0, kb, k0;
-  bool split;
 };
 
-// VEC: a's scales of a row start at multiples of 16 bytes. PARTS: a cluster's
-// pairs each take a part of the reduction of one tile.
-template <int MODE, bool VEC, bool PARTS>
+// PARTS > 1: a cluster of as many CTAs has one tile, each a part of the reduction.
+template <int MODE, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_fp8_kernel(const __grid_constant__ Fp8Maps m, const Fp8Params p) {
   constexpr bool kA_MN = MODE == kFp8WeightGrad, kB_MN = MODE == kFp8WeightGrad || MODE == kFp8Transposed;
   constexpr int kCols = MODE == kFp8GateUp ? 128 : 256;  // result columns per tile
-  constexpr int kStages = stages(MODE), kStgWarp = stg_warp(MODE), kStgBytes = kEpiWarps * kStgWarp;
-  constexpr int kBars = bars_of(MODE), kBarBytes = bar_bytes(MODE);
+  constexpr int kWide = stages(MODE, false), kStages = stages(MODE, true);  // kStages: the most
+  constexpr int kStgWarp = stg_warp(MODE), kStgBytes = kEpiWarps * kStgWarp, kRing = ring_bytes(MODE);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
   uint8_t* base = smem_raw + pad;
   const uint32_t sm0 = raw_addr + pad;
-  // Shared memory (the same in both CTAs): A ring | B ring | staging | column factors | barriers | tables.
-  const uint32_t b_ring = sm0 + kStages * kHalf;
-  uint8_t* staging = base + 2 * kStages * kHalf;
+  // Shared memory: A ring | B ring | staging | factors, maxima | barriers | tables.
+  uint8_t* staging = base + kRing;
   float* factors = reinterpret_cast<float*>(staging + kStgBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStgBytes + kColBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -285,21 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* tile_start = reinterpret_cast<int32_t*>(staging + kStgBytes + kColBytes + kBarBytes);
   int32_t* row_start = tile_start + kMaxGroups + 8;
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };                    // leader: both CTAs' stage s
-  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };       // each CTA
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kStages + a); };   // each CTA
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kStages + 2 + a); };  // leader
-  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
-  // Each CTA, GATE_UP: a tile's maxima are there, by q; of split tiles two by turns,
-  // as the other CTA may be a tile ahead. PARTS: a warp's slices (turn: its half).
-  auto join_bar = [&](int q) { return bar0 + 8u * (2 * kStages + 5 + q); };
-  auto split_bar = [&](int q, uint32_t turn) { return bar0 + 8u * (2 * kStages + 9 + 4 * turn + q); };
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMostStages + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMostStages + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMostStages + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kMostStages + 4);
+  auto join_bar = [&](int q) { return bar0 + 8u * (2 * kMostStages + 5 + q); };   // GATE_UP: a tile's maxima are there
+  auto slice_bar = [&](int w) { return bar0 + 8u * (2 * kMostStages + 9 + w); };  // PARTS: a warp's slices are
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank(), leader = PARTS ? crank & ~1u : 0u, rank = crank - leader;  // 0: leader
-  const uint16_t pair_mask = (uint16_t)(kPairMask << leader);
-  const int part = (int)leader / 2;
-  const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
+  const int part = PARTS > 1 ? (int)cluster_ctarank() : 0;
+  const int worker = PARTS > 1 ? (int)cluster_id_x() : (int)blockIdx.x, workers = PARTS > 1 ? (int)ncluster_x() : (int)gridDim.x;
   const int G = p.G;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -308,20 +294,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1 + kScaleWarps);
-      mbar_init(tempty_bar(a), 2 * kEpiWarps);
+      mbar_init(tempty_bar(a), kEpiWarps);
     }
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < 4; ++i) {  // this CTA's two warps; the other's come as bytes
-      mbar_init(join_bar(i), 2);
-      mbar_init(split_bar(i, 0), PARTS ? 1 : 2);
-      mbar_init(split_bar(i, 1), PARTS ? 1 : 2);
-    }
+    for (int i = 0; i < 4; ++i) mbar_init(join_bar(i), 2);  // the two warps of 32 rows
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(slice_bar(i), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {  // one warp of each CTA of the pair, together
-    tmem_alloc_pair(smem_u32(tmem_slot), 512);
-    tmem_relinquish_pair();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
   }
   wait_for_previous_launch();
   allow_next_launch();
@@ -330,21 +313,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     row_start[g] = v < 0 ? 0 : (v > p.rows ? p.rows : v);
   }
   __syncthreads();
-  const int n_wt = (p.N + kCols - 1) / kCols, n_kt = (p.K + 255) / 256;
+  int most = 0;  // rows of a group
+  const int n_wt = MODE == kFp8WeightGrad ? (p.N + 127) / 128 : (p.N + kCols - 1) / kCols, n_kt = (p.K + 255) / 256;
   for (int g = threadIdx.x; g < G; g += kThreads) {
     const int n = row_start[g + 1] - row_start[g];
+    most = n > most ? n : most;
     // WEIGHT_GRAD: blocks of 128 rows before the group; else tiles before it.
-    tile_start[g] = MODE == kFp8WeightGrad ? (n > 0 ? (n + 127) / 128 : 0) : (n > 0 ? n_wt * ((n + 255) / 256) : 0);
+    tile_start[g] = MODE == kFp8WeightGrad ? (n > 0 ? (n + 127) / 128 : 0) : (n > 0 ? n_wt * ((n + 127) / 128) : 0);
   }
-  __syncthreads();
+  const bool narrow = !__syncthreads_or(MODE == kFp8WeightGrad || most > kNarrowRows);
+  const int nstages = narrow ? kStages : kWide;
+  const uint32_t a_step = narrow ? kNarrowRows * 128 : kTileBytes, b_ring = sm0 + nstages * a_step;
   if (warp == 0) scan_warp(tile_start, G, lane);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the other CTA's barriers and TMEM are there
+  if (PARTS > 1) cluster_sync_all();  // the other CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // PARTS: at most one tile per cluster.
-  const int all = MODE == kFp8WeightGrad ? G * n_wt * n_kt : tile_start[G], total = PARTS && all > npairs ? npairs : all;
+  const int all = MODE == kFp8WeightGrad ? G * n_wt * n_kt : tile_start[G], total = PARTS > 1 && all > workers ? workers : all;
 
   auto decode = [&](int tile) {
     Tile t;
@@ -352,13 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per = n_wt * n_kt;
       t.g = tile / per;
       const int at = tile - t.g * per;
-      t.m0 = at / n_kt * 256;
+      t.m0 = at / n_kt * 128;
       t.n0 = (at - at / n_kt * n_kt) * 256;
       t.row0 = tile_start[t.g] * 128;
       t.nrows = row_start[t.g + 1] - row_start[t.g];
       t.kb = t.nrows > 0 ? (t.nrows + 127) / 128 : 0;
       t.k0 = 0;
-      t.split = false;
       return t;
     }
     int lo = 0, hi = G;  // tile_start[lo] <= tile < tile_start[hi]
@@ -367,29 +353,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tile_start[mid] <= tile) lo = mid; else hi = mid;
     }
     t.g = lo;
-    const int n = row_start[lo + 1] - row_start[lo], n_tt = (n + 255) / 256;
+    const int n = row_start[lo + 1] - row_start[lo], n_tt = (n + 127) / 128;
     const int local = tile - tile_start[lo], wt = local / n_tt;
-    t.m0 = (local - wt * n_tt) * 256;
+    t.m0 = (local - wt * n_tt) * 128;
     t.n0 = wt * kCols;
     t.row0 = row_start[lo] + t.m0;
     t.nrows = n - t.m0;
     t.k0 = 0;
     t.kb = (p.K + 127) / 128;
-    if (PARTS) {
-      const int per = (t.kb + kParts - 1) / kParts, left = t.kb - part * per;
+    if (PARTS > 1) {
+      const int per = (t.kb + PARTS - 1) / PARTS, left = t.kb - part * per;
       t.k0 = part * per;
       t.kb = left < 0 ? 0 : (left < per ? left : per);
     }
-    t.split = n <= kSplitRows;
     return t;
   };
-  auto first_row = [&](const Tile& t) { return t.split ? 0 : (int)rank * 128; };  // of this CTA's A
-  // Rows of A that CTA r of the pair has in a tile, and the box that covers them (0: none).
-  auto rows_of = [&](const Tile& t, int r) {
-    const int n = t.nrows - (t.split ? 0 : 128 * r);
-    return n < 0 ? 0 : (n > 128 ? 128 : n);
-  };
-  auto box_of = [&](int n) { return n > 64 ? 128 : (n > 32 ? 64 : (n > 16 ? 32 : (n > 0 ? 16 : 0))); };
+  auto box_of = [&](int n) { return n > 64 ? 128 : (n > 32 ? 64 : (n > 16 ? 32 : 16)); };  // rows of A that are loaded
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
@@ -397,36 +376,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ producer
       Ring rg;
       bool ok = true;
-      for (int tile = pair; ok && tile < total; tile += npairs) {
+      for (int tile = worker; ok && tile < total; tile += workers) {
         const Tile t = decode(tile);
-        const int box = kA_MN ? 128 : box_of(rows_of(t, (int)rank));
-        const int boxes = kA_MN ? 256 : box_of(rows_of(t, 0)) + box_of(rows_of(t, 1));
-        const uint32_t bytes = (uint32_t)boxes * 128u + 2u * kHalf;
-        const CUtensorMap* amap = &m.a[kA_MN || box == 128 ? 0 : (box == 64 ? 1 : (box == 32 ? 2 : 3))];
-        const CUtensorMap* bmap = MODE == kFp8GateUp && rank == 1 ? &m.b1 : &m.b0;
-        const int bn = t.n0 + (MODE == kFp8GateUp ? 0 : (int)rank * 128);
+        const int box = kA_MN ? 128 : box_of(t.nrows);
+        const uint32_t bytes = (uint32_t)box * 128u + 2u * kTileBytes;
+        const CUtensorMap* amap = &m.a[box == 128 ? 0 : (box == 64 ? 1 : (box == 32 ? 2 : 3))];
         for (int kb = 0; kb < t.kb; ++kb) {
           if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty_bar(rg.s), rg.ph ^ 1u, abort_flag, p.status,
                                                          MOE_DEV_TIMEOUT_PRODUCER, p.limit_ns))) {
             ok = false;
             break;
           }
-          const uint32_t full = full_bar(rg.s);
-          const uint32_t bar = rank == 0 ? full : mapa_shared(full, leader);
+          const uint32_t bar = full_bar(rg.s);
           if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(bar, bytes);  // both CTAs' bytes (the other's may land first)
-            const uint32_t da = sm0 + rg.s * kHalf, db = b_ring + rg.s * kHalf;
+            mbar_arrive_expect_tx(bar, bytes);
+            const uint32_t da = sm0 + rg.s * a_step, db = b_ring + rg.s * 2 * kTileBytes, db1 = db + kTileBytes;
+            const int k = (t.k0 + kb) * 128, r = t.row0 + kb * 128;
             if (kA_MN) {
-              tma_load_3d_pair(da, amap, bar, t.m0 + (int)rank * 128, t.row0 + kb * 128, 0);
-              tma_load_3d_pair(db, bmap, bar, bn, t.row0 + kb * 128, 0);
+              tma_load_3d(da, amap, bar, t.m0, r, 0);
+              tma_load_3d(db, &m.b0, bar, t.n0, r, 0);
+              tma_load_3d(db1, &m.b0, bar, t.n0 + 128, r, 0);
             } else {
-              if (box) tma_load_3d_pair(da, amap, bar, (t.k0 + kb) * 128, t.row0 + first_row(t), 0);
-              if (kB_MN) tma_load_3d_pair(db, bmap, bar, bn, (t.k0 + kb) * 128, t.g);
-              else tma_load_3d_pair(db, bmap, bar, (t.k0 + kb) * 128, bn, t.g);
+              tma_load_3d(da, amap, bar, k, t.row0, 0);
+              if (MODE == kFp8GateUp) {
+                tma_load_3d(db, &m.b0, bar, k, t.n0, t.g);
+                tma_load_3d(db1, &m.b1, bar, k, t.n0, t.g);
+              } else if (kB_MN) {
+                tma_load_3d(db, &m.b0, bar, t.n0, k, t.g);
+                tma_load_3d(db1, &m.b0, bar, t.n0 + 128, k, t.g);
+              } else {
+                tma_load_3d(db, &m.b0, bar, k, t.n0, t.g);
+                tma_load_3d(db1, &m.b0, bar, k, t.n0 + 128, t.g);
+              }
             }
           }
           __syncwarp();
-          rg.next(kStages);
+          rg.next(nstages);
         }
       }
       if (!ok) {  // let copies already issued land before the CTA leaves: 5 ms
@@ -436,43 +421,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      if (rank == 0) {
-        constexpr uint32_t kIdesc = idesc_e4m3(256, 256, kA_MN, kB_MN);
-        constexpr uint32_t kStepA = kA_MN ? 4096 >> 4 : 32 >> 4, kStepB = kB_MN ? 4096 >> 4 : 32 >> 4;  // 32 of k
-        auto wait_all = [&](uint32_t bar, uint32_t parity) {
-          return warp_wait(bar, parity, abort_flag, p.status, MOE_DEV_TIMEOUT_MMA, p.limit_ns);
-        };
-        Ring rg;
-        Ring acc;  // TMEM buffer of the block
-        bool ok = true, issued = false;
-        for (int tile = pair; ok && tile < total; tile += npairs) {
-          const Tile t = decode(tile);
-          for (int kb = 0; kb < t.kb; ++kb) {
-            const uint64_t da = kA_MN ? mn_desc(sm0 + rg.s * kHalf) : sw128_kmajor_desc(sm0 + rg.s * kHalf);
-            const uint64_t db = kB_MN ? mn_desc(b_ring + rg.s * kHalf) : sw128_kmajor_desc(b_ring + rg.s * kHalf);
-            if (!wait_all(full_bar(rg.s), rg.ph) || !wait_all(tempty_bar(acc.s), acc.ph ^ 1u)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc.s * 256);
-            if (elect_one()) {
-              umma_e4m3_pair(d, da, db, kIdesc, 0u);
-  #pragma unroll
-              for (int k = 1; k < 4; ++k) umma_e4m3_pair(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
-              umma_commit_pair_mc(empty_bar(rg.s), pair_mask);
-              umma_commit_pair_mc(tfull_bar(acc.s), pair_mask);
-            }
-            __syncwarp();
-            issued = true;
-            rg.next(kStages);
-            acc.next(2);
+      constexpr uint32_t kIdesc = idesc_e4m3(128, 256, kA_MN, kB_MN);
+      constexpr uint32_t kStepA = kA_MN ? 4096 >> 4 : 32 >> 4, kStepB = kB_MN ? 4096 >> 4 : 32 >> 4;  // 32 of k
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        return warp_wait(bar, parity, abort_flag, p.status, MOE_DEV_TIMEOUT_MMA, p.limit_ns);
+      };
+      Ring rg;
+      Ring acc;  // TMEM buffer of the block
+      bool ok = true, issued = false;
+      for (int tile = worker; ok && tile < total; tile += workers) {
+        const Tile t = decode(tile);
+        for (int kb = 0; kb < t.kb; ++kb) {
+          const uint64_t da = kA_MN ? mn_desc(sm0 + rg.s * a_step) : sw128_kmajor_desc(sm0 + rg.s * a_step);
+          const uint64_t db = kB_MN ? mn_desc(b_ring + rg.s * 2 * kTileBytes) : sw128_kmajor_desc(b_ring + rg.s * 2 * kTileBytes);
+          if (!wait_all(full_bar(rg.s), rg.ph) || !wait_all(tempty_bar(acc.s), acc.ph ^ 1u)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          const uint32_t d = tmem_base + (uint32_t)(acc.s * 256);
+          if (elect_one()) {
+            umma_e4m3(d, da, db, kIdesc, 0u);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) umma_e4m3(d, da + k * kStepA, db + k * kStepB, kIdesc, 1u);
+            umma_commit(empty_bar(rg.s));
+            umma_commit(tfull_bar(acc.s));
+          }
+          __syncwarp();
+          issued = true;
+          rg.next(nstages);
+          acc.next(2);
         }
-        if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
-          umma_commit_pair(drain_bar);
-          drain_wait(drain_bar, 0, 200000000ull);
-        }
+      }
+      if (!ok && issued && lane == 0) {  // every issued MMA is done before TMEM is freed
+        umma_commit(drain_bar);
+        drain_wait(drain_bar, 0, 200000000ull);
       }
     } else {
       // ------------------------------------------------------------ scales
@@ -496,10 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot = (slot + 1) % kFactorSlots;
         acc.next(2);
       };
-      for (int tile = pair; ok && tile < total; tile += npairs) {
+      for (int tile = worker; ok && tile < total; tile += workers) {
         const Tile t = decode(tile);
         if (MODE == kFp8WeightGrad) {
-          const int n0 = t.m0 + (int)rank * 128 + s0, n1 = n0 + 32, c0 = t.n0 + (warp - kScaleWarp0) * 128 + 4 * lane;
+          const int n0 = t.m0 + s0, n1 = n0 + 32, c0 = t.n0 + (warp - kScaleWarp0) * 128 + 4 * lane;
           const int c = c0 < p.K ? c0 : p.K - 4;
           const int r0 = n0 < p.N ? n0 : p.N - 1, r1 = n1 < p.N ? n1 : p.N - 1;
           const int blocks = p.rows / 128 + G;  // that there are; offsets that fall could ask for more
@@ -526,13 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // Rows past the group's end take its last row's scales: their results are not stored.
-          const int last = t.nrows - 1, a0 = first_row(t) + s0;
-          if (PARTS && t.kb == 0) continue;
+          const int last = t.nrows - 1, a0 = s0;
+          if (PARTS > 1 && t.kb == 0) continue;
           const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs + t.k0;
           const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs + t.k0;
           const int left = kbs - t.k0;  // blocks from this part's first on
           auto load_a = [&](const float* sa, int kb) {
-            if (VEC) return load_now(reinterpret_cast<const float4*>(sa + (kb < left ? kb : left - 4)));
             const int e = left - 1;
             return make_float4(load_now(sa + (kb < e ? kb : e)), load_now(sa + (kb + 1 < e ? kb + 1 : e)),
                                load_now(sa + (kb + 2 < e ? kb + 2 : e)), load_now(sa + (kb + 3 < e ? kb + 3 : e)));
@@ -572,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    if (PARTS && pair < total) cluster_sync_all();
+    if (PARTS > 1 && worker < total) cluster_sync_all();
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
@@ -580,22 +562,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - kEpiWarp0) >> 2;    // its 128 columns (GATE_UP: 64 of gate, 64 of up)
     uint8_t* stg = staging + (warp - kEpiWarp0) * kStgWarp;
     bool idle = false;  // PARTS: the cluster's rings are
-    const uint32_t tempty0 = rank == 0 ? tempty_bar(0) : mapa_shared(tempty_bar(0), leader);
     auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive(tempty0 + 8u * buf);
-        else mbar_arrive_remote(tempty0 + 8u * buf);
-      }
+      if (lane == 0) mbar_arrive(tempty_bar(buf));
     };
     Ring acc;
     bool ok = true;
     int slot = 0;
-    uint32_t split_phase = 0, joined = 0;  // GATE_UP: tiles whose maxima were put together, split and not
-    for (int tile = pair; ok && tile < total; tile += npairs) {
+    uint32_t joined = 0;  // GATE_UP: tiles whose maxima were put together
+    for (int tile = worker; ok && tile < total; tile += workers) {
       const Tile c_t = decode(tile);
-      const int r0 = first_row(c_t) + q * 32;  // this warp's first row of the tile
+      const int r0 = q * 32;  // this warp's first row of the tile
       if (MODE != kFp8WeightGrad && c_t.nrows <= r0) {  // none of this warp's rows: keep step
         for (int kb = 0; ok && kb < c_t.kb; ++kb) {
           ok = warp_wait(tfull_bar(acc.s), acc.ph, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
@@ -605,11 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      // Columns of the tile that this warp adds: `wide` from col0 on (GATE_UP: of the
-      // gates, and as many of the ups), 32 of them at a time.
-      const bool split = MODE != kFp8WeightGrad && c_t.split;
-      const int wide = (MODE == kFp8GateUp ? 64 : 128) >> (split ? 1 : 0);
-      const int col0 = (split ? 2 * (int)rank + half : half) * wide;
+      const int col0 = (MODE == kFp8GateUp ? 64 : 128) * half;  // the first column that this warp adds
       // The accumulators live in the loops below: nothing but their end and the results
       // read them, so that no copies join them with another path's.
       float sum[128];
@@ -639,8 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto take_factors = [&] {
         f = factors + slot * kFactors;
         slot = (slot + 1) % kFactorSlots;
-        const int part = MODE == kFp8GateUp || MODE == kFp8WeightGrad ? 0 : (split ? (int)rank : half);
-        f0 = f[part * 128 + q * 32 + lane];
+        f0 = f[(MODE == kFp8GateUp || MODE == kFp8WeightGrad ? 0 : half * 128) + q * 32 + lane];
         f1 = MODE == kFp8GateUp ? f[128 + q * 32 + lane] : f0;
         f += 128 + 128 * half;  // WEIGHT_GRAD: the columns'
       };
@@ -687,20 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-      } else if (split) {
-#pragma unroll 1
-        for (int kb = 0; kb < c_t.kb; ++kb) {
-          take_factors();
-          arrived(v0);
-          tmem_ld_32x32b_x32(tb + (MODE == kFp8GateUp ? 128 : 32), v1);
-          add(0, f0, v0);
-          arrived(v1);
-          release(acc.s);
-          acc.next(2);
-          const float y = f1;
-          if (kb + 1 < c_t.kb && !begin()) goto done;
-          add(1, y, v1);
-        }
       } else {
         auto at = [&](int c) { return tb + (MODE == kFp8GateUp ? (c & 1) * 32 + (c >> 1) * 128 : 32 * c); };
 #pragma unroll 1
@@ -722,95 +681,84 @@ __global__ void __launch_bounds__(kThreads, 1)
           add(3, f1, v1);
         }
       }
-      if constexpr (PARTS) {
-        // The pairs' sums are put together: each CTA takes a slice of every warp's
-        // columns, a warp's 32 rows of it from the same warp of its counterparts in
-        // the other pairs, through its ring, which is idle by then (16 bytes of 32
-        // rows at a time: 512 bytes in order).
+      if constexpr (PARTS > 1) {
+        // The parts' sums are put together: each CTA takes a slice of every warp's
+        // columns, a warp's 32 rows of it from the same warp of the other CTAs, through
+        // its ring, which is idle by then (16 bytes of 32 rows at a time: 512 bytes in
+        // order).
+        constexpr int kKinds = MODE == kFp8GateUp ? 2 : 1;       // gates and ups
+        constexpr int kN = 32 / kKinds, kPer = kN / PARTS;       // groups of four columns: of the warp, of a slice
         cluster_sync_all();
         idle = true;
-        auto join = [&](auto n) {
-          constexpr int kKinds = MODE == kFp8GateUp ? 2 : 1;  // gates and ups
-          constexpr int kN = n.value / kKinds, kPer = kN / kParts;  // groups of four columns: of the warp, of a slice
-          auto at = [&](int from, int c) { return base + ((from * kEpiWarps + warp - kEpiWarp0) * (kPer * kKinds) + c) * 512 + lane * 16; };
-          const uint32_t bar = split_bar(q, (uint32_t)half);
-          if (lane == 0) mbar_arrive_expect_tx(bar, kParts * kPer * kKinds * 512);
+        auto place = [&](int from, int c) { return base + ((from * kEpiWarps + warp - kEpiWarp0) * (kPer * kKinds) + c) * 512 + lane * 16; };
+        const uint32_t bar = slice_bar(warp - kEpiWarp0);
+        if (lane == 0) mbar_arrive_expect_tx(bar, PARTS * kPer * kKinds * 512);
 #pragma unroll
-          for (int c = 0; c < kN * kKinds; ++c) {
-            const int kind = c / kN, to = c % kN / kPer;
-            const uint32_t cta = 2 * to + rank;
-            st_async4(mapa_shared(smem_u32(at(part, kind * kPer + c % kPer)), cta),
-                      make_float4(sum[4 * c], sum[4 * c + 1], sum[4 * c + 2], sum[4 * c + 3]), mapa_shared(bar, cta));
+        for (int c = 0; c < 32; ++c) {
+          const int to = c % kN / kPer;
+          st_async4(mapa_shared(smem_u32(place(part, c / kN * kPer + c % kPer)), to),
+                    make_float4(sum[4 * c], sum[4 * c + 1], sum[4 * c + 2], sum[4 * c + 3]), mapa_shared(bar, to));
+        }
+        if (!warp_wait(bar, 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) goto done;
+        float x[4 * kPer * kKinds];
+#pragma unroll
+        for (int c = 0; c < kPer * kKinds; ++c) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(place(i, c));
+            v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
           }
-          if (!warp_wait(bar, 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return;
-          float x[4 * kPer * kKinds];
+          x[4 * c] = v.x;
+          x[4 * c + 1] = v.y;
+          x[4 * c + 2] = v.z;
+          x[4 * c + 3] = v.w;
+        }
+        const int r = r0 + lane, first = c_t.n0 + col0 + part * kPer * 4;
+        const bool live = r < c_t.nrows;
+        const size_t row = (size_t)(c_t.row0 + r) * p.N + first;
+        if constexpr (MODE == kFp8GateUp) {
+          uint32_t top = 0;
 #pragma unroll
-          for (int c = 0; c < kPer * kKinds; ++c) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-              const float4 y = *reinterpret_cast<const float4*>(at(i, c));
-              v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
-            }
-            x[4 * c] = v.x;
-            x[4 * c + 1] = v.y;
-            x[4 * c + 2] = v.z;
-            x[4 * c + 3] = v.w;
+          for (int i = 0; i < 4 * kPer; ++i) {
+            x[i] = silu_fast(x[i]) * x[4 * kPer + i];
+            const uint32_t b = fp8_abs_bits(x[i]);
+            top = b > top ? b : top;
           }
-          const int r = r0 + lane, first = c_t.n0 + col0 + part * kPer * 4;
-          const bool live = r < c_t.nrows;
-          const size_t row = (size_t)(c_t.row0 + r) * p.N + first;
-          if constexpr (MODE == kFp8GateUp) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 4 * kPer; ++i) {
-              x[i] = silu_fast(x[i]) * x[4 * kPer + i];
-              const uint32_t b = fp8_abs_bits(x[i]);
-              top = b > top ? b : top;
-            }
-            // The maxima of each CTA's warps, behind the slices, to all CTAs that have these rows.
-            constexpr bool kSplit = n.value == 16;
-            constexpr uint32_t kStep = kSplit ? 1 : 2, kFrom = 2 * kParts / kStep;
-            uint32_t* tops = reinterpret_cast<uint32_t*>(base + 4 * 2 * kHalf) + q * 32 + lane;
-            if (lane == 0) {
-              if (half == 0) mbar_arrive_expect_tx(join_bar(q), kFrom * 2 * 32 * 4);
-              else mbar_arrive(join_bar(q));
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < kFrom; ++i) {
-              const uint32_t cta = kSplit ? i : 2 * i + rank;
-              st_async(mapa_shared(smem_u32(tops + (2 * crank + half) * 128), cta), top, mapa_shared(join_bar(q), cta));
-            }
-            if (!warp_wait(join_bar(q), 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) return;
-#pragma unroll
-            for (uint32_t i = 0; i < 2 * kFrom; ++i) {
-              const uint32_t from = kSplit ? i / 2 : i / 2 * 2 + rank;
-              const uint32_t t = tops[(2 * from + (i & 1)) * 128];
-              top = t > top ? t : top;
-            }
-            const Fp8Block blk(fp8_scale(top));
-            if (live && half == 0 && part == 0 && (!kSplit || rank == 0))
-              p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = blk.scale;
-#pragma unroll
-            for (int c = 0; c < kPer; ++c)
-              if (live && first + 4 * c < p.N)
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row + 4 * c) =
-                    blk.code4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-              if (!live || first + 4 * c >= p.N) break;
-              if (p.out_f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row + 4 * c) =
-                    make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-              else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row + 4 * c) =
-                    make_uint2(pack_bf16(x[4 * c], x[4 * c + 1]), pack_bf16(x[4 * c + 2], x[4 * c + 3]));
-            }
+          // The maxima of each CTA's warps go to all CTAs, behind the slices.
+          uint32_t* tops = reinterpret_cast<uint32_t*>(base + 8 * kTileBytes) + q * 32 + lane;
+          if (lane == 0) {
+            if (half == 0) mbar_arrive_expect_tx(join_bar(q), PARTS * 2 * 32 * 4);
+            else mbar_arrive(join_bar(q));
           }
-        };
-        if (split) join(std::integral_constant<int, 16>());
-        else join(std::integral_constant<int, 32>());
+#pragma unroll
+          for (int to = 0; to < PARTS; ++to)
+            st_async(mapa_shared(smem_u32(tops + (2 * part + half) * 128), to), top, mapa_shared(join_bar(q), to));
+          if (!warp_wait(join_bar(q), 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) goto done;
+#pragma unroll
+          for (int i = 0; i < 2 * PARTS; ++i) {
+            const uint32_t t = tops[i * 128];
+            top = t > top ? t : top;
+          }
+          const Fp8Block blk(fp8_scale(top));
+          if (live && half == 0 && part == 0) p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = blk.scale;
+#pragma unroll
+          for (int c = 0; c < kPer; ++c)
+            if (live && first + 4 * c < p.N)
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row + 4 * c) =
+                  blk.code4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kPer; ++c) {
+            if (!live || first + 4 * c >= p.N) break;
+            if (p.out_f32)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row + 4 * c) =
+                  make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row + 4 * c) =
+                  make_uint2(pack_bf16(x[4 * c], x[4 * c + 1]), pack_bf16(x[4 * c + 2], x[4 * c + 3]));
+          }
+        }
         __syncwarp();
         continue;
       }
@@ -826,29 +774,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bulk_wait_group_read0();
         __syncwarp();
       };
-      // Block h of the staging: `bytes` (64 or 128) of each row, from column col0 of `esize` bytes on.
-      auto send = [&](int h, int bytes, int esize, int col0) {
+      // The staging: `bytes` (64 or 128) of each row, from column col of `esize` bytes on.
+      auto send = [&](int bytes, int esize, int col) {
         if (whole) {
-          if (lane == 0 && col0 < width && r0 < live_rows) {
-            const uint32_t src = smem_u32(stg + h * kStgBlock);
-            if (MODE == kFp8WeightGrad) tma_store_3d(&m.out, src, col0, c_t.m0 + r0, c_t.g);
-            else tma_store_3d(&m.out, src, col0, c_t.row0 + r0, 0);
+          if (lane == 0 && col < width && r0 < live_rows) {
+            if (MODE == kFp8WeightGrad) tma_store_3d(&m.out, smem_u32(stg), col, c_t.m0 + r0, c_t.g);
+            else tma_store_3d(&m.out, smem_u32(stg), col, c_t.row0 + r0, 0);
             bulk_commit_group();
           }
           return;
         }
-        const int per = bytes / 16, col = col0 + 16 / esize * (lane % per);  // 16-byte chunks of a row
-        uint8_t* out = static_cast<uint8_t*>(p.out) + ((size_t)(c_t.row0 + r0) * width + col) * esize;
+        const int per = bytes / 16, c = col + 16 / esize * (lane % per);  // 16-byte chunks of a row
+        uint8_t* out = static_cast<uint8_t*>(p.out) + ((size_t)(c_t.row0 + r0) * width + c) * esize;
         for (int i = lane / per; i < 32; i += 32 / per) {
           const int chunk = (lane % per) ^ (bytes == 128 ? i & 7 : (i >> 1) & 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(stg + h * kStgBlock + i * bytes + 16 * chunk);
-          if (col < width && r0 + i < live_rows) *reinterpret_cast<uint4*>(out + (size_t)i * width * esize) = v;
+          const uint4 v = *reinterpret_cast<const uint4*>(stg + i * bytes + 16 * chunk);
+          if (c < width && r0 + i < live_rows) *reinterpret_cast<uint4*>(out + (size_t)i * width * esize) = v;
         }
       };
       if (MODE == kFp8GateUp) {
-        // h of 64 columns (32 of a split tile); the block's largest is the largest of
-        // the two warps' (four: two in each CTA). Two slots of either kind by turns:
-        // another warp may still read the last such tile's.
+        // h of 64 columns; the block's largest is the largest of the two warps', in two
+        // slots by turns: the other warp may still read the last tile's.
         uint32_t top = 0;
         auto finish = [&](float g, float u) {
           const float x = silu_fast(g) * u;
@@ -857,43 +803,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           return x;
         };
         uint32_t* tops = reinterpret_cast<uint32_t*>(factors + kFactorSlots * kFactors) + q * 32 + lane;
-        if (split) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sum[i] = finish(sum[i], sum[32 + i]);
-          const uint32_t turn = split_phase & 1, bar = split_bar(q, turn);
-          tops += turn * 512;
-          uint32_t* mine = tops + (2 * rank + half) * 128;
-          *mine = top;
-          st_async(mapa_shared(smem_u32(mine), rank ^ 1u), top, mapa_shared(bar, rank ^ 1u));
-          __syncwarp();
-          if (lane == 0) {
-            if (half == 0) mbar_arrive_expect_tx(bar, 2 * 32 * 4);
-            else mbar_arrive(bar);
-          }
-          ok = warp_wait(bar, (split_phase >> 1) & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
-          if (!ok) goto done;
-          ++split_phase;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = *reinterpret_cast<volatile uint32_t*>(tops + i * 128);
-            top = x > top ? x : top;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) sum[i] = finish(sum[i], sum[64 + i]);
-          tops += 1024 + (joined & 1) * 256;
-          tops[half * 128] = top;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(join_bar(q));
-          ok = warp_wait(join_bar(q), joined & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
-          if (!ok) goto done;
-          ++joined;
-          const uint32_t other = *reinterpret_cast<volatile uint32_t*>(tops + (half ^ 1) * 128);
-          top = other > top ? other : top;
-        }
+        for (int i = 0; i < 64; ++i) sum[i] = finish(sum[i], sum[64 + i]);
+        tops += (joined & 1) * 256;
+        tops[half * 128] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(join_bar(q));
+        ok = warp_wait(join_bar(q), joined & 1u, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns);
+        if (!ok) goto done;
+        ++joined;
+        const uint32_t other = *reinterpret_cast<volatile uint32_t*>(tops + (half ^ 1) * 128);
+        top = other > top ? other : top;
         const float scale = fp8_scale(top);
         const int r = r0 + lane;
-        if (half == 0 && (!split || rank == 0) && r < c_t.nrows)
+        if (half == 0 && r < c_t.nrows)
           p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = scale;
         const Fp8Block blk(scale);
         auto codes = [&](int c) {  // 16 of them
@@ -906,57 +829,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           return make_uint4(w[0], w[1], w[2], w[3]);
         };
         reuse();
-        if (split) {  // 32 bytes of each row, sixteen rows per store: chunk c of row i at c ^ (i / 4) % 2
 #pragma unroll
-          for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(stg + lane * 32 + ((c ^ ((lane >> 2) & 1)) << 4)) = codes(c);
-          __syncwarp();
-          const int col = c_t.n0 + col0 + 16 * (lane & 1);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int i = 16 * j + (lane >> 1);
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 32 + (((lane & 1) ^ ((i >> 2) & 1)) << 4));
-            if (r0 + i < c_t.nrows && col < p.N)
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (size_t)(c_t.row0 + r0 + i) * p.N + col) = v;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = codes(c);
-          fence_proxy_async_smem();
-          __syncwarp();
-          send(0, 64, 1, c_t.n0 + col0);
-        }
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = codes(c);
+        fence_proxy_async_smem();
+        __syncwarp();
+        send(64, 1, c_t.n0 + col0);
       } else {
         const int c0 = c_t.n0 + col0;
+        uint8_t* mine = stg + lane * 128;
         if (p.out_f32) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (g == 1 && split) break;
+          for (int g = 0; g < 4; ++g) {  // 32 columns
             reuse();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int e = 64 * g + 4 * j;
-              *reinterpret_cast<float4*>(stg + (j >> 3) * kStgBlock + lane * 128 + (((j & 7) ^ (lane & 7)) << 4)) =
-                  make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+            for (int j = 0; j < 8; ++j) {
+              const float* x = sum + 32 * g + 4 * j;
+              *reinterpret_cast<float4*>(mine + ((j ^ (lane & 7)) << 4)) = make_float4(x[0], x[1], x[2], x[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            send(0, 128, 4, c0 + 64 * g);
-            send(1, 128, 4, c0 + 64 * g + 32);
+            send(128, 4, c0 + 32 * g);
           }
         } else {
-          reuse();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            uint32_t w[4];
+          for (int g = 0; g < 2; ++g) {  // 64
+            reuse();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack_bf16(sum[8 * j + 2 * i], sum[8 * j + 2 * i + 1]);
-            *reinterpret_cast<uint4*>(stg + (j >> 3) * kStgBlock + lane * 128 + (((j & 7) ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 8; ++j) {
+              const float* x = sum + 64 * g + 8 * j;
+              *reinterpret_cast<uint4*>(mine + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            send(128, 2, c0 + 64 * g);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          send(0, 128, 2, c0);
-          if (!split) send(1, 128, 2, c0 + 64);
         }
       }
     }
@@ -964,36 +871,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_ld_wait();
     bulk_wait_group0();
     __syncwarp();
-    if (PARTS && pair < total && !idle) cluster_sync_all();
+    if (PARTS > 1 && worker < total && !idle) cluster_sync_all();
   }
 
-  // Both CTAs arrive here only when their roles are done (every wait is
-  // bounded), so neither frees TMEM or leaves while the other may still touch
-  // its shared memory or barriers.
+  // The CTAs of a cluster arrive here only when their roles are done (every wait is
+  // bounded), so none leaves while another may still write to its shared memory.
   tc_fence_before();
   __syncwarp();
-  cluster_sync_all();
-  if (*abort_flag) {  // the other CTA's last stores and arrivals here land: 5 ms
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 5000000ull) {
+  if (PARTS > 1) {
+    cluster_sync_all();
+    if (*abort_flag) {  // the others' last stores and arrivals here land: 5 ms
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 5000000ull) {
+      }
     }
+  } else {
+    __syncthreads();
   }
   __syncwarp();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, 512);
+    tmem_dealloc(tmem_base, 512);
   }
 }
 
-// Whether kParts pairs share each tile's reduction. Up to 15 clusters of eight CTAs
-// run at once (7 rows x 3840 x 4096, 15 tiles: 14.6 us, in parts 8.2; 16 tiles take
-// two waves, 15.3). The exchange of the sums costs as much as rows / 8 blocks (10
-// tiles, K = 1024 and 2048: 32 rows 7.1 -> 6.1 and 9.5 -> 6.8 us, 128 rows 7.9 -> 9.3
-// and 10.4 -> 10.0), of tiles higher than 128 rows more (160 rows, K = 2560 and
-// 4096: 13.8 -> 15.4, 18.5 -> 16.5).
-bool in_parts(long long tiles, int rows, int blocks) {
-  const int least = rows > 128 ? 28 : (rows / 8 > 4 ? rows / 8 : 4);
-  return tiles <= 15 && blocks >= least;
+// CTAs that share each tile's reduction, where there are few tiles: as many as make
+// one wave (clusters of eight: 15, of four: 36 and more). The exchange of the sums
+// costs about 2 us for up to 32 rows (K = 4096, 15 tiles: 15.3 us, in four parts 9.0,
+// in eight 8.2; K = 1024: 7.1, 6.7, 6.9; 30 tiles 7.2, 7.4), 4 for 64 (K = 2048 and
+// 1024, 30 tiles: 10.6, in four parts 11.2; 16 tiles 10.4, 10.0 and 7.5, 9.3), 8 for
+// 128 (K = 4096: 16.9, 17.3).
+int parts_of(long long tiles, int rows, int blocks) {
+  if (rows > 64 || tiles > 36 || blocks < (rows > 32 ? 20 : 10)) return 1;
+  return tiles <= 15 && blocks >= 24 ? 8 : 4;
 }
 
 template <int MODE>
@@ -1032,35 +942,33 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
   p.limit_ns = a.wait_limit_ns;
   const int cols = MODE == kFp8GateUp ? 128 : 256;
   const long long n_wt = (a.N + cols - 1) / cols;
-  const long long tiles = MODE == kFp8WeightGrad ? G * n_wt * ((a.K + 255) / 256) : n_wt * (a.rows / 256 + G);
-  const long long most = a.num_sms / 2;
-  const int pairs = (int)(tiles < most ? tiles : most);
-  if (pairs < 1) return cudaErrorInvalidValue;
-  if constexpr (MODE != kFp8WeightGrad) {
-    const long long filled = n_wt * (a.rows / 256 + (G < a.rows ? G : a.rows));  // tiles of groups that have rows
-    if (in_parts(filled, a.rows, fp8_blocks(a.K)))
-      return launch_dependent(grouped_gemm_fp8_kernel<MODE, false, true>, (int)(2 * kParts * filled), kThreads, smem_of(MODE), s,
-                              true, /*cluster=*/2 * kParts, m, p);
+  auto launch = [&](auto kernel, long long tiles, int parts) {
+    const long long grid = parts > 1 ? parts * tiles : (tiles < a.num_sms ? tiles : a.num_sms);
+    return launch_dependent(kernel, (int)grid, kThreads, smem_of(MODE), s, true, /*cluster=*/parts, m, p);
+  };
+  if constexpr (MODE == kFp8WeightGrad) {
+    return launch(grouped_gemm_fp8_kernel<MODE, 1>, (long long)G * ((a.N + 127) / 128) * ((a.K + 255) / 256), 1);
+  } else {
+    const long long tiles = n_wt * (a.rows / 128 + (G < a.rows ? G : a.rows));  // at most: of groups that have rows
+    const int parts = parts_of(tiles, a.rows, fp8_blocks(a.K));
+    if (parts == 8) return launch(grouped_gemm_fp8_kernel<MODE, 8>, tiles, 8);
+    if (parts == 4) return launch(grouped_gemm_fp8_kernel<MODE, 4>, tiles, 4);
+    return launch(grouped_gemm_fp8_kernel<MODE, 1>, tiles, 1);
   }
-  const bool vec = MODE == kFp8WeightGrad || fp8_blocks(a.K) % 4 == 0;
-  if (vec) return launch_dependent(grouped_gemm_fp8_kernel<MODE, true, false>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
-  return launch_dependent(grouped_gemm_fp8_kernel<MODE, MODE == kFp8WeightGrad, false>, 2 * pairs, kThreads, smem_of(MODE), s, true, /*cluster=*/2, m, p);
 }
 
-}  // namespace
-
-namespace {
-template <int MODE, bool VEC, bool PARTS = false>
+template <int MODE, int PARTS>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, VEC, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(MODE));
+  return cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(MODE));
 }
+
 }  // namespace
 
 cudaError_t gemm_fp8_prepare_device() {
-  const cudaError_t errs[] = {allow_smem<kFp8Forward, true>(),    allow_smem<kFp8Forward, false>(),    allow_smem<kFp8Forward, false, true>(),
-                              allow_smem<kFp8Transposed, true>(), allow_smem<kFp8Transposed, false>(), allow_smem<kFp8Transposed, false, true>(),
-                              allow_smem<kFp8GateUp, true>(),     allow_smem<kFp8GateUp, false>(),     allow_smem<kFp8GateUp, false, true>(),
-                              allow_smem<kFp8WeightGrad, true>()};
+  const cudaError_t errs[] = {allow_smem<kFp8Forward, 1>(),    allow_smem<kFp8Forward, 4>(),    allow_smem<kFp8Forward, 8>(),
+                              allow_smem<kFp8Transposed, 1>(), allow_smem<kFp8Transposed, 4>(), allow_smem<kFp8Transposed, 8>(),
+                              allow_smem<kFp8GateUp, 1>(),     allow_smem<kFp8GateUp, 4>(),     allow_smem<kFp8GateUp, 8>(),
+                              allow_smem<kFp8WeightGrad, 1>()};
   for (cudaError_t e : errs)
     if (e != cudaSuccess) return e;
   return cudaSuccess;

@@ -218,14 +218,15 @@ def test_dense_product(handle, rows, transposed):
 
 
 FEW = [([1], 512, 4096), ([33], 272, 1616), ([128], 256, 2048), ([129], 1536, 4096), ([0, 0, 3, 0, 70, 0, 0], 256, 1920),
-       ([296], 400, 3728), ([130, 0, 200], 512, 3600), ([3, 9], 272, 528), ([250, 6, 128], 2064, 2048)]
+       ([296], 400, 3728), ([130, 0, 200], 512, 3600), ([3, 9], 272, 528), ([250, 6, 128], 2064, 2048),
+       ([20], 272, 1616), ([50], 272, 3728), ([5, 0, 40], 2304, 2704), ([1] * 10, 256, 1360), ([62], 512, 3088)]
 
 
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
 @pytest.mark.parametrize("counts, N, K", FEW)
 def test_few_tiles(handle, counts, N, K, out_dtype, transposed):
-    """Few tiles and a long reduction: parts of it on several pairs of SMs, of like and unlike lengths."""
+    """Few tiles and a long reduction: parts of it on several SMs, of like and unlike lengths."""
     product(handle, counts, N, K, transposed, out_dtype)
 
 
@@ -234,7 +235,7 @@ def test_many_groups(handle):
 
 
 def test_many_tiles_per_pair(handle):
-    """More tiles than pairs of SMs, several rounds of every ring."""
+    """More tiles than SMs, several rounds of every ring."""
     product(handle, [400, 0, 300, 513], 4096, 1536, False, F32)
     product(handle, [400, 0, 300, 513], 4096, 1536, True, BF16)
 
