@@ -83,7 +83,9 @@ def grad64(logits, counts, ends, dloss, score, coef, E, K):
 
 CASES = [(1, 8, 2, [0, 1]), (1, 1, 1, [0, 1]), (17, 64, 6, [0, 17]), (61, 192, 8, [0, 61]), (1000, 192, 8, [0, 1000]), (333, 33, 5, [0, 333]),
          (700, 256, 8, [0, 0, 1, 33, 33, 64, 640, 690]), (96, 1024, 32, [5, 40, 96]), (40, 512, 3, [0, 13, 40]), (3000, 100, 4, [0, 3000]),
-         (20000, 65, 1, [0, 9999, 20000]), (300, 16, 2, list(range(0, 301, 3)))]
+         (20000, 65, 1, [0, 9999, 20000]), (300, 16, 2, list(range(0, 301, 3))),
+         (6, 24, 1, [0, 0, 0, 2] + [3] * 40 + [6] * 40), (84, 56, 3, sorted((i * 37) % 80 for i in range(64))),
+         (9001, 4, 2, [i * i * 2 for i in range(65)] + [9001]), (5000, 128, 8, [0, 0, 1, 2, 40, 41, 3000, 3000, 3001, 4990])]
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
