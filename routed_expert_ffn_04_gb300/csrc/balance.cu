@@ -16,8 +16,8 @@
 // blocks of a cluster sharing the experts. The logits are read once; many tokens are
 // bound by instructions and waits rather than HBM (65536 x 256 in 29 sequences: 21.3
 // us, of them 4 the second launch; bytes 10.2), few by the launch (64 x 192: 4.3 us).
-// The gradient reads and writes each logit once: 65536 x 256 with an addend 39 us at
-// 5.1 TB/s, 8192 x 192 6.3.
+// The gradient reads and writes each logit once: 65536 x 256 with an addend 34 us at
+// 5.9 TB/s, 8192 x 192 5.6.
 //
 // Scores that all underflow (every logit far below 0) keep their ratios: the
 // shares are then taken relative to the largest. A token whose scores are all 0
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) balance_one_kernel(const Balan
 }
 
 template <class S, bool SOFTMAX>
-__global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(kGradThreads, S::V > 16 ? 1 : 2) balance_grad_kernel(const BalanceParams p) {
   constexpr int V = S::V, L = S::L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, E = p.E;
   wait_for_previous_launch();
@@ -465,12 +465,18 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
 #pragma unroll
     for (int j = 0; j < V; ++j)
       f[j] = S::is(j, sub, E) ? (float)__ldcg(p.counts + (size_t)b * E + S::expert(j, sub)) * per : 0.0f;
+    // The next tokens' logits are on their way meanwhile (52362 x 241, sigmoid: 74 -> 25 us).
+    float next[V];
+    auto load = [&](int t) { S::load(next, p.logits + (size_t)(t + lane / L < hi ? t + lane / L : t) * E, E, sub, -INFINITY); };
+    load(lo);
     for (int t = lo; t < hi; t += S::kTokens) {
       const bool live = t + lane / L < hi;
       const size_t at = (size_t)(live ? t + lane / L : t) * E;
       float x[V], slope[V], add[V];
-      S::load(x, p.logits + at, E, sub, -INFINITY);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = next[j];
       if (p.add) S::load(add, p.add + at, E, sub, 0.0f);
+      if (t + S::kTokens < hi) load(t + S::kTokens);
       const float inv = scores<S, SOFTMAX, true>(x, slope, p.logits + at, E, sub);
       float c = 0.0f;
 #pragma unroll

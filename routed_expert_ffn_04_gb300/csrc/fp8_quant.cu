@@ -6,7 +6,10 @@
 //            operands: the reduction runs over the rows; each group starts at a
 //            multiple of 128 rows of the result, and zero rows fill its last block)
 // One pass: a block's values stay in registers between its maximum and its
-// codes. Bound by HBM: 2 (4) bytes in and 1 out per value.
+// codes. Floors are of HBM, 2 (4) bytes in and 1 out per value; the rows take 75% of
+// the issue slots beside it (maxima of two bf16 values at a time: 23.6 -> 18.4 us).
+// 33.6 million bf16 values (floor 15 us): rows of 4096 17.9, squares 18.5, columns of
+// uneven groups 24.2; fp32 (24.9): rows 27.8, columns 35.9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -77,8 +77,6 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(128 * kRegsFew + 32 * kEpiWarps * kRegsMany == kThreads * kRegsLaunch, "registers");
 constexpr int kStgBlock = 4096;  // staging: 32 rows of 128 bytes
-// Stages of the ring, and staging per warp: GATE_UP's rows of a warp are 64 bytes
-// of codes, the others' 256 bytes (two blocks).
 // The ring, of stages of A (128 rows) and B (256), and staging per warp: GATE_UP's
 // rows of a warp are 64 bytes of codes, the others' 256 or 512, 128 at a time. Four
 // stages instead of three: 828 -> 809 us for GATE_UP's 341 rows.
@@ -191,8 +189,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 // x sigma(x), 2 ulp: the approximate quotient, which is 0 past 2^126 as it should be here.
 __device__ __forceinline__ float silu_fast(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
-// Bounded wait by a whole warp. The waits suspend (polling took issue slots from
-// the epilogue: 1053 -> 946 us for gate and up at 192 x 341 rows).
+// Bounded wait by a whole warp. The waits suspend: polling took issue slots from
+// the epilogue (a tenth of the time of gate and up at 192 x 341 rows).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int code,
                                           uint64_t limit_ns) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
@@ -509,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // Rows past the group's end take its last row's scales: their results are not stored.
-          const int last = t.nrows - 1, a0 = s0;
+          const int last = t.nrows - 1;
           if (PARTS > 1 && t.kb == 0) continue;
-          const float* sa0 = p.sa + (size_t)(t.row0 + (a0 < last ? a0 : last)) * kbs + t.k0;
-          const float* sa1 = p.sa + (size_t)(t.row0 + (a0 + 32 < last ? a0 + 32 : last)) * kbs + t.k0;
+          const float* sa0 = p.sa + (size_t)(t.row0 + (s0 < last ? s0 : last)) * kbs + t.k0;
+          const float* sa1 = p.sa + (size_t)(t.row0 + (s0 + 32 < last ? s0 + 32 : last)) * kbs + t.k0;
           const int left = kbs - t.k0;  // blocks from this part's first on
           auto load_a = [&](const float* sa, int kb) {
             const int e = left - 1;
@@ -625,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MODE == kFp8WeightGrad) {
         // Columns' factors as well. They are read before the wait for their columns
         // (which the compiler moves no load across): with 32 columns at a time there
-        // were no registers for that, and each read was waited for (192 x 341 rows:
-        // 871 -> 788 us). Every lane reads all 128, which fills the shared memory's
-        // port (648 us without); TMEM loads of 16 lanes x 256 bits, with which a lane
-        // has four rows and a quarter of the columns, were no faster (798, 64 columns
-        // at a time 817).
+        // were no registers for that, and each read was waited for (192 x 341 rows, by
+        // pairs of CTAs: 871 -> 788 us). Every lane reads all 128, which fills the shared
+        // memory's port (648 us without); TMEM loads of 16 lanes x 256 bits, with which a
+        // lane has four rows and a quarter of the columns, were no faster (798, 64
+        // columns at a time 817).
 #pragma unroll 1
         for (int kb = 0; kb < c_t.kb; ++kb) {
           take_factors();
