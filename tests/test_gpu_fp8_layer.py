@@ -101,6 +101,20 @@ def test_layer_is_its_pieces(shape):
     assert torch.equal(xp, xp2) and torch.equal(sp, sp2)
 
 
+def test_shared_expert_on_few_sms():
+    """The shared expert's products stay on the SMs that an option gives them: its reduction is not shared out then."""
+    shape = synth.MoEShape("fd", T=9, H=4096, E=3, K=1, I=128, I_shared=256, dtype="fp8")
+    x, logits, w = problem(shape, 2)
+    layer = moe.MoELayer(shape, w, device=0)
+    out = layer(x, logits)
+    layer.handle.set_option(moe.MOE_OPT_SHARED_SMS, 8)
+    few = layer(x, logits)
+    ref = layer64(shape, x, logits, w)
+    for o in (out, few):
+        assert float((o.to(F64) - ref).norm() / ref.norm()) <= 2.0 ** -8 + 1e-3
+    assert layer.handle.device_status() == 0
+
+
 def test_layer_in_a_graph_host_and_gated():
     shape = SHAPES[1]
     x, logits, w = problem(shape, 2)
