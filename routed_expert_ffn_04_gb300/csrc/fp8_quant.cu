@@ -9,7 +9,7 @@
 // codes. Floors are of HBM, 2 (4) bytes in and 1 out per value; the rows take 75% of
 // the issue slots beside it (maxima of two bf16 values at a time: 23.6 -> 18.4 us).
 // 33.6 million bf16 values (floor 15 us): rows of 4096 17.9, squares 18.5, columns of
-// uneven groups 24.2; fp32 (24.9): rows 27.8, columns 35.9.
+// uneven groups 22.7; fp32 (24.9): rows 27.8, columns 34.2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -109,9 +109,10 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const uint8_
 constexpr int kTileThreads = 256;
 constexpr int kMaxGroups = 1024;
 
-template <bool F32>
+template <bool F32, int COLS = 128>
 struct TileRegs {
-  static constexpr int kN = Vec<F32>::kN, kLanes = 128 / kN, kStep = kTileThreads / kLanes, kRows = 128 / kStep;
+  static constexpr int kThreads = kTileThreads * COLS / 128;
+  static constexpr int kN = Vec<F32>::kN, kLanes = COLS / kN, kStep = kThreads / kLanes, kRows = 128 / kStep;
   Vec<F32> v[kRows];
   int col, row;  // of this thread's first value in the tile
   __device__ __forceinline__ TileRegs() : col(threadIdx.x % kLanes * kN), row(threadIdx.x / kLanes) {}
@@ -162,18 +163,22 @@ __global__ void __launch_bounds__(kTileThreads)
   }
 }
 
+// Tiles of 128 rows x kCols: twice the thread blocks per SM of tiles of 128 columns,
+// whose loads, maxima and codes alternate (24.9 -> 22.7 us; of 32 columns 27.2).
+constexpr int kCols = 64, kColThreads = TileRegs<false, kCols>::kThreads;
+
 template <bool F32>
-__global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
+__global__ void __launch_bounds__(kColThreads, F32 ? 4 : 6)
     quantize_columns_kernel(const uint8_t* x, int rows, int cols, const int32_t* offsets, int G, uint8_t* q, float* scale) {
-  using T = TileRegs<F32>;
-  __shared__ __align__(16) uint32_t part[T::kStep][128];
-  __shared__ __align__(16) float scales[128], invs[128];
+  using T = TileRegs<F32, kCols>;
+  __shared__ __align__(16) uint32_t part[T::kStep][kCols];
+  __shared__ __align__(16) float scales[kCols], invs[kCols];
   __shared__ int where[2], starts[kMaxGroups + 1];
   wait_for_previous_launch();
   allow_next_launch();
   // The group whose blocks of 128 rows this one is of: every lane of a warp takes
   // some groups, and the one whose blocks end past blockIdx.x looks for it.
-  for (int g = threadIdx.x; g <= G; g += kTileThreads) {
+  for (int g = threadIdx.x; g <= G; g += kColThreads) {
     const int v = offsets ? __ldcg(offsets + g) : (g == 0 ? 0 : rows);
     starts[g] = v < 0 ? 0 : (v > rows ? rows : v);
   }
@@ -207,10 +212,10 @@ __global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
   __syncthreads();
   const int row0 = where[0], nr = where[1];
   if (nr < 0) return;  // behind the last group
-  for (int cb = blockIdx.y; cb * 128 < cols; cb += gridDim.y) {
-    const int nc = cols - cb * 128;
+  for (int cb = blockIdx.y; cb * kCols < cols; cb += gridDim.y) {
+    const int nc = cols - cb * kCols;
     T t;
-    t.load(x + ((long long)row0 * cols + cb * 128) * (F32 ? 4 : 2), cols, nr, nc);
+    t.load(x + ((long long)row0 * cols + cb * kCols) * (F32 ? 4 : 2), cols, nr, nc);
     using V = Vec<F32>;
     uint32_t top[4];
 #pragma unroll
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
       mine[1] = make_uint4(top[2] << 16, top[2] & 0xFFFF0000u, top[3] << 16, top[3] & 0xFFFF0000u);
     }
     __syncthreads();
-    if (threadIdx.x < 128) {
+    if (threadIdx.x < kCols) {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < T::kStep; ++i) {
@@ -237,11 +242,11 @@ __global__ void __launch_bounds__(kTileThreads, F32 ? 2 : 3)
       const Fp8Block blk(fp8_scale(m));
       scales[threadIdx.x] = blk.scale;
       invs[threadIdx.x] = blk.inv;
-      if ((int)threadIdx.x < nc) scale[(long long)blockIdx.x * cols + cb * 128 + threadIdx.x] = blk.scale;
+      if ((int)threadIdx.x < nc) scale[(long long)blockIdx.x * cols + cb * kCols + threadIdx.x] = blk.scale;
     }
     __syncthreads();
     if (t.col < nc) {
-      uint8_t* at = q + ((long long)blockIdx.x * 128 + t.row) * cols + cb * 128 + t.col;
+      uint8_t* at = q + ((long long)blockIdx.x * 128 + t.row) * cols + cb * kCols + t.col;
       // Four columns at a time, so that four scales and reciprocals are in registers.
       uint32_t w[T::kRows][T::kN / 4];
 #pragma unroll
@@ -296,13 +301,13 @@ cudaError_t launch_fp8_quantize_squares(const void* x, bool f32, int64_t batch, 
 cudaError_t launch_fp8_quantize_columns(const void* x, bool f32, int rows, int cols, const int32_t* offsets, int G,
                                         uint8_t* q, float* scale, cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
-  const int blocks = (int)(fp8_padded_rows(rows, G) / 128), cb = fp8_blocks(cols);
-  // About a thousand thread blocks share the column blocks of each row block, so
+  const int blocks = (int)(fp8_padded_rows(rows, G) / 128), cb = (cols + kCols - 1) / kCols;
+  // About two thousand thread blocks share the column blocks of each row block, so
   // that each looks for its group once for several of them.
-  const int share = (1024 + blocks - 1) / blocks;
+  const int share = (2048 + blocks - 1) / blocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks, (unsigned)(cb < share ? cb : share), 1);
-  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.blockDim = dim3(kColThreads, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -230,6 +230,38 @@ def test_few_tiles(handle, counts, N, K, out_dtype, transposed):
     product(handle, counts, N, K, transposed, out_dtype)
 
 
+def test_few_tiles_same_bits(handle):
+    """Sums exchanged between thread blocks: launches back to back, in a graph and on two streams give the same bits."""
+    g, rows, N, K = gen(21), 40, 512, 4096
+    a, sa, w, sw = codes(g, rows, K), scales(g, rows, 32), codes(g, 1, N, K), scales(g, 1, 4, 32)
+    wu, su = codes(g, 1, N, K), scales(g, 1, 4, 32, std=2e-4)
+    first = torch.empty((rows, N), dtype=F32, device="cuda")
+    fq, fs = torch.empty((rows, N), dtype=U8, device="cuda"), torch.empty((rows, 4), device="cuda")
+    outs, qs, ss = torch.zeros((30, rows, N), device="cuda"), torch.zeros((30, rows, N), dtype=U8, device="cuda"), torch.zeros((30, rows, 4), device="cuda")
+    h2 = moe.Handle(0)
+
+    def call(h, o, q, s):
+        moe.grouped_gemm_fp8(h, a, sa, None, w, sw, o, num_groups=1, N=N, K=K)
+        moe.grouped_gate_up_fp8(h, a, sa, None, wu, su, wu, su, q, s, num_groups=1, H=K, I=N)
+
+    call(handle, first, fq, fs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(10):
+            call(handle, outs[i], qs[i], ss[i])
+    graph.replay()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(10, 30):
+        with torch.cuda.stream(streams[i % 2]):
+            call(handle if i % 2 else h2, outs[i], qs[i], ss[i])
+    torch.cuda.synchronize()
+    for i in range(30):
+        assert torch.equal(outs[i], first) and torch.equal(qs[i], fq) and torch.equal(ss[i], fs)
+    assert handle.device_status() == 0 and h2.device_status() == 0
+
+
 def test_many_groups(handle):
     product(handle, [(i * 7) % 5 for i in range(1024)], 128, 256, False, BF16)
 
