@@ -196,6 +196,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, code, limit_ns)) != 0;
 }
+// The same for what other CTAs of the cluster have stored (st_async): the wait
+// acquires at this CTA's scope, which does not order their stores before reads
+// here, so the phase is looked at once more, acquiring at the cluster's.
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                  int code, uint64_t limit_ns) {
+  if (!warp_wait(bar, parity, abort_flag, status, code, limit_ns)) return false;
+  mbar_acquire_cluster(bar, parity);
+  return true;
+}
 
 // ---- tensor maps (3-D: a group's matrix is cut off at its own edge)
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           st_async4(mapa_shared(smem_u32(place(part, c / kN * kPer + c % kPer)), to),
                     make_float4(sum[4 * c], sum[4 * c + 1], sum[4 * c + 2], sum[4 * c + 3]), mapa_shared(bar, to));
         }
-        if (!warp_wait(bar, 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) goto done;
+        if (!warp_wait_cluster(bar, 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) goto done;
         float x[4 * kPer * kKinds];
 #pragma unroll
         for (int c = 0; c < kPer * kKinds; ++c) {
@@ -732,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int to = 0; to < PARTS; ++to)
             st_async(mapa_shared(smem_u32(tops + (2 * part + half) * 128), to), top, mapa_shared(join_bar(q), to));
-          if (!warp_wait(join_bar(q), 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) goto done;
+          if (!warp_wait_cluster(join_bar(q), 0, abort_flag, p.status, MOE_DEV_TIMEOUT_EPILOGUE, p.limit_ns)) goto done;
 #pragma unroll
           for (int i = 0; i < 2 * PARTS; ++i) {
             const uint32_t t = tops[i * 128];
