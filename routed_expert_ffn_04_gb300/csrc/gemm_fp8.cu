@@ -749,11 +749,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const Fp8Block blk(fp8_scale(top));
           if (live && half == 0 && part == 0) p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = blk.scale;
+          fp8_by_size(blk.small(), [&](auto small) {
 #pragma unroll
-          for (int c = 0; c < kPer; ++c)
-            if (live && first + 4 * c < p.N)
-              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row + 4 * c) =
-                  blk.code4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            for (int c = 0; c < kPer; ++c)
+              if (live && first + 4 * c < p.N)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row + 4 * c) =
+                    blk.code4<decltype(small)::value>(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          });
         } else {
 #pragma unroll
           for (int c = 0; c < kPer; ++c) {
@@ -826,18 +828,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 0 && r < c_t.nrows)
           p.out_scale[(size_t)(c_t.row0 + r) * fp8_blocks(p.N) + c_t.n0 / 128] = scale;
         const Fp8Block blk(scale);
-        auto codes = [&](int c) {  // 16 of them
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 16 * c + 4 * i;
-            w[i] = blk.code4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-          }
-          return make_uint4(w[0], w[1], w[2], w[3]);
-        };
         reuse();
+        fp8_by_size(blk.small(), [&](auto small) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = codes(c);
+          for (int c = 0; c < 4; ++c) {  // 16 codes
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int e = 16 * c + 4 * i;
+              w[i] = blk.code4<decltype(small)::value>(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+            }
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        });
         fence_proxy_async_smem();
         __syncwarp();
         send(64, 1, c_t.n0 + col0);
