@@ -141,7 +141,9 @@ typedef enum {
    * both streams' GEMMs size their grids to every SM, and the shared
    * kernels fill the SMs that routing and permutation leave idle (no fixed
    * split measured faster on the decode, MX, skewed or prefill workloads).
-   * k > 0 = k SMs (at most half). The result is the same either way. */
+   * k > 0 = k SMs (at most half; products of FP8_BLOCK128 layers that are few
+   * tiles with a long reduction share that out and take the SMs that they take
+   * without the option). The result is the same either way. */
   MOE_OPT_SHARED_SMS = 4,
   /* 1 (default) = in bf16 layers whose routed GEMM-1 takes the tokens-as-M
    * tiling (more than 48 rows per expert on average, or mode 2), the GEMM-1

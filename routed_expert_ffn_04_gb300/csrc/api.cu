@@ -219,6 +219,7 @@ cudaError_t swiglu_fp8(moe_handle_t h, int G, const int32_t* offsets, int rows, 
   g.offsets = offsets;
   g.rows = rows;
   g.num_sms = num_sms;
+  g.device_sms = h->num_sms;
   g.status = h->status;
   g.wait_limit_ns = h->wait_limit_ns;
   g.N = I;

@@ -53,7 +53,7 @@ Fp8GemmArgs base_args(moe_handle_t h, int G, const int32_t* offsets, int rows, i
   g.rows = rows;
   g.N = N;
   g.K = K;
-  g.num_sms = handle_num_sms(h);
+  g.num_sms = g.device_sms = handle_num_sms(h);
   g.status = handle_status_word(h);
   g.wait_limit_ns = handle_wait_limit_ns(h);
   return g;

@@ -910,7 +910,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // costs about 2 us for up to 32 rows (K = 4096, 15 tiles: 15.3 us, in four parts 9.0,
 // in eight 8.2; K = 1024: 7.1, 6.7, 6.9; 30 tiles 7.2, 7.4), 4 for 64 (K = 2048 and
 // 1024, 30 tiles: 10.6, in four parts 11.2; 16 tiles 10.4, 10.0 and 7.5, 9.3), 8 for
-// 128 (K = 4096: 16.9, 17.3).
+// 128 (K = 4096: 16.9, 17.3). The order of the sums is the parts', so the sizes and the
+// device decide, not how many SMs the call may take: few tiles take one wave of the
+// device all the same.
 int parts_of(long long tiles, int rows, int blocks, int num_sms) {
   if (rows > 64 || tiles > 36 || blocks < (rows > 32 ? 20 : 10)) return 1;
   if (tiles <= 15 && blocks >= 24 && 8 * tiles <= num_sms) return 8;
@@ -961,7 +963,7 @@ cudaError_t run_fp8(const Fp8GemmArgs& a, cudaStream_t s) {
     return launch(grouped_gemm_fp8_kernel<MODE, 1>, (long long)G * ((a.N + 127) / 128) * ((a.K + 255) / 256), 1);
   } else {
     const long long tiles = n_wt * (a.rows / 128 + (G < a.rows ? G : a.rows));  // at most: of groups that have rows
-    const int parts = parts_of(tiles, a.rows, fp8_blocks(a.K), a.num_sms);
+    const int parts = parts_of(tiles, a.rows, fp8_blocks(a.K), a.device_sms);
     if (parts == 8) return launch(grouped_gemm_fp8_kernel<MODE, 8>, tiles, 8);
     if (parts == 4) return launch(grouped_gemm_fp8_kernel<MODE, 4>, tiles, 4);
     return launch(grouped_gemm_fp8_kernel<MODE, 1>, tiles, 1);

@@ -285,7 +285,8 @@ struct Fp8GemmArgs {
   void* out;               // [rows, N] bf16 or fp32; GATE_UP: codes; WEIGHT_GRAD: [G, N, K]
   int out_f32;
   float* out_scale;        // GATE_UP: [rows, N/128]
-  int num_sms;
+  int num_sms;             // SMs to take; device_sms: that there are, which decide how sums are split
+  int device_sms;
   int* status;
   uint64_t wait_limit_ns;
 };

@@ -1,9 +1,11 @@
-"""E4M3 with one fp32 scale per block of 128 at its edges: scales so small that a quotient's remainder is subnormal, and
-sums shared between thread blocks over many launches."""
+"""E4M3 with one fp32 scale per block of 128 at its edges: scales so small that a quotient's remainder is subnormal, the
+layer's answer under an option that only sizes its launches, and sums shared between thread blocks over many launches."""
 import pytest
 import torch
 
 import routed_expert_ffn_04_gb300 as moe
+import synth
+from test_gpu_fp8_layer import problem
 
 pytestmark = pytest.mark.gpu
 
@@ -126,6 +128,22 @@ def test_gate_up_of_small_scales(handle, rows, H, I):
         got.append((q, s))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1] * 2.0 ** -100, got[1][1])
     assert (got[1][1] < 2.0 ** -80).all()
+
+
+# ---------------------------------------------------------------- the layer's option for the shared expert's SMs
+@pytest.mark.parametrize("shape", [
+    synth.MoEShape("fd", T=9, H=4096, E=3, K=1, I=128, I_shared=256, dtype="fp8"),
+    synth.MoEShape("fe", T=33, H=2560, E=4, K=2, I=2560, I_shared=2560, dtype="fp8"),
+    synth.MoEShape("ff", T=300, H=512, E=32, K=4, I=256, I_shared=256, dtype="fp8")], ids=lambda s: s.name)
+def test_shared_sms_do_not_change_the_result(shape):
+    """MOE_OPT_SHARED_SMS gives the same bits whatever it is, also where a product's reduction is shared out."""
+    x, logits, w = problem(shape, 2)
+    layer = moe.MoELayer(shape, w, device=0)
+    out = layer(x, logits).clone()
+    for k in (1, 4, 8, 40, 60, 1000):
+        layer.handle.set_option(moe.MOE_OPT_SHARED_SMS, k)
+        assert torch.equal(layer(x, logits), out), f"{k} SMs"
+    assert layer.handle.device_status() == 0
 
 
 # ---------------------------------------------------------------- parts of a reduction
