@@ -51,6 +51,7 @@ class MoEBlock:
         if balance_coef:
             self.load, self.prob, self.balance = new(1, E, dt=i32), new(1, E, dt=f32), new(1, dt=f32)
             self.one = torch.ones(1, device=self.dev)
+            torch.cuda.current_stream(self.dev).synchronize()  # forward() and backward() may run on any stream
             sizes.append(moe.balance_loss_workspace_size(self.cfg))
         self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=self.dev)  # one stream: the calls take turns
 
