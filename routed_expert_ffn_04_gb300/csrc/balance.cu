@@ -19,9 +19,9 @@
 // The gradient reads and writes each logit once: 65536 x 256 with an addend 34 us at
 // 5.9 TB/s, 8192 x 192 5.6.
 //
-// Scores that all underflow (every logit far below 0) keep their ratios: the
-// shares are then taken relative to the largest. A token whose scores are all 0
-// (every logit -infinity) adds nothing and gets a zero gradient.
+// Scores that are all small (every logit far below 0) keep their ratios: where a
+// token's sum is below 2^-25 the shares are taken relative to the largest. A token
+// whose scores are all 0 (every logit -infinity) adds nothing and gets a zero gradient.
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -189,8 +189,10 @@ __device__ __forceinline__ float scores(float (&x)[S::V], float (&slope)[SLOPE ?
       sum += x[j];
     }
     sum = lanes_sum<S::L>(sum);
-    const bool tiny = sum < 1e-30f;
-    if (__any_sync(0xFFFFFFFFu, tiny)) {  // sigma(x) = exp(x) there: from the logits once more
+    // Below 2^-25 sigma(x) is exp(x) to half an ulp, and scores far below the largest
+    // would be flushed to 0 although their shares are not: from the logits once more.
+    const bool tiny = sum < 2.98023224e-8f;
+    if (__any_sync(0xFFFFFFFFu, tiny)) {
       float sg[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) sg[j] = x[j];
