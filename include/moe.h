@@ -246,7 +246,7 @@ MOE_API moe_status_t moe_grouped_gemm_workspace_size(int rows, int num_groups, i
  *   scales and a as in MXFP8.
  * FP8_BLOCK128: a and w_* E4M3 codes, a_scale [rows, H/128] and s_gate, s_up,
  *   s_down (per square) fp32; h is rounded as moe_grouped_gate_up_fp8 does.
- *   H % 128 == 0, I % 128 == 0.
+ *   H % 128 == 0, I % 128 == 0, both up to 65536, rows <= 2^30.
  * offsets (device): [num_groups + 1] int32, non-decreasing, offsets[0] = 0,
  *   offsets[num_groups] <= rows; NULL means one group of all rows (a dense
  *   SwiGLU MLP, used for the shared expert).
@@ -622,12 +622,13 @@ typedef enum { MOE_FLOAT_BF16 = 0, MOE_FLOAT_F32 = 1 } moe_float_t;
  * codes of NaN. x (device): bf16 or fp32. q (device): [batch, rows, cols]
  * uint8; scale (device): [batch, rows, ceil(cols/128)] or [batch,
  * ceil(rows/128), ceil(cols/128)] fp32. q and scale overlap neither x nor each
- * other. Limits: cols % 16 == 0, batch * rows * cols <= 2^40. */
+ * other. Limits: cols % 16 == 0, rows <= 2^30, batch * rows * cols <= 2^40, fewer
+ * than 2^31 squares. */
 MOE_API moe_status_t moe_quantize_fp8(moe_handle_t h, const void* x, moe_float_t x_type, int64_t batch, int rows,
                                       int cols, int squares, uint8_t* q, float* scale, moe_stream_t stream);
 
 /* Rows that any `rows` rows in num_groups groups take with each group padded
- * to a multiple of 128 (host-only): 128 (rows / 128 + num_groups). */
+ * to a multiple of 128 (host-only): 128 (rows / 128 + num_groups). rows <= 2^30. */
 MOE_API moe_status_t moe_fp8_padded_rows(int rows, int num_groups, int64_t* padded);
 
 /* Quantise x [rows, cols] along its rows, group by group, for
@@ -654,7 +655,7 @@ MOE_API moe_status_t moe_quantize_fp8_columns(moe_handle_t h, const void* x, moe
  * out (device): [rows, N] bf16 or fp32, rounded once; rows of no group are
  * not written, and such rows of a may hold anything. No overlap of out with an
  * input (MOE_ERR_INVALID_ARG). Limits: num_groups <= 1024, N and K multiples
- * of 16 up to 65536, rows * max(N, K) < 2^40. */
+ * of 16 up to 65536, rows <= 2^30, rows * max(N, K) < 2^40. */
 MOE_API moe_status_t moe_grouped_gemm_fp8(moe_handle_t h, int num_groups, int rows, int N, int K, int transposed,
                                           const uint8_t* a, const float* a_scale, const int32_t* offsets,
                                           const uint8_t* w, const float* w_scale, moe_float_t out_type, void* out,

@@ -481,7 +481,7 @@ MOE_API moe_status_t moe_grouped_swiglu_gemm(moe_handle_t h, int num_groups, int
   if (mx && (!a_scale || !s_gate || !s_down || H % 128 || I % 128)) return MOE_ERR_INVALID_ARG;
   if (w4 && !weights_aligned32(w_gate, w_up, w_down)) return MOE_ERR_INVALID_ARG;
   // MXFP8: s_gate holds the gate and up scale atoms together, s_up is unused.
-  if (fp8 && (!a_scale || !s_gate || !s_up || !s_down || H % 128 || I % 128 || H > 65536 || I > 65536))
+  if (fp8 && (!a_scale || !s_gate || !s_up || !s_down || H % 128 || I % 128 || H > 65536 || I > 65536 || rows > kFp8MostRows))
     return MOE_ERR_INVALID_ARG;
   if (fp8 && (!aligned16(a_scale) || !aligned16(s_up))) return MOE_ERR_INVALID_ARG;
   const void* ptrs[] = {a, offsets, w_gate, w_up, w_down, y, ws, s_gate, s_down};

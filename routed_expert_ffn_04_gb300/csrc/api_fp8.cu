@@ -41,7 +41,7 @@ bool clash(const Span& out, const Span& out2, const Span (&in)[N]) {
 
 // Groups, rows, and the two sizes of a product's weights.
 bool shape_ok(int G, int rows, int a, int b, const int32_t* offsets) {
-  return G > 0 && G <= 1024 && rows >= 0 && a > 0 && b > 0 && a % 16 == 0 && b % 16 == 0 && a <= 65536 && b <= 65536 &&
+  return G > 0 && G <= 1024 && rows >= 0 && rows <= kFp8MostRows && a > 0 && b > 0 && a % 16 == 0 && b % 16 == 0 && a <= 65536 && b <= 65536 &&
          (long long)rows * (a > b ? a : b) < (1ll << 40) && (offsets || G == 1);
 }
 size_t squares(int a, int b) { return (size_t)fp8_blocks(a) * fp8_blocks(b); }
@@ -66,8 +66,9 @@ extern "C" {
 MOE_API moe_status_t moe_quantize_fp8(moe_handle_t h, const void* x, moe_float_t x_type, int64_t batch, int rows,
                                       int cols, int squares_, uint8_t* q, float* scale, moe_stream_t stream) {
   if (!type_ok(x_type) || batch < 0 || rows < 0 || cols <= 0 || cols % 16) return MOE_ERR_INVALID_ARG;
-  if (batch > (1ll << 31) || (rows && batch * rows > (1ll << 40) / cols)) return MOE_ERR_INVALID_ARG;
+  if (rows > kFp8MostRows || batch > (1ll << 31) || (rows && batch * rows > (1ll << 40) / cols)) return MOE_ERR_INVALID_ARG;
   const int64_t all = batch * rows;
+  if (squares_ && batch * fp8_blocks(rows) * fp8_blocks(cols) >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
   if (all > 0 && (!x || !q || !scale)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(x, q, scale)) return MOE_ERR_INVALID_ARG;
   const size_t n = (size_t)all * cols;
@@ -83,7 +84,7 @@ MOE_API moe_status_t moe_quantize_fp8(moe_handle_t h, const void* x, moe_float_t
 }
 
 MOE_API moe_status_t moe_fp8_padded_rows(int rows, int num_groups, int64_t* padded) {
-  if (!padded || rows < 0 || num_groups <= 0 || num_groups > 1024) return MOE_ERR_INVALID_ARG;
+  if (!padded || rows < 0 || rows > kFp8MostRows || num_groups <= 0 || num_groups > 1024) return MOE_ERR_INVALID_ARG;
   *padded = fp8_padded_rows(rows, num_groups);
   return MOE_OK;
 }

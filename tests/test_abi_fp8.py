@@ -124,3 +124,46 @@ def test_python_refuses_host_tensors():
         assert e.value.status == INVALID
     with pytest.raises(TypeError):
         moe.balance_loss(H, c, f, i, i, f, f, f, coef="much")
+
+
+def test_row_limits(lib):
+    """Rows up to 2^30: rows and tiles are counted in 32 bits, with every group padded to a multiple of 128. Allowed calls
+    get as far as the device, which this handle names wrongly (and they are left out where a device could be found)."""
+    wrong = ctypes.create_string_buffer(1 << 16)
+    ctypes.memmove(wrong, (1 << 20).to_bytes(4, "little"), 4)
+    h = ctypes.cast(wrong, P)
+    far = [P((i + 1) << 44) for i in range(9)]
+    x, s, off, w, sw, o, s2 = far[:7]
+    T = 1 << 30
+
+    def gemm(r, tr=0):
+        return lib.moe_grouped_gemm_fp8(h, 2, r, 16, 16, tr, x, s, off, w, sw, 0, o, None)
+
+    def gate_up(r):
+        return lib.moe_grouped_gate_up_fp8(h, 2, r, 16, 16, x, s, off, w, sw, far[7], far[8], o, s2, None)
+
+    def wgrad(r):
+        return lib.moe_grouped_weight_grad_fp8(h, 2, r, 16, 16, x, s, w, sw, off, 0, o, None)
+
+    def swiglu(r):
+        return lib.moe_grouped_swiglu_gemm(h, 2, r, 128, 128, moe.MOE_FP8_BLOCK128, x, s, off, w, far[7], far[8], sw, sw, sw,
+                                           o, s2, 1 << 42, None)
+
+    def quantize(r, squares=0, batch=1):
+        return lib.moe_quantize_fp8(h, x, 0, batch, r, 16, squares, o, s, None)
+
+    def columns(r):
+        return lib.moe_quantize_fp8_columns(h, x, 0, 2, r, 16, off, o, s, None)
+
+    calls = [gemm, lambda r: gemm(r, 1), gate_up, wgrad, swiglu, quantize, lambda r: quantize(r, 1), columns]
+    for call in calls:
+        for r in (T + 1, 2**31 - 129, 2**31 - 1):
+            assert call(r) == INVALID
+        if not torch.cuda.is_available():
+            assert call(T) == moe.MOE_ERR_CUDA
+    assert quantize(1, 1, 1 << 31) == INVALID  # squares
+    if not torch.cuda.is_available():
+        assert quantize(1, 1, (1 << 31) - 1) == moe.MOE_ERR_CUDA and quantize(1, 0, 1 << 31) == moe.MOE_ERR_CUDA
+    n = ctypes.c_int64(0)
+    assert lib.moe_fp8_padded_rows(T, 1024, ctypes.byref(n)) == 0 and n.value == T + 1024 * 128
+    assert lib.moe_fp8_padded_rows(T + 1, 1, ctypes.byref(n)) == INVALID
