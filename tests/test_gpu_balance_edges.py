@@ -1,10 +1,11 @@
-"""The balance loss of the smallest scores, and the block's on a stream of its own."""
+"""The balance loss of the smallest scores, for every number of experts in its two-launch form, and the block's on a
+stream of its own."""
 import pytest
 import torch
 
 import routed_expert_ffn_04_gb300 as moe
 import synth
-from test_gpu_balance import F64, I32, SCORES, grad64, run, share_tol, shares64
+from test_gpu_balance import F64, I32, SCORES, grad64, problem, reference, run, share_tol, shares64
 
 pytestmark = pytest.mark.gpu
 
@@ -38,6 +39,36 @@ def test_small_sigmoid_scores_keep_their_ratios(handle, top):
     want = grad64(logits, counts, [0, T], [1.0], "sigmoid", 1.0, E, K)
     f = float(counts.max()) * E / (K * T)
     assert ((dl.to(F64) - want).abs() <= 2 * f / T * p * tol).all()
+
+
+# ---------------------------------------------------------------- shapes of the two-launch form
+# More logits than one launch takes (2^14 or 2^16 per thread block of a cluster), for each number of lanes and values.
+STRIPS = [(100000, 8, 2, 1), (100000, 7, 2, 3), (20000, 16, 3, 1), (60000, 13, 3, 3), (30000, 32, 4, 1), (30000, 30, 4, 2),
+          (9000, 64, 4, 1), (9000, 63, 4, 2), (5000, 120, 8, 2), (5000, 160, 8, 1), (3000, 256, 8, 1), (3000, 250, 8, 2),
+          (3000, 255, 8, 1), (2000, 512, 8, 1), (2000, 500, 8, 2), (1500, 1000, 8, 2), (1500, 1024, 32, 1), (1500, 1023, 8, 1)]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T, E, K, B", STRIPS)
+def test_strips(handle, T, E, K, B, score):
+    assert T * E > (1 << (14 if B == 1 else 16)) * 8
+    logits, idx, g = problem(T, E, K, seed=T + E)
+    ends = [0] + [T * i // B + 3 * i for i in range(1, B)] + [T]
+    cfg, seq, counts, prob, loss = run(handle, logits, idx, ends, score, 0.25, E, K)
+    rc, rp, rl = reference(logits, idx, ends, score, 0.25, E, K)
+    assert torch.equal(counts, rc)
+    tol = share_tol(E) + (T / 512 + 64) * 2.0 ** -24  # as test_gpu_balance: a warp's tokens in a row, then warps, strips
+    assert ((prob.to(F64) - rp).abs() <= tol * rp).all()
+    assert ((loss.to(F64) - rl).abs() <= (tol + (E / 32 + 16) * 2.0 ** -24) * rl).all()
+    dloss = torch.rand(B, device="cuda", generator=g) + 0.5
+    dl = torch.full((T, E), 7.0, device="cuda")
+    moe.balance_loss_backward(handle, cfg, logits, counts, dloss, dl, coef=0.25, score=SCORES[score], seq_offsets=seq)
+    want = grad64(logits, counts, ends, dloss, score, 0.25, E, K)
+    p = shares64(logits.to(F64), score)
+    for b in range(B):
+        lo, hi = ends[b], ends[b + 1]
+        size = float(dloss[b]) * 0.25 / (hi - lo) * float(counts[b].max()) * E / (K * (hi - lo))
+        assert ((dl[lo:hi].to(F64) - want[lo:hi]).abs() <= size * p[lo:hi] * (2 * share_tol(E) + 2.0 ** -20) + 1e-30).all()
 
 
 # ---------------------------------------------------------------- the block on a stream of its own

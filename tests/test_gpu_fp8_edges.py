@@ -5,6 +5,7 @@ import torch
 
 import routed_expert_ffn_04_gb300 as moe
 import synth
+from test_gpu_fp8 import quantize64
 from test_gpu_fp8_layer import problem
 
 pytestmark = pytest.mark.gpu
@@ -128,6 +129,24 @@ def test_gate_up_of_small_scales(handle, rows, H, I):
         got.append((q, s))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1] * 2.0 ** -100, got[1][1])
     assert (got[1][1] < 2.0 ** -80).all()
+
+
+@pytest.mark.parametrize("form", ["rows", "squares", "columns"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32])
+@pytest.mark.parametrize("R, C", [(301, 4112), (33, 2064), (1000, 1040), (2, 65536), (5, 65520)])
+def test_wide_rows(handle, R, C, dtype, form):
+    """More blocks per row than a thread block takes at a time, whole ones and not, up to the widest that products take."""
+    x = torch.randn((R, C), device="cuda", generator=torch.Generator(device="cuda").manual_seed(R + C)).to(dtype)
+    height, width = {"rows": (1, 128), "squares": (128, 128), "columns": (128, 1)}[form]
+    want, sw = quantize64(x, height, width)
+    P = moe.fp8_padded_rows(R) if form == "columns" else R
+    q = torch.empty((P, C), dtype=U8, device="cuda")
+    s = torch.empty((P // 128 if form == "columns" else sw.shape[0], sw.shape[1]), device="cuda")
+    if form == "columns":
+        moe.quantize_fp8_columns(handle, x, None, q, s, num_groups=1)
+    else:
+        moe.quantize_fp8(handle, x, q, s, squares=form == "squares")
+    assert torch.equal(s[:sw.shape[0]], sw[:, :s.shape[1]]) and torch.equal(q[:R].view(E4M3).float(), want.view(E4M3).float())
 
 
 # ---------------------------------------------------------------- the layer's option for the shared expert's SMs
