@@ -622,7 +622,7 @@ typedef enum { MOE_FLOAT_BF16 = 0, MOE_FLOAT_F32 = 1 } moe_float_t;
  * codes of NaN. x (device): bf16 or fp32. q (device): [batch, rows, cols]
  * uint8; scale (device): [batch, rows, ceil(cols/128)] or [batch,
  * ceil(rows/128), ceil(cols/128)] fp32. q and scale overlap neither x nor each
- * other. Limits: cols % 16 == 0, rows <= 2^30, batch * rows * cols <= 2^40, fewer
+ * other. Limits: cols % 16 == 0, rows and cols <= 2^30, batch * rows * cols <= 2^40, fewer
  * than 2^31 squares. */
 MOE_API moe_status_t moe_quantize_fp8(moe_handle_t h, const void* x, moe_float_t x_type, int64_t batch, int rows,
                                       int cols, int squares, uint8_t* q, float* scale, moe_stream_t stream);

@@ -66,7 +66,7 @@ extern "C" {
 MOE_API moe_status_t moe_quantize_fp8(moe_handle_t h, const void* x, moe_float_t x_type, int64_t batch, int rows,
                                       int cols, int squares_, uint8_t* q, float* scale, moe_stream_t stream) {
   if (!type_ok(x_type) || batch < 0 || rows < 0 || cols <= 0 || cols % 16) return MOE_ERR_INVALID_ARG;
-  if (rows > kFp8MostRows || batch > (1ll << 31) || (rows && batch * rows > (1ll << 40) / cols)) return MOE_ERR_INVALID_ARG;
+  if (rows > kFp8MostRows || cols > kFp8MostRows || batch > (1ll << 31) || (rows && batch * rows > (1ll << 40) / cols)) return MOE_ERR_INVALID_ARG;
   const int64_t all = batch * rows;
   if (squares_ && batch * fp8_blocks(rows) * fp8_blocks(cols) >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
   if (all > 0 && (!x || !q || !scale)) return MOE_ERR_INVALID_ARG;

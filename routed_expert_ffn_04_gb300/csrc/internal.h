@@ -292,7 +292,7 @@ struct Fp8GemmArgs {
 };
 cudaError_t gemm_fp8_prepare_device();
 cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, int mode, cudaStream_t s);
-// Rows of a call at most: rows and tiles, with every group padded, are counted in 32 bits.
+// Rows of a call at most (and a quantiser's columns): rows and tiles, with every group padded, are counted in 32 bits.
 constexpr int kFp8MostRows = 1 << 30;
 // Rows that hold any `rows` rows in G groups with each group's padded to a multiple of 128.
 inline int64_t fp8_padded_rows(int64_t rows, int64_t G) { return (rows / 128 + G) * 128; }

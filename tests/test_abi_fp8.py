@@ -164,6 +164,9 @@ def test_row_limits(lib):
     assert quantize(1, 1, 1 << 31) == INVALID  # squares
     if not torch.cuda.is_available():
         assert quantize(1, 1, (1 << 31) - 1) == moe.MOE_ERR_CUDA and quantize(1, 0, 1 << 31) == moe.MOE_ERR_CUDA
+    for c in (T + 16, 2**31 - 16):
+        for sq in (0, 1):
+            assert lib.moe_quantize_fp8(h, x, 0, 1, 1, c, sq, o, s, None) == INVALID
     n = ctypes.c_int64(0)
     assert lib.moe_fp8_padded_rows(T, 1024, ctypes.byref(n)) == 0 and n.value == T + 1024 * 128
     assert lib.moe_fp8_padded_rows(T + 1, 1, ctypes.byref(n)) == INVALID
