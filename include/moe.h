@@ -647,7 +647,8 @@ MOE_API moe_status_t moe_quantize_fp8_columns(moe_handle_t h, const void* x, moe
 /* out[r] = sum_k a[r,k] w[g][n,k] for the rows r of each group g; with
  * `transposed`, sum_k a[r,k] w[g][k,n] (the gradient of an input from the
  * forward's weights as they are). fp32 accumulation, each block's exact
- * products times its two scales.
+ * products times its two scales, whose product is formed first, in fp32: it
+ * loses bits below 2^-126 and is infinite from 2^128 on.
  * a (device): [rows, K] codes, a_scale [rows, ceil(K/128)] (rows). w (device):
  * [num_groups, N, K] codes (transposed: [num_groups, K, N]), w_scale
  * [num_groups] x squares of them. offsets (device): as
@@ -663,7 +664,8 @@ MOE_API moe_status_t moe_grouped_gemm_fp8(moe_handle_t h, int num_groups, int ro
 
 /* The first half of the SwiGLU experts: h = silu(a W_gate^T) * (a W_up^T) per
  * group, quantised to rows of E4M3 in the same pass (the fp32 h, by the rule of
- * moe_quantize_fp8): the next moe_grouped_gemm_fp8's a.
+ * moe_quantize_fp8): the next moe_grouped_gemm_fp8's a. silu's exponential is
+ * the fast one (2 + 1.2 |x| ulp); gates below -87.3 (silu above -1.1e-36) give 0.
  * a [rows, H] codes with a_scale [rows, ceil(H/128)]; w_gate, w_up
  * [num_groups, I, H] codes with s_gate, s_up, their squares' scales; q
  * [rows, I] and scale [rows, ceil(I/128)] out (all device). The rest as

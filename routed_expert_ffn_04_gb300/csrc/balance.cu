@@ -13,9 +13,12 @@
 // cluster of blocks per sequence. Else a block takes a strip of tokens, and for each
 // sequence in it writes one row of partial sums (row strip + sequence: unique, since
 // both only grow), and a second launch adds a sequence's rows in a fixed order, eight
-// blocks of a cluster sharing the experts. The logits are read once; many tokens are
-// bound by instructions and waits rather than HBM (65536 x 256 in 29 sequences: 21.3
-// us, of them 4 the second launch; bytes 10.2), few by the launch (64 x 192: 4.3 us).
+// blocks of a cluster sharing the experts. The logits are read once. Many tokens are
+// bound by waits (65536 x 256 in 29 sequences: 22 us, of them 4 the second launch;
+// bytes 10.2): the first launch issues in 43% of its cycles, DRAM is at 41%, and of a
+// warp's time between two instructions a third is for loaded logits, an eighth each
+// for shuffles and exponentials and for barriers, a seventh the instructions' own
+// latency. Few tokens are bound by the launch (64 x 192: 4.3 us).
 // The gradient reads and writes each logit once: 65536 x 256 with an addend 34 us at
 // 5.9 TB/s, 8192 x 192 5.6.
 //
@@ -143,8 +146,9 @@ struct Shape {
   }
 };
 
-// exp(x) and 1 / x to 2 ulp, tiny results as 0: two instructions each, where the
-// forms that keep subnormals take five.
+// exp(x) to 2 + 1.2 |x| ulp (the product with log2 e is rounded) and 1 / x to 2,
+// results below 2^-126 as 0: two instructions and one, where the forms that keep
+// subnormals take five.
 __device__ __forceinline__ float exp_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
@@ -594,9 +598,12 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
   p.part = static_cast<float*>(a.scratch);
   p.part_n = reinterpret_cast<int32_t*>(p.part + ((size_t)strips + a.B) * a.E);
   // One launch where a cluster of up to eight blocks is enough even if one sequence has
-  // all tokens: 512 x 192 5.6 -> 4.6 us, 1024 x 256 6.2 -> 6.4. With many sequences a
-  // strip's blocks take them one by one, and more is worth it: 84 x 56 in 63 sequences
-  // 23.1 -> 5.1, 8192 x 64 in 17 28 -> 10.8 with nearly all tokens in the first.
+  // all tokens (its length is known on the device alone). In a graph, two launches and
+  // one, us: 512 x 192 5.6, 4.8; 1024 x 256 6.4, 6.3; 8192 x 192 8.0, 19.0. With many
+  // sequences a strip's blocks take them one by one, and more is worth it: 84 x 56 in 63
+  // 20.3, 5.0; 8192 x 64 in 17 with nearly all tokens in the first 26.9, 10.6. The bound
+  // is for such batches: past it even sequences would be better off in one launch too
+  // (8192 x 64 in 64 9.2, 5.3; 2000 x 64 in 200 10.0, 5.8; 20000 x 64 in 1000 19.1, 18.4).
   int cluster = 8;
   while (cluster > 1 && a.B * cluster > 152) cluster /= 2;
   if ((long long)a.T * a.E <= (a.B == 1 ? 1 << 14 : 1 << 16) * (long long)cluster) return pick<kOne>(p, a.softmax, cluster, s);

@@ -8,8 +8,8 @@
 // One pass: a block's values stay in registers between its maximum and its
 // codes. Floors are of HBM, 2 (4) bytes in and 1 out per value; the rows take 75% of
 // the issue slots beside it (maxima of two bf16 values at a time: 23.6 -> 18.4 us).
-// 33.6 million bf16 values (floor 15 us): rows of 4096 17.9, squares 18.5, columns of
-// uneven groups 22.7; fp32 (24.9): rows 27.8, columns 34.2.
+// 33.6 million bf16 values (floor 15 us): rows of 4096 18.1, squares 18.6, columns of
+// uneven groups 23.0; fp32 (24.9): rows 27.9, squares 33.6, columns 34.2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -53,8 +53,7 @@ struct Vec {
 // A block of a row per 16 lanes (bf16) or warp (fp32), kInFlight of them loading
 // at a time. WHOLE: rows of whole blocks, so that block b is values 128 b .. of
 // the matrix; else a thread finds its first block's row by one division and
-// steps from there (a division per block took as long as the bytes: 23.6 us for
-// 8192 x 4096 bf16, 16.9 without).
+// steps from there (with a division per block they took half as long again).
 constexpr int kRowThreads = 256;
 constexpr int kInFlight = 4;
 

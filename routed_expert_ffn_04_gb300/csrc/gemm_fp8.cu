@@ -39,11 +39,15 @@
 // 700 cycles (265 for the additions of a scheduler's two warps and 100-280 for its
 // reads of TMEM, which hardly overlap, and the barriers) against 512 of MMAs, and the
 // tile's own end (GATE_UP: 4000 cycles of SwiGLU and codes, half of them waits for
-// exp and the quotient). Measured, H 4096, I 1536, 192 groups:
-//   GATE_UP      341 rows 809 us, 2.0 PFLOP/s; 4 rows 361 us, 6.7 TB/s
-//   FORWARD      341 rows 544 us, 1.5 PFLOP/s and 4.4 TB/s (2.4 GB, 1.1 of fp32 results)
-//   WEIGHT_GRAD  341 rows 773 us (2.8 GB, of them 2.4 of bf16 results)
-//   FORWARD      dense 8192 x 4096 x 4096 111 us, 2.5 PFLOP/s
+// exp and the quotient). Measured, H 4096, I 1536, 192 groups, 341 rows each and (in
+// brackets) routed ones of that mean:
+//   GATE_UP      809 us, 2.0 PFLOP/s (908); of 4 rows 361 us, 6.7 TB/s
+//   FORWARD      544 us, 1.5 PFLOP/s and 4.4 TB/s (573; 2.4 GB, 1.1 of fp32 results)
+//   WEIGHT_GRAD  773 us (777; 2.8 GB, of them 2.4 of bf16 results)
+//   FORWARD      dense 8192 x 4096 x 4096 118 us, 2.3 PFLOP/s
+// TRANSPOSED with a short reduction is bound by neither: 16384 uneven rows of 64
+// groups, K 768, N 2048 take 46 us, 1500 cycles a block, in which the MMAs are at work
+// a third of the time, instructions issue in 37% and L2 hands out 27% of its rate.
 //
 // Roles (12 warps, each walking its tiles in step): 0 loads, 1 issues the MMAs, 2
 // and 3 multiply each block's scales into factors ahead of the epilogue, 4-11 are
@@ -186,7 +190,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
-// x sigma(x), 2 ulp: the approximate quotient, which is 0 past 2^126 as it should be here.
+// x sigma(x) to 4 + 1.2 |x| ulp (exp's argument is rounded), and the approximate
+// quotient, which is 0 past 2^126: gates below -87.3 give 0 instead of -1e-36 and less.
 __device__ __forceinline__ float silu_fast(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 // Bounded wait by a whole warp. The waits suspend: polling took issue slots from
@@ -632,11 +637,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MODE == kFp8WeightGrad) {
         // Columns' factors as well. They are read before the wait for their columns
         // (which the compiler moves no load across): with 32 columns at a time there
-        // were no registers for that, and each read was waited for (192 x 341 rows, by
-        // pairs of CTAs: 871 -> 788 us). Every lane reads all 128, which fills the shared
-        // memory's port (648 us without); TMEM loads of 16 lanes x 256 bits, with which a
-        // lane has four rows and a quarter of the columns, were no faster (798, 64
-        // columns at a time 817).
+        // were no registers for that, and each read was waited for (192 x 341 rows, in
+        // tiles of 256 rows on pairs of CTAs: 871 -> 788 us; on single ones 773). Every
+        // lane reads all 128, which fills the shared memory's port (648 us without); TMEM
+        // loads of 16 lanes x 256 bits, with which a lane has four rows and a quarter of
+        // the columns, were no faster (798, 64 columns at a time 817).
 #pragma unroll 1
         for (int kb = 0; kb < c_t.kb; ++kb) {
           take_factors();
